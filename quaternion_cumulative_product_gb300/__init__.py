@@ -17,8 +17,10 @@ chunk carries between the two), ``quat_cumprod_fwd_bf16`` /
 ``quat_cumprod_bwd_bf16`` (bfloat16 tensors), ``quat_cumprod_bwd_noalloc``
 (no allocation), ``quat_cumprod_fwd_bwd_host`` (a whole step on host
 tensors, copies overlapped with the kernels), ``quat_cumprod_plan`` and
-``quat_cumprod_status``.  The
-autograd wrapper is in :mod:`quaternion_cumulative_product_gb300.autograd`.
+``quat_cumprod_status``.  The operators around the scan (norm and rotation of
+queries and keys, the gated delta rule) are in
+:mod:`quaternion_cumulative_product_gb300.mixer` and reached from here too.  The
+autograd wrappers are in :mod:`quaternion_cumulative_product_gb300.autograd`.
 """
 from __future__ import annotations
 
@@ -35,6 +37,9 @@ __all__ = [
     "quat_cumprod_fwd_bf16", "quat_cumprod_bwd_bf16",
     "quat_cumprod_bwd_noalloc", "quat_cumprod_fwd_bwd_host", "quat_cumprod_plan", "quat_cumprod_status",
     "quat_cumprod_strerror",
+    "QS_DELTA_STEPS", "QS_DELTA_MAX_D", "QS_ROTATE_MAX_D",
+    "quat_norm_rotate_fwd", "quat_norm_rotate_bwd", "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd",
+    "quat_delta_step",
 ]
 
 QS_OK = 0
@@ -439,3 +444,8 @@ def quat_cumprod_status(stream=None, device=None):
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(device):
         return load_library().quat_cumprod_status(_stream_handle(stream, device))
+
+
+from .mixer import (  # noqa: E402  (uses the helpers above)
+    QS_DELTA_MAX_D, QS_DELTA_STEPS, QS_ROTATE_MAX_D, quat_delta_bwd, quat_delta_fwd, quat_delta_fwd_carries,
+    quat_delta_step, quat_norm_rotate_bwd, quat_norm_rotate_fwd)

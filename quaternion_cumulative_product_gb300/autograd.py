@@ -16,14 +16,20 @@ The page keeps only the leaves on purpose; this is the measured alternative.
 slice of ``cum``.  As in the page's module documentation, its cotangent then
 reaches the node already added into ``d_cum[:, S-1]``; the node itself has a
 single output.
+
+``quat_norm_rotate`` and ``quat_delta`` are the differentiable forms of the
+operators around the scan (:mod:`.mixer`).
 """
 from __future__ import annotations
 
 import torch
 
-from . import quat_cumprod_bwd, quat_cumprod_bwd_carries, quat_cumprod_fwd, quat_cumprod_fwd_carries
+from . import (
+    quat_cumprod_bwd, quat_cumprod_bwd_carries, quat_cumprod_fwd, quat_cumprod_fwd_carries, quat_delta_bwd,
+    quat_delta_fwd, quat_delta_fwd_carries, quat_norm_rotate_bwd, quat_norm_rotate_fwd)
 
-__all__ = ["QuatCumprod", "quat_cumprod", "quat_cumprod_recalculated"]
+__all__ = ["QuatCumprod", "quat_cumprod", "quat_cumprod_recalculated", "QuatNormRotate", "quat_norm_rotate",
+           "QuatDelta", "quat_delta"]
 
 
 class QuatCumprod(torch.autograd.Function):
@@ -68,3 +74,55 @@ def quat_cumprod_recalculated(q, init, *, save_carries: bool = False):
     """``(cum, final_carry)`` with ``final_carry = cum[:, -1]`` (a slice of ``cum``)."""
     cum = quat_cumprod(q, init, save_carries=save_carries)
     return cum, cum[:, -1]
+
+
+class QuatNormRotate(torch.autograd.Function):
+    """Norm and rotation of queries and keys; the backward recomputes from the inputs."""
+
+    @staticmethod
+    def forward(ctx, q, k, cum, w_q, w_k, norm, eps):
+        cum = cum.contiguous()
+        ctx.norm, ctx.eps = norm, eps
+        ctx.save_for_backward(q, k, cum, w_q, w_k)
+        return quat_norm_rotate_fwd(q, k, cum, w_q, w_k, norm=norm, eps=eps)
+
+    @staticmethod
+    def backward(ctx, d_q_out, d_k_out):
+        q, k, cum, w_q, w_k = ctx.saved_tensors
+        d = quat_norm_rotate_bwd(q, k, cum, d_q_out.contiguous(), d_k_out.contiguous(), w_q, w_k,
+                                 norm=ctx.norm, eps=ctx.eps)
+        return (*[g if need else None for g, need in zip(d, ctx.needs_input_grad)], None, None)
+
+
+def quat_norm_rotate(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6):
+    """Differentiable :func:`quat_norm_rotate_fwd`: ``(q_out, k_out)``."""
+    return QuatNormRotate.apply(q, k, cum, w_q, w_k, norm, eps)
+
+
+class QuatDelta(torch.autograd.Function):
+    """Gated delta rule over whole sequences; tracked calls keep the carries and the errors."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, init, scale, offsets, tracked):
+        g, beta = g.contiguous(), beta.contiguous()
+        ctx.scale, ctx.has_init = scale, init is not None
+        if not tracked:
+            return quat_delta_fwd(q, k, v, g, beta, init, scale=scale, offsets=offsets)
+        o, final, carries, errors = quat_delta_fwd_carries(q, k, v, g, beta, init, scale=scale, offsets=offsets)
+        ctx.save_for_backward(q, k, v, g, beta, carries, errors, offsets)
+        return o, final
+
+    @staticmethod
+    def backward(ctx, d_o, d_final):
+        *inputs, offsets = ctx.saved_tensors
+        d_final = None if d_final is None else d_final.contiguous()
+        d = quat_delta_bwd(*inputs, d_o.contiguous(), d_final, scale=ctx.scale, offsets=offsets)
+        return (*[g if need else None for g, need in zip(d, ctx.needs_input_grad)], None, None, None)
+
+
+def quat_delta(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
+    """Differentiable :func:`quat_delta_fwd`: ``(o, final_state)``."""
+    inputs = [t for t in (q, k, v, g, beta, init) if t is not None]
+    tracked = torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+    init = None if init is None else init.contiguous()
+    return QuatDelta.apply(q, k, v, g, beta, init, scale, offsets, tracked)

@@ -1,7 +1,8 @@
 """Builds ``libquatscan.so`` (the CUDA library behind ``include/quat_cumprod.h``).
 
-One translation unit, compiled for sm_103a only, with the static CUDA runtime,
-in place next to this file.  Used by ``__graft_entry__.build()``.
+Its translation units are compiled side by side for sm_103a only and linked with
+the static CUDA runtime, in place next to this file.  Used by
+``__graft_entry__.build()``.
 """
 from __future__ import annotations
 
@@ -9,15 +10,18 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "quat_scan.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in
+           ("quat_scan.cu", "norm_rotate.cu", "delta_rule.cu", "delta_step.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("quat_device.cuh", "quat_common.cuh", "quat_tiles.cuh", "quat_chain.cuh", "quat_walk.cuh",
             "quat_segwalk.cuh", "quat_segwalk_ws.cuh", "quat_segwalk_bwd.cuh", "quat_segwalk_tab.cuh",
-            "quat_short.cuh")]
-DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", "quat_cumprod.h")]
+            "quat_short.cuh", "quat_host.h", "mixer_device.cuh", "delta_common.cuh")]
+DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", f) for f in ("quat_cumprod.h", "quat_mixer.h")]
 LIB = os.path.join(HERE, "libquatscan.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -29,9 +33,14 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found (CUDA toolkit required to build libquatscan.so)")
 
 
-def command(out: str = LIB, extra=()) -> list:
+def command(source: str, out: str, extra=()) -> list:
+    """Compiles one translation unit to an object file."""
     return [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
-            "-shared", "-I", os.path.join(ROOT, "include"), *extra, *SOURCES, "-o", out]
+            "-c", "-I", os.path.join(ROOT, "include"), *extra, source, "-o", out]
+
+
+def link_command(objects, out: str) -> list:
+    return [nvcc_path(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objects, "-o", out]
 
 
 def is_stale() -> bool:
@@ -46,12 +55,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     extra = ("-Xptxas", "-v") if verbose else ()
-    proc = subprocess.run(command(tmp, extra), capture_output=True, text=True)
-    if proc.returncode != 0:
-        sys.stderr.write(proc.stdout + proc.stderr)
-        raise RuntimeError("nvcc failed to build libquatscan.so")
+
+    def run(cmd):
+        proc = subprocess.run(cmd, capture_output=True, text=True)
+        if proc.returncode != 0:
+            sys.stderr.write(proc.stdout + proc.stderr)
+            raise RuntimeError("nvcc failed to build libquatscan.so")
+        return proc.stderr
+
+    with tempfile.TemporaryDirectory() as objdir, ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = [os.path.join(objdir, os.path.basename(s) + ".o") for s in SOURCES]
+        said = list(pool.map(lambda so: run(command(*so, extra)), zip(SOURCES, objects)))
+        run(link_command(objects, tmp))
     if verbose:
-        sys.stderr.write(proc.stderr)
+        sys.stderr.write("".join(said))
     os.replace(tmp, LIB)
     return LIB
 

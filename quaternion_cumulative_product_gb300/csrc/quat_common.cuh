@@ -35,7 +35,7 @@ __device__ __forceinline__ unsigned char *align128(unsigned char *p) {
     return reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(p) + 127) & ~uintptr_t(127));
 }
 
-__device__ void record_error(WsHeader *h, int item) {
+__device__ inline void record_error(WsHeader *h, int item) {
     if (atomicCAS(&h->err_code, 0u, 1u) == 0u) h->err_item = static_cast<unsigned long long>(item);
     atomicAdd(&h->err_count, 1u);
 }

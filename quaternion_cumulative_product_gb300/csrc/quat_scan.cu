@@ -1963,3 +1963,25 @@ extern "C" int quat_cumprod_bwd_noalloc(const float *q, const float *init, const
     if (noalloc_tiles(B, S, HJ) > QS_NOALLOC_MAX_TILES) return QS_ERR_SCRATCH;
     return noalloc_launch(q, init, d_cum, d_q, d_init, B, S, HJ, stream);
 }
+
+// ---------------------------------------------------------------------------
+// Services for the library's other translation units (quat_host.h).
+// ---------------------------------------------------------------------------
+#include "quat_host.h"
+
+namespace qsh {
+
+int device(int *dev, int *sms) {
+    DevInfo *di = nullptr;
+    const int rc = device_info(&di, dev);
+    if (rc == QS_OK) *sms = di->sms;
+    return rc;
+}
+
+int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base) {
+    return ensure_workspace(dev, stream, need, base);
+}
+
+unsigned long long timeout_ns() { return g_timeout_ns; }
+
+}  // namespace qsh
