@@ -2,7 +2,7 @@
 // backward from the forward's carries and errors.
 #include <cstring>
 
-#include "delta_common.cuh"
+#include "delta_fwd_tc.cuh"
 
 namespace {
 
@@ -365,6 +365,26 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, lo
 // ---------------------------------------------------------------------------
 int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA; }
 
+// Launches a walk kernel with its shared memory.
+template <typename K>
+int launch_walk(K kernel, const DeltaArgs &a, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return QS_ERR_CUDA;
+    }
+    kernel<<<grid, threads, smem, stream>>>(a);
+    return launched();
+}
+
+template <typename T, int NT>
+int launch_fwd(const DeltaArgs &a, cudaStream_t stream) {
+    constexpr int STAGES = NT == 1 ? 2 : 1;
+    const unsigned grid = (unsigned)(a.N * a.Hv);
+    if (a.Dk <= 64)
+        return launch_walk(delta_fwd_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, WalkLayout<NT, 64, STAGES>::BYTES, stream);
+    return launch_walk(delta_fwd_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, WalkLayout<NT, 128, STAGES>::BYTES, stream);
+}
+
 template <typename S, typename K>
 int launch(K kernel, const DeltaArgs &a, unsigned grid, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S)) != cudaSuccess) {
@@ -449,8 +469,11 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.init = init, a.o = o, a.fin = final_state;
     a.carries = carries, a.errors = errors;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return dtype == QS_BF16 ? launch<FwdSmem>(delta_fwd_simple_kernel<__nv_bfloat16>, a, (unsigned)(N * Hv), stream)
-                            : launch<FwdSmem>(delta_fwd_simple_kernel<float>, a, (unsigned)(N * Hv), stream);
+    unsigned char *ws = nullptr;
+    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader), &ws);
+    if (wc != QS_OK) return wc;
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
+    return dtype == QS_BF16 ? launch_fwd<__nv_bfloat16, 1>(a, stream) : launch_fwd<float, 3>(a, stream);
 }
 
 extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
