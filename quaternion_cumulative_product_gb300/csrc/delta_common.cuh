@@ -105,9 +105,18 @@ __device__ __forceinline__ Sum2 sum2_add(const Sum2 a, const Sum2 b) {   // Knut
 
 // A step's log decay.  Below -256 exp() is zero in fp32 by far, and so is every
 // product of decays <= 1 over it: the clamp makes -inf (a cleared state) finite.
-__device__ __forceinline__ float clamp_gate(float g) { return g < -256.f ? -256.f : g; }
+// In base-2 units, so that a decay is one exp2.
+__device__ __forceinline__ float clamp_gate(float g) { return (g < -256.f ? -256.f : g) * 1.4426950408889634f; }
 
-__device__ __forceinline__ float decay(const Sum2 t, const Sum2 s) { return expf((t.hi - s.hi) + (t.lo - s.lo)); }
+// 2^x (the instruction: 2^-22 off at most).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// exp(G_t - G_s) from sums kept in base-2 units.
+__device__ __forceinline__ float decay(const Sum2 t, const Sum2 s) { return exp2_fast((t.hi - s.hi) + (t.lo - s.lo)); }
 
 // Lanes 0..31 hold steps 2l and 2l+1: inclusive sums over the 64 steps.
 __device__ __forceinline__ void chunk_sums(float g0, float g1, Sum2 *s0, Sum2 *s1) {

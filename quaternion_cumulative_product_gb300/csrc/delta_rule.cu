@@ -72,79 +72,10 @@ __device__ __forceinline__ void load_gates(Gates &s, const DeltaArgs &a, const S
         const int t = 2 * threadIdx.x;
         s.sum[t] = s0, s.sum[t + 1] = s1;
         s.beta[t] = be[0], s.beta[t + 1] = be[1];
-        s.grown[t] = expf(s0.hi + s0.lo), s.grown[t + 1] = expf(s1.hi + s1.lo);
+        s.grown[t] = decay(s0, {0.f, 0.f}), s.grown[t + 1] = decay(s1, {0.f, 0.f});
         s.left[t] = decay(end, s0), s.left[t + 1] = decay(end, s1);
         if (threadIdx.x == 31) s.whole = s.grown[63];
     }
-}
-
-struct FwdSmem {
-    float q[DC][LD], k[DC][LD], v[DC][LD];
-    float m[QS_DELTA_MAX_D][LD];
-    float a[DC][LC], p[DC][LC];
-    Gates g;
-};
-
-// One CTA per (sequence, value head) walks its chunks; the state stays in shared memory.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) delta_fwd_simple_kernel(const DeltaArgs a) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    FwdSmem &s = *reinterpret_cast<FwdSmem *>(raw);
-    const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk);
-    const long long n = blockIdx.x / a.Hv;
-    const Seq seq = seq_of(a, n);
-    const size_t state = ((size_t)n * a.Hv + head) * a.Dk * a.Dv;
-    for (int i = threadIdx.x; i < 128 * 128; i += kThreads) {
-        const int x = i / 128, y = i % 128;
-        s.m[x][y] = a.init && x < a.Dk && y < a.Dv ? a.init[state + (size_t)x * a.Dv + y] : 0.f;
-    }
-    for (long long t0 = 0; t0 < seq.len; t0 += DC) {
-        __syncthreads();
-        load_tile<T>(s.q, a.q, a.sq, seq, t0, kh, a.Dk);
-        load_tile<T>(s.k, a.k, a.sk, seq, t0, kh, a.Dk);
-        load_tile<T>(s.v, a.v, a.sv, seq, t0, head, a.Dv);
-        load_gates(s.g, a, seq, t0, head);
-        if (a.carries) {
-            float *c = a.carries + ((size_t)(seq.slot0 + t0 / DC) * a.Hv + head) * a.Dk * a.Dv;
-            for (int i = threadIdx.x; i < a.Dk * a.Dv; i += kThreads) c[i] = s.m[i / a.Dv][i % a.Dv];
-        }
-        __syncthreads();
-        auto gram = [&](float(*x)[LD], float(*out)[LC], bool diag, float f) {
-            product<64, 64>(a.Dk, [&](int i, int k) { return x[i][k]; }, [&](int k, int j) { return s.k[j][k]; },
-                            [&](int i, int j, float v) { out[i][j] = j < i || (diag && j == i) ? f * decay(s.g.sum[i], s.g.sum[j]) * v : 0.f; });
-        };
-        gram(s.k, s.a, false, 1.f);
-        gram(s.q, s.p, true, a.scale);
-        product<64, 128>(a.Dk, [&](int i, int k) { return s.k[i][k]; }, [&](int k, int j) { return s.m[k][j]; },
-                         [&](int i, int j, float v) { s.v[i][j] -= s.g.grown[i] * v; });
-        __syncthreads();
-        if (threadIdx.x < 128) {   // one thread per value column solves the triangular system
-            for (int t = 1; t < DC; ++t) {
-                float e = s.v[t][threadIdx.x];
-                for (int r = 0; r < t; ++r) e = fmaf(-s.a[t][r] * s.g.beta[r], s.v[r][threadIdx.x], e);
-                s.v[t][threadIdx.x] = e;
-            }
-        }
-        __syncthreads();
-        const long long row0 = seq.b * a.S + seq.s0 + t0;
-        float oi[4][8];
-        product<64, 128>(a.Dk, [&](int i, int k) { return s.q[i][k]; }, [&](int k, int j) { return s.m[k][j]; },
-                         [&](int i, int j, float v) { oi[i % 4][j / 16] = a.scale * s.g.grown[i] * v; });
-        product<64, 128>(DC, [&](int i, int k) { return s.p[i][k]; }, [&](int k, int j) { return s.g.beta[k] * s.v[k][j]; },
-                         [&](int i, int j, float v) {
-                             if (t0 + i < seq.len && j < a.Dv) {
-                                 const size_t at = ((size_t)(row0 + i) * a.Hv + head) * a.Dv + j;
-                                 store1(static_cast<T *>(a.o) + at, oi[i % 4][j / 16] + v);
-                                 if (a.errors) a.errors[at] = s.v[i][j];
-                             }
-                         });
-        __syncthreads();
-        product<128, 128>(DC, [&](int i, int k) { return s.k[k][i]; }, [&](int k, int j) { return s.g.left[k] * s.g.beta[k] * s.v[k][j]; },
-                          [&](int i, int j, float v) { s.m[i][j] = fmaf(s.g.whole, s.m[i][j], v); });
-    }
-    __syncthreads();
-    if (a.fin)
-        for (int i = threadIdx.x; i < a.Dk * a.Dv; i += kThreads) a.fin[state + i] = s.m[i / a.Dv][i % a.Dv];
 }
 
 struct ChainSmem {
@@ -381,8 +312,8 @@ int launch_fwd(const DeltaArgs &a, cudaStream_t stream) {
     constexpr int STAGES = NT == 1 ? 2 : 1;
     const unsigned grid = (unsigned)(a.N * a.Hv);
     if (a.Dk <= 64)
-        return launch_walk(delta_fwd_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, WalkLayout<NT, 64, STAGES>::BYTES, stream);
-    return launch_walk(delta_fwd_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, WalkLayout<NT, 128, STAGES>::BYTES, stream);
+        return launch_walk(delta_fwd_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 64, STAGES>::BYTES, stream);
+    return launch_walk(delta_fwd_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 128, STAGES>::BYTES, stream);
 }
 
 template <typename S, typename K>

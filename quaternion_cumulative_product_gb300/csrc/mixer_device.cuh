@@ -45,6 +45,8 @@ __device__ __forceinline__ void store_quads<2, __nv_bfloat16>(__nv_bfloat16 *p, 
     *reinterpret_cast<uint4 *>(p) = make_uint4(a.x, a.y, b.x, b.y);
 }
 
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float load1(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }

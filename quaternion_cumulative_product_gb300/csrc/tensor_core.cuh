@@ -2,8 +2,8 @@
 // products of fp32 precision, as the delta rule's kernels use them.
 //
 // Precision.  tcgen05.mma multiplies bfloat16 values exactly and adds in fp32.
-// An fp32 value x is carried as three bfloat16 terms x = x0 + x1 + x2 (24 bits:
-// each term is the rounded rest of the ones before), a bfloat16 input as itself.
+// An fp32 value x is carried as three bfloat16 terms x = x0 + x1 + x2 (eight
+// bits each: all 24), a bfloat16 input as itself.
 // A product of values with terms i and j keeps the pairs i + j <= 2: what is left
 // out is below 2^-24 of the product.  So a product costs 1 (bf16 x bf16), 3 (fp32 x
 // bf16) or 6 (fp32 x fp32) tensor-core passes.
@@ -120,20 +120,45 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ float2 fma2(const float2 a, const float2 b, const float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&r))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)), "l"(*reinterpret_cast<const unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&c)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(const float2 a, const float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&r))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)), "l"(*reinterpret_cast<const unsigned long long *>(&b)));
+    return r;
+}
+
+// The terms of a pair.  All but the last of two are cut off, not rounded: cutting
+// takes eight bits of the 24 exactly, so three terms hold an fp32 value as it is.
+// (Infinities become NaN, NaNs stay.)
+template <int TERMS>
+__device__ __forceinline__ void split2(float2 x, uint32_t *t) {
+    const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        if (i == TERMS - 1 && TERMS < 3) {
+            t[i] = pack_bf16(x.x, x.y);
+        } else {
+            t[i] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+            if (i < TERMS - 1)
+                x = fma2(make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
+                         minus, x);
+        }
+    }
+}
 template <int TERMS>
 __device__ __forceinline__ void split2(float a, float b, uint32_t *t) {
-    t[0] = pack_bf16(a, b);
-    if constexpr (TERMS > 1) {
-        a -= bf16_lo(t[0]), b -= bf16_hi(t[0]);
-        t[1] = pack_bf16(a, b);
-    }
-    if constexpr (TERMS > 2) {
-        a -= bf16_lo(t[1]), b -= bf16_hi(t[1]);
-        t[2] = pack_bf16(a, b);
-    }
+    split2<TERMS>(make_float2(a, b), t);
 }
 
 // Byte offset of 16-byte unit u of row r in a tile of 128-byte rows.
