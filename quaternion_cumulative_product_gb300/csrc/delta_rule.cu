@@ -2,6 +2,7 @@
 // backward from the forward's carries and errors.
 #include <cstring>
 
+#include "delta_bwd_tc.cuh"
 #include "delta_fwd_tc.cuh"
 
 namespace {
@@ -161,117 +162,6 @@ __global__ void __launch_bounds__(kThreads) delta_chain_simple_kernel(const Delt
             }
 }
 
-struct ChunkSmem {
-    float q[DC][LD], k[DC][LD], d[DC][LD], u[DC][LD], w[DC][LD];
-    float x[DC][LC], y[DC][LC];
-    float dgp[DC][17], beta_grad[DC];
-    Gates g;
-    float dot;
-};
-
-// Backward, second kernel: one CTA per (chunk, value head).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) delta_chunk_simple_kernel(const DeltaArgs a) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    ChunkSmem &s = *reinterpret_cast<ChunkSmem *>(raw);
-    const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk);
-    Seq seq;
-    long long c;
-    if (!chunk_of(a, blockIdx.x / a.Hv, &seq, &c)) return;
-    const long long t0 = c * DC, row0 = seq.b * a.S + seq.s0 + t0;
-    const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
-    const size_t at0 = ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv;
-    const float *m = a.carries_in + at0, *dm = a.ds + at0;
-    load_tile<T>(s.q, a.q, a.sq, seq, t0, kh, a.Dk);
-    load_tile<T>(s.k, a.k, a.sk, seq, t0, kh, a.Dk);
-    load_tile<T>(s.d, a.d_o, so, seq, t0, head, a.Dv);
-    load_tile<float>(s.u, a.errors_in, so, seq, t0, head, a.Dv);
-    load_tile<float>(s.w, a.w, so, seq, t0, head, a.Dv);
-    load_gates(s.g, a, seq, t0, head);
-    if (threadIdx.x == 0) s.dot = 0.f;
-    __syncthreads();
-    {   // dbeta = <e, w>, then u = beta e and dv = beta w in place
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        for (int t = warp; t < DC; t += 8) {
-            float d = 0.f;
-            for (int j = lane; j < a.Dv; j += 32) {
-                d = fmaf(s.u[t][j], s.w[t][j], d);
-                s.u[t][j] *= s.g.beta[t];
-                s.w[t][j] *= s.g.beta[t];
-            }
-            for (int o = 16; o; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (lane == 0 && t0 + t < seq.len) store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, d);
-        }
-        float d = 0.f;
-        for (int i = threadIdx.x; i < a.Dk * a.Dv; i += kThreads) d = fmaf(m[i], dm[i], d);
-        for (int o = 16; o; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if (lane == 0) s.dgp[warp][16] = d;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float d = 0.f;
-        for (int i = 0; i < 8; ++i) d += s.dgp[i][16];
-        s.dot = d * s.g.whole;
-    }
-    product<64, 64>(a.Dv, [&](int i, int k) { return s.d[i][k]; }, [&](int k, int j) { return s.u[j][k]; },
-                    [&](int i, int j, float v) { s.x[i][j] = j <= i ? a.scale * decay(s.g.sum[i], s.g.sum[j]) * v : 0.f; });
-    product<64, 64>(a.Dv, [&](int i, int k) { return s.w[i][k]; }, [&](int k, int j) { return s.u[j][k]; },
-                    [&](int i, int j, float v) { s.y[i][j] = j < i ? -decay(s.g.sum[i], s.g.sum[j]) * v : 0.f; });
-    __syncthreads();
-    float dq[4][8], row[4][8], col[4][8];
-    float sum[4] = {0.f, 0.f, 0.f, 0.f}, last[4] = {0.f, 0.f, 0.f, 0.f};
-    auto mrow = [&](const float *p, int j, int k) { return j < a.Dk ? __ldg(p + (size_t)j * a.Dv + k) : 0.f; };
-    product<64, 128>(a.Dv, [&](int i, int k) { return s.d[i][k]; }, [&](int k, int j) { return mrow(m, j, k); },
-                     [&](int i, int j, float v) { dq[i % 4][j / 16] = a.scale * s.g.grown[i] * v; });
-    product<64, 128>(DC, [&](int i, int k) { return s.x[i][k]; }, [&](int k, int j) { return s.k[k][j]; },
-                     [&](int i, int j, float v) { dq[i % 4][j / 16] += v; sum[i % 4] = fmaf(dq[i % 4][j / 16], s.q[i][j], sum[i % 4]); });
-    product<64, 128>(a.Dv, [&](int i, int k) { return s.w[i][k]; }, [&](int k, int j) { return mrow(m, j, k); },
-                     [&](int i, int j, float v) { row[i % 4][j / 16] = -s.g.grown[i] * v; });
-    product<64, 128>(DC, [&](int i, int k) { return s.y[i][k]; }, [&](int k, int j) { return s.k[k][j]; },
-                     [&](int i, int j, float v) { row[i % 4][j / 16] += v; sum[i % 4] = fmaf(row[i % 4][j / 16], s.k[i][j], sum[i % 4]); });
-    product<64, 128>(a.Dv, [&](int i, int k) { return s.u[i][k]; }, [&](int k, int j) { return mrow(dm, j, k); },
-                     [&](int i, int j, float v) { v *= s.g.left[i]; col[i % 4][j / 16] = v; last[i % 4] = fmaf(v, s.k[i][j], last[i % 4]); });
-    product<64, 128>(DC, [&](int i, int k) { return s.x[k][i]; }, [&](int k, int j) { return s.q[k][j]; },
-                     [&](int i, int j, float v) { col[i % 4][j / 16] += v; });
-    product<64, 128>(DC, [&](int i, int k) { return s.y[k][i]; }, [&](int k, int j) { return s.k[k][j]; },
-                     [&](int i, int j, float v) { col[i % 4][j / 16] += v; sum[i % 4] = fmaf(-col[i % 4][j / 16], s.k[i][j], sum[i % 4]); });
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const bool shared = a.Hv != a.Hk;
-    for (int i = 0; i < 4; ++i) {
-        const int t = ty * 4 + i;
-        if (t0 + t < seq.len)
-            for (int j = 0; j < 8; ++j) {
-                const int x = tx + 16 * j;
-                if (x >= a.Dk) continue;
-                const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dk + x;
-                if (shared) {
-                    a.dqh[at] = dq[i][j];
-                    a.dkh[at] = row[i][j] + col[i][j];
-                } else {
-                    store1(static_cast<T *>(a.dq) + at, dq[i][j]);
-                    store1(static_cast<T *>(a.dk) + at, row[i][j] + col[i][j]);
-                }
-            }
-        for (int o = 8; o; o /= 2) {
-            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-            last[i] += __shfl_xor_sync(0xffffffffu, last[i], o);
-        }
-        if (tx == 0) {
-            s.dgp[t][0] = sum[i];
-            s.dgp[t][1] = last[i];
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float run = s.dot;
-        for (int t = 0; t < DC; ++t) run += s.dgp[t][1];
-        for (int t = DC - 1; t >= 0; --t) {
-            run += s.dgp[t][0];
-            if (t0 + t < seq.len) store_any(a.dg, a.gate16, (row0 + t) * a.Hv + head, run);
-        }
-    }
-}
-
 // dq, dk of a key head: the sum over the value heads that share it.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, long long quads) {
@@ -314,6 +204,14 @@ int launch_fwd(const DeltaArgs &a, cudaStream_t stream) {
     if (a.Dk <= 64)
         return launch_walk(delta_fwd_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 64, STAGES>::BYTES, stream);
     return launch_walk(delta_fwd_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 128, STAGES>::BYTES, stream);
+}
+
+template <typename T, int NT, int CT>
+int launch_chunks(const DeltaArgs &a, cudaStream_t stream) {
+    const unsigned grid = (unsigned)(a.slots * a.Hv);
+    if (a.Dk <= 64)
+        return launch_walk(delta_chunk_tc_kernel<T, NT, CT, 64>, a, grid, kChunkThreads, ChunkLayout<NT, CT, 64>::BYTES, stream);
+    return launch_walk(delta_chunk_tc_kernel<T, NT, CT, 128>, a, grid, kChunkThreads, ChunkLayout<NT, CT, 128>::BYTES, stream);
 }
 
 template <typename S, typename K>
@@ -448,12 +346,13 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     unsigned char *p = ws + sizeof(WsHeader);
     a.ds = reinterpret_cast<float *>(p), a.w = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + nds + nw), a.dkh = reinterpret_cast<float *>(p + nds + nw + nh);
-    const unsigned chains = (unsigned)(N * Hv), chunks = (unsigned)(a.slots * Hv);
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
+    const unsigned chains = (unsigned)(N * Hv);
     rc = dtype == QS_BF16 ? launch<ChainSmem>(delta_chain_simple_kernel<__nv_bfloat16>, a, chains, stream)
                           : launch<ChainSmem>(delta_chain_simple_kernel<float>, a, chains, stream);
     if (rc != QS_OK || !some) return rc;
-    rc = dtype == QS_BF16 ? launch<ChunkSmem>(delta_chunk_simple_kernel<__nv_bfloat16>, a, chunks, stream)
-                          : launch<ChunkSmem>(delta_chunk_simple_kernel<float>, a, chunks, stream);
+    if (dtype != QS_BF16) rc = launch_chunks<float, 3, 3>(a, stream);
+    else rc = gate_dtype == QS_BF16 ? launch_chunks<__nv_bfloat16, 1, 2>(a, stream) : launch_chunks<__nv_bfloat16, 1, 3>(a, stream);
     if (rc != QS_OK || !shared) return rc;
     const long long quads = B * S * Hk * Dk / 4;
     const unsigned grid = (unsigned)((quads + 255) / 256);
