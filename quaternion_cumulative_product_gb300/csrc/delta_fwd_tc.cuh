@@ -78,7 +78,7 @@ __device__ __forceinline__ void warp_gates(ChunkGates &s, const RawGates &raw) {
 // K and Q of a stage: [term][half of D]{K tile, Q tile}; then a third tensor's rows
 // [64][128] as they are (V; d_o in the backward), T and P.
 constexpr uint32_t TILE = 8192;
-constexpr int FLD = 68;   // padded rows of the fp32 64 x 64 scratch (16-byte aligned)
+constexpr int FLD = 68;   // padded rows of a 64 x 64 fp32 matrix (16-byte aligned)
 
 template <typename T, int NT, int DK, int STAGES>
 struct WalkLayout {
@@ -86,7 +86,7 @@ struct WalkLayout {
     static constexpr uint32_t KQ = NT * HALVES * 2 * TILE;   // bytes of K and Q
     static constexpr int PT = NT == 1 ? 2 : 3;               // terms of P and U (o's precision)
     static constexpr uint32_t V_AT = KQ, T_AT = V_AT + DC * 128 * sizeof(T), P_AT = T_AT + 3 * TILE, STAGE = P_AT + PT * TILE;
-    static constexpr uint32_t A_AT = STAGES * STAGE, F_AT = A_AT + DC * FLD * 4, Y_AT = F_AT + DC * FLD * 4;
+    static constexpr uint32_t F_AT = STAGES * STAGE, Y_AT = F_AT + DC * FLD * 4;
     static constexpr uint32_t GATES_AT = Y_AT + 32 * 36 * 4;
     static constexpr uint32_t BARS_AT = GATES_AT + STAGES * sizeof(ChunkGates);
     static constexpr uint32_t BYTES = BARS_AT + 256 + 1024;   // + alignment of the tiles to 1024 bytes
@@ -94,16 +94,17 @@ struct WalkLayout {
     static_assert(BYTES > 116736, "one CTA per SM: it takes all of the tensor memory");
 };
 
-// Rows of one head into a stage's tiles as bfloat16 terms (`which`: 0 K, 1 Q);
-// zeros past the sequence and past D.  bfloat16 rows are copied asynchronously.
+// Rows of one head into tiles as bfloat16 terms, `half` bytes from one half of D to
+// the next and `term` from one term; zeros past the sequence and past D.  bfloat16
+// rows are copied asynchronously.
 template <typename T, int NT, int DK>
-__device__ __forceinline__ void load_rows(uint32_t stage, int which, const void *p, const qsh::Strides &st, const Seq &seq,
-                                          long long t0, int head, int D, int tid) {
+__device__ __forceinline__ void load_rows(uint32_t tiles, uint32_t half, uint32_t term, const void *p, const qsh::Strides &st,
+                                          const Seq &seq, long long t0, int head, int D, int tid) {
     constexpr int UNITS = DK / 8, STEP = 128 / UNITS;   // 16-byte units of bfloat16 in a row; rows per round
     const int u = tid % UNITS, r0 = tid / UNITS;
     const T *base = static_cast<const T *>(p) + seq.b * st.b + (seq.s0 + t0) * st.s + (long long)head * st.h;
     const long long left = seq.len - t0;
-    const uint32_t at0 = stage + (uint32_t)((u / 8) * 2 + which) * TILE;
+    const uint32_t at0 = tiles + (uint32_t)(u / 8) * half;
 #pragma unroll 4
     for (int r = r0; r < DC; r += STEP) {
         const bool in = r < left && u * 8 < D;
@@ -118,8 +119,8 @@ __device__ __forceinline__ void load_rows(uint32_t stage, int which, const void 
             split2<3>(x.x, x.y, t[0]), split2<3>(x.z, x.w, t[1]), split2<3>(y.x, y.y, t[2]), split2<3>(y.z, y.w, t[3]);
 #pragma unroll
             for (int j = 0; j < 3; ++j)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + j * (DK / 64) * 2 * TILE), "r"(t[0][j]),
-                             "r"(t[1][j]), "r"(t[2][j]), "r"(t[3][j])
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + j * term), "r"(t[0][j]), "r"(t[1][j]),
+                             "r"(t[2][j]), "r"(t[3][j])
                              : "memory");
         }
     }
@@ -169,30 +170,32 @@ __device__ __forceinline__ void store_terms(uint32_t tiles, int r, int u, const 
     }
 }
 
-// tf = (1 + af)^-1 on and below the diagonal, for the strictly lower triangular
-// af [64][FLD] (zeros on and above the diagonal inside its diagonal blocks); 128
+// tf [64][FLD], strictly lower triangular (zeros on and above the diagonal inside
+// its diagonal blocks), becomes (1 + tf)^-1 on and below the diagonal blocks; 128
 // threads (barrier `bar`).  yf: 32 x 36 of scratch.
-__device__ __forceinline__ void invert_64(const float *af, float *tf, float *yf, int tid, int bar) {
+__device__ __forceinline__ void invert_64(float *tf, float *yf, int tid, int bar) {
     const int blk = tid / 32, j = tid % 32;
     if (blk < 2) {   // a diagonal block per warp, a column per thread, by substitution
-        const float *a = af + blk * 32 * (FLD + 1);
+        float *a = tf + blk * 32 * (FLD + 1);
         float2 x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            float2 s = make_float2(0.f, 0.f);
+            float2 s = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int m = 0; m < i; m += 4) {   // terms past i meet zeros
                 const float4 r = *reinterpret_cast<const float4 *>(a + i * FLD + m);
                 s = fma2(make_float2(r.x, r.y), x[m / 2], s);
-                if (m + 2 < i) s = fma2(make_float2(r.z, r.w), x[m / 2 + 1], s);
+                if (m + 2 < i) s1 = fma2(make_float2(r.z, r.w), x[m / 2 + 1], s1);
             }
-            const float v = (i == j ? 1.f : 0.f) - (s.x + s.y);
+            const float v = (i == j ? 1.f : 0.f) - ((s.x + s1.x) + (s.y + s1.y));
             if (i % 2) x[i / 2].y = v;
             else x[i / 2].x = v;
-            tf[(blk * 32 + i) * FLD + blk * 32 + j] = v;
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a[i * FLD + j] = i % 2 ? x[i / 2].y : x[i / 2].x;
     }
     named_bar_sync(bar, 128);
     const int r = tid / 8 * 2, c = tid % 8 * 4;   // a 2 x 4 piece of the corner per thread
@@ -218,7 +221,7 @@ __device__ __forceinline__ void invert_64(const float *af, float *tf, float *yf,
         out[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
     };
     float4 y[2];
-    corner(af + 32 * FLD, tf, FLD, 32, y);   // (what T11 holds above its diagonal is zero)
+    corner(tf + 32 * FLD, tf, FLD, 32, y);   // A21 T11 (T11 holds zeros above its diagonal)
     store4(yf + r * 36 + c, y[0]);
     store4(yf + (r + 1) * 36 + c, y[1]);
     named_bar_sync(bar, 128);
@@ -226,6 +229,19 @@ __device__ __forceinline__ void invert_64(const float *af, float *tf, float *yf,
     store4(tf + (32 + r) * FLD + c, make_float4(-y[0].x, -y[0].y, -y[0].z, -y[0].w));
     store4(tf + (33 + r) * FLD + c, make_float4(-y[1].x, -y[1].y, -y[1].z, -y[1].w));
     named_bar_sync(bar, 128);
+}
+
+// Writes the rows of tf as the terms of T (what lies above the diagonal blocks stays).
+__device__ __forceinline__ void store_inverse(uint32_t tiles, const float *tf, int tid) {
+    const int r = tid / 2;   // two 16-byte units of an upper row, four of a lower one, per thread
+#pragma unroll 1
+    for (int u = (tid & 1) * (r < 32 ? 2 : 4), e = u + (r < 32 ? 2 : 4); u < e; ++u) {
+        float x[8];
+        const float4 p = *reinterpret_cast<const float4 *>(tf + r * FLD + u * 8);
+        const float4 q = *reinterpret_cast<const float4 *>(tf + r * FLD + u * 8 + 4);
+        x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
+        store_terms<3>(tiles, r, u, x);
+    }
 }
 
 // The Gram product [K;Q] K^T of a stage into tensor memory; one thread.
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_fwd_tc_kernel(const __g
 
     if (wg == 2) {
         // ------------------------------------------------------------ prep
-        float *af = reinterpret_cast<float *>(sm + L::A_AT), *tf = reinterpret_cast<float *>(sm + L::F_AT);
+        float *tf = reinterpret_cast<float *>(sm + L::F_AT);
         float *yf = reinterpret_cast<float *>(sm + L::Y_AT);
         RawGates raw_gates = {};
         if (tid < 32 && chunks > 0) raw_gates = read_gates(a, seq, 0, head);
@@ -380,8 +396,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_fwd_tc_kernel(const __g
             const long long t0 = (long long)c * DC;
             ChunkGates &gt = gates[st];
             tc_wait_warp(&bar.empty[st], ((c / STAGES) & 1) ^ 1, gone, a.ctl);
-            load_rows<T, NT, DK>(stage, 0, a.k, a.sk, seq, t0, kh, a.Dk, tid);
-            load_rows<T, NT, DK>(stage, 1, a.q, a.sq, seq, t0, kh, a.Dk, tid);
+            load_rows<T, NT, DK>(stage, 2 * TILE, L::HALVES * 2 * TILE, a.k, a.sk, seq, t0, kh, a.Dk, tid);
+            load_rows<T, NT, DK>(stage + TILE, 2 * TILE, L::HALVES * 2 * TILE, a.q, a.sq, seq, t0, kh, a.Dk, tid);
             load_plain<T>(stage + L::V_AT, a.v, a.sv, seq, t0, head, a.Dv, tid);
             if (c + 1 < chunks) {
                 prefetch_rows<T>(a.k, a.sk, seq, t0 + DC, kh, a.Dk, tid);
@@ -412,7 +428,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_fwd_tc_kernel(const __g
                         float y[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) y[j] = s0 + i + j == t ? 0.f : x[i + j] * b4[j];
-                        store4(af + t * FLD + s0 + i, make_float4(y[0], y[1], y[2], y[3]));
+                        store4(tf + t * FLD + s0 + i, make_float4(y[0], y[1], y[2], y[3]));
                     }
                 } else {          // P_ts
 #pragma unroll
@@ -423,18 +439,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) delta_fwd_tc_kernel(const __g
             });
             tc_fence_before();
             named_bar_sync(2, 128);
-            invert_64(af, tf, yf, tid, 2);
-            {   // T's rows: 32 values of the lower half's two blocks, 16 of the upper half's one, per thread
-                const int r = tid / 2;
-#pragma unroll 1
-                for (int u = (tid & 1) * (r < 32 ? 2 : 4), e = u + (r < 32 ? 2 : 4); u < e; ++u) {
-                    float x[8];
-                    const float4 p = *reinterpret_cast<const float4 *>(tf + r * FLD + u * 8);
-                    const float4 q = *reinterpret_cast<const float4 *>(tf + r * FLD + u * 8 + 4);
-                    x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-                    store_terms<3>(stage + L::T_AT, r, u, x);
-                }
-            }
+            invert_64(tf, yf, tid, 2);
+            store_inverse(stage + L::T_AT, tf, tid);
             fence_proxy_async_smem();
             named_bar_sync(2, 128);
             if (tid == 0) mbar_arrive(&bar.full[st]);
