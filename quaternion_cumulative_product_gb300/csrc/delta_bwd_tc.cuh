@@ -21,7 +21,7 @@
 // rounding is 2^-9.
 #pragma once
 
-#include "delta_fwd_tc.cuh"
+#include "delta_prep.cuh"
 
 namespace qs {
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
     if (warp == 0) tmem_alloc_all(&bar.tmem);
     if (warp == 1) warp_gates(gt, read_gates(a, seq, t0, head));
-    load_rows<T, NT, DK>(sm32 + L::QK_AT + wg * TILE, 2 * TILE, L::HALVES * 2 * TILE, wg ? a.k : a.q, wg ? a.sk : a.sq, seq, t0, kh, a.Dk, tid);
+    load_rows<T, NT, DK, 128>(sm32 + L::QK_AT + wg * TILE, 2 * TILE, L::HALVES * 2 * TILE, wg ? a.k : a.q, wg ? a.sk : a.sq, seq, t0, kh, a.Dk, tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -34,41 +34,45 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, lo
 // ---------------------------------------------------------------------------
 int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA; }
 
-// Launches a walk kernel with its shared memory.
-template <typename K>
-int launch_walk(K kernel, const DeltaArgs &a, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return QS_ERR_CUDA;
+// A walk over the chunks, one CTA per (sequence, value head).  fp32 inputs take three
+// times the space of K and Q: one stage.
+template <bool BWD, typename T, int NT>
+int launch_walks(const DeltaArgs &a, cudaStream_t stream) {
+    constexpr int STAGES = NT == 1 ? 2 : 1, PT = BWD || NT == 3 ? 3 : 2;
+    CUtensorMap maps[3];
+    if (NT == 1 && a.B * a.S > 0) {
+        const qsh::Strides so = {(long long)(a.S * a.Hv * a.Dv), (long long)a.Hv * a.Dv, a.Dv};
+        int rc = qsh::head_map(&maps[0], a.k, a.sk, a.B, a.S, a.Hk, a.Dk);
+        if (rc == QS_OK) rc = qsh::head_map(&maps[1], a.q, a.sq, a.B, a.S, a.Hk, a.Dk);
+        if (rc == QS_OK) rc = BWD ? qsh::head_map(&maps[2], a.d_o, so, a.B, a.S, a.Hv, a.Dv)
+                                  : qsh::head_map(&maps[2], a.v, a.sv, a.B, a.S, a.Hv, a.Dv);
+        if (rc != QS_OK) return rc;
     }
-    kernel<<<grid, threads, smem, stream>>>(a);
-    return launched();
-}
-
-template <typename T, int NT>
-int launch_fwd(const DeltaArgs &a, cudaStream_t stream) {
-    constexpr int STAGES = NT == 1 ? 2 : 1;
-    const unsigned grid = (unsigned)(a.N * a.Hv);
-    if (a.Dk <= 64)
-        return launch_walk(delta_fwd_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 64, STAGES>::BYTES, stream);
-    return launch_walk(delta_fwd_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, WalkLayout<T, NT, 128, STAGES>::BYTES, stream);
-}
-
-template <typename T, int NT>
-int launch_chain(const DeltaArgs &a, cudaStream_t stream) {
-    constexpr int STAGES = NT == 1 ? 2 : 1;
-    const unsigned grid = (unsigned)(a.N * a.Hv);
-    if (a.Dk <= 64)
-        return launch_walk(delta_chain_tc_kernel<T, NT, 64, STAGES>, a, grid, kWalkThreads, ChainLayout<NT, 64, STAGES>::BYTES, stream);
-    return launch_walk(delta_chain_tc_kernel<T, NT, 128, STAGES>, a, grid, kWalkThreads, ChainLayout<NT, 128, STAGES>::BYTES, stream);
+    auto go = [&](auto kernel, size_t smem) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return (int)QS_ERR_CUDA;
+        }
+        kernel<<<(unsigned)(a.N * a.Hv), kWalkThreads, smem, stream>>>(a, maps[0], maps[1], maps[2]);
+        return launched();
+    };
+    constexpr size_t small = WalkLayout<NT, 64, STAGES, PT>::BYTES, large = WalkLayout<NT, 128, STAGES, PT>::BYTES;
+    if constexpr (BWD) return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, STAGES>, small) : go(delta_chain_tc_kernel<T, NT, 128, STAGES>, large);
+    else return a.Dk <= 64 ? go(delta_fwd_tc_kernel<T, NT, 64, STAGES>, small) : go(delta_fwd_tc_kernel<T, NT, 128, STAGES>, large);
 }
 
 template <typename T, int NT, int CT>
 int launch_chunks(const DeltaArgs &a, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(a.slots * a.Hv);
-    if (a.Dk <= 64)
-        return launch_walk(delta_chunk_tc_kernel<T, NT, CT, 64>, a, grid, kChunkThreads, ChunkLayout<NT, CT, 64>::BYTES, stream);
-    return launch_walk(delta_chunk_tc_kernel<T, NT, CT, 128>, a, grid, kChunkThreads, ChunkLayout<NT, CT, 128>::BYTES, stream);
+    auto go = [&](auto kernel, size_t smem) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return (int)QS_ERR_CUDA;
+        }
+        kernel<<<(unsigned)(a.slots * a.Hv), kChunkThreads, smem, stream>>>(a);
+        return launched();
+    };
+    return a.Dk <= 64 ? go(delta_chunk_tc_kernel<T, NT, CT, 64>, ChunkLayout<NT, CT, 64>::BYTES)
+                      : go(delta_chunk_tc_kernel<T, NT, CT, 128>, ChunkLayout<NT, CT, 128>::BYTES);
 }
 
 // Checks of sizes: QS_OK, an error, or 1 when there are no steps.
@@ -131,7 +135,8 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     const int es = dtype == QS_BF16 ? 2 : 4, ge = gate_dtype == QS_BF16 ? 2 : 4;
     DeltaArgs a{};
     geometry(a, strides, offsets, N, B, S, Hk, Hv, Dk, Dv, gate_dtype, scale);
-    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es)))
+    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es) ||
+                    qsh::has_flat_dim(a.sq, B, S, Hk) || qsh::has_flat_dim(a.sk, B, S, Hk) || qsh::has_flat_dim(a.sv, B, S, Hv)))
         return QS_ERR_MISALIGNED;
     const size_t gates = (size_t)B * S * Hv * ge, states = (size_t)N * Hv * Dk * Dv * 4, rows = (size_t)B * S * Hv * Dv;
     const Sized ins[] = {{q, qsh::span_bytes(a.sq, B, S, Hk, Dk, es)}, {k, qsh::span_bytes(a.sk, B, S, Hk, Dk, es)},
@@ -149,7 +154,7 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     const int wc = qsh::workspace(dev, stream, sizeof(WsHeader), &ws);
     if (wc != QS_OK) return wc;
     a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
-    return dtype == QS_BF16 ? launch_fwd<__nv_bfloat16, 1>(a, stream) : launch_fwd<float, 3>(a, stream);
+    return dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1>(a, stream) : launch_walks<false, float, 3>(a, stream);
 }
 
 extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
@@ -170,7 +175,8 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     const int es = dtype == QS_BF16 ? 2 : 4, ge = gate_dtype == QS_BF16 ? 2 : 4;
     DeltaArgs a{};
     geometry(a, strides, offsets, N, B, S, Hk, Hv, Dk, Dv, gate_dtype, scale);
-    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es)))
+    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es) ||
+                    qsh::has_flat_dim(a.sq, B, S, Hk) || qsh::has_flat_dim(a.sk, B, S, Hk) || qsh::has_flat_dim(a.sv, B, S, Hv)))
         return QS_ERR_MISALIGNED;
     const size_t gates = (size_t)B * S * Hv * ge, states = (size_t)N * Hv * Dk * Dv * 4, rows = (size_t)B * S * Hv * Dv;
     const size_t keys = (size_t)B * S * Hk * Dk, kept = (size_t)a.slots * Hv * Dk * Dv;
@@ -194,7 +200,7 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     a.ds = reinterpret_cast<float *>(p), a.w = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + nds + nw), a.dkh = reinterpret_cast<float *>(p + nds + nw + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
-    rc = dtype == QS_BF16 ? launch_chain<__nv_bfloat16, 1>(a, stream) : launch_chain<float, 3>(a, stream);
+    rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1>(a, stream) : launch_walks<true, float, 3>(a, stream);
     if (rc != QS_OK || !some) return rc;
     if (dtype != QS_BF16) rc = launch_chunks<float, 3, 3>(a, stream);
     else rc = gate_dtype == QS_BF16 ? launch_chunks<__nv_bfloat16, 1, 2>(a, stream) : launch_chunks<__nv_bfloat16, 1, 3>(a, stream);

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "quat_cumprod.h"
@@ -48,10 +49,20 @@ inline bool bad_strides(const Strides &t, int elem) {
     return t.b < 0 || t.s < 0 || t.h < 0 || t.b % m || t.s % m || t.h % m;
 }
 
+// Whether a dimension of more than one entry has no extent in memory (an expanded
+// view): tensor maps cannot hold it.
+inline bool has_flat_dim(const Strides &t, int64_t B, int64_t S, int64_t H) {
+    return (t.b == 0 && B > 1) || (t.s == 0 && S > 1) || (t.h == 0 && H > 1);
+}
+
 // Bytes from the first to past the last element.
 inline size_t span_bytes(const Strides &t, int64_t B, int64_t S, int64_t H, int64_t D, int elem) {
     if (B <= 0 || S <= 0 || H <= 0) return 0;
     return (size_t)((B - 1) * t.b + (S - 1) * t.s + (H - 1) * t.h + D) * elem;
 }
+
+// Tensor map of a bfloat16 tensor [B, S, H, D] for boxes of 64 steps x 64 values of
+// one head, 128-byte swizzle; what lies outside reads as zeros.
+QS_HIDDEN int head_map(CUtensorMap *map, const void *p, const Strides &t, int64_t B, int64_t S, int64_t H, int64_t D);
 
 }  // namespace qsh

@@ -1984,4 +1984,17 @@ int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base) {
 
 unsigned long long timeout_ns() { return g_timeout_ns; }
 
+int head_map(CUtensorMap *map, const void *p, const Strides &t, int64_t B, int64_t S, int64_t H, int64_t D) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return QS_ERR_CUDA;
+    const cuuint64_t any = 16;   // a stride that no box crosses
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+    cuuint64_t strides[3] = {H > 1 ? (cuuint64_t)t.h * 2 : any, S > 1 ? (cuuint64_t)t.s * 2 : any, B > 1 ? (cuuint64_t)t.b * 2 : any};
+    cuuint32_t box[4] = {64, 1, 64, 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QS_OK : QS_ERR_CUDA;
+}
+
 }  // namespace qsh
