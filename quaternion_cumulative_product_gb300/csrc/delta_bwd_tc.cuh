@@ -2,8 +2,8 @@
 // gradients of one chunk from the state that enters it, the cotangent of the
 // state that leaves it, its errors e and its w.
 //
-// One CTA per (chunk, value head), two warpgroups that share the 128 rows of each
-// product (each takes half of the columns).  Rows of queries and of keys are
+// One CTA per (chunk, value head), four warpgroups that share the 128 rows of each
+// product (each takes a quarter of the columns).  Rows of queries and of keys are
 // stacked, so that one product serves both:
 //
 //     [dO; dV] U^T                -> X, Y (64 + 64 rows, with the decays)
@@ -25,7 +25,7 @@
 
 namespace qs {
 
-constexpr int kChunkThreads = 256;
+constexpr int kChunkThreads = 512;
 
 template <int NT, int CT, int DK>
 struct ChunkLayout {
@@ -38,7 +38,7 @@ struct ChunkLayout {
     static constexpr uint32_t M_AT = QK_AT + NT * HALVES * 2 * TILE;     // M: [term][half of dv][DK rows]
     static constexpr uint32_t M_BYTES = CT * M_TERM > CT * 2 * TILE ? CT * M_TERM : CT * 2 * TILE;   // then [X;Y]: [term][128 rows]
     static constexpr uint32_t GATES_AT = M_AT + M_BYTES, ROWS_AT = GATES_AT + sizeof(ChunkGates);
-    static constexpr uint32_t BARS_AT = ROWS_AT + (2 * 128 + 8 + 8) * 4;
+    static constexpr uint32_t BARS_AT = ROWS_AT + (4 * 128 + 32) * 4;
     static constexpr uint32_t NEED = BARS_AT + 256 + 1024;
     static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;     // one CTA per SM: it takes all of the tensor memory
     static_assert(BYTES <= 232448, "227 KB of shared memory");
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     const uint32_t sm32 = smem_addr(sm);
     ChunkBars &bar = *reinterpret_cast<ChunkBars *>(sm + L::BARS_AT);
     ChunkGates &gt = *reinterpret_cast<ChunkGates *>(sm + L::GATES_AT);
-    float *rows = reinterpret_cast<float *>(sm + L::ROWS_AT);   // [2][128] row sums, then 16 sums of the warps
+    float *rows = reinterpret_cast<float *>(sm + L::ROWS_AT);   // [4][128] row sums, then 2 x 16 sums of the warps
     volatile int *gone = &bar.gone;
 
     const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     if (!chunk_of(a, blockIdx.x / a.Hv, &seq, &c)) return;
     const long long t0 = c * DC, row0 = seq.b * a.S + seq.s0 + t0;
     const int left = (int)min((long long)DC, seq.len - t0);
-    const int wg = threadIdx.x / 128, tid = threadIdx.x % 128, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int t = tid % 64;
     const bool live = t < left, keys = tid >= 64;   // this thread's row: a query's or a key's
     const size_t at0 = ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv;
@@ -134,16 +134,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
     if (warp == 0) tmem_alloc_all(&bar.tmem);
     if (warp == 1) warp_gates(gt, read_gates(a, seq, t0, head));
-    load_rows<T, NT, DK, 128>(sm32 + L::QK_AT + wg * TILE, 2 * TILE, L::HALVES * 2 * TILE, wg ? a.k : a.q, wg ? a.sk : a.sq, seq, t0, kh, a.Dk, tid);
+    {   // Q by half of the threads, K by the others
+        const int w = wg / 2;
+        load_rows<T, NT, DK, 256>(sm32 + L::QK_AT + w * TILE, 2 * TILE, L::HALVES * 2 * TILE, w ? a.k : a.q, w ? a.sk : a.sq, seq, t0, kh,
+                                  a.Dk, threadIdx.x % 256);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = bar.tmem, tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
+    const uint32_t tm = (uint32_t)warp_uniform((int)bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
 
     // M (or the first half of dv of it) into tiles: eight values per step of a thread.
     auto load_m = [&](int half0, int halves) {
         const int units = halves * 8;   // per row
-#pragma unroll 2
+#pragma unroll 4
         for (int i = threadIdx.x; i < DK * units; i += kChunkThreads) {
             const int r = i / units, u = i - r * units, x0 = half0 * 64 + u * 8;
             const bool in = r < a.Dk && x0 < a.Dv;
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         for (int i = CT - 1; i >= 0; --i)
 #pragma unroll
             for (int j = CT - 1 - i; j >= 0; --j)
-#pragma unroll 1
+#pragma unroll 4
                 for (int k = k0; k < k1; ++k) {
                     mma_ts(d, tm + bwd_tmem::A + i * 64 + k * 8, base + ((j * b_term + (k - k0) / 4 * b_half + k % 4 * 32) >> 4), idesc, add);
                     add = true;
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         const float be = gt.beta[t];
         float dot = 0.f;
 #pragma unroll 1
-        for (int x0 = wg * dvp / 2; x0 < (wg + 1) * dvp / 2; x0 += 16) {
+        for (int x0 = wg * dvp / 4; x0 < (wg + 1) * dvp / 4; x0 += 16) {
             float x[16], e[16];
             load16_upto(ep, live, x0, a.Dv, e);
             if (keys) {
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     fence_proxy_async_smem();
     __syncthreads();
     const uint32_t id_dk = mma_desc(128, DK), id_s = mma_desc(128, 64);
-    if (threadIdx.x == 0) {
+    if (warp == 0 && elect_one()) {
         tc_fence_after();
         issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 0, min(ksteps, 4 * L::MHALVES), false);
         mma_commit(&bar.m);
@@ -227,7 +231,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         mma_commit(&bar.xy);
     }
     if (wg == 1 && !keys && live)
-        store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, rows[64 + t] + rows[192 + t]);
+        store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head,
+                  (rows[64 + t] + rows[192 + t]) + (rows[320 + t] + rows[448 + t]));
     __syncwarp();
     uint32_t m_phase = 0;
     tc_wait_warp(&bar.m, m_phase, gone, a.ctl);
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         load_m(1, 1);
         fence_proxy_async_smem();
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (warp == 0 && elect_one()) {
             tc_fence_after();
             issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 4, 8, true);
             mma_commit(&bar.m);
@@ -245,15 +250,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         tc_wait_warp(&bar.m, m_phase, gone, a.ctl);
     }
 
-    // X and Y with their decays into tiles over M.  Each warpgroup takes the 16-column
-    // pieces p with p % 2 == wg.
+    // X and Y with their decays into tiles over M.  Each warpgroup takes 16
+    // columns.
     tc_wait_warp(&bar.xy, 0, gone, a.ctl);
     {
         const Sum2 mine = gt.sum[t];
         const float sign = keys ? -1.f : a.scale;
         const int last = keys ? t - 1 : t;   // the last column of this row
-#pragma unroll 1
-        for (int s0 = wg * 16; s0 < DC; s0 += 32) {
+        {
+            const int s0 = wg * 16;
             uint32_t g[16];
             tmem_ld16(tl + bwd_tmem::XY + s0, g);
             tmem_wait_ld();
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     tc_fence_before();
     __syncthreads();
     constexpr uint32_t qk_term = L::HALVES * 2 * TILE;
-    if (threadIdx.x == 0) {   // [Q;K]^T [X;Y]: both MN-major, 128 rows of K
+    if (warp == 0 && elect_one()) {   // [Q;K]^T [X;Y]: both MN-major, 128 rows of K
         tc_fence_after();
         const uint32_t id = mma_desc(128, 64, true, true);   // (rows past DK hold nothing and are not read)
         const uint64_t qk = smem_desc(sm32 + L::QK_AT, 2 * TILE, 1024), xy = smem_desc(sm32 + L::M_AT, 16, 1024);
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
 #pragma unroll
             for (int j = CT - 1; j >= 0; --j) {
                 if (i + j > CT - 1) continue;
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     mma_ss(tm + bwd_tmem::C, qk + ((i * qk_term + k * 2048) >> 4), xy + ((j * 2 * TILE + k * 2048) >> 4), id, add);
                     add = true;
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         const float f = keys ? -gt.grown[t] : a.scale * gt.grown[t];
         const float2 f2 = make_float2(f, f);
 #pragma unroll 1
-        for (int x0 = wg * DK / 2; x0 < (wg + 1) * DK / 2; x0 += 16) {
+        for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
             uint32_t r[16];
             tmem_ld16(tl + bwd_tmem::R + x0, r);
             tmem_wait_ld();
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         float dot = 0.f;
         const bool in = tid < a.Dk;
 #pragma unroll 1
-        for (int x0 = wg * dvp / 2; x0 < (wg + 1) * dvp / 2; x0 += 16) {
+        for (int x0 = wg * dvp / 4; x0 < (wg + 1) * dvp / 4; x0 += 16) {
             float x[16], y[16];
             load16_upto(dm + (size_t)tid * a.Dv, in, x0, a.Dv, x);
             load16_upto(m + (size_t)tid * a.Dv, in, x0, a.Dv, y);
@@ -331,12 +336,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         dot *= gt.whole;
 #pragma unroll
         for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) rows[256 + warp] = dot;
+        if (lane == 0) rows[512 + warp] = dot;
     }
     tmem_wait_st();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (warp == 0 && elect_one()) {
         tc_fence_after();
         issue_a(tm + bwd_tmem::E, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, ksteps, false);
         mma_commit(&bar.e);
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
 #pragma unroll
             for (int j = NT - 1; j >= 0; --j) {
                 if (i + j > CT - 1) continue;
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_ss(tm + bwd_tmem::R, xy + ((i * 2 * TILE + k * 32) >> 4), kk + ((j * qk_term + k * 2048) >> 4), id, true);
             }
@@ -373,25 +378,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     {
         float part = 0.f;
         const bool in = tid < DK;
-        const int s0 = wg * 32;
-        uint32_t x[32], y[32];
-        tmem_ld32(tl + bwd_tmem::C + s0, x);
-        tmem_ld32(tl + bwd_tmem::E + s0, y);
+        const int s0 = wg * 16;
+        uint32_t x[16], y[16];
+        tmem_ld16(tl + bwd_tmem::C + s0, x);
+        tmem_ld16(tl + bwd_tmem::E + s0, y);
         tmem_wait_ld();
         if (in)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 const float e = gt.left[s0 + i] * __uint_as_float(y[i]);
                 part = fmaf(e, qk_value(1, s0 + i, tid), part);
                 x[i] = __float_as_uint(__uint_as_float(x[i]) + e);
             }
 #pragma unroll
         for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
-        if (lane == 0) rows[264 + warp] = part;
+        if (lane == 0) rows[528 + warp] = part;
         // (U's last reader is done: bar.e.)
         if (in)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) col[(s0 + i) * L::CLD + tid] = __uint_as_float(x[i]);
+            for (int i = 0; i < 16; ++i) col[(s0 + i) * L::CLD + tid] = __uint_as_float(x[i]);
     }
     tc_wait_warp(&bar.r, 0, gone, a.ctl);
     __syncthreads();
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dk;
         float sum = 0.f;
 #pragma unroll 1
-        for (int x0 = wg * DK / 2; x0 < (wg + 1) * DK / 2; x0 += 16) {
+        for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
             uint32_t r[16];
             __syncwarp();
             tmem_ld16(tl + bwd_tmem::R + x0, r);
@@ -443,15 +448,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
     __syncthreads();
     if (warp == 0) {   // dg: suffix sums of dG, the last step's own part included in all
-        float tail = lane < 16 ? rows[256 + lane] : 0.f;
+        float tail = rows[512 + lane];
 #pragma unroll
-        for (int o = 8; o; o /= 2) tail += __shfl_xor_sync(0xffffffffu, tail, o);
-        tail = __shfl_sync(0xffffffffu, tail, 0);
+        for (int o = 16; o; o /= 2) tail += __shfl_xor_sync(0xffffffffu, tail, o);
         float d[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int s = 2 * lane + i;
-            d[i] = rows[s] + rows[128 + s] + rows[64 + s] + rows[192 + s];
+            d[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) d[i] += rows[64 * w + s];
         }
         float run = d[0] + d[1];
 #pragma unroll

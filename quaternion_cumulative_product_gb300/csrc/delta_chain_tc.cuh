@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const long long n = blockIdx.x / a.Hv;
     const Seq seq = seq_of(a, n);
     const int chunks = (int)((seq.len + DC - 1) / DC);
-    const int wg = threadIdx.x / 128, tid = threadIdx.x % 128, warp = threadIdx.x / 32;
+    const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L, STAGES, 3>(bar, sm32, 1 + 128);   // a stage is free after the products, and `out` done with beta
 
     if (wg >= 2) {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const ChunkGates &gt = gates[st];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             tc_wait_warp(&bar.full[st], (it / STAGES) & 1, gone, a.ctl);
-            if (threadIdx.x == 0)   // R = dO^T P
+            if (warp == 0 && elect_one())   // R = dO^T P
                 issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(stage + L::V_AT, TILE, 1024), L::V_TERM,
                                             smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
             __syncwarp();
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc_fence_before();
             named_bar_sync(1, 256);
             if (wg == 0) {
-                if (tid == 0) {
+                if (warp == 0 && elect_one()) {
                     tc_fence_after();
                     issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
                                                 mma_desc(128, 64), TmemK(), KMajor());
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_sync(3, 128);
-                if (tid == 0) {
+                if (warp == 0 && elect_one()) {
                     tc_fence_after();
                     issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
                                                mma_desc(128, 64, false, true), TmemK(), MNMajor());
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (threadIdx.x == 0) {
+            if (warp == 0 && elect_one()) {
                 tc_fence_after();
                 const uint32_t id = mma_desc(128, DK, false, true);
                 issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP, 32, smem_desc(stage + TILE, 2 * TILE, 1024), L::KQ_TERM,

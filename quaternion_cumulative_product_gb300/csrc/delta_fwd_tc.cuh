@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const long long n = blockIdx.x / a.Hv;
     const Seq seq = seq_of(a, n);
     const int chunks = (int)((seq.len + DC - 1) / DC);
-    const int wg = threadIdx.x / 128, tid = threadIdx.x % 128, warp = threadIdx.x / 32;
+    const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L, STAGES, PT>(bar, sm32, 1);
 
     if (wg >= 2) {
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc_wait_warp(&bar.full[st], (c / STAGES) & 1, gone, a.ctl);
             whole = gt.whole;
             if (wg == 0) {
-                if (tid == 0) {
+                if (warp == 0 && elect_one()) {
                     tc_fence_after();
                     issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
                                                 mma_desc(128, 128), TmemK(), KMajor());
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_sync(3, 128);
-                if (tid == 0) {
+                if (warp == 0 && elect_one()) {
                     tc_fence_after();
                     issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
                                                mma_desc(128, 64), TmemK(), KMajor1());
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_sync(3, 128);
-                if (tid == 0) {
+                if (warp == 0 && elect_one()) {
                     tc_wait(&bar.yread, c & 1, gone, a.ctl);   // Y has moved: dM takes its place, o adds up on it
                     tc_fence_after();
                     issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,

@@ -313,7 +313,7 @@ __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32, int
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    return bar.tmem;
+    return (uint32_t)warp_uniform((int)bar.tmem);
 }
 
 // The role of prep's threads (ptid 0 .. 255).  BWD: the backward's order and N.
@@ -323,7 +323,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const CUtensorMap 
                                           const void *third, const qsh::Strides &st3, WalkBars &bar, unsigned char *sm,
                                           const Seq &seq, int chunks, int head, uint32_t tm, uint32_t gram_at) {
     using L = WalkLayout<NT, DK, STAGES, PT>;
-    const int ptid = threadIdx.x - 256, warp = ptid / 32, kh = head / (a.Hv / a.Hk), half = ptid / 128;
+    const int ptid = threadIdx.x - 256, warp = warp_uniform(ptid / 32), kh = head / (a.Hv / a.Hk), half = ptid / 128;
     const uint32_t sm32 = smem_addr(sm);
     volatile int *gone = &bar.gone;
     float *tf = reinterpret_cast<float *>(sm + L::F_AT), *yf = reinterpret_cast<float *>(sm + L::Y_AT);
@@ -340,7 +340,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const CUtensorMap 
         ChunkGates &gt = gates[st];
         tc_wait_warp(&bar.empty[st], ((it / STAGES) & 1) ^ 1, gone, a.ctl);
         if constexpr (NT == 1) {
-            if (ptid == 0) {
+            if (warp == 0 && elect_one()) {
                 const int boxes = 2 * L::HALVES + (a.Dv > 64 ? 2 : 1);
                 const int s = (int)(seq.s0 + t0), b = (int)seq.b;
                 mbar_arrive_expect_tx(&bar.rows[st], boxes * TILE);
@@ -385,7 +385,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const CUtensorMap 
         }
         fence_proxy_async_smem();
         named_bar_sync(2, kPrepThreads);
-        if (ptid == 0) {   // Gram: rows 0-63 K K^T, rows 64-127 Q K^T
+        if (warp == 0 && elect_one()) {   // Gram: rows 0-63 K K^T, rows 64-127 Q K^T
             tc_fence_after();
             const uint64_t kq = smem_desc(stage, 16, 1024);
             issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());

@@ -77,6 +77,17 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
 // ---------------------------------------------------------------------------
 // Descriptors and products.
 // ---------------------------------------------------------------------------
+// One thread of a converged warp.  Products are issued under it, with operands that
+// are the same for the whole warp: their descriptors stay in uniform registers
+// (under `threadIdx.x == 0` each product costs several moves to them, and 85 to 125
+// clocks instead of the 64 that the tensor cores take).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int warp_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Shared-memory operand, 128-byte swizzle.  K-major: `sbo` = bytes between groups
 // of 8 rows.  MN-major: `lbo` = bytes between blocks of 64 values along M or N,
 // `sbo` = bytes between groups of 8 along K.
