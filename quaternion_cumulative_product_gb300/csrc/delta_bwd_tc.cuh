@@ -6,19 +6,25 @@
 // product (each takes a quarter of the columns).  Rows of queries and of keys are
 // stacked, so that one product serves both:
 //
-//     [dO; dV] U^T                -> X, Y (64 + 64 rows, with the decays)
-//     [dO; dV] M^T                -> the states' part of dq and of row
-//     [X; Y] K                    -> the rest of dq and of row
-//     [Q; K]^T [X; Y]  (dk x s)   -> col, transposed
-//     dM' U^T          (dk x s)   -> the state's part of col
+//     R  = [dO; dV] M^T            the states' part of dq and of row
+//     S  = [dO; dV] U^T            X, Y (64 + 64 rows) once the decays are on
+//     C  = U dM'^T                 the states' part of col (rows 64 .. 127)
+//     R += [X; Y] K                after R's rows have got their decays
+//     C += [X; Y]^T [Q; K]         likewise
 //
-// (names as in delta_common.cuh).  The stacked left operand and dM' are in tensor
-// memory, the others in shared memory; [X;Y] is a K-major operand in one product and
-// an MN-major one in the other.
+// (names as in delta_common.cuh).  The stacked left operand is in tensor memory, the
+// others in shared memory; [X;Y] is a K-major operand in one product and an MN-major
+// one in the other.  C's left operands have 64 rows; they stand in rows 64 .. 127 of
+// 128 (what lies before them in shared memory fills the others, which nobody
+// reads), so that a key's row and its col meet in one thread.
 //
 // Terms: CT bfloat16 terms per computed value: three (fp32 precision) where any
 // output is fp32; two (16 bits) where outputs and gates are bfloat16, whose own
 // rounding is 2^-9.
+//
+// Bound: the latency of its phases (loads, conversions, five products), one CTA per
+// SM.  Global loads run along the rows (a warp covers whole lines): loads by the
+// thread that owns a row touch 32 lines each, and were half of the kernel's time.
 #pragma once
 
 #include "delta_prep.cuh"
@@ -30,14 +36,19 @@ constexpr int kChunkThreads = 512;
 template <int NT, int CT, int DK>
 struct ChunkLayout {
     static constexpr int HALVES = DK / 64;
-    static constexpr int MHALVES = NT == 1 ? 2 : 1;                      // halves of dv of M held at a time
-    static constexpr uint32_t M_HALF = DK * 128, M_TERM = MHALVES * M_HALF;
-    static constexpr int CLD = DK + 4;                                   // col [64][CLD] fp32, over U
-    static constexpr uint32_t U_NEED = CT * 2 * TILE, C_NEED = (64 * CLD * 4 + 1023) / 1024 * 1024;
-    static constexpr uint32_t U_AT = 0, QK_AT = U_NEED > C_NEED ? U_NEED : C_NEED;   // U: [term][half of dv][64 rows]
-    static constexpr uint32_t M_AT = QK_AT + NT * HALVES * 2 * TILE;     // M: [term][half of dv][DK rows]
-    static constexpr uint32_t M_BYTES = CT * M_TERM > CT * 2 * TILE ? CT * M_TERM : CT * 2 * TILE;   // then [X;Y]: [term][128 rows]
-    static constexpr uint32_t GATES_AT = M_AT + M_BYTES, ROWS_AT = GATES_AT + sizeof(ChunkGates);
+    static constexpr int SH = NT == 1 ? 2 : 1;                           // halves of dv held at a time
+    static constexpr bool BOTH = NT == 1 && CT == 2;                     // M and dM' have room side by side
+    static constexpr uint32_t QK_TERM = HALVES * 2 * TILE;
+    static constexpr uint32_t M_HALF = DK * 128, M_TERM = SH * M_HALF;   // M, dM': [term][half of dv][DK rows]
+    static constexpr uint32_t A_HALF = 2 * TILE, A_TERM = SH * A_HALF;   // [dO; dV] on its way: [term][half of dv][128 rows]
+    static constexpr uint32_t QK_AT = 0, U_AT = NT * QK_TERM;            // U: [term][half of dv][64 rows]
+    static constexpr uint32_t M_AT = U_AT + CT * 2 * TILE;
+    static constexpr uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+    static constexpr uint32_t M_BYTES = max2(CT * M_TERM, max2(CT * 2 * TILE, BOTH ? 0 : CT * A_TERM));   // later [X;Y]: [term][128 rows]
+    static constexpr uint32_t DM_AT = BOTH ? M_AT + M_BYTES : M_AT;
+    static constexpr uint32_t A_AT = DM_AT;
+    static constexpr uint32_t GATES_AT = BOTH ? DM_AT + max2(CT * M_TERM, CT * A_TERM) : M_AT + M_BYTES;
+    static constexpr uint32_t ROWS_AT = GATES_AT + sizeof(ChunkGates);
     static constexpr uint32_t BARS_AT = ROWS_AT + (4 * 128 + 32) * 4;
     static constexpr uint32_t NEED = BARS_AT + 256 + 1024;
     static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;     // one CTA per SM: it takes all of the tensor memory
@@ -45,63 +56,30 @@ struct ChunkLayout {
 };
 
 namespace bwd_tmem {
-constexpr uint32_t A = 0;      // terms (3 x 64) of [dO; dV], then of dM'
-constexpr uint32_t XY = 192;   // [dO; dV] U^T (64)
-constexpr uint32_t R = 256;    // dq and row (128)
-constexpr uint32_t C = 384, E = 448;   // [Q;K]^T [X;Y] and dM' U^T (64 each)
+constexpr uint32_t A = 0;      // terms (3 x 64) of [dO; dV]
+constexpr uint32_t S = 192;    // [dO; dV] U^T (64)
+constexpr uint32_t R = 256, C = 384;
 }  // namespace bwd_tmem
 
 struct ChunkBars {
-    uint64_t m, xy, c, e, r;
+    uint64_t m, s, e, r;
     uint32_t tmem;
     int gone;
 };
 
-// Sixteen fp32 values of row r from value 16p into CT terms: tensor-memory columns.
+// Eight fp32 values at a row's unit u as CT terms, `term` bytes apart.
 template <int CT>
-__device__ __forceinline__ void terms_to_tmem(uint32_t at, uint32_t term, const float *x) {
-    uint32_t t[CT][8];
+__device__ __forceinline__ void unit_terms(uint32_t at, uint32_t term, const float4 p, const float4 q) {
+    uint32_t s[4][3];
+    split2<CT>(p.x, p.y, s[0]), split2<CT>(p.z, p.w, s[1]), split2<CT>(q.x, q.y, s[2]), split2<CT>(q.z, q.w, s[3]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t p[3];
-        split2<CT>(x[2 * i], x[2 * i + 1], p);
-#pragma unroll
-        for (int j = 0; j < CT; ++j) t[j][i] = p[j];
-    }
-#pragma unroll
-    for (int j = 0; j < CT; ++j) tmem_st8(at + j * term, t[j]);
-}
-
-__device__ __forceinline__ void load16(const float *p, bool in, float *x) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = in ? __ldg(reinterpret_cast<const float4 *>(p) + i) : q_zero();
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, bool in, float *x) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
-        const float4 a = IoBF16::get(make_uint2(v.x, v.y)), b = IoBF16::get(make_uint2(v.z, v.w));
-        x[8 * i] = a.x, x[8 * i + 1] = a.y, x[8 * i + 2] = a.z, x[8 * i + 3] = a.w;
-        x[8 * i + 4] = b.x, x[8 * i + 5] = b.y, x[8 * i + 6] = b.z, x[8 * i + 7] = b.w;
+    for (int j = 0; j < CT; ++j) {
+        const uint32_t v[4] = {s[0][j], s[1][j], s[2][j], s[3][j]};
+        st_shared16(at + j * term, v);
     }
 }
 
-// Sixteen values of a head row of length D from x0, as far as they exist (D is a multiple of 8).
-template <typename T>
-__device__ __forceinline__ void load16_upto(const T *p, bool in, int x0, int D, float *x) {
-    if (x0 + 16 <= D) {
-        load16(p + x0, in, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const float4 v = in && x0 + i < D ? load4(p + x0 + i) : q_zero();
-            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-        }
-    }
-}
+__device__ __forceinline__ float4 scaled(const float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
 
 template <typename T, int NT, int CT, int DK>
 __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const __grid_constant__ DeltaArgs a) {
@@ -120,15 +98,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     if (!chunk_of(a, blockIdx.x / a.Hv, &seq, &c)) return;
     const long long t0 = c * DC, row0 = seq.b * a.S + seq.s0 + t0;
     const int left = (int)min((long long)DC, seq.len - t0);
-    const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int t = tid % 64;
-    const bool live = t < left, keys = tid >= 64;   // this thread's row: a query's or a key's
+    const int wg = warp_uniform(threadIdx.x / 128), warp = warp_uniform(threadIdx.x / 32);
+    const int tid = threadIdx.x % 128, lane = threadIdx.x % 32, t = tid % 64;
+    const bool live = t < left, keys = warp % 4 >= 2;   // this thread's row of the products: a query's or a key's
     const size_t at0 = ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv;
-    const float *m = a.carries_in + at0, *dm = a.ds + at0;
-    const int dvp = a.Dv <= 64 ? 64 : 128, ksteps = dvp / 16;
+    const int dvh = a.Dv <= 64 ? 1 : 2;                 // halves of dv in use
 
     if (threadIdx.x == 0) {
-        for (uint64_t *b : {&bar.m, &bar.xy, &bar.c, &bar.e, &bar.r}) mbar_init(b, 1);
+        for (uint64_t *b : {&bar.m, &bar.s, &bar.e, &bar.r}) mbar_init(b, 1);
         *gone = 0;
         fence_mbar_init();
     }
@@ -136,176 +113,219 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     if (warp == 1) warp_gates(gt, read_gates(a, seq, t0, head));
     {   // Q by half of the threads, K by the others
         const int w = wg / 2;
-        load_rows<T, NT, DK, 256>(sm32 + L::QK_AT + w * TILE, 2 * TILE, L::HALVES * 2 * TILE, w ? a.k : a.q, w ? a.sk : a.sq, seq, t0, kh,
-                                  a.Dk, threadIdx.x % 256);
+        load_rows<T, NT, DK, 256>(sm32 + L::QK_AT + w * TILE, 2 * TILE, L::QK_TERM, w ? a.k : a.q, w ? a.sk : a.sq, seq, t0, kh, a.Dk,
+                                  threadIdx.x % 256);
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = (uint32_t)warp_uniform((int)bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
 
-    // M (or the first half of dv of it) into tiles: eight values per step of a thread.
-    auto load_m = [&](int half0, int halves) {
-        const int units = halves * 8;   // per row
-#pragma unroll 4
-        for (int i = threadIdx.x; i < DK * units; i += kChunkThreads) {
-            const int r = i / units, u = i - r * units, x0 = half0 * 64 + u * 8;
-            const bool in = r < a.Dk && x0 < a.Dv;
-            const float4 p = in ? __ldg(reinterpret_cast<const float4 *>(m + (size_t)r * a.Dv + x0)) : q_zero();
-            const float4 q = in ? __ldg(reinterpret_cast<const float4 *>(m + (size_t)r * a.Dv + x0 + 4)) : q_zero();
-            uint32_t s[4][3];
-            split2<CT>(p.x, p.y, s[0]), split2<CT>(p.z, p.w, s[1]), split2<CT>(q.x, q.y, s[2]), split2<CT>(q.z, q.w, s[3]);
+    // M and dM' as they are read: JT units of eight values per thread, unit j of a thread at
+    // the same place of either.
+    constexpr int UNITS = 8 * L::SH, JT = DK * 16 / kChunkThreads, JR = JT * L::SH / 2;   // units per row and round; per thread and round
+    auto unit_row = [&](int j) { return (int)(threadIdx.x + kChunkThreads * (j % JR)) / UNITS; };
+    auto unit_x = [&](int j) { return (int)(threadIdx.x % UNITS) * 8 + j / JR * 64; };   // first value
+    auto read_state = [&](const float *p, float4 (*v)[2]) {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+            const int r = unit_row(j), x = unit_x(j);
+            const bool in = r < a.Dk && x < a.Dv;
+            const float4 *src = reinterpret_cast<const float4 *>(p + at0 + (in ? (size_t)r * a.Dv + x : 0));
+            const float4 lo = __ldg(src), hi = __ldg(src + 1);
+            v[j][0] = in ? lo : q_zero(), v[j][1] = in ? hi : q_zero();
+        }
+    };
+    auto put_state = [&](uint32_t at, const float4 (*v)[2], int round) {   // the units of one round
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+            if (j / JR == round) {
+                const int r = unit_row(j), x = unit_x(j) - round * 64;
+                unit_terms<CT>(at + x / 64 * L::M_HALF + swizzled(r, x % 64 / 8), L::M_TERM, v[j][0], v[j][1]);
+            }
+    };
+    float4 m[JT][2], dm[JT][2];
+    read_state(a.carries_in, m);
+    if (L::BOTH) read_state(a.ds, dm);
+    __syncthreads();   // the gates
+
+    // D (+)= [dO; dV] x B, K steps k0 .. of the operand in tensor memory, B K-major.
+    uint32_t tm = 0;
+    auto issue_a = [&](uint32_t d, uint32_t b, uint32_t b_term, uint32_t b_half, uint32_t idesc, int k0, int halves, bool add) {
+        const uint64_t base = smem_desc(b, 16, 1024);
+#pragma unroll 1
+        for (int i = CT - 1; i >= 0; --i)
+#pragma unroll 1
+            for (int j = CT - 1 - i; j >= 0; --j)
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mma_ts(d, tm + bwd_tmem::A + i * 64 + (k0 + h * 4 + k) * 8, base + ((j * b_term + h * b_half + k * 32) >> 4), idesc, add);
+                        add = true;
+                    }
+    };
+    const uint32_t id_dk = mma_desc(128, DK), id_s = mma_desc(128, 64);
+
+    // Rows: U, [dO; dV] and dbeta = <e, w>, in rounds of SH halves of dv; M alongside.
+    const int rounds = (dvh + L::SH - 1) / L::SH;
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+        constexpr int RJ = DC * UNITS / kChunkThreads;
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            const int i = threadIdx.x + kChunkThreads * j, r = i / UNITS, x = i % UNITS * 8 + round * 64, xr = x - round * 64;
+            const bool in = r < left && x < a.Dv;
+            const size_t at = in ? ((size_t)(row0 + r) * a.Hv + head) * a.Dv + x : 0;
+            const float4 *ep = reinterpret_cast<const float4 *>(a.errors_in + at), *wp = reinterpret_cast<const float4 *>(a.w + at);
+            float4 e0 = __ldg(ep), e1 = __ldg(ep + 1), w0 = __ldg(wp), w1 = __ldg(wp + 1);
+            if (!in) e0 = e1 = w0 = w1 = q_zero();
+            const uint32_t stage = sm32 + L::A_AT + xr / 64 * L::A_HALF;
+            if constexpr (NT == 1) {
+                cp_async16_or_zero(stage + swizzled(r, xr % 64 / 8), static_cast<const T *>(a.d_o) + at, in);
+            } else {
+                const float4 *dp = reinterpret_cast<const float4 *>(static_cast<const float *>(a.d_o) + at);
+                const float4 d0 = __ldg(dp), d1 = __ldg(dp + 1);
+                unit_terms<CT>(stage + swizzled(r, xr % 64 / 8), L::A_TERM, in ? d0 : q_zero(), in ? d1 : q_zero());
+            }
+            float dot = dot4(e0, w0) + dot4(e1, w1);
+#pragma unroll
+            for (int o = UNITS / 2; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (threadIdx.x % UNITS == 0) rows[r] = round ? rows[r] + dot : dot;
+            const float be = gt.beta[r];
+            unit_terms<CT>(sm32 + L::U_AT + x / 64 * TILE + swizzled(r, x % 64 / 8), 2 * TILE, scaled(e0, be), scaled(e1, be));
+            unit_terms<CT>(stage + swizzled(64 + r, xr % 64 / 8), L::A_TERM, scaled(w0, be), scaled(w1, be));
+        }
+        cp_async_wait_all();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (round == 0) tm = (uint32_t)warp_uniform((int)bar.tmem);
+        const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
+#pragma unroll
+        for (int p = 0; p < L::SH; ++p) {   // 16 values of this thread's row
+            const int x = (wg * L::SH + p) * 16;
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
-                const uint32_t v[4] = {s[0][j], s[1][j], s[2][j], s[3][j]};
-                st_shared16(sm32 + L::M_AT + j * L::M_TERM + (u / 8) * L::M_HALF + swizzled(r, u % 8), v);
-            }
-        }
-    };
-    // D (+)= A terms (tensor memory, K steps k0 ..) x B terms (K-major).
-    auto issue_a = [&](uint32_t d, uint32_t b, uint32_t b_term, uint32_t b_half, uint32_t idesc, int k0, int k1, bool add) {
-        const uint64_t base = smem_desc(b, 16, 1024);
+                uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (NT == 3 || j == 0 || keys)
 #pragma unroll
-        for (int i = CT - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = CT - 1 - i; j >= 0; --j)
-#pragma unroll 4
-                for (int k = k0; k < k1; ++k) {
-                    mma_ts(d, tm + bwd_tmem::A + i * 64 + k * 8, base + ((j * b_term + (k - k0) / 4 * b_half + k % 4 * 32) >> 4), idesc, add);
-                    add = true;
-                }
-    };
-
-    // Rows of [dO; dV] into tensor memory and of U into tiles; dbeta = <e, w>.
-    {
-        const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dv;
-        const T *dop = static_cast<const T *>(a.d_o) + at;
-        const float *ep = a.errors_in + at, *wp = a.w + at;
-        const float be = gt.beta[t];
-        float dot = 0.f;
-#pragma unroll 1
-        for (int x0 = wg * dvp / 4; x0 < (wg + 1) * dvp / 4; x0 += 16) {
-            float x[16], e[16];
-            load16_upto(ep, live, x0, a.Dv, e);
-            if (keys) {
-                load16_upto(wp, live, x0, a.Dv, x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    dot = fmaf(x[i], e[i], dot);
-                    x[i] *= be;
-                }
-            } else {
-                load16_upto(dop, live, x0, a.Dv, x);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) e[i] *= be;
-                const uint32_t u = sm32 + L::U_AT + x0 / 64 * TILE;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t s[4][3];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) split2<CT>(e[8 * i + 2 * k], e[8 * i + 2 * k + 1], s[k]);
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) {
-                        const uint32_t v[4] = {s[0][j], s[1][j], s[2][j], s[3][j]};
-                        st_shared16(u + j * 2 * TILE + swizzled(t, x0 % 64 / 8 + i), v);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(sm + L::A_AT + j * L::A_TERM + x / 64 * L::A_HALF + swizzled(tid, x % 64 / 8 + u));
+                        v[4 * u] = q.x, v[4 * u + 1] = q.y, v[4 * u + 2] = q.z, v[4 * u + 3] = q.w;
                     }
-                }
+                tmem_st8(tl + bwd_tmem::A + j * 64 + round * 32 + x / 2, v);
             }
-            __syncwarp();
-            terms_to_tmem<CT>(tl + bwd_tmem::A + x0 / 2, 64, x);
         }
-        rows[wg * 128 + tid] = dot;
+        if (L::BOTH) put_state(sm32 + L::M_AT, m, 0);   // (elsewhere than the rows on their way)
+        tmem_wait_st();
+        tc_fence_before();
+        __syncthreads();
     }
-    load_m(0, L::MHALVES);
-    cp_async_wait_all();
-    tmem_wait_st();
-    tc_fence_before();
-    fence_proxy_async_smem();
-    __syncthreads();
-    const uint32_t id_dk = mma_desc(128, DK), id_s = mma_desc(128, 64);
-    if (warp == 0 && elect_one()) {
-        tc_fence_after();
-        issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 0, min(ksteps, 4 * L::MHALVES), false);
-        mma_commit(&bar.m);
-        issue_a(tm + bwd_tmem::XY, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, ksteps, false);
-        mma_commit(&bar.xy);
-    }
-    if (wg == 1 && !keys && live)
-        store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head,
-                  (rows[64 + t] + rows[192 + t]) + (rows[320 + t] + rows[448 + t]));
-    __syncwarp();
-    uint32_t m_phase = 0;
-    tc_wait_warp(&bar.m, m_phase, gone, a.ctl);
-    if (L::MHALVES == 1 && ksteps > 4) {   // the second half of dv
-        m_phase = 1;
-        load_m(1, 1);
+    tc_fence_after();
+    const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
+    if (wg == 0 && !keys && live) store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, rows[t]);
+
+    // R and S; then C, dM' beside M or in its place.
+    float md = 0.f;
+    if (L::BOTH) {
+        put_state(sm32 + L::DM_AT, dm, 0);
         fence_proxy_async_smem();
         __syncthreads();
         if (warp == 0 && elect_one()) {
             tc_fence_after();
-            issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 4, 8, true);
-            mma_commit(&bar.m);
+            issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 0, dvh, false);
+            issue_a(tm + bwd_tmem::S, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, dvh, false);
+            mma_commit(&bar.s);
         }
+    } else {
+#pragma unroll 1
+        for (int round = 0; round < rounds; ++round) {
+            if (round) tc_wait_warp(&bar.m, 0, gone, a.ctl);   // the first half of dv is done with
+            put_state(sm32 + L::M_AT, m, round);
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, round * 4, min(dvh, L::SH), round > 0);
+                if (round + 1 < rounds) mma_commit(&bar.m);
+                else {
+                    issue_a(tm + bwd_tmem::S, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, dvh, false);
+                    mma_commit(&bar.s);
+                }
+            }
+            __syncwarp();
+        }
+        read_state(a.ds, dm);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < JT; ++j) md += dot4(m[j][0], dm[j][0]) + dot4(m[j][1], dm[j][1]);
+    md *= gt.whole;
+#pragma unroll
+    for (int o = 16; o; o /= 2) md += __shfl_xor_sync(0xffffffffu, md, o);
+    if (lane == 0) rows[512 + warp] = md;
+    auto issue_c = [&](int round, int halves) {   // C (+)= U dM'^T, U in rows 64 .. 127
+        const uint64_t u = smem_desc(sm32 + L::U_AT - TILE, 16, 1024), d = smem_desc(sm32 + L::DM_AT, 16, 1024);
+        bool add = round > 0;
+#pragma unroll 1
+        for (int i = CT - 1; i >= 0; --i)
+#pragma unroll 1
+            for (int j = CT - 1 - i; j >= 0; --j)
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mma_ss(tm + bwd_tmem::C, u + ((i * 2 * TILE + (round + h) * TILE + k * 32) >> 4),
+                               d + ((j * L::M_TERM + h * L::M_HALF + k * 32) >> 4), id_dk, add);
+                        add = true;
+                    }
+        mma_commit(&bar.e);
+    };
+    uint32_t e_phase = 0;
+    if (L::BOTH) {
+        if (warp == 0 && elect_one()) issue_c(0, dvh);
         __syncwarp();
-        tc_wait_warp(&bar.m, m_phase, gone, a.ctl);
+        tc_wait_warp(&bar.s, 0, gone, a.ctl);
+    } else {
+        tc_wait_warp(&bar.s, 0, gone, a.ctl);
+#pragma unroll 1
+        for (int round = 0; round < rounds; ++round) {
+            if (round) {
+                tc_wait_warp(&bar.e, 0, gone, a.ctl);
+                e_phase = 1;
+            }
+            put_state(sm32 + L::DM_AT, dm, round);
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_c(round, min(dvh, L::SH));
+            }
+            __syncwarp();
+        }
     }
 
-    // X and Y with their decays into tiles over M.  Each warpgroup takes 16
-    // columns.
-    tc_wait_warp(&bar.xy, 0, gone, a.ctl);
+    // X and Y with their decays (16 columns per warpgroup), as tiles over M once its last
+    // reader is done.
     {
         const Sum2 mine = gt.sum[t];
         const float sign = keys ? -1.f : a.scale;
-        const int last = keys ? t - 1 : t;   // the last column of this row
-        {
-            const int s0 = wg * 16;
-            uint32_t g[16];
-            tmem_ld16(tl + bwd_tmem::XY + s0, g);
-            tmem_wait_ld();
-            float x[16];
+        const int last = keys ? t - 1 : t, s0 = wg * 16;   // the last column of this row
+        uint32_t g[16];
+        tmem_ld16(tl + bwd_tmem::S + s0, g);
+        tmem_wait_ld();
+        float x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const Sum2 o = gt.sum[s0 + i];
-                const bool on = s0 + i <= last;
-                x[i] = on ? __uint_as_float(g[i]) * (sign * exp2_fast(on ? (mine.hi - o.hi) + (mine.lo - o.lo) : 0.f)) : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t s[4][3];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) split2<CT>(x[8 * i + 2 * k], x[8 * i + 2 * k + 1], s[k]);
-#pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    const uint32_t v[4] = {s[0][j], s[1][j], s[2][j], s[3][j]};
-                    st_shared16(sm32 + L::M_AT + j * 2 * TILE + swizzled(tid, s0 / 8 + i), v);
-                }
-            }
+        for (int i = 0; i < 16; ++i) {
+            const Sum2 o = gt.sum[s0 + i];
+            const bool on = s0 + i <= last;
+            x[i] = on ? __uint_as_float(g[i]) * (sign * exp2_fast(on ? (mine.hi - o.hi) + (mine.lo - o.lo) : 0.f)) : 0.f;
         }
+        if (!L::BOTH) tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            unit_terms<CT>(sm32 + L::M_AT + swizzled(tid, s0 / 8 + i), 2 * TILE, make_float4(x[8 * i], x[8 * i + 1], x[8 * i + 2], x[8 * i + 3]),
+                           make_float4(x[8 * i + 4], x[8 * i + 5], x[8 * i + 6], x[8 * i + 7]));
     }
     fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    constexpr uint32_t qk_term = L::HALVES * 2 * TILE;
-    if (warp == 0 && elect_one()) {   // [Q;K]^T [X;Y]: both MN-major, 128 rows of K
-        tc_fence_after();
-        const uint32_t id = mma_desc(128, 64, true, true);   // (rows past DK hold nothing and are not read)
-        const uint64_t qk = smem_desc(sm32 + L::QK_AT, 2 * TILE, 1024), xy = smem_desc(sm32 + L::M_AT, 16, 1024);
-        bool add = false;
-#pragma unroll
-        for (int i = NT - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = CT - 1; j >= 0; --j) {
-                if (i + j > CT - 1) continue;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mma_ss(tm + bwd_tmem::C, qk + ((i * qk_term + k * 2048) >> 4), xy + ((j * 2 * TILE + k * 2048) >> 4), id, add);
-                    add = true;
-                }
-            }
-        mma_commit(&bar.c);
-    }
-    __syncwarp();
-    // The states' part of dq and row gets its decay; dM' takes [dO; dV]'s place; <M, dM'>.
+    // R's rows get their decay.
     {
         const float f = keys ? -gt.grown[t] : a.scale * gt.grown[t];
         const float2 f2 = make_float2(f, f);
@@ -321,127 +341,97 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             }
             tmem_st16(tl + bwd_tmem::R + x0, r);
         }
-        float dot = 0.f;
-        const bool in = tid < a.Dk;
-#pragma unroll 1
-        for (int x0 = wg * dvp / 4; x0 < (wg + 1) * dvp / 4; x0 += 16) {
-            float x[16], y[16];
-            load16_upto(dm + (size_t)tid * a.Dv, in, x0, a.Dv, x);
-            load16_upto(m + (size_t)tid * a.Dv, in, x0, a.Dv, y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dot = fmaf(x[i], y[i], dot);
-            __syncwarp();
-            terms_to_tmem<CT>(tl + bwd_tmem::A + x0 / 2, 64, x);
-        }
-        dot *= gt.whole;
-#pragma unroll
-        for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) rows[512 + warp] = dot;
     }
     tmem_wait_st();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && elect_one()) {   // R += [X;Y] K: rows of K are the K dimension
         tc_fence_after();
-        issue_a(tm + bwd_tmem::E, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, ksteps, false);
-        mma_commit(&bar.e);
-        // [X;Y] K: rows of K are the K dimension
-        const uint32_t id = mma_desc(128, DK, false, true);
-        const uint64_t xy = smem_desc(sm32 + L::M_AT, 16, 1024), kk = smem_desc(sm32 + L::QK_AT + TILE, 2 * TILE, 1024);
-#pragma unroll
-        for (int i = CT - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = NT - 1; j >= 0; --j) {
-                if (i + j > CT - 1) continue;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss(tm + bwd_tmem::R, xy + ((i * 2 * TILE + k * 32) >> 4), kk + ((j * qk_term + k * 2048) >> 4), id, true);
-            }
+        issue_ss<CT, NT, CT - 1, 4>(tm + bwd_tmem::R, smem_desc(sm32 + L::M_AT, 16, 1024), 2 * TILE,
+                                    smem_desc(sm32 + L::QK_AT + TILE, 2 * TILE, 1024), L::QK_TERM, mma_desc(128, DK, false, true), KMajor1(),
+                                    MNMajor(), true);
         mma_commit(&bar.r);
     }
     __syncwarp();
-
-    // One value of K (from its terms) at row s, column x.
-    auto qk_value = [&](int which, int s, int x) {
-        float v = 0.f;
+    // Eight values of this thread's row of Q or K, from x0 on.
+    auto qk_row = [&](int x0, float *f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = 0.f;
 #pragma unroll
         for (int j = NT - 1; j >= 0; --j) {
-            const unsigned char *p = sm + L::QK_AT + j * qk_term + (x / 64 * 2 + which) * TILE + swizzled(s, x % 64 / 8) + x % 8 * 2;
-            v += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
+            const uint4 p = *reinterpret_cast<const uint4 *>(sm + L::QK_AT + j * L::QK_TERM + (x0 / 64 * 2 + keys) * TILE + swizzled(t, x0 % 64 / 8));
+            const float4 lo = IoBF16::get(make_uint2(p.x, p.y)), hi = IoBF16::get(make_uint2(p.z, p.w));
+            f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w, f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
         }
-        return v;
     };
-    // col, transposed back through shared memory over U; the sum of exp(G_C - G_t) <k_t, dM' u_t>.
-    tc_wait_warp(&bar.c, 0, gone, a.ctl);
-    tc_wait_warp(&bar.e, 0, gone, a.ctl);
-    float *col = reinterpret_cast<float *>(sm + L::U_AT);
-    {
-        float part = 0.f;
-        const bool in = tid < DK;
-        const int s0 = wg * 16;
-        uint32_t x[16], y[16];
-        tmem_ld16(tl + bwd_tmem::C + s0, x);
-        tmem_ld16(tl + bwd_tmem::E + s0, y);
-        tmem_wait_ld();
-        if (in)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = gt.left[s0 + i] * __uint_as_float(y[i]);
-                part = fmaf(e, qk_value(1, s0 + i, tid), part);
-                x[i] = __float_as_uint(__uint_as_float(x[i]) + e);
-            }
-#pragma unroll
-        for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
-        if (lane == 0) rows[528 + warp] = part;
-        // (U's last reader is done: bar.e.)
-        if (in)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) col[(s0 + i) * L::CLD + tid] = __uint_as_float(x[i]);
-    }
-    tc_wait_warp(&bar.r, 0, gone, a.ctl);
-    __syncthreads();
-    {
-        const bool shared = a.Hv != a.Hk;
-        const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dk;
-        float sum = 0.f;
+    // C's rows (the keys') get theirs; the sum of exp(G_C - G_t) <k_t, dM' u_t>.
+    float part = 0.f;
+    tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+    if (keys) {
+        const float2 f2 = make_float2(gt.left[t], gt.left[t]);
 #pragma unroll 1
         for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
             uint32_t r[16];
-            __syncwarp();
-            tmem_ld16(tl + bwd_tmem::R + x0, r);
+            tmem_ld16(tl + bwd_tmem::C + x0, r);
             tmem_wait_ld();
-            float v[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {   // <q, dq> or <k, row - col>
-                float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 2; ++h) {
+                float f[8];
+                qk_row(x0 + 8 * h, f);
 #pragma unroll
-                for (int j = NT - 1; j >= 0; --j) {
-                    const uint4 p = *reinterpret_cast<const uint4 *>(sm + L::QK_AT + j * qk_term + (x0 / 64 * 2 + keys) * TILE +
-                                                                     swizzled(t, x0 % 64 / 8 + i));
-                    const float4 lo = IoBF16::get(make_uint2(p.x, p.y)), hi = IoBF16::get(make_uint2(p.z, p.w));
-                    f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w, f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
-                }
-                float cl[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (keys) {
-                    const float4 lo = *reinterpret_cast<const float4 *>(col + t * L::CLD + x0 + 8 * i);
-                    const float4 hi = *reinterpret_cast<const float4 *>(col + t * L::CLD + x0 + 8 * i + 4);
-                    cl[0] = lo.x, cl[1] = lo.y, cl[2] = lo.z, cl[3] = lo.w, cl[4] = hi.x, cl[5] = hi.y, cl[6] = hi.z, cl[7] = hi.w;
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float w = __uint_as_float(r[8 * i + k]);
-                    sum = fmaf(f[k], w - cl[k], sum);
-                    v[8 * i + k] = w + cl[k];
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 8 * h + 2 * i;
+                    const float2 y = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2);
+                    part = fmaf(y.x, f[2 * i], fmaf(y.y, f[2 * i + 1], part));
+                    r[k] = __float_as_uint(y.x), r[k + 1] = __float_as_uint(y.y);
                 }
             }
-            if (live) {
+            __syncwarp();
+            tmem_st16(tl + bwd_tmem::C + x0, r);
+        }
+    }
 #pragma unroll
-                for (int i = 0; i < 16; i += 8)
-                    if (x0 + i < a.Dk) {
-                        const float4 p[2] = {make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7])};
-                        if (shared) store_quads<2>((keys ? a.dkh : a.dqh) + at + x0 + i, p);
-                        else store_quads<2>(static_cast<T *>(keys ? a.dk : a.dq) + at + x0 + i, p);
-                    }
+    for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) rows[528 + warp] = part;
+    tmem_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && elect_one()) {   // C += [X;Y]^T [Q;K], [X;Y]'s columns in rows 64 .. 127
+        tc_fence_after();
+        issue_ss<CT, NT, CT - 1, 8>(tm + bwd_tmem::C, smem_desc(sm32 + L::M_AT - TILE, TILE, 1024), 2 * TILE,
+                                    smem_desc(sm32 + L::QK_AT, 2 * TILE, 1024), L::QK_TERM, mma_desc(128, DK, true, true), MNMajor(), MNMajor(),
+                                    true);
+        mma_commit(&bar.m);   // (its phases: the first half of dv, where there were two, then this)
+    }
+    __syncwarp();
+    tc_wait_warp(&bar.r, 0, gone, a.ctl);
+    tc_wait_warp(&bar.m, !L::BOTH && rounds > 1 ? 1 : 0, gone, a.ctl);
+    {
+        const bool shared = a.Hv != a.Hk;
+        const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dk;
+        float sum = 0.f;   // <q, dq> or <k, row - col>
+#pragma unroll 1
+        for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
+            uint32_t r[16], cl[16];
+            __syncwarp();
+            tmem_ld16(tl + bwd_tmem::R + x0, r);
+            tmem_ld16(tl + bwd_tmem::C + x0, cl);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float f[8], v[8];
+                qk_row(x0 + 8 * h, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float w = __uint_as_float(r[8 * h + k]), col = keys ? __uint_as_float(cl[8 * h + k]) : 0.f;
+                    sum = fmaf(f[k], w - col, sum);
+                    v[k] = w + col;
+                }
+                if (live && x0 + 8 * h < a.Dk) {
+                    const float4 p[2] = {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+                    if (shared) store_quads<2>((keys ? a.dkh : a.dqh) + at + x0 + 8 * h, p);
+                    else store_quads<2>(static_cast<T *>(keys ? a.dk : a.dq) + at + x0 + 8 * h, p);
+                }
             }
         }
         rows[wg * 128 + tid] = sum;
