@@ -110,6 +110,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc_all(&bar.tmem);
+    // What the CTA that follows on this SM reads, on its way into L2 meanwhile.
+    if (blockIdx.x + a.ahead < gridDim.x) {
+        const int nh = (blockIdx.x + a.ahead) % a.Hv;
+        Seq ns;
+        long long nc;
+        if (chunk_of(a, (blockIdx.x + a.ahead) / a.Hv, &ns, &nc)) {
+            const size_t nat = ((size_t)(ns.slot0 + nc) * a.Hv + nh) * a.Dk * a.Dv;
+            const long long nrow = ns.b * a.S + ns.s0 + nc * DC;
+            if (threadIdx.x < 64 && nc * DC + t < ns.len) {
+                const size_t row = ((size_t)(nrow + t) * a.Hv + nh) * a.Dv;
+                l2_prefetch(a.errors_in + row, a.Dv * 4);
+                l2_prefetch(a.w + row, a.Dv * 4);
+            } else if (threadIdx.x == 64) {
+                l2_prefetch(a.carries_in + nat, a.Dk * a.Dv * 4);
+                l2_prefetch(a.ds + nat, a.Dk * a.Dv * 4);
+            }
+        }
+    }
     if (warp == 1) warp_gates(gt, read_gates(a, seq, t0, head));
     {   // Q by half of the threads, K by the others
         const int w = wg / 2;
@@ -406,9 +424,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     __syncwarp();
     tc_wait_warp(&bar.r, 0, gone, a.ctl);
     tc_wait_warp(&bar.m, !L::BOTH && rounds > 1 ? 1 : 0, gone, a.ctl);
+    // dq and dk: rows to tiles in shared memory (every operand is done with), then whole lines out.
+    constexpr uint32_t OUT_ROW = DK * 4 + 16;   // padded fp32 rows
+    static_assert(L::U_AT + 128 * OUT_ROW <= L::GATES_AT, "the operands' place holds the rows of dq and dk");
     {
-        const bool shared = a.Hv != a.Hk;
-        const size_t at = ((size_t)(row0 + t) * a.Hv + head) * a.Dk;
         float sum = 0.f;   // <q, dq> or <k, row - col>
 #pragma unroll 1
         for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
@@ -417,6 +436,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             tmem_ld16(tl + bwd_tmem::R + x0, r);
             tmem_ld16(tl + bwd_tmem::C + x0, cl);
             tmem_wait_ld();
+            float *out = reinterpret_cast<float *>(sm + L::U_AT + tid * OUT_ROW) + x0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float f[8], v[8];
@@ -427,16 +447,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                     sum = fmaf(f[k], w - col, sum);
                     v[k] = w + col;
                 }
-                if (live && x0 + 8 * h < a.Dk) {
-                    const float4 p[2] = {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
-                    if (shared) store_quads<2>((keys ? a.dkh : a.dqh) + at + x0 + 8 * h, p);
-                    else store_quads<2>(static_cast<T *>(keys ? a.dk : a.dq) + at + x0 + 8 * h, p);
-                }
+                store4(out + 8 * h, make_float4(v[0], v[1], v[2], v[3]));
+                store4(out + 8 * h + 4, make_float4(v[4], v[5], v[6], v[7]));
             }
         }
         rows[wg * 128 + tid] = sum;
     }
     __syncthreads();
+    {
+        const bool shared = a.Hv != a.Hk;
+        constexpr int PER = 8, UN = DK / PER;   // values per store of a thread
+#pragma unroll 2
+        for (int i = threadIdx.x; i < 128 * UN; i += kChunkThreads) {
+            const int r = i / UN, x = i % UN * PER, s = r % 64;
+            if (s < left && x < a.Dk) {
+                const float *src = reinterpret_cast<const float *>(sm + L::U_AT + r * OUT_ROW) + x;
+                const float4 v[2] = {*reinterpret_cast<const float4 *>(src), *reinterpret_cast<const float4 *>(src + 4)};
+                const size_t at = ((size_t)(row0 + s) * a.Hv + head) * a.Dk + x;
+                if (shared) store_quads<2>((r < 64 ? a.dqh : a.dkh) + at, v);
+                else store_quads<2>(static_cast<T *>(r < 64 ? a.dq : a.dk) + at, v);
+            }
+        }
+    }
     if (warp == 0) {   // dg: suffix sums of dG, the last step's own part included in all
         float tail = rows[512 + lane];
 #pragma unroll

@@ -10,9 +10,8 @@
 //     w = (exp(G_C - G) X + R) T
 //     dM = exp(G_C) dM' + (scale exp(G) dO)^T Q - (exp(G) beta w)^T K
 //
-//   chain   X, w and w's part of the update; half of dM's columns
-//   out     dO's part of the update; the other half; writes w and dv
-//   prep    as in the forward (delta_prep.cuh)
+// Two warpgroups walk (half of the columns each between two products; w's part of the
+// update one, dO's the other), two prepare, as in the forward (delta_prep.cuh).
 //
 // T and P are read across their rows (MN-major), dO^T as an MN-major left operand.
 #pragma once
@@ -46,7 +45,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const Seq seq = seq_of(a, n);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
-    const uint32_t tm = walk_setup<L, STAGES, 3>(bar, sm32, 1 + 128);   // a stage is free after the products, and `out` done with beta
+    const uint32_t tm = walk_setup<L, STAGES, 3>(bar, sm32, 1 + 256);   // a stage is free after the products, and the walk done with beta
 
     if (wg >= 2) {
         const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
@@ -104,40 +103,40 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (wg == 0) {
-                if (warp == 0 && elect_one()) {
-                    tc_fence_after();
-                    issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
-                                                mma_desc(128, 64), TmemK(), KMajor());
-                    mma_commit(&bar.x);
-                }
-                __syncwarp();
-                tc_wait_warp(&bar.x, it & 1, gone, a.ctl);
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
+                                            mma_desc(128, 64), TmemK(), KMajor());
+                mma_commit(&bar.x);
+            }
+            __syncwarp();
+            tc_wait_warp(&bar.x, it & 1, gone, a.ctl);
 #pragma unroll 1
-                for (int h = 0; h < DC; h += 16) {
-                    uint32_t r[16], y[16];
-                    float2 e[8];
-                    tmem_ld16(tl + chain_tmem::X + h, r);
-                    tmem_ld16(tl + chain_tmem::R + h, y);
-                    tmem_wait_ld();
+            for (int h = wg * 32; h < wg * 32 + 32; h += 16) {
+                uint32_t r[16], y[16];
+                float2 e[8];
+                tmem_ld16(tl + chain_tmem::X + h, r);
+                tmem_ld16(tl + chain_tmem::R + h, y);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        e[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                    *reinterpret_cast<const float2 *>(&gt.left[h + 2 * i]),
-                                    make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
-                    put_terms3(tl + chain_tmem::SP + h / 2, 32, e);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                named_bar_sync(3, 128);
-                if (warp == 0 && elect_one()) {
-                    tc_fence_after();
-                    issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
-                                               mma_desc(128, 64, false, true), TmemK(), MNMajor());
-                    mma_commit(&bar.e);
-                }
-                __syncwarp();
-                tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
+                for (int i = 0; i < 8; ++i)
+                    e[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                                *reinterpret_cast<const float2 *>(&gt.left[h + 2 * i]),
+                                make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
+                put_terms3(tl + chain_tmem::SP + h / 2, 32, e);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(1, 256);
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
+                                           mma_desc(128, 64, false, true), TmemK(), MNMajor());
+                mma_commit(&bar.e);
+            }
+            __syncwarp();
+            tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
+            if (wg == 0) {
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {   // -exp(G) beta w
                     uint32_t r[16];
@@ -151,8 +150,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                     *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]));
                     put_terms3(tl + chain_tmem::SP + 96 + h / 2, 32, z);
                 }
-            } else {
-                tc_wait_warp(&bar.e, it & 1, gone, a.ctl);   // the terms of X + R give way to scale exp(G) dO
+            } else {   // scale exp(G) dO, where the terms of X + R were
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {
                     float v[16];
@@ -179,15 +177,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.empty[st]);
             }
             __syncwarp();
-            if (wg == 1) {   // w and dv
-                const size_t at = ((size_t)(row0 + (long long)c * DC) * a.Hv + head) * a.Dv + dv;
+            {   // w and dv, half of the steps each, while the products run
+                const int h0 = wg * 32;
+                const size_t at = ((size_t)(row0 + (long long)c * DC + h0) * a.Hv + head) * a.Dv + dv;
+                float *wo = a.w + at;
+                T *vo = static_cast<T *>(a.dv) + at;
 #pragma unroll 1
-                for (int h = 0; h < DC; h += 16) {
+                for (int h = h0; h < h0 + 32; h += 16, wo += 16 * step, vo += 16 * step) {
                     uint32_t r[16];
                     tmem_ld16(tl + chain_tmem::X + h, r);
                     tmem_wait_ld();
-                    float *wo = a.w + at + h * step;
-                    T *vo = static_cast<T *>(a.dv) + at + h * step;
                     if (in)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)

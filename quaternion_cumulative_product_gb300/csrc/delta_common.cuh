@@ -56,6 +56,7 @@ struct DeltaArgs {
     int Hk, Hv, Dk, Dv;
     bool gate16;
     float scale;
+    unsigned ahead;   // CTAs in flight of the backward's chunk kernel
     Control ctl;
 };
 

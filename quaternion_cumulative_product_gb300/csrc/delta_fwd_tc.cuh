@@ -2,16 +2,17 @@
 //
 // One CTA walks the chunks of one (sequence, value head).  Everything that the
 // chain of states goes through is laid out transposed: the state M^T [dv][dk], the
-// errors e^T [dv][t] and so on have one value row dv per tensor-memory lane, so
-// one thread owns one row of every product of the chain, and no value crosses
-// threads between two of them.  Four warpgroups:
+// errors e^T [dv][t] and so on have one value row dv per tensor-memory lane:
+// threads own rows of every product of the chain, and no value crosses threads
+// between two of them.  Four warpgroups:
 //
-//   chain   [X Y] = M^T [K;Q]^T;  e = (v - exp(G) X) T^T;  dM = (beta left e)^T K;
-//           half of the state's columns
-//   out     o = scale exp(G) Y + U P^T; the other half
+//   walk    two warpgroups: [X Y] = M^T [K;Q]^T;  e = (v - exp(G) X) T^T;
+//           dM = (beta left e)^T K;  o = scale exp(G) Y + U P^T.  Each converts half of
+//           the columns between two products; the second one also takes care of o
+//           while the products run
 //   prep    two warpgroups, one chunk ahead (delta_prep.cuh)
 //
-// The state stays in the registers of `chain` and `out` (fp32, half of dk each): adding
+// The state stays in the registers of `walk` (fp32, half of dk each): adding
 // dM to it there rounds once, where adding up in the tensor cores would cut off the
 // state's last bit with every one of the product's passes.
 //
@@ -132,93 +133,40 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             named_bar_sync(1, 256);
             tc_wait_warp(&bar.full[st], (c / STAGES) & 1, gone, a.ctl);
             whole = gt.whole;
-            if (wg == 0) {
-                if (warp == 0 && elect_one()) {
-                    tc_fence_after();
-                    issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
-                                                mma_desc(128, 128), TmemK(), KMajor());
-                    mma_commit(&bar.x);
-                }
-                __syncwarp();
-                tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
+                                            mma_desc(128, 128), TmemK(), KMajor());
+                mma_commit(&bar.x);
+            }
+            __syncwarp();
+            if (wg == 1 && c > 0) write_o(c - 1);
+            tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
 #pragma unroll 1
-                for (int h = 0; h < DC; h += 16) {
-                    uint32_t r[16];
-                    float v[16];
-                    float2 e[8];
-                    tmem_ld16(tl + fwd_tmem::D + h, r);
-                    third_column<NT>(sm + st * L::STAGE + L::V_AT, dv, h, v);
-                    tmem_wait_ld();
+            for (int h = wg * 32; h < wg * 32 + 32; h += 16) {   // v - exp(G) X
+                uint32_t r[16];
+                float v[16];
+                float2 e[8];
+                tmem_ld16(tl + fwd_tmem::D + h, r);
+                third_column<NT>(sm + st * L::STAGE + L::V_AT, dv, h, v);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        e[i] = fma2(make_float2(-__uint_as_float(r[2 * i]), -__uint_as_float(r[2 * i + 1])),
-                                    *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]), make_float2(v[2 * i], v[2 * i + 1]));
-                    put_terms3(tl + fwd_tmem::SP + h / 2, 32, e);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                named_bar_sync(3, 128);
-                if (warp == 0 && elect_one()) {
-                    tc_fence_after();
-                    issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
-                                               mma_desc(128, 64), TmemK(), KMajor1());
-                    mma_commit(&bar.e);
-                }
-                __syncwarp();
-                tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
-                float *eo = a.errors ? a.errors + ((size_t)(row0 + (long long)c * DC) * a.Hv + head) * a.Dv + dv : nullptr;
-#pragma unroll 1
-                for (int h = 0; h < DC; h += 32) {   // (U takes the place of 32 columns of e: both halves are read first)
-                    uint32_t r[32];
-                    tmem_ld32(tl + fwd_tmem::X + h, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (eo && in) {
-                            float *out = eo + (h + q * 16) * step;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (h + q * 16 + i < left) out[i * step] = __uint_as_float(r[q * 16 + i]);
-                        }
-                        __syncwarp();
-                        float2 u[8];
-                        uint32_t t[PT][8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int s = q * 16 + 2 * i;
-                            u[i] = mul2(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])),
-                                        *reinterpret_cast<const float2 *>(&gt.beta[h + s]));
-                            uint32_t p[3];
-                            split2<PT>(u[i], p);
-#pragma unroll
-                            for (int j = 0; j < PT; ++j) t[j][i] = p[j];
-                            u[i] = mul2(u[i], *reinterpret_cast<const float2 *>(&gt.left[h + s]));
-                        }
-#pragma unroll
-                        for (int j = 0; j < PT; ++j)
-                            tmem_st8(tl + (kEarly ? fwd_tmem::X + h + j * 16 : fwd_tmem::SP + j * 32 + h / 2) + q * 8, t[j]);
-                        put_terms3(tl + fwd_tmem::SP + 96 + (h + q * 16) / 2, 32, u);
-                    }
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                named_bar_sync(3, 128);
-                if (warp == 0 && elect_one()) {
-                    tc_wait(&bar.yread, c & 1, gone, a.ctl);   // Y has moved: dM takes its place, o adds up on it
-                    tc_fence_after();
-                    issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
-                                                mma_desc(128, DK, false, true), TmemK(), MNMajor());
-                    mma_commit(&bar.s);
-                    issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
-                                                      smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
-                                                      KMajor1(), true);
-                    mma_commit(&bar.o);
-                    mma_commit(&bar.empty[st]);
-                }
-                __syncwarp();
-            } else {
-                if (c > 0) write_o(c - 1);
-                tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
+                for (int i = 0; i < 8; ++i)
+                    e[i] = fma2(make_float2(-__uint_as_float(r[2 * i]), -__uint_as_float(r[2 * i + 1])),
+                                *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]), make_float2(v[2 * i], v[2 * i + 1]));
+                put_terms3(tl + fwd_tmem::SP + h / 2, 32, e);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(1, 256);
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
+                                           mma_desc(128, 64), TmemK(), KMajor1());
+                mma_commit(&bar.e);
+            }
+            __syncwarp();
+            if (wg == 1) {   // Y moves, so that dM can take its place and o add up on it
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {
                     uint32_t r[16];
@@ -232,10 +180,55 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     }
                     tmem_st16(tl + fwd_tmem::O + h, r);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&bar.yread);
             }
+            tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
+            {
+                const int h = wg * 32;
+                float *eo = a.errors ? a.errors + ((size_t)(row0 + (long long)c * DC + h) * a.Hv + head) * a.Dv + dv : nullptr;
+                uint32_t r[32];   // (U takes the place of 32 columns of e: all are read first)
+                tmem_ld32(tl + fwd_tmem::X + h, r);
+                tmem_wait_ld();
+                if (eo && in)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (h + i < left) eo[i * step] = __uint_as_float(r[i]);
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float2 u[8];
+                    uint32_t t[PT][8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int s = q * 16 + 2 * i;
+                        u[i] = mul2(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])),
+                                    *reinterpret_cast<const float2 *>(&gt.beta[h + s]));
+                        uint32_t p[3];
+                        split2<PT>(u[i], p);
+#pragma unroll
+                        for (int j = 0; j < PT; ++j) t[j][i] = p[j];
+                        u[i] = mul2(u[i], *reinterpret_cast<const float2 *>(&gt.left[h + s]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < PT; ++j)
+                        tmem_st8(tl + (kEarly ? fwd_tmem::X + h + j * 16 : fwd_tmem::SP + j * 32 + h / 2) + q * 8, t[j]);
+                    put_terms3(tl + fwd_tmem::SP + 96 + (h + q * 16) / 2, 32, u);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(1, 256);
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
+                                            mma_desc(128, DK, false, true), TmemK(), MNMajor());
+                mma_commit(&bar.s);
+                issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
+                                                  smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
+                                                  KMajor1(), true);
+                mma_commit(&bar.o);
+                mma_commit(&bar.empty[st]);
+            }
+            __syncwarp();
         }
         if (chunks > 0) {
             tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);

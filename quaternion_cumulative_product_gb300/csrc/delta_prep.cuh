@@ -268,7 +268,7 @@ struct TmemK {     // 8 columns of a left operand in tensor memory
 
 // Barriers and flags of a walk's CTA.
 struct WalkBars {
-    uint64_t full[2], empty[2], rows[2], x, e, s, o, g, yread;
+    uint64_t full[2], empty[2], rows[2], x, e, s, o, g;
     uint32_t tmem;
     int gone;
 };
@@ -288,7 +288,7 @@ struct WalkLayout {
     static_assert(BYTES > 116736, "one CTA per SM: it takes all of the tensor memory");
 };
 
-constexpr int kWalkThreads = 512;   // chain, out, and prep's two warpgroups
+constexpr int kWalkThreads = 512;   // two warpgroups that walk, two of prep
 
 // What a walk's CTA sets up before its roles part; returns the tensor memory's base.
 template <typename L, int STAGES, int PT>
@@ -300,7 +300,6 @@ __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32, int
             mbar_init(&bar.rows[i], 1);
         }
         for (uint64_t *b : {&bar.x, &bar.e, &bar.s, &bar.o, &bar.g}) mbar_init(b, 1);
-        mbar_init(&bar.yread, 128);
         *reinterpret_cast<volatile int *>(&bar.gone) = 0;
         fence_mbar_init();
     }

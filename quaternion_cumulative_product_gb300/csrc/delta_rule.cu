@@ -200,6 +200,7 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     a.ds = reinterpret_cast<float *>(p), a.w = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + nds + nw), a.dkh = reinterpret_cast<float *>(p + nds + nw + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
+    a.ahead = (unsigned)sms;
     rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1>(a, stream) : launch_walks<true, float, 3>(a, stream);
     if (rc != QS_OK || !some) return rc;
     if (dtype != QS_BF16) rc = launch_chunks<float, 3, 3>(a, stream);
