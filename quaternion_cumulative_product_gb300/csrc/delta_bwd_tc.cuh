@@ -144,26 +144,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     read_state(a.carries_in, m);
     if (L::BOTH) read_state(a.ds, dm);
     __syncthreads();   // the gates
-    // What the CTA that follows on this SM reads, on its way into L2 while this one computes
-    // (all CTAs load at about the same time, which is the only time that memory is busy).
-    if (blockIdx.x + a.ahead < gridDim.x) {
-        const int nh = (blockIdx.x + a.ahead) % a.Hv;
-        Seq ns;
-        long long nc;
-        if (chunk_of(a, (blockIdx.x + a.ahead) / a.Hv, &ns, &nc)) {
-            if (threadIdx.x == 0) {
-                const size_t nat = ((size_t)(ns.slot0 + nc) * a.Hv + nh) * a.Dk * a.Dv;
-                l2_prefetch(a.carries_in + nat, a.Dk * a.Dv * 4);
-                l2_prefetch(a.ds + nat, a.Dk * a.Dv * 4);
-            }
-            const int i = threadIdx.x / 8, x = threadIdx.x % 4 * 32;   // a line of e or w per thread
-            if (nc * DC + i < ns.len && x < a.Dv) {
-                const float *p = threadIdx.x % 8 < 4 ? a.errors_in : a.w;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + ((size_t)(ns.b * a.S + ns.s0 + nc * DC + i) * a.Hv + nh) * a.Dv + x));
-            }
-        }
-    }
-    __syncwarp();
 
     // D (+)= [dO; dV] x B, K steps k0 .. of the operand in tensor memory, B K-major.
     uint32_t tm = 0;

@@ -28,7 +28,8 @@ constexpr uint32_t R = 384;
 constexpr uint32_t G = 448;
 }  // namespace chain_tmem
 
-template <typename T, int NT, int DK, int STAGES>
+// SUM: sums a segment up (delta_prep.cuh) and writes neither dM' nor w.
+template <typename T, int NT, int DK, int STAGES, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
@@ -40,9 +41,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     volatile int *gone = &bar.gone;
     const ChunkGates *gates = reinterpret_cast<const ChunkGates *>(sm + L::GATES_AT);
 
-    const int head = blockIdx.x % a.Hv;
-    const long long n = blockIdx.x / a.Hv;
-    const Seq seq = seq_of(a, n);
+    const Walk walk = walk_of<SUM, true>(a);
+    const int head = walk.head;
+    const long long n = walk.n;
+    Seq seq = seq_of(a, n);
+    if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L, STAGES, 3>(bar, sm32, 1 + 256);   // a stage is free after the products, and the walk done with beta
@@ -54,14 +57,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         constexpr int HALF = DK / 2;             // columns of dM per thread
         const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
         const int dv = tid, col0 = wg * HALF;
-        const bool in = dv < a.Dv;
+        const WalkRow row(a, walk, tid);
+        const bool in = row.in;
         const size_t state = ((size_t)n * a.Hv + head) * a.Dk * a.Dv + dv, step = (size_t)a.Hv * a.Dv;
         const long long row0 = seq.b * a.S + seq.s0;
         float2 m[HALF / 2];
         float whole = 0.f;
+        const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.d_final ? a.d_final + state : nullptr;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
-            const float v = a.d_final && in && col0 + i < a.Dk ? __ldg(a.d_final + state + (size_t)(col0 + i) * a.Dv) : 0.f;
+            float v;
+            if (SUM) v = row.map && col0 + i == row.row ? 1.f : 0.f;
+            else v = from && in && col0 + i < a.Dk ? __ldg(from + (size_t)(col0 + i) * a.Dv) : 0.f;
             if (i % 2) m[i / 2].y = v;
             else m[i / 2].x = v;
         }
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (it > 0) add_update(p);
-                if (in) {
+                if (!SUM && in) {
                     float *out = ds + (size_t)(col0 + p * 16) * a.Dv;
 #pragma unroll
                     for (int i = 0; i < 16; ++i, out += a.Dv)
@@ -122,7 +129,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 for (int i = 0; i < 8; ++i)
                     e[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
                                 *reinterpret_cast<const float2 *>(&gt.left[h + 2 * i]),
-                                make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
+                                SUM && row.map ? make_float2(0.f, 0.f) : make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
                 put_terms3(tl + chain_tmem::SP + h / 2, 32, e);
             }
             tmem_wait_st();
@@ -158,7 +165,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     third_column<NT>(sm + st * L::STAGE + L::V_AT, dv, h, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        z[i] = mul2(mul2(make_float2(v[2 * i], v[2 * i + 1]), *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i])),
+                        z[i] = mul2(mul2(SUM && row.map ? make_float2(0.f, 0.f) : make_float2(v[2 * i], v[2 * i + 1]), *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i])),
                                     make_float2(a.scale, a.scale));
                     put_terms3(tl + chain_tmem::SP + h / 2, 32, z);
                 }
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.empty[st]);
             }
             __syncwarp();
-            {   // w and dv, half of the steps each, while the products run
+            if (!SUM) {   // w and dv, half of the steps each, while the products run
                 const int h0 = wg * 32;
                 const size_t at = ((size_t)(row0 + (long long)c * DC + h0) * a.Hv + head) * a.Dv + dv;
                 float *wo = a.w + at;
@@ -197,15 +204,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     __syncwarp();
                 }
                 tc_fence_before();
-                mbar_arrive(&bar.empty[st]);
             }
+            mbar_arrive(&bar.empty[st]);
         }
         if (chunks > 0) {
             tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) add_update(p);
         }
-        if (a.d_init && in)
+        if (SUM) {
+            if (in)
+#pragma unroll
+                for (int i = 0; i < HALF; ++i)
+                    if (col0 + i < a.Dk) *row.sum_out(a, walk, col0 + i) = i % 2 ? m[i / 2].y : m[i / 2].x;
+        } else if (a.d_init && in && walk.seg == 0)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.d_init[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;

@@ -53,10 +53,16 @@ struct DeltaArgs {
     qsh::Strides sq, sk, sv;
     const int *offsets;
     long long B, S, N, NC, slots;   // NC: chunks per sequence without offsets
+    // A sequence cut into segments (few sequences, long ones): segments, chunks in each;
+    // the state that enters each segment (backward: the cotangent of the one that leaves
+    // it) [N, Hv, segs, Dk, Dv]; a segment's own part and its map, [.., Dk, Dv] and [.., Dk, Dk].
+    int segs;
+    long long seg_chunks;
+    const float *seg_m;
+    float *seg_own, *seg_map;
     int Hk, Hv, Dk, Dv;
     bool gate16;
     float scale;
-    unsigned ahead;   // CTAs in flight of the backward's chunk kernel
     Control ctl;
 };
 
@@ -71,6 +77,13 @@ __device__ __forceinline__ Seq seq_of(const DeltaArgs &a, long long n) {
     const long long s0 = lo < 0 ? 0 : lo > a.S ? a.S : lo;
     const long long s1 = hi < s0 ? s0 : hi > a.S ? a.S : hi;
     return {0, s0, s1 - s0, s0 / DC + n};
+}
+
+// Segment `seg` of a sequence.
+__device__ __forceinline__ Seq segment_of(const DeltaArgs &a, const Seq &s, int seg) {
+    const long long c0 = seg * a.seg_chunks, off = c0 * DC, most = a.seg_chunks * DC;
+    const long long left = s.len > off ? s.len - off : 0;
+    return {s.b, s.s0 + off, left < most ? left : most, s.slot0 + c0};
 }
 
 // The sequence and chunk in a carry slot; false when the slot holds no chunk.

@@ -41,7 +41,8 @@ struct UAt {   // U's columns: K step k of a term
     __device__ __forceinline__ uint32_t operator()(int k) const { return early ? (uint32_t)(k / 2 * 32 + k % 2 * 8) : (uint32_t)(k * 8); }
 };
 
-template <typename T, int NT, int DK, int STAGES>
+// SUM: sums a segment up (delta_prep.cuh) and writes no o.
+template <typename T, int NT, int DK, int STAGES, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_fwd_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap vmap) {
@@ -54,9 +55,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     volatile int *gone = &bar.gone;
     const ChunkGates *gates = reinterpret_cast<const ChunkGates *>(sm + L::GATES_AT);
 
-    const int head = blockIdx.x % a.Hv;
-    const long long n = blockIdx.x / a.Hv;
-    const Seq seq = seq_of(a, n);
+    const Walk walk = walk_of<SUM, false>(a);
+    const int head = walk.head;
+    const long long n = walk.n;
+    Seq seq = seq_of(a, n);
+    if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L, STAGES, PT>(bar, sm32, 1);
@@ -68,14 +71,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         constexpr bool kEarly = NT == 1;         // U has a place of its own: the next chunk need not wait for o
         const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
         const int dv = tid, col0 = wg * HALF;
-        const bool in = dv < a.Dv;
+        const WalkRow row(a, walk, tid);
+        const bool in = row.in;
         const size_t state = ((size_t)n * a.Hv + head) * a.Dk * a.Dv + dv, step = (size_t)a.Hv * a.Dv;
         const long long row0 = seq.b * a.S + seq.s0;
         float2 m[HALF / 2];
         float whole = 0.f;
+        const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.init ? a.init + state : nullptr;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
-            const float v = a.init && in && col0 + i < a.Dk ? __ldg(a.init + state + (size_t)(col0 + i) * a.Dv) : 0.f;
+            float v;
+            if (SUM) v = row.map && col0 + i == row.row ? 1.f : 0.f;
+            else v = from && in && col0 + i < a.Dk ? __ldg(from + (size_t)(col0 + i) * a.Dv) : 0.f;
             if (i % 2) m[i / 2].y = v;
             else m[i / 2].x = v;
         }
@@ -114,8 +121,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const ChunkGates &gt = gates[st];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             if (c > 0) tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
-            if (!kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
-            float *carry = a.carries ? a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + dv : nullptr;
+            if (!SUM && !kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
+            float *carry = !SUM && a.carries ? a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + dv : nullptr;
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (c > 0) add_dm(p);
@@ -136,11 +143,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
-                                            mma_desc(128, 128), TmemK(), KMajor());
+                                            mma_desc(128, SUM ? 64 : 128), TmemK(), KMajor());
                 mma_commit(&bar.x);
             }
             __syncwarp();
-            if (wg == 1 && c > 0) write_o(c - 1);
+            if (!SUM && wg == 1 && c > 0) write_o(c - 1);
             tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {   // v - exp(G) X
@@ -153,7 +160,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     e[i] = fma2(make_float2(-__uint_as_float(r[2 * i]), -__uint_as_float(r[2 * i + 1])),
-                                *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]), make_float2(v[2 * i], v[2 * i + 1]));
+                                *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]),
+                                SUM && row.map ? make_float2(0.f, 0.f) : make_float2(v[2 * i], v[2 * i + 1]));
                 put_terms3(tl + fwd_tmem::SP + h / 2, 32, e);
             }
             tmem_wait_st();
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.e);
             }
             __syncwarp();
-            if (wg == 1) {   // Y moves, so that dM can take its place and o add up on it
+            if (!SUM && wg == 1) {   // Y moves, so that dM can take its place and o add up on it
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {
                     uint32_t r[16];
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
             {
                 const int h = wg * 32;
-                float *eo = a.errors ? a.errors + ((size_t)(row0 + (long long)c * DC + h) * a.Hv + head) * a.Dv + dv : nullptr;
+                float *eo = !SUM && a.errors ? a.errors + ((size_t)(row0 + (long long)c * DC + h) * a.Hv + head) * a.Dv + dv : nullptr;
                 uint32_t r[32];   // (U takes the place of 32 columns of e: all are read first)
                 tmem_ld32(tl + fwd_tmem::X + h, r);
                 tmem_wait_ld();
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                         u[i] = mul2(u[i], *reinterpret_cast<const float2 *>(&gt.left[h + s]));
                     }
 #pragma unroll
-                    for (int j = 0; j < PT; ++j)
+                    for (int j = 0; j < (SUM ? 0 : PT); ++j)
                         tmem_st8(tl + (kEarly ? fwd_tmem::X + h + j * 16 : fwd_tmem::SP + j * 32 + h / 2) + q * 8, t[j]);
                     put_terms3(tl + fwd_tmem::SP + 96 + (h + q * 16) / 2, 32, u);
                 }
@@ -222,10 +230,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.s);
-                issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
-                                                  smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
-                                                  KMajor1(), true);
-                mma_commit(&bar.o);
+                if (!SUM) {
+                    issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
+                                                      smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
+                                                      KMajor1(), true);
+                    mma_commit(&bar.o);
+                }
                 mma_commit(&bar.empty[st]);
             }
             __syncwarp();
@@ -234,9 +244,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) add_dm(p);
-            if (wg == 1) write_o(chunks - 1);
+            if (!SUM && wg == 1) write_o(chunks - 1);
         }
-        if (a.fin && in)
+        if (SUM) {
+            if (in)
+#pragma unroll
+                for (int i = 0; i < HALF; ++i)
+                    if (col0 + i < a.Dk) *row.sum_out(a, walk, col0 + i) = i % 2 ? m[i / 2].y : m[i / 2].x;
+        } else if (a.fin && in && walk.seg == a.segs - 1)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.fin[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;

@@ -290,6 +290,51 @@ struct WalkLayout {
 
 constexpr int kWalkThreads = 512;   // two warpgroups that walk, two of prep
 
+// Which walk a CTA takes: sequence, head, segment.  SUM: the walk over a segment that
+// sums it up as an affine map of the state (for all segments but the last; backward:
+// but the first).  Its rows hold the segment's own part (from the zero state on) and, from
+// row `map_from`, the map's columns (from the identity on, without inputs).
+struct Walk {
+    long long n;
+    int head, seg, map_from;
+    size_t at;   // (n * Hv + head) * segs + seg
+};
+template <bool SUM, bool BWD>
+__device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
+    Walk w;
+    unsigned i = blockIdx.x;
+    w.map_from = 128;
+    int segs = a.segs;
+    if (SUM) {
+        segs -= 1;
+        if (a.Dk <= 64 && a.Dv <= 64) {
+            w.map_from = 64;
+        } else {   // own part and map in CTAs of their own
+            if (i % 2) w.map_from = 0;
+            i /= 2;
+        }
+    }
+    w.head = i % a.Hv, i /= a.Hv;
+    w.seg = i % segs + (SUM && BWD ? 1 : 0);
+    w.n = i / segs;
+    w.at = ((size_t)w.n * a.Hv + w.head) * a.segs + w.seg;
+    return w;
+}
+
+// The element (column x of dk) that this thread's row starts with, and where the row ends up.
+struct WalkRow {
+    bool map, in;    // a row of the map; a row at all
+    int row;         // value row, or column of the map
+    __device__ __forceinline__ WalkRow(const DeltaArgs &a, const Walk &w, int tid) {
+        map = tid >= w.map_from;
+        row = map ? tid - w.map_from : tid;
+        in = map ? row < a.Dk : row < a.Dv;
+    }
+    __device__ __forceinline__ float *sum_out(const DeltaArgs &a, const Walk &w, int x) const {
+        return map ? a.seg_map + (w.at * a.Dk + x) * a.Dk + row : a.seg_own + (w.at * a.Dk + x) * a.Dv + row;
+    }
+};
+
 // What a walk's CTA sets up before its roles part; returns the tensor memory's base.
 template <typename L, int STAGES, int PT>
 __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32, int empty_count) {

@@ -29,15 +29,82 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, lo
     store4(static_cast<T *>(a.dk) + out, k);
 }
 
+// Joins the segments of a sequence: from the state that enters the first (backward: the
+// cotangent that leaves the last), the state that enters each, m' = map m + own.  A CTA
+// takes 16 value columns of one (sequence, head); two threads a row of dk.
+template <bool BWD>
+__global__ void __launch_bounds__(256) delta_join_kernel(const DeltaArgs a, const float *first, float *out) {
+    __shared__ float m[QS_DELTA_MAX_D][20];
+    const int r = threadIdx.x / 2, c = threadIdx.x % 2 * 8, x0 = blockIdx.y * 16 + c;
+    const bool in = r < a.Dk && x0 < a.Dv;
+    const size_t nh = blockIdx.x, elem = (size_t)r * a.Dv + x0;
+    float4 v[2] = {q_zero(), q_zero()};
+    if (first && in) {
+        const float4 *p = reinterpret_cast<const float4 *>(first + nh * a.Dk * a.Dv + elem);
+        v[0] = __ldg(p), v[1] = __ldg(p + 1);
+    }
+    for (int i = 0; i < a.segs; ++i) {
+        const size_t at = nh * a.segs + (BWD ? a.segs - 1 - i : i);
+        if (in) {
+            float *p = out + at * a.Dk * a.Dv + elem;
+            store4(p, v[0]), store4(p + 4, v[1]);
+        }
+        if (i + 1 == a.segs) break;
+        __syncthreads();
+        store4(&m[r][c], v[0]), store4(&m[r][c + 4], v[1]);
+        __syncthreads();
+        v[0] = v[1] = q_zero();
+        if (in) {
+            const float4 *p = reinterpret_cast<const float4 *>(a.seg_own + at * a.Dk * a.Dv + elem);
+            v[0] = __ldg(p), v[1] = __ldg(p + 1);
+            const float4 *f = reinterpret_cast<const float4 *>(a.seg_map + (at * a.Dk + r) * a.Dk);
+            for (int j = 0; j < a.Dk; j += 4) {
+                const float4 w4 = __ldg(f + j / 4);
+                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&m[j + k][c]), y = *reinterpret_cast<const float4 *>(&m[j + k][c + 4]);
+                    v[0] = make_float4(fmaf(w[k], x.x, v[0].x), fmaf(w[k], x.y, v[0].y), fmaf(w[k], x.z, v[0].z), fmaf(w[k], x.w, v[0].w));
+                    v[1] = make_float4(fmaf(w[k], y.x, v[1].x), fmaf(w[k], y.y, v[1].y), fmaf(w[k], y.z, v[1].z), fmaf(w[k], y.w, v[1].w));
+                }
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA; }
 
-// A walk over the chunks, one CTA per (sequence, value head).  fp32 inputs take three
-// times the space of K and Q: one stage.
+// Cuts each sequence into segments where there are too few (sequence, head) pairs to fill
+// the GPU: a first walk sums every segment but one up as an affine map of its state, the
+// join runs over the segments, and the real walk starts each from its own state.  The
+// rule is the cost in chunk steps: waves of CTAs times chunks per segment, a summing
+// walk counted as 0.7 of a real one, a join step as 0.4 of a chunk, the two launches as 3.
+// (1 x 131072 x 16 x 64: 9 segments; 8 x 4096 x 16 x 128 has enough pairs: one.)
+void cut(DeltaArgs &a, int sms) {
+    a.segs = 1, a.seg_chunks = a.NC;
+    if (a.offsets || a.NC < 4) return;
+    const long long pairs = a.N * a.Hv, kinds = a.Dk <= 64 && a.Dv <= 64 ? 1 : 2;
+    double best = (double)a.NC * ((pairs + sms - 1) / sms) * 0.9;   // cut only for a clear gain
+    for (long long want = 2; want <= 64 && want <= a.NC && pairs * want <= 2 * sms; ++want) {
+        const long long sc = (a.NC + want - 1) / want, n = (a.NC + sc - 1) / sc;
+        if (n < 2) continue;
+        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.7 * (double)((pairs * kinds * (n - 1) + sms - 1) / sms);
+        const double cost = waves * sc + 0.4 * n + 3;
+        if (cost < best) best = cost, a.segs = (int)n, a.seg_chunks = sc;
+    }
+}
+
+size_t seg_floats(const DeltaArgs &a) {   // of seg_m, seg_own and seg_map, one after the other
+    return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * ((size_t)a.Dk * a.Dv * 2 + (size_t)a.Dk * a.Dk) : 0;
+}
+
+// A walk over the chunks, one CTA per (sequence, value head) or segment of one.  fp32
+// inputs take three times the space of K and Q: one stage.
 template <bool BWD, typename T, int NT>
-int launch_walks(const DeltaArgs &a, cudaStream_t stream) {
+int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
     constexpr int STAGES = NT == 1 ? 2 : 1, PT = BWD || NT == 3 ? 3 : 2;
     CUtensorMap maps[3];
     if (NT == 1 && a.B * a.S > 0) {
@@ -48,17 +115,35 @@ int launch_walks(const DeltaArgs &a, cudaStream_t stream) {
                                   : qsh::head_map(&maps[2], a.v, a.sv, a.B, a.S, a.Hv, a.Dv);
         if (rc != QS_OK) return rc;
     }
-    auto go = [&](auto kernel, size_t smem) {
+    auto go = [&](auto kernel, size_t smem, long long grid) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
             cudaGetLastError();
             return (int)QS_ERR_CUDA;
         }
-        kernel<<<(unsigned)(a.N * a.Hv), kWalkThreads, smem, stream>>>(a, maps[0], maps[1], maps[2]);
+        kernel<<<(unsigned)grid, kWalkThreads, smem, stream>>>(a, maps[0], maps[1], maps[2]);
         return launched();
     };
-    constexpr size_t small = WalkLayout<NT, 64, STAGES, PT>::BYTES, large = WalkLayout<NT, 128, STAGES, PT>::BYTES;
-    if constexpr (BWD) return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, STAGES>, small) : go(delta_chain_tc_kernel<T, NT, 128, STAGES>, large);
-    else return a.Dk <= 64 ? go(delta_fwd_tc_kernel<T, NT, 64, STAGES>, small) : go(delta_fwd_tc_kernel<T, NT, 128, STAGES>, large);
+    auto walk = [&](auto sum, long long grid) {
+        constexpr bool SUM = decltype(sum)::value;
+        constexpr size_t small = WalkLayout<NT, 64, STAGES, PT>::BYTES, large = WalkLayout<NT, 128, STAGES, PT>::BYTES;
+        if constexpr (BWD)
+            return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, STAGES, SUM>, small, grid)
+                              : go(delta_chain_tc_kernel<T, NT, 128, STAGES, SUM>, large, grid);
+        else
+            return a.Dk <= 64 ? go(delta_fwd_tc_kernel<T, NT, 64, STAGES, SUM>, small, grid)
+                              : go(delta_fwd_tc_kernel<T, NT, 128, STAGES, SUM>, large, grid);
+    };
+    const long long pairs = a.N * a.Hv;
+    if (a.segs > 1) {
+        const size_t states = (size_t)pairs * a.segs * a.Dk * a.Dv;
+        a.seg_m = seg, a.seg_own = seg + states, a.seg_map = seg + 2 * states;
+        int rc = walk(std::true_type(), pairs * (a.segs - 1) * (a.Dk <= 64 && a.Dv <= 64 ? 1 : 2));
+        if (rc != QS_OK) return rc;
+        delta_join_kernel<BWD><<<dim3((unsigned)pairs, (unsigned)(a.Dv + 15) / 16), 256, 0, stream>>>(a, BWD ? a.d_final : a.init, seg);
+        rc = launched();
+        if (rc != QS_OK) return rc;
+    }
+    return walk(std::false_type(), pairs * a.segs);
 }
 
 template <typename T, int NT, int CT>
@@ -151,10 +236,12 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     a.carries = carries, a.errors = errors;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     unsigned char *ws = nullptr;
-    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader), &ws);
+    cut(a, sms);
+    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + seg_floats(a) * 4, &ws);
     if (wc != QS_OK) return wc;
+    float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
-    return dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1>(a, stream) : launch_walks<false, float, 3>(a, stream);
+    return dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1>(a, seg, stream) : launch_walks<false, float, 3>(a, seg, stream);
 }
 
 extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
@@ -192,7 +279,8 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     const size_t nds = align256(kept * 4), nw = align256(rows * 4), nh = shared ? align256((size_t)B * S * Hv * Dk * 4) : 0;
     unsigned char *ws = nullptr;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nds + nw + 2 * nh, &ws);
+    cut(a, sms);
+    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nds + nw + 2 * nh + seg_floats(a) * 4, &ws);
     if (rc != QS_OK) return rc;
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.carries_in = carries, a.errors_in = errors, a.d_o = d_o;
     a.d_final = d_final, a.dq = d_q, a.dk = d_k, a.dv = d_v, a.dg = d_g, a.dbeta = d_beta, a.d_init = d_init;
@@ -200,8 +288,8 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     a.ds = reinterpret_cast<float *>(p), a.w = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + nds + nw), a.dkh = reinterpret_cast<float *>(p + nds + nw + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
-    a.ahead = (unsigned)sms;
-    rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1>(a, stream) : launch_walks<true, float, 3>(a, stream);
+    float *seg = reinterpret_cast<float *>(p + nds + nw + 2 * nh);
+    rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1>(a, seg, stream) : launch_walks<true, float, 3>(a, seg, stream);
     if (rc != QS_OK || !some) return rc;
     if (dtype != QS_BF16) rc = launch_chunks<float, 3, 3>(a, stream);
     else rc = gate_dtype == QS_BF16 ? launch_chunks<__nv_bfloat16, 1, 2>(a, stream) : launch_chunks<__nv_bfloat16, 1, 3>(a, stream);

@@ -172,11 +172,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t *t) {
     split2<TERMS>(make_float2(a, b), t);
 }
 
-// Brings `bytes` (a multiple of 16, from a 16-byte boundary) into L2.
-__device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // Byte offset of 16-byte unit u of row r in a tile of 128-byte rows.
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
 

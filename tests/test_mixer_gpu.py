@@ -206,6 +206,13 @@ def test_delta(torch, dims, dt, gates):
     check_delta(delta_inputs(torch, *dims, dt, gates), dt, gates)
 
 
+@pytest.mark.parametrize("dims", [(1, 1500, 1, 2, 64, 64), (1, 2000, 1, 1, 128, 128), (2, 1290, 1, 1, 128, 40), (1, 1217, 1, 3, 24, 96)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_delta_long_sequences(torch, dims, dt):
+    """Few long sequences: cut into segments that are joined (forward and backward)."""
+    check_delta(delta_inputs(torch, *dims, dt, "f32", seed=11), dt, "f32")
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_delta_without_states(torch, dt):
     check_delta(delta_inputs(torch, 2, 140, 1, 2, 64, 64, dt, "f32"), dt, "f32", init=False, final=False, scale=0.7)
