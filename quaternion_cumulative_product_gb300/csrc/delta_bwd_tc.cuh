@@ -6,13 +6,15 @@
 // product (each takes a quarter of the columns).  Rows of queries and of keys are
 // stacked, so that one product serves both:
 //
-//     R  = [dO; dV] M^T            the states' part of dq and of row
-//     S  = [dO; dV] U^T            X, Y (64 + 64 rows) once the decays are on
-//     C  = U dM'^T                 the states' part of col (rows 64 .. 127)
-//     R += [X; Y] K                after R's rows have got their decays
-//     C += [X; Y]^T [Q; K]         likewise
+//     R = [dO; dV] M^T            the states' part of dq and of row
+//     S = [dO; dV] U^T            X, Y (64 + 64 rows) once the decays are on
+//     C = U dM'^T                 the states' part of col (rows 64 .. 127)
+//     I = [X; Y] K                the chunk's part of dq and of row
+//     J = [X; Y]^T [Q; K]         the chunk's part of col
 //
-// (names as in delta_common.cuh).  The stacked left operand is in tensor memory, the
+// (names as in delta_common.cuh).  I and J have accumulators of their own, and are added
+// to R and C, with the decays of their rows, in registers: adding up on R and C in the
+// tensor cores would cut off their last bit with each of 24 to 48 passes.  The stacked left operand is in tensor memory, the
 // others in shared memory; [X;Y] is a K-major operand in one product and an MN-major
 // one in the other.  C's left operands have 64 rows; they stand in rows 64 .. 127 of
 // 128 (what lies before them in shared memory fills the others, which nobody
@@ -59,6 +61,7 @@ namespace bwd_tmem {
 constexpr uint32_t A = 0;      // terms (3 x 64) of [dO; dV]
 constexpr uint32_t S = 192;    // [dO; dV] U^T (64)
 constexpr uint32_t R = 256, C = 384;
+constexpr uint32_t I = 0, J = 128;   // over A and S
 }  // namespace bwd_tmem
 
 struct ChunkBars {
@@ -325,31 +328,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                            make_float4(x[8 * i + 4], x[8 * i + 5], x[8 * i + 6], x[8 * i + 7]));
     }
     fence_proxy_async_smem();
-    // R's rows get their decay.
-    {
-        const float f = keys ? -gt.grown[t] : a.scale * gt.grown[t];
-        const float2 f2 = make_float2(f, f);
-#pragma unroll 1
-        for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tl + bwd_tmem::R + x0, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2);
-                r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
-            }
-            tmem_st16(tl + bwd_tmem::R + x0, r);
-        }
-    }
-    tmem_wait_st();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && elect_one()) {   // R += [X;Y] K: rows of K are the K dimension
+    if (warp == 0 && elect_one()) {
         tc_fence_after();
-        issue_ss<CT, NT, CT - 1, 4>(tm + bwd_tmem::R, smem_desc(sm32 + L::M_AT, 16, 1024), 2 * TILE,
+        // I: rows of K are the K dimension.  J: [X;Y]'s columns in rows 64 .. 127.
+        issue_ss<CT, NT, CT - 1, 4>(tm + bwd_tmem::I, smem_desc(sm32 + L::M_AT, 16, 1024), 2 * TILE,
                                     smem_desc(sm32 + L::QK_AT + TILE, 2 * TILE, 1024), L::QK_TERM, mma_desc(128, DK, false, true), KMajor1(),
-                                    MNMajor(), true);
+                                    MNMajor());
+        issue_ss<CT, NT, CT - 1, 8>(tm + bwd_tmem::J, smem_desc(sm32 + L::M_AT - TILE, TILE, 1024), 2 * TILE,
+                                    smem_desc(sm32 + L::QK_AT, 2 * TILE, 1024), L::QK_TERM, mma_desc(128, DK, true, true), MNMajor(), MNMajor());
         mma_commit(&bar.r);
     }
     __syncwarp();
@@ -364,59 +352,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w, f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
         }
     };
-    // C's rows (the keys') get theirs; the sum of exp(G_C - G_t) <k_t, dM' u_t>.
-    float part = 0.f;
     tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
-    if (keys) {
-        const float2 f2 = make_float2(gt.left[t], gt.left[t]);
-#pragma unroll 1
-        for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tl + bwd_tmem::C + x0, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float f[8];
-                qk_row(x0 + 8 * h, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = 8 * h + 2 * i;
-                    const float2 y = mul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2);
-                    part = fmaf(y.x, f[2 * i], fmaf(y.y, f[2 * i + 1], part));
-                    r[k] = __float_as_uint(y.x), r[k + 1] = __float_as_uint(y.y);
-                }
-            }
-            __syncwarp();
-            tmem_st16(tl + bwd_tmem::C + x0, r);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) rows[528 + warp] = part;
-    tmem_wait_st();
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0 && elect_one()) {   // C += [X;Y]^T [Q;K], [X;Y]'s columns in rows 64 .. 127
-        tc_fence_after();
-        issue_ss<CT, NT, CT - 1, 8>(tm + bwd_tmem::C, smem_desc(sm32 + L::M_AT - TILE, TILE, 1024), 2 * TILE,
-                                    smem_desc(sm32 + L::QK_AT, 2 * TILE, 1024), L::QK_TERM, mma_desc(128, DK, true, true), MNMajor(), MNMajor(),
-                                    true);
-        mma_commit(&bar.m);   // (its phases: the first half of dv, where there were two, then this)
-    }
-    __syncwarp();
     tc_wait_warp(&bar.r, 0, gone, a.ctl);
-    tc_wait_warp(&bar.m, !L::BOTH && rounds > 1 ? 1 : 0, gone, a.ctl);
     // dq and dk: rows to tiles in shared memory (every operand is done with), then whole lines out.
     constexpr uint32_t OUT_ROW = DK * 4 + 16;   // padded fp32 rows
     static_assert(L::U_AT + 128 * OUT_ROW <= L::GATES_AT, "the operands' place holds the rows of dq and dk");
     {
-        float sum = 0.f;   // <q, dq> or <k, row - col>
+        float sum = 0.f, part = 0.f;   // <q, dq> or <k, row - col>; exp(G_C - G_t) <k_t, dM' u_t>
+        const float fr = keys ? -gt.grown[t] : a.scale * gt.grown[t], fc = keys ? gt.left[t] : 0.f;
 #pragma unroll 1
         for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
-            uint32_t r[16], cl[16];
+            uint32_t r[16], i2[16], c1[16], j2[16];
             __syncwarp();
             tmem_ld16(tl + bwd_tmem::R + x0, r);
-            tmem_ld16(tl + bwd_tmem::C + x0, cl);
+            tmem_ld16(tl + bwd_tmem::I + x0, i2);
+            tmem_ld16(tl + bwd_tmem::C + x0, c1);
+            tmem_ld16(tl + bwd_tmem::J + x0, j2);
             tmem_wait_ld();
             float *out = reinterpret_cast<float *>(sm + L::U_AT + tid * OUT_ROW) + x0;
 #pragma unroll
@@ -425,7 +376,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                 qk_row(x0 + 8 * h, f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float w = __uint_as_float(r[8 * h + k]), col = keys ? __uint_as_float(cl[8 * h + k]) : 0.f;
+                    const float w = fmaf(fr, __uint_as_float(r[8 * h + k]), __uint_as_float(i2[8 * h + k]));
+                    float cs = 0.f, col = 0.f;   // (a query's rows of C and J hold nothing)
+                    if (keys) cs = fc * __uint_as_float(c1[8 * h + k]), col = cs + __uint_as_float(j2[8 * h + k]);
+                    part = fmaf(f[k], cs, part);
                     sum = fmaf(f[k], w - col, sum);
                     v[k] = w + col;
                 }
@@ -433,6 +387,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                 store4(out + 8 * h + 4, make_float4(v[4], v[5], v[6], v[7]));
             }
         }
+#pragma unroll
+        for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (lane == 0) rows[528 + warp] = part;
         rows[wg * 128 + tid] = sum;
     }
     __syncthreads();
