@@ -446,6 +446,14 @@ def quat_cumprod_status(stream=None, device=None):
         return load_library().quat_cumprod_status(_stream_handle(stream, device))
 
 
-from .mixer import (  # noqa: E402  (uses the helpers above)
-    QS_DELTA_MAX_D, QS_DELTA_STEPS, QS_ROTATE_MAX_D, quat_delta_bwd, quat_delta_fwd, quat_delta_fwd_carries,
-    quat_delta_step, quat_norm_rotate_bwd, quat_norm_rotate_fwd)
+# The operators around the scan, loaded (with torch) at their first use.
+_MIXER = ("QS_DELTA_MAX_D", "QS_DELTA_STEPS", "QS_ROTATE_MAX_D", "quat_delta_bwd", "quat_delta_fwd",
+          "quat_delta_fwd_carries", "quat_delta_step", "quat_norm_rotate_bwd", "quat_norm_rotate_fwd")
+
+
+def __getattr__(name):
+    if name not in _MIXER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import mixer
+    globals().update({n: getattr(mixer, n) for n in _MIXER})
+    return globals()[name]

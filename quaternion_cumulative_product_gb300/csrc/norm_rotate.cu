@@ -46,8 +46,9 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // One group of LANES lanes per (step, rotation head); V quaternions per lane.
-template <typename T, typename C, int V, int LANES>
-__global__ void __launch_bounds__(kThreads) rotate_fwd_kernel(const RotateArgs a) {
+// SINGLE: one query and one key head per rotation (no loop, fewer registers).
+template <typename T, typename C, int V, int LANES, bool SINGLE>
+__global__ void __launch_bounds__(kThreads, SINGLE ? 6 : 4) rotate_fwd_kernel(const RotateArgs a) {
     const unsigned groups = kThreads / LANES;
     const unsigned item = blockIdx.x * groups + threadIdx.x / LANES;
     const unsigned lane = threadIdx.x % LANES, x0 = lane * V * 4;
@@ -97,8 +98,13 @@ __global__ void __launch_bounds__(kThreads) rotate_fwd_kernel(const RotateArgs a
     float4 xq[V], xk[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) xq[i] = xk[i] = qs::q_zero();
-    if (in && a.nq) qs::load_quads<V>(qp, xq);
-    if (in && a.nk) qs::load_quads<V>(kp, xk);
+    if (in && (SINGLE || a.nq)) qs::load_quads<V>(qp, xq);
+    if (in && (SINGLE || a.nk)) qs::load_quads<V>(kp, xk);
+    if constexpr (SINGLE) {
+        row(xq, a.wq, qo);
+        row(xk, a.wk, ko);
+        return;
+    }
     for (unsigned j = 0; j < a.nq; ++j) {
         float4 nx[V];
 #pragma unroll
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) rotate_fwd_kernel(const RotateArgs a
 // groups up in a fixed order and writes one partial row, and
 // rotate_weights_kernel adds the CTAs' partial rows up.
 template <typename T, typename C, int V, int LANES, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads) rotate_bwd_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 2) rotate_bwd_kernel(const RotateArgs a) {
     const unsigned groups = kThreads / LANES;
     const unsigned lane = threadIdx.x % LANES, x0 = lane * V * 4;
     const unsigned rounds = (a.items + gridDim.x * groups - 1) / (gridDim.x * groups);
@@ -242,18 +248,21 @@ __global__ void __launch_bounds__(kThreads) rotate_bwd_kernel(const RotateArgs a
     }
 }
 
-// d_w[x] = sum of the CTAs' partial rows, in CTA order within each of 8 strands.
-__global__ void __launch_bounds__(256) rotate_weights_kernel(const float *part, float *dwq, float *dwk, unsigned ctas, unsigned D) {
-    __shared__ float strand[8][33];
+// d_w[x] = sum of the CTAs' partial rows: 32 strands of CTAs, each in order, then
+// the strands in order.
+__global__ void __launch_bounds__(1024) rotate_weights_kernel(const float *part, float *dwq, float *dwk, unsigned ctas, unsigned D) {
+    __shared__ float strand[32][33];
     const unsigned x = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
     float sum = 0.f;
     if (x < 2 * D)
-        for (unsigned i = k; i < ctas; i += 8) sum += part[(size_t)i * 2 * D + x];
+#pragma unroll 4
+        for (unsigned i = k; i < ctas; i += 32) sum += part[(size_t)i * 2 * D + x];
     strand[k][threadIdx.x % 32] = sum;
     __syncthreads();
     if (k == 0 && x < 2 * D) {
         sum = 0.f;
-        for (int i = 0; i < 8; ++i) sum += strand[i][threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum += strand[i][threadIdx.x];
         float *out = x < D ? dwq : dwk;
         if (out) out[x < D ? x : x - D] = sum;
     }
@@ -261,12 +270,13 @@ __global__ void __launch_bounds__(256) rotate_weights_kernel(const float *part, 
 
 using Kernel = void (*)(RotateArgs);
 
-template <bool BWD, bool WEIGHTS, typename T, typename C, int V>
+// `FLAG`: with weights (backward), one head of either kind per rotation (forward).
+template <bool BWD, bool FLAG, typename T, typename C, int V>
 Kernel pick_lanes(int lanes) {
     auto one = [](auto l) -> Kernel {
         constexpr int L = decltype(l)::value;
-        if constexpr (BWD) return rotate_bwd_kernel<T, C, V, L, WEIGHTS>;
-        else return rotate_fwd_kernel<T, C, V, L>;
+        if constexpr (BWD) return rotate_bwd_kernel<T, C, V, L, FLAG>;
+        else return rotate_fwd_kernel<T, C, V, L, FLAG>;
     };
     switch (lanes) {
         case 1: return one(std::integral_constant<int, 1>());
@@ -278,17 +288,17 @@ Kernel pick_lanes(int lanes) {
     }
 }
 
-template <bool BWD, bool WEIGHTS>
+template <bool BWD, bool FLAG>
 Kernel pick(int dtype, int cum_dtype, int v, int lanes) {
     using bf = __nv_bfloat16;
     if (dtype == QS_F32) {
         if (cum_dtype == QS_F32)
-            return v == 2 ? pick_lanes<BWD, WEIGHTS, float, float, 2>(lanes) : pick_lanes<BWD, WEIGHTS, float, float, 1>(lanes);
-        return v == 2 ? pick_lanes<BWD, WEIGHTS, float, bf, 2>(lanes) : pick_lanes<BWD, WEIGHTS, float, bf, 1>(lanes);
+            return v == 2 ? pick_lanes<BWD, FLAG, float, float, 2>(lanes) : pick_lanes<BWD, FLAG, float, float, 1>(lanes);
+        return v == 2 ? pick_lanes<BWD, FLAG, float, bf, 2>(lanes) : pick_lanes<BWD, FLAG, float, bf, 1>(lanes);
     }
     if (cum_dtype == QS_F32)
-        return v == 2 ? pick_lanes<BWD, WEIGHTS, bf, float, 2>(lanes) : pick_lanes<BWD, WEIGHTS, bf, float, 1>(lanes);
-    return v == 2 ? pick_lanes<BWD, WEIGHTS, bf, bf, 2>(lanes) : pick_lanes<BWD, WEIGHTS, bf, bf, 1>(lanes);
+        return v == 2 ? pick_lanes<BWD, FLAG, bf, float, 2>(lanes) : pick_lanes<BWD, FLAG, bf, float, 1>(lanes);
+    return v == 2 ? pick_lanes<BWD, FLAG, bf, bf, 2>(lanes) : pick_lanes<BWD, FLAG, bf, bf, 1>(lanes);
 }
 
 // Checks shared by the two directions: QS_OK, an error, or 1 for no rows at all.
@@ -317,10 +327,11 @@ int launched() {
     return QS_OK;
 }
 
-// CTAs of 256 threads per SM that the persistent backward runs: eight fill the
-// SM's 2048 threads where registers allow it; more CTAs than run at once only
-// add partial rows.
-constexpr int kBwdCtasPerSm = 4;
+// CTAs per SM that the persistent backward runs, as many as its registers let run at
+// once.  One quaternion per lane (heads up to 128) keeps it at 64 registers, two take
+// twice that: on 2 x 4099 rows with 32 + 8 heads of 96 the first runs in 60% of the
+// second's time, although its bfloat16 accesses are 8 bytes instead of 16.
+constexpr int bwd_ctas_per_sm(int v) { return v == 1 ? 4 : 2; }
 
 }  // namespace
 
@@ -352,7 +363,7 @@ extern "C" int quat_norm_rotate_fwd(int dtype, int cum_dtype, int norm, float ep
     a.nq = (unsigned)(Hq / H), a.nk = (unsigned)(Hk / H), a.items = (unsigned)(B * S * H);
     a.eps = eps, a.inv_div = norm == QS_NORM_RMS ? 1.f / (float)D : 1.f;
     const int v = D % 8 == 0 ? 2 : 1, lanes = lanes_of(D, v), groups = kThreads / lanes;
-    const Kernel fn = pick<false, false>(dtype, cum_dtype, v, lanes);
+    const Kernel fn = a.nq == 1 && a.nk == 1 ? pick<false, true>(dtype, cum_dtype, v, lanes) : pick<false, false>(dtype, cum_dtype, v, lanes);
     fn<<<(a.items + groups - 1) / groups, kThreads, 0, static_cast<cudaStream_t>(stream_)>>>(a);
     return launched();
 }
@@ -409,13 +420,13 @@ extern "C" int quat_norm_rotate_bwd(int dtype, int cum_dtype, int norm, float ep
     a.S = (unsigned)S, a.H = (unsigned)H, a.J = (unsigned)J, a.D = (unsigned)D;
     a.nq = (unsigned)(Hq / H), a.nk = (unsigned)(Hk / H), a.items = (unsigned)(B * S * H);
     a.eps = eps, a.inv_div = norm == QS_NORM_RMS ? 1.f / (float)D : 1.f;
-    const int v = D % 8 == 0 ? 2 : 1, lanes = lanes_of(D, v), groups = kThreads / lanes;
+    const int v = D > 128 ? 2 : 1, lanes = lanes_of(D, v), groups = kThreads / lanes;
     const unsigned all = (a.items + groups - 1) / groups;
     if (!w_q && !w_k) {
         pick<true, false>(dtype, cum_dtype, v, lanes)<<<all, kThreads, 0, stream>>>(a);
         return launched();
     }
-    const unsigned most = (unsigned)sms * kBwdCtasPerSm, grid = all < most ? all : most;
+    const unsigned most = (unsigned)(sms * bwd_ctas_per_sm(v)), grid = all < most ? all : most;
     unsigned char *ws = nullptr;
     rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)grid * 2 * D * 4, &ws);
     if (rc != QS_OK) return rc;
@@ -423,7 +434,7 @@ extern "C" int quat_norm_rotate_bwd(int dtype, int cum_dtype, int norm, float ep
     pick<true, true>(dtype, cum_dtype, v, lanes)<<<grid, kThreads, 0, stream>>>(a);
     rc = launched();
     if (rc != QS_OK) return rc;
-    rotate_weights_kernel<<<(unsigned)(2 * D + 31) / 32, 256, 0, stream>>>(a.dw_part, w_q ? d_w_q : nullptr,
+    rotate_weights_kernel<<<(unsigned)(2 * D + 31) / 32, 1024, 0, stream>>>(a.dw_part, w_q ? d_w_q : nullptr,
                                                                           w_k ? d_w_k : nullptr, grid, (unsigned)D);
     return launched();
 }

@@ -17,7 +17,9 @@ from __future__ import annotations
 
 import ctypes
 
-from . import QS_OK, QuatScanError, _on_device, _stream_handle, _torch, load_library
+import torch
+
+from . import QS_OK, QuatScanError, _on_device, _stream_handle, load_library
 
 __all__ = ["QS_DELTA_STEPS", "QS_DELTA_MAX_D", "QS_ROTATE_MAX_D", "quat_norm_rotate_fwd", "quat_norm_rotate_bwd",
            "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd", "quat_delta_step"]
@@ -27,6 +29,11 @@ QS_DELTA_MAX_D = 128    # largest head dimensions of the delta rule
 QS_ROTATE_MAX_D = 256   # largest head dimension of quat_norm_rotate_*
 
 _NORMS = {"rms": 0, "l2": 1}
+_F32, _BF16 = torch.float32, torch.bfloat16
+_get_device = getattr(torch._C, "_cuda_getDevice", lambda: None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    _get_device = lambda: None  # noqa: E731  (then always through a Stream object)
 _ready = None
 
 
@@ -49,12 +56,12 @@ def _lib():
 
 
 def _code(t, name):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _BF16:
         return 1
-    if t.dtype is torch.float32:
+    if dtype is _F32:
         return 0
-    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
 
 
 def _need(name, t, shape, device, dtype, contiguous=True):
@@ -71,7 +78,6 @@ def _need(name, t, shape, device, dtype, contiguous=True):
 
 def _first(name, t, dims):
     """The first tensor of a call: CUDA, of the right number of dimensions; returns its device."""
-    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -83,13 +89,17 @@ def _first(name, t, dims):
 
 def _strides(*tensors):
     """The ``strides`` argument: NULL when all are contiguous."""
-    if all(t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return None
     out = []
-    for i, t in enumerate(tensors):
+    for t in tensors:
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("the last dimension must be contiguous")
-        out += [t.stride(0), t.stride(1), t.stride(2)]
+        # A dimension of one entry has no stride to speak of.
+        out += [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
     return (ctypes.c_int64 * len(out))(*out)
 
 
@@ -97,9 +107,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(t):
+    """A contiguous tensor like ``t``."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _run(fn, where, device, stream, *args):
-    with _on_device(device):
-        rc = fn(*args, _stream_handle(stream, device))
+    """Calls the library with ``stream`` (default: the current one) on ``device``."""
+    if stream is None and _get_device() == device.index:   # the usual call, without a context or a Stream object
+        rc = fn(*args, _raw_stream(device.index))
+    else:
+        with _on_device(device):
+            rc = fn(*args, _stream_handle(stream, device))
     if rc != QS_OK:
         raise QuatScanError(rc, where)
 
@@ -108,7 +127,6 @@ def _run(fn, where, device, stream, *args):
 # Norm and rotation of queries and keys.
 # ---------------------------------------------------------------------------
 def _rotate_args(q, k, cum, w_q, w_k, norm):
-    torch = _torch()
     device = _first("q", q, 4)
     _first("k", k, 4)
     _first("cum", cum, 5)
@@ -141,14 +159,13 @@ def quat_norm_rotate_fwd(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6,
     ``norm``: ``"rms"`` (mean of squares) or ``"l2"`` (sum of squares); ``w_q``,
     ``w_k``: float32 [D] weights or None.  Returns contiguous ``(q_out, k_out)``.
     """
-    torch = _torch()
     device, code, cum_code, dims = _rotate_args(q, k, cum, w_q, w_k, norm)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        q_out = _empty(q)
     else:
         _need("q_out", q_out, q.shape, device, q.dtype)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+        k_out = _empty(k)
     else:
         _need("k_out", k_out, k.shape, device, k.dtype)
     _run(_lib().quat_norm_rotate_fwd, "quat_norm_rotate_fwd", device, stream, code, cum_code, _NORMS[norm], eps,
@@ -164,12 +181,11 @@ def quat_norm_rotate_bwd(q, k, cum, d_q_out, d_k_out, w_q=None, w_k=None, *, nor
     that share a rotation and goes to the scan's backward as it is; the weights'
     gradients are float32, None where there is no weight.
     """
-    torch = _torch()
     device, code, cum_code, dims = _rotate_args(q, k, cum, w_q, w_k, norm)
     _need("d_q_out", d_q_out, q.shape, device, q.dtype)
     _need("d_k_out", d_k_out, k.shape, device, k.dtype)
-    d_q = torch.empty(q.shape, dtype=q.dtype, device=device)
-    d_k = torch.empty(k.shape, dtype=k.dtype, device=device)
+    d_q = _empty(q)
+    d_k = _empty(k)
     d_cum = torch.empty_like(cum)
     d_w_q = None if w_q is None else torch.empty_like(w_q)
     d_w_k = None if w_k is None else torch.empty_like(w_k)
@@ -203,7 +219,6 @@ def _delta_args(q, k, v, g, beta):
 
 def _sequences(offsets, B, S, device):
     """(number of sequences, carry slots' leading shape)."""
-    torch = _torch()
     if offsets is None:
         return B, (B, -(-S // QS_DELTA_STEPS))
     if offsets.dim() != 1 or offsets.shape[0] < 1:
@@ -216,12 +231,11 @@ def _sequences(offsets, B, S, device):
 
 
 def _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, keep):
-    torch = _torch()
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
     N, slots = _sequences(offsets, B, S, device)
     if init is not None:
         _need("init", init, (N, Hv, Dk, Dv), device, torch.float32)
-    o = torch.empty((B, S, Hv, Dv), dtype=v.dtype, device=device)
+    o = _empty(v)
     final = torch.empty((N, Hv, Dk, Dv), dtype=torch.float32, device=device)
     carries = errors = None
     if keep:
@@ -262,7 +276,6 @@ def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scal
 
     ``d_o``: cotangent of ``o`` (contiguous), ``d_final``: of the final state or None.
     """
-    torch = _torch()
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
     N, slots = _sequences(offsets, B, S, device)
     _need("carries", carries, (*slots, Hv, Dk, Dv), device, torch.float32)
@@ -270,8 +283,8 @@ def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scal
     _need("d_o", d_o, (B, S, Hv, Dv), device, v.dtype)
     if d_final is not None:
         _need("d_final", d_final, (N, Hv, Dk, Dv), device, torch.float32)
-    d_q, d_k = torch.empty(q.shape, dtype=q.dtype, device=device), torch.empty(k.shape, dtype=k.dtype, device=device)
-    d_v = torch.empty(v.shape, dtype=v.dtype, device=device)
+    d_q, d_k = _empty(q), _empty(k)
+    d_v = _empty(v)
     d_g, d_beta = torch.empty_like(g), torch.empty_like(beta)
     d_init = torch.empty((N, Hv, Dk, Dv), dtype=torch.float32, device=device)
     _run(_lib().quat_delta_bwd, "quat_delta_bwd", device, stream, code, gate, Dk ** -0.5 if scale is None else scale,
@@ -289,7 +302,6 @@ def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None, 
     ``state[slots[n]]`` (int32 [N]; None: ``state[n]``); a slot outside the pool
     (-1) marks an idle row, whose output is zero.  No two rows may share a slot.
     """
-    torch = _torch()
     device, code, gate, (N, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
     _first("state", state, 4)
     P = state.shape[0]
@@ -299,7 +311,7 @@ def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None, 
     elif N > P:
         raise ValueError(f"{N} rows without slots need as many states, got {P}")
     if o is None:
-        o = torch.empty((N, T, Hv, Dv), dtype=v.dtype, device=device)
+        o = _empty(v)
     else:
         _need("o", o, (N, T, Hv, Dv), device, v.dtype)
     _run(_lib().quat_delta_step, "quat_delta_step", device, stream, code, gate, Dk ** -0.5 if scale is None else scale,

@@ -326,6 +326,29 @@ def test_step(torch, dims, dt, gates):
     assert torch.isnan(pool[free]).all()
 
 
+@pytest.mark.parametrize("dims", [(130, 1, 4, 8, 64, 64), (240, 3, 2, 4, 24, 40), (80, 2, 8, 16, 128, 128), (310, 1, 4, 4, 8, 16)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_step_many_states(torch, dims, dt):
+    """Enough states to be streamed through shared memory; some rows idle, the first and the last among them."""
+    N, T, Hk, Hv, Dk, Dv = dims
+    x = delta_inputs(torch, N, T, Hk, Hv, Dk, Dv, dt, "f32", seed=13)
+    slots = torch.randperm(N + 2, device="cuda")[:N].to(torch.int32)
+    slots[torch.tensor([0, 5, 6, N - 1], device="cuda")] = torch.tensor([-1, -7, N + 2, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    pool = 0.3 * torch.randn(N + 2, Hv, Dk, Dv, device="cuda")
+    before = wide(pool)
+    o = qs.quat_delta_step(*[x[n] for n in FIVE], pool, slots=slots)
+    assert qs.quat_cumprod_status() == qs.QS_OK
+    n, after = {k: wide(v) for k, v in x.items()}, wide(pool)
+    want_o, want_pool = np.zeros(n["v"].shape), before.copy()
+    for i, s in enumerate(slots.tolist()):
+        if 0 <= s < N + 2:
+            want_o[i], want_pool[s] = ref.delta(*[n[k][i] for k in FIVE], before[s], Dk ** -0.5)
+    close(o, want_o, dt, "o")
+    assert np.abs(after - want_pool).max() <= TOL["f32"] * np.abs(want_pool).max()
+    untouched = sorted(set(range(N + 2)) - set(slots.tolist()))
+    assert (after[untouched] == before[untouched]).all()
+
+
 def test_step_idle_rows(torch):
     x = delta_inputs(torch, 4, 2, 1, 2, 64, 64, "bf16", "f32")
     x["v"][1] = float("nan")
