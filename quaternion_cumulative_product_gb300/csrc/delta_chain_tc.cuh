@@ -93,17 +93,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                             smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
             __syncwarp();
             if (it > 0) tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
-            float *ds = a.ds + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + dv;
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (it > 0) add_update(p);
-                if (!SUM && in) {
-                    float *out = ds + (size_t)(col0 + p * 16) * a.Dv;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i, out += a.Dv)
-                        if (col0 + p * 16 + i < a.Dk) *out = i % 2 ? m[p * 8 + i / 2].y : m[p * 8 + i / 2].x;
-                }
-                __syncwarp();
                 put_terms3(tl + chain_tmem::SP + (col0 + p * 16) / 2, 64, m + p * 8);
             }
             whole = gt.whole;
@@ -115,6 +107,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, 64), TmemK(), KMajor());
                 mma_commit(&bar.x);
+            }
+            __syncwarp();
+            if (!SUM && in) {   // while X is under way
+                float *out = a.ds + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
+#pragma unroll
+                for (int i = 0; i < HALF; ++i, out += a.Dv)
+                    if (col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
             }
             __syncwarp();
             tc_wait_warp(&bar.x, it & 1, gone, a.ctl);

@@ -8,8 +8,8 @@
 //
 //   walk    two warpgroups: [X Y] = M^T [K;Q]^T;  e = (v - exp(G) X) T^T;
 //           dM = (beta left e)^T K;  o = scale exp(G) Y + U P^T.  Each converts half of
-//           the columns between two products; the second one also takes care of o
-//           while the products run
+//           the columns between two products; what the chain does not wait for (o, the
+//           stores) runs while the products do
 //   prep    two warpgroups, one chunk ahead (delta_prep.cuh)
 //
 // The state stays in the registers of `walk` (fp32, half of dk each): adding
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             for (int i = 0; i < 8; ++i)
                 m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
         };
-        // o of chunk c.
+        // o of chunk c, this warpgroup's half of the steps.
         auto write_o = [&](int c) {
             tc_wait_warp(&bar.o, c & 1, gone, a.ctl);
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
-            T *out = static_cast<T *>(a.o) + ((size_t)(row0 + (long long)c * DC) * a.Hv + head) * a.Dv + dv;
+            T *out = static_cast<T *>(a.o) + ((size_t)(row0 + (long long)c * DC + wg * 32) * a.Hv + head) * a.Dv + dv;
 #pragma unroll 1
-            for (int h = 0; h < DC; h += 16, out += 16 * step) {
+            for (int h = wg * 32; h < wg * 32 + 32; h += 16, out += 16 * step) {
                 uint32_t r[16];
                 tmem_ld16(tl + fwd_tmem::O + h, r);
                 tmem_wait_ld();
@@ -122,17 +122,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             if (c > 0) tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
             if (!SUM && !kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
-            float *carry = !SUM && a.carries ? a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + dv : nullptr;
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (c > 0) add_dm(p);
-                if (carry && in) {
-                    float *out = carry + (size_t)(col0 + p * 16) * a.Dv;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i, out += a.Dv)
-                        if (col0 + p * 16 + i < a.Dk) *out = i % 2 ? m[p * 8 + i / 2].y : m[p * 8 + i / 2].x;
-                }
-                __syncwarp();
                 put_terms3(tl + fwd_tmem::SP + (col0 + p * 16) / 2, 64, m + p * 8);
             }
             tmem_wait_st();
@@ -147,7 +139,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.x);
             }
             __syncwarp();
-            if (!SUM && wg == 1 && c > 0) write_o(c - 1);
+            // While X and Y are under way: the state that entered the chunk, and the last chunk's o.
+            if (!SUM && a.carries && in) {
+                float *out = a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
+#pragma unroll
+                for (int i = 0; i < HALF; ++i, out += a.Dv)
+                    if (col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
+            }
+            __syncwarp();
+            if (!SUM && c > 0) write_o(c - 1);
             tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {   // v - exp(G) X
@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.e);
             }
             __syncwarp();
-            if (!SUM && wg == 1) {   // Y moves, so that dM can take its place and o add up on it
+            if (!SUM) {   // Y moves, so that dM can take its place and o add up on it
 #pragma unroll 1
-                for (int h = 0; h < DC; h += 16) {
+                for (int h = wg * 32; h < wg * 32 + 32; h += 16) {
                     uint32_t r[16];
                     tmem_ld16(tl + fwd_tmem::D + 64 + h, r);
                     tmem_wait_ld();
@@ -190,37 +190,32 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
             }
             tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
+            const int h0 = wg * 32;
+            float2 u[16];   // beta e
             {
-                const int h = wg * 32;
-                float *eo = !SUM && a.errors ? a.errors + ((size_t)(row0 + (long long)c * DC + h) * a.Hv + head) * a.Dv + dv : nullptr;
                 uint32_t r[32];   // (U takes the place of 32 columns of e: all are read first)
-                tmem_ld32(tl + fwd_tmem::X + h, r);
+                tmem_ld32(tl + fwd_tmem::X + h0, r);
                 tmem_wait_ld();
-                if (eo && in)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (h + i < left) eo[i * step] = __uint_as_float(r[i]);
-                __syncwarp();
+                for (int i = 0; i < 16; ++i) u[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            }
+            if (!SUM && a.errors && in) {
+                float *eo = a.errors + ((size_t)(row0 + (long long)c * DC + h0) * a.Hv + head) * a.Dv + dv;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float2 u[8];
-                    uint32_t t[PT][8];
+                for (int i = 0; i < 32; ++i)
+                    if (h0 + i < left) eo[i * step] = i % 2 ? u[i / 2].y : u[i / 2].x;
+            }
+            __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int s = q * 16 + 2 * i;
-                        u[i] = mul2(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])),
-                                    *reinterpret_cast<const float2 *>(&gt.beta[h + s]));
-                        uint32_t p[3];
-                        split2<PT>(u[i], p);
+            for (int q = 0; q < 2; ++q) {   // the state's update first: the chain waits for it
+                float2 k[8];
 #pragma unroll
-                        for (int j = 0; j < PT; ++j) t[j][i] = p[j];
-                        u[i] = mul2(u[i], *reinterpret_cast<const float2 *>(&gt.left[h + s]));
-                    }
-#pragma unroll
-                    for (int j = 0; j < (SUM ? 0 : PT); ++j)
-                        tmem_st8(tl + (kEarly ? fwd_tmem::X + h + j * 16 : fwd_tmem::SP + j * 32 + h / 2) + q * 8, t[j]);
-                    put_terms3(tl + fwd_tmem::SP + 96 + (h + q * 16) / 2, 32, u);
+                for (int i = 0; i < 8; ++i) {
+                    const int s = q * 16 + 2 * i;
+                    u[s / 2] = mul2(u[s / 2], *reinterpret_cast<const float2 *>(&gt.beta[h0 + s]));
+                    k[i] = mul2(u[s / 2], *reinterpret_cast<const float2 *>(&gt.left[h0 + s]));
                 }
+                put_terms3(tl + fwd_tmem::SP + 96 + (h0 + q * 16) / 2, 32, k);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -230,21 +225,43 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.s);
-                if (!SUM) {
+                if (SUM) mma_commit(&bar.empty[st]);
+            }
+            __syncwarp();
+            if (!SUM) {   // U, for o
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t t[PT][8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t p[3];
+                        split2<PT>(u[q * 8 + i], p);
+#pragma unroll
+                        for (int j = 0; j < PT; ++j) t[j][i] = p[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < PT; ++j)
+                        tmem_st8(tl + (kEarly ? fwd_tmem::X + h0 + j * 16 : fwd_tmem::SP + j * 32 + h0 / 2) + q * 8, t[j]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                named_bar_sync(1, 256);
+                if (warp == 0 && elect_one()) {
+                    tc_fence_after();
                     issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
                                                       smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
                                                       KMajor1(), true);
                     mma_commit(&bar.o);
+                    mma_commit(&bar.empty[st]);
                 }
-                mma_commit(&bar.empty[st]);
+                __syncwarp();
             }
-            __syncwarp();
         }
         if (chunks > 0) {
             tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) add_dm(p);
-            if (!SUM && wg == 1) write_o(chunks - 1);
+            if (!SUM) write_o(chunks - 1);
         }
         if (SUM) {
             if (in)
