@@ -29,11 +29,11 @@ constexpr uint32_t G = 448;
 }  // namespace chain_tmem
 
 // SUM: sums a segment up (delta_prep.cuh) and writes neither dM' nor w.
-template <typename T, int NT, int DK, int STAGES, bool SUM>
+template <typename T, int NT, int DK, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
-    using L = WalkLayout<NT, DK, STAGES, 3>;
+    using L = WalkLayout<NT, DK, 3, 1>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024u - smem_addr(raw) % 1024u) % 1024u);
     const uint32_t sm32 = smem_addr(sm);
@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
-    const uint32_t tm = walk_setup<L, STAGES, 3>(bar, sm32, 1 + 256);   // a stage is free after the products, and the walk done with beta
+    const uint32_t tm = walk_setup<L, 3, 1>(bar, sm32);
 
     if (wg >= 2) {
         const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
-        walk_prep<T, NT, DK, STAGES, 3, true>(a, &kmap, &qmap, &omap, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
+        walk_prep<T, NT, DK, 3, 1, true>(a, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of dM per thread
         const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
@@ -81,18 +81,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
         };
 
+        if (NT == 1 && warp == 0 && elect_one())
+            for (int i = 0; i < 3; ++i) fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, i, chunks, head);
+        __syncwarp();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
-            const int st = it % STAGES, c = chunks - 1 - it;
-            const uint32_t stage = sm32 + st * L::STAGE;
-            const ChunkGates &gt = gates[st];
+            const int c = chunks - 1 - it;
+            const uint32_t rows = sm32 + it % L::KS * L::ROWS, tile_t = sm32 + L::T_AT, tile_p = sm32 + L::P_AT;
+            const ChunkGates &gt = gates[it & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
-            tc_wait_warp(&bar.full[st], (it / STAGES) & 1, gone, a.ctl);
-            if (warp == 0 && elect_one())   // R = dO^T P
-                issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(stage + L::V_AT, TILE, 1024), L::V_TERM,
-                                            smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
+            tc_wait_warp(&bar.full, it & 1, gone, a.ctl);
+            if (NT == 1) tc_wait_warp(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);   // (dO is read by all)
+            if (warp == 0 && elect_one()) {   // R = dO^T P
+                issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(rows + L::V_AT, TILE, 1024), L::V_TERM,
+                                            smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
+                mma_commit(&bar.empty[0]);
+            }
             __syncwarp();
-            if (it > 0) tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
+            if (it > 0) {
+                tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
+                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with
+                    fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, it + 2, chunks, head);
+                __syncwarp();
+            }
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (it > 0) add_update(p);
@@ -104,7 +115,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             named_bar_sync(1, 256);
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
+                issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, 64), TmemK(), KMajor());
                 mma_commit(&bar.x);
             }
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             named_bar_sync(1, 256);
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
+                issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.e);
             }
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 for (int h = 0; h < DC; h += 16) {
                     float v[16];
                     float2 z[8];
-                    third_column<NT>(sm + st * L::STAGE + L::V_AT, dv, h, v);
+                    third_column<NT>(sm + it % L::KS * L::ROWS + L::V_AT, dv, h, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         z[i] = mul2(mul2(SUM && row.map ? make_float2(0.f, 0.f) : make_float2(v[2 * i], v[2 * i + 1]), *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i])),
@@ -175,12 +186,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
                 const uint32_t id = mma_desc(128, DK, false, true);
-                issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP, 32, smem_desc(stage + TILE, 2 * TILE, 1024), L::KQ_TERM,
+                issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP, 32, smem_desc(rows + TILE, 2 * TILE, 1024), L::KQ_TERM,
                                             id, TmemK(), MNMajor());
-                issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
+                issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP + 96, 32, smem_desc(rows, 2 * TILE, 1024), L::KQ_TERM,
                                             id, TmemK(), MNMajor(), true);
                 mma_commit(&bar.s);
-                mma_commit(&bar.empty[st]);
             }
             __syncwarp();
             if (!SUM) {   // w and dv, half of the steps each, while the products run
@@ -193,18 +203,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     uint32_t r[16];
                     tmem_ld16(tl + chain_tmem::X + h, r);
                     tmem_wait_ld();
-                    if (in)
+                    float x[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (h + i < left) {
-                                wo[i * step] = __uint_as_float(r[i]);
-                                store1(vo + i * step, gt.beta[h + i] * __uint_as_float(r[i]));
-                            }
-                    __syncwarp();
+                    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+                    store_columns(wo, step, left - h, in, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] *= gt.beta[h + i];
+                    store_columns(vo, step, left - h, in, x);
                 }
                 tc_fence_before();
             }
-            mbar_arrive(&bar.empty[st]);
         }
         if (chunks > 0) {
             tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);

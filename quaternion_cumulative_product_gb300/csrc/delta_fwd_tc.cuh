@@ -42,12 +42,13 @@ struct UAt {   // U's columns: K step k of a term
 };
 
 // SUM: sums a segment up (delta_prep.cuh) and writes no o.
-template <typename T, int NT, int DK, int STAGES, bool SUM>
+template <typename T, int NT, int DK, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_fwd_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap vmap) {
     constexpr int PT = NT == 1 ? 2 : 3;   // terms of what only o is made of: bfloat16's own rounding is 2^-9
-    using L = WalkLayout<NT, DK, STAGES, PT>;
+    constexpr int PS = NT == 1 ? 2 : 1;
+    using L = WalkLayout<NT, DK, PT, PS>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024u - smem_addr(raw) % 1024u) % 1024u);
     const uint32_t sm32 = smem_addr(sm);
@@ -62,10 +63,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
-    const uint32_t tm = walk_setup<L, STAGES, PT>(bar, sm32, 1);
+    const uint32_t tm = walk_setup<L, PT, PS>(bar, sm32);
 
     if (wg >= 2) {
-        walk_prep<T, NT, DK, STAGES, PT, false>(a, &kmap, &qmap, &vmap, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
+        walk_prep<T, NT, DK, PT, PS, false>(a, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of the state per thread
         constexpr bool kEarly = NT == 1;         // U has a place of its own: the next chunk need not wait for o
@@ -106,21 +107,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 uint32_t r[16];
                 tmem_ld16(tl + fwd_tmem::O + h, r);
                 tmem_wait_ld();
-                if (in)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (h + i < left) store1(out + i * step, __uint_as_float(r[i]));
-                __syncwarp();
+                store_columns(out, step, left - h, in, reinterpret_cast<const float *>(r));
             }
         };
 
+        if (NT == 1 && warp == 0 && elect_one())
+            for (int i = 0; i < 3; ++i) fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, i, chunks, head);
+        __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int st = c % STAGES;
-            const uint32_t stage = sm32 + st * L::STAGE;
-            const ChunkGates &gt = gates[st];
+            const uint32_t rows = sm32 + c % L::KS * L::ROWS, tile_t = sm32 + L::T_AT, tile_p = sm32 + L::P_AT + c % PS * L::P_SIZE;
+            const ChunkGates &gt = gates[c & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
-            if (c > 0) tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
+            if (c > 0) {
+                tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
+                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with
+                    fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, c + 2, chunks, head);
+                __syncwarp();
+            }
             if (!SUM && !kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
@@ -130,11 +134,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            tc_wait_warp(&bar.full[st], (c / STAGES) & 1, gone, a.ctl);
+            tc_wait_warp(&bar.full, c & 1, gone, a.ctl);
+            if (NT == 1) tc_wait_warp(&bar.rows[c % 3], (c / 3) & 1, gone, a.ctl);   // (V is read by all)
             whole = gt.whole;
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(stage, 16, 1024), L::KQ_TERM,
+                issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, SUM ? 64 : 128), TmemK(), KMajor());
                 mma_commit(&bar.x);
             }
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 float v[16];
                 float2 e[8];
                 tmem_ld16(tl + fwd_tmem::D + h, r);
-                third_column<NT>(sm + st * L::STAGE + L::V_AT, dv, h, v);
+                third_column<NT>(sm + c % L::KS * L::ROWS + L::V_AT, dv, h, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             named_bar_sync(1, 256);
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(stage + L::T_AT, 16, 1024), TILE,
+                issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64), TmemK(), KMajor1());
                 mma_commit(&bar.e);
             }
@@ -222,10 +227,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             named_bar_sync(1, 256);
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(stage, 2 * TILE, 1024), L::KQ_TERM,
+                issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(rows, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.s);
-                if (SUM) mma_commit(&bar.empty[st]);
+                if (SUM) mma_commit(&bar.empty[c % PS]);
             }
             __syncwarp();
             if (!SUM) {   // U, for o
@@ -249,10 +254,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 if (warp == 0 && elect_one()) {
                     tc_fence_after();
                     issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
-                                                      smem_desc(stage + L::P_AT, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
+                                                      smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
                                                       KMajor1(), true);
                     mma_commit(&bar.o);
-                    mma_commit(&bar.empty[st]);
+                    mma_commit(&bar.empty[c % PS]);
                 }
                 __syncwarp();
             }

@@ -7,8 +7,11 @@
 // (forward) or diag(beta) A (backward): 16 x 16 diagonal blocks by substitution, then
 // twice the corner of a block as -T22 N21 T11.  All in fp32; T and P leave as terms.
 //
-// bfloat16 tensors come by TMA (swizzled boxes of 64 steps x 64 values, the next
-// chunk's prefetched into L2), fp32 ones through registers, which split them.
+// bfloat16 tensors come by TMA (swizzled boxes of 64 steps x 64 values) into a ring of
+// three chunks that the walk refills, and a chunk's Gram products run while the chunk
+// before is inverted: prep's own time per chunk (the decays and the inverse) is what
+// bounds the walks.  fp32 tensors go through registers, which split them, one chunk at
+// a time: their terms take three times the space.
 #pragma once
 
 #include <type_traits>
@@ -122,9 +125,10 @@ constexpr int kPrepThreads = 256;
 
 // tf [64][FLD], strictly lower triangular (zeros on and above the diagonal inside
 // its 16 x 16 and 32 x 32 diagonal blocks), becomes (1 + tf)^-1 on and below the
-// diagonal of its 32 x 32 blocks and in the lower corner; kPrepThreads threads
-// (barrier `bar`).  yf: 32 x 36 of scratch.
-__device__ __forceinline__ void invert_64(float *tf, float *yf, int tid, int bar) {
+// diagonal of its 32 x 32 blocks and in the lower corner (the upper one is scratch);
+// kPrepThreads threads (barrier `bar`).
+__device__ __forceinline__ void invert_64(float *tf, int tid, int bar) {
+    float *yf = tf + 32;
     const int warp = tid / 32, j = tid % 32;
     if (warp < 4 && j < 16) {   // a diagonal block per half warp, a column per thread, by substitution
         float *a = tf + warp * 16 * (FLD + 1);
@@ -151,7 +155,7 @@ __device__ __forceinline__ void invert_64(float *tf, float *yf, int tid, int bar
     named_bar_sync(bar, kPrepThreads);
     {   // 16 -> 32: two corners, 1 x 2 values per thread
         const int b = tid / 128, r = tid % 128 / 8, c = tid % 8 * 2;
-        float *d = tf + b * 32 * (FLD + 1), *y = yf + b * 16 * 20;   // y: 16 x 20
+        float *d = tf + b * 32 * (FLD + 1), *y = yf + b * 16;
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int m = 0; m < 16; m += 4) {
@@ -161,16 +165,16 @@ __device__ __forceinline__ void invert_64(float *tf, float *yf, int tid, int bar
             v = fma2(make_float2(p.z, p.z), *reinterpret_cast<const float2 *>(d + (m + 2) * FLD + c), v);
             v = fma2(make_float2(p.w, p.w), *reinterpret_cast<const float2 *>(d + (m + 3) * FLD + c), v);
         }
-        *reinterpret_cast<float2 *>(y + r * 20 + c) = v;
+        *reinterpret_cast<float2 *>(y + r * FLD + c) = v;
         named_bar_sync(bar, kPrepThreads);
         v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int m = 0; m < 16; m += 4) {
             const float4 p = *reinterpret_cast<const float4 *>(d + (16 + r) * FLD + 16 + m);
-            v = fma2(make_float2(p.x, p.x), *reinterpret_cast<const float2 *>(y + m * 20 + c), v);
-            v = fma2(make_float2(p.y, p.y), *reinterpret_cast<const float2 *>(y + (m + 1) * 20 + c), v);
-            v = fma2(make_float2(p.z, p.z), *reinterpret_cast<const float2 *>(y + (m + 2) * 20 + c), v);
-            v = fma2(make_float2(p.w, p.w), *reinterpret_cast<const float2 *>(y + (m + 3) * 20 + c), v);
+            v = fma2(make_float2(p.x, p.x), *reinterpret_cast<const float2 *>(y + m * FLD + c), v);
+            v = fma2(make_float2(p.y, p.y), *reinterpret_cast<const float2 *>(y + (m + 1) * FLD + c), v);
+            v = fma2(make_float2(p.z, p.z), *reinterpret_cast<const float2 *>(y + (m + 2) * FLD + c), v);
+            v = fma2(make_float2(p.w, p.w), *reinterpret_cast<const float2 *>(y + (m + 3) * FLD + c), v);
         }
         *reinterpret_cast<float2 *>(d + (16 + r) * FLD + c) = make_float2(-v.x, -v.y);
     }
@@ -194,10 +198,10 @@ __device__ __forceinline__ void invert_64(float *tf, float *yf, int tid, int bar
         };
         float2 v[2];
         corner(tf + 32 * FLD, tf, FLD, v);
-        *reinterpret_cast<float2 *>(yf + r * 36 + c) = v[0];
-        *reinterpret_cast<float2 *>(yf + (r + 1) * 36 + c) = v[1];
+        *reinterpret_cast<float2 *>(yf + r * FLD + c) = v[0];
+        *reinterpret_cast<float2 *>(yf + (r + 1) * FLD + c) = v[1];
         named_bar_sync(bar, kPrepThreads);
-        corner(tf + 32 * FLD + 32, yf, 36, v);
+        corner(tf + 32 * FLD + 32, yf, FLD, v);
         *reinterpret_cast<float2 *>(tf + (32 + r) * FLD + c) = make_float2(-v[0].x, -v[0].y);
         *reinterpret_cast<float2 *>(tf + (33 + r) * FLD + c) = make_float2(-v[1].x, -v[1].y);
     }
@@ -268,24 +272,26 @@ struct TmemK {     // 8 columns of a left operand in tensor memory
 
 // Barriers and flags of a walk's CTA.
 struct WalkBars {
-    uint64_t full[2], empty[2], rows[2], x, e, s, o, g;
+    uint64_t full, empty[2], rows[3], x, e, s, o, g;
     uint32_t tmem;
     int gone;
 };
 
-// Shared memory of a walk.  A stage: K and Q [term][half of D]{K tile, Q tile}; the
-// third tensor [term][half of D] (fp32 V: [64][128] as it is); T [3 terms], P [PT].
-template <int NT, int DK, int STAGES, int PT>
+// Shared memory of a walk.  KS chunks of rows: K and Q [term][half of D]{K tile, Q tile},
+// the third tensor [term][half of D]; T [3 terms]; PS times P [PT terms].  T is written
+// after the chunk before has used it; P by turns.
+template <int NT, int DK, int PT, int PS>
 struct WalkLayout {
+    static constexpr int KS = NT == 1 ? 3 : 1;
     static constexpr int HALVES = DK / 64;
-    static constexpr uint32_t KQ_TERM = HALVES * 2 * TILE, KQ = NT * KQ_TERM;
-    static constexpr uint32_t V_AT = KQ, V_TERM = 2 * TILE, T_AT = V_AT + NT * V_TERM, P_AT = T_AT + 3 * TILE, STAGE = P_AT + PT * TILE;
-    static constexpr uint32_t F_AT = STAGES * STAGE, Y_AT = F_AT + DC * FLD * 4;
-    static constexpr uint32_t GATES_AT = Y_AT + 32 * 36 * 4;
-    static constexpr uint32_t BARS_AT = GATES_AT + STAGES * sizeof(ChunkGates);
-    static constexpr uint32_t BYTES = BARS_AT + 256 + 1024;   // + alignment of the tiles to 1024 bytes
+    static constexpr uint32_t KQ_TERM = HALVES * 2 * TILE, V_AT = NT * KQ_TERM, V_TERM = 2 * TILE, ROWS = V_AT + NT * V_TERM;
+    static constexpr uint32_t T_AT = KS * ROWS, P_AT = T_AT + 3 * TILE, P_SIZE = PT * TILE;
+    static constexpr uint32_t F_AT = P_AT + PS * P_SIZE;
+    static constexpr uint32_t GATES_AT = F_AT + DC * FLD * 4;
+    static constexpr uint32_t BARS_AT = GATES_AT + 4 * sizeof(ChunkGates);
+    static constexpr uint32_t NEED = BARS_AT + 256 + 1024;            // + alignment of the tiles to 1024 bytes
+    static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;  // one CTA per SM: it takes all of the tensor memory
     static_assert(BYTES <= 232448, "227 KB of shared memory");
-    static_assert(BYTES > 116736, "one CTA per SM: it takes all of the tensor memory");
 };
 
 constexpr int kWalkThreads = 512;   // two warpgroups that walk, two of prep
@@ -336,23 +342,20 @@ struct WalkRow {
 };
 
 // What a walk's CTA sets up before its roles part; returns the tensor memory's base.
-template <typename L, int STAGES, int PT>
-__device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32, int empty_count) {
+template <typename L, int PT, int PS>
+__device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], empty_count);
-            mbar_init(&bar.rows[i], 1);
-        }
-        for (uint64_t *b : {&bar.x, &bar.e, &bar.s, &bar.o, &bar.g}) mbar_init(b, 1);
+        for (uint64_t *b : {&bar.full, &bar.empty[0], &bar.empty[1], &bar.rows[0], &bar.rows[1], &bar.rows[2], &bar.x, &bar.e, &bar.s,
+                            &bar.o, &bar.g})
+            mbar_init(b, 1);
         *reinterpret_cast<volatile int *>(&bar.gone) = 0;
         fence_mbar_init();
     }
-    for (int st = 0; st < STAGES; ++st)   // T and P are zero above the diagonal blocks, where prep never writes
-        for (uint32_t i = threadIdx.x; i < (3 + PT) * TILE / 16; i += kWalkThreads) {
-            const uint32_t z[4] = {0, 0, 0, 0};
-            st_shared16(sm32 + st * L::STAGE + L::T_AT + i * 16, z);
-        }
+    // T and P are zero above the diagonal blocks, where prep never writes.
+    for (uint32_t i = threadIdx.x; i < (3 + PS * PT) * TILE / 16; i += kWalkThreads) {
+        const uint32_t z[4] = {0, 0, 0, 0};
+        st_shared16(sm32 + L::T_AT + i * 16, z);
+    }
     if (threadIdx.x < 32) tmem_alloc_all(&bar.tmem);
     tc_fence_before();
     __syncthreads();
@@ -360,83 +363,92 @@ __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32, int
     return (uint32_t)warp_uniform((int)bar.tmem);
 }
 
+// First step of the it-th chunk that a walk comes to.
+template <bool BWD>
+__device__ __forceinline__ long long chunk_start(int it, int chunks) {
+    return (long long)(BWD ? chunks - 1 - it : it) * DC;
+}
+
+// Sends for the rows of the it-th chunk (bfloat16); one thread of the walk, once the
+// chunk three before is done with.
+template <typename L, bool BWD>
+__device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
+                                           WalkBars &bar, unsigned char *sm, const Seq &seq, int it, int chunks, int head) {
+    if (it >= chunks) return;
+    unsigned char *dst = sm + it % 3 * L::ROWS;
+    uint64_t *full = &bar.rows[it % 3];
+    const int kh = head / (a.Hv / a.Hk), s = (int)(seq.s0 + chunk_start<BWD>(it, chunks)), b = (int)seq.b;
+    mbar_arrive_expect_tx(full, (2 * L::HALVES + (a.Dv > 64 ? 2 : 1)) * TILE);
+#pragma unroll
+    for (int h = 0; h < L::HALVES; ++h) {
+        tma_load_4d(dst + h * 2 * TILE, kmap, h * 64, kh, s, b, full);
+        tma_load_4d(dst + h * 2 * TILE + TILE, qmap, h * 64, kh, s, b, full);
+    }
+    for (int h = 0; h * 64 < a.Dv; ++h) tma_load_4d(dst + L::V_AT + h * TILE, vmap, h * 64, head, s, b, full);
+}
+
 // The role of prep's threads (ptid 0 .. 255).  BWD: the backward's order and N.
-// kmap, qmap, vmap: tensor maps of K, Q and the third tensor (bfloat16).
-template <typename T, int NT, int DK, int STAGES, int PT, bool BWD>
-__device__ __forceinline__ void walk_prep(const DeltaArgs &a, const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
-                                          const void *third, const qsh::Strides &st3, WalkBars &bar, unsigned char *sm,
+template <typename T, int NT, int DK, int PT, int PS, bool BWD>
+__device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third, const qsh::Strides &st3, WalkBars &bar, unsigned char *sm,
                                           const Seq &seq, int chunks, int head, uint32_t tm, uint32_t gram_at) {
-    using L = WalkLayout<NT, DK, STAGES, PT>;
+    using L = WalkLayout<NT, DK, PT, PS>;
     const int ptid = threadIdx.x - 256, warp = warp_uniform(ptid / 32), kh = head / (a.Hv / a.Hk), half = ptid / 128;
     const uint32_t sm32 = smem_addr(sm);
     volatile int *gone = &bar.gone;
-    float *tf = reinterpret_cast<float *>(sm + L::F_AT), *yf = reinterpret_cast<float *>(sm + L::Y_AT);
+    float *tf = reinterpret_cast<float *>(sm + L::F_AT);
     ChunkGates *gates = reinterpret_cast<ChunkGates *>(sm + L::GATES_AT);
     const uint32_t g_at = tm + ((uint32_t)(warp % 4 * 32) << 16) + gram_at;
-    auto start = [&](int it) { return (long long)(BWD ? chunks - 1 - it : it) * DC; };
-    RawGates raw = {};
-    if (warp == 7 && chunks > 0) raw = read_gates(a, seq, start(0), head);
-#pragma unroll 1
-    for (int it = 0; it < chunks; ++it) {
-        const int st = it % STAGES;
-        const uint32_t stage = sm32 + st * L::STAGE;
-        const long long t0 = start(it);
-        ChunkGates &gt = gates[st];
-        tc_wait_warp(&bar.empty[st], ((it / STAGES) & 1) ^ 1, gone, a.ctl);
-        if constexpr (NT == 1) {
-            if (warp == 0 && elect_one()) {
-                const int boxes = 2 * L::HALVES + (a.Dv > 64 ? 2 : 1);
-                const int s = (int)(seq.s0 + t0), b = (int)seq.b;
-                mbar_arrive_expect_tx(&bar.rows[st], boxes * TILE);
-#pragma unroll
-                for (int h = 0; h < L::HALVES; ++h) {
-                    tma_load_4d(sm + st * L::STAGE + h * 2 * TILE, kmap, h * 64, kh, s, b, &bar.rows[st]);
-                    tma_load_4d(sm + st * L::STAGE + h * 2 * TILE + TILE, qmap, h * 64, kh, s, b, &bar.rows[st]);
-                }
-                for (int h = 0; h * 64 < a.Dv; ++h)
-                    tma_load_4d(sm + st * L::STAGE + L::V_AT + h * TILE, vmap, h * 64, head, s, b, &bar.rows[st]);
-                if (it + 1 < chunks) {
-                    const int s1 = (int)(seq.s0 + start(it + 1));
-#pragma unroll
-                    for (int h = 0; h < L::HALVES; ++h) {
-                        tma_prefetch_4d(kmap, h * 64, kh, s1, b);
-                        tma_prefetch_4d(qmap, h * 64, kh, s1, b);
-                    }
-                    for (int h = 0; h * 64 < a.Dv; ++h) tma_prefetch_4d(vmap, h * 64, head, s1, b);
-                }
-            }
-            __syncwarp();
-        } else {
-            if (half == 0) load_rows<T, NT, DK, 128>(stage, 2 * TILE, L::KQ_TERM, a.k, a.sk, seq, t0, kh, a.Dk, ptid);
-            else load_rows<T, NT, DK, 128>(stage + TILE, 2 * TILE, L::KQ_TERM, a.q, a.sq, seq, t0, kh, a.Dk, ptid - 128);
-            load_rows<T, NT, 128, kPrepThreads>(stage + L::V_AT, TILE, L::V_TERM, third, st3, seq, t0, head, a.Dv, ptid);
-        }
-        if (warp == 7) {
-            warp_gates(gt, raw);
-            if (it + 1 < chunks) raw = read_gates(a, seq, start(it + 1), head);
-        }
-        if constexpr (NT == 1) {
-            tc_wait_warp(&bar.rows[st], (it / STAGES) & 1, gone, a.ctl);
+    // Gram: rows 0-63 K K^T, rows 64-127 Q K^T, once the rows are there.
+    auto gram = [&](int it) {
+        const uint32_t rows = sm32 + it % L::KS * L::ROWS;
+        if (NT == 1) {
+            const int left = (int)min((long long)DC, seq.len - chunk_start<BWD>(it, chunks));
             // Rows past a packed sequence's end are another sequence's (past S, TMA fills with zeros).
-            if (a.offsets && seq.len - t0 < DC) {
-                const int left = (int)(seq.len - t0);
+            if (a.offsets && left < DC) {
+                tc_wait_warp(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);
                 const uint32_t z[4] = {0, 0, 0, 0};
                 for (int i = ptid; i < (DC - left) * 8; i += kPrepThreads) {
-                    const uint32_t at = stage + (left + i / 8) * 128 + i % 8 * 16;
-                    for (uint32_t tile = 0; tile < L::T_AT; tile += TILE) st_shared16(at + tile, z);
+                    const uint32_t at = rows + (left + i / 8) * 128 + i % 8 * 16;
+                    for (uint32_t tile = 0; tile < L::ROWS; tile += TILE) st_shared16(at + tile, z);
                 }
+                fence_proxy_async_smem();
+                named_bar_sync(2, kPrepThreads);
             }
         }
-        fence_proxy_async_smem();
-        named_bar_sync(2, kPrepThreads);
-        if (warp == 0 && elect_one()) {   // Gram: rows 0-63 K K^T, rows 64-127 Q K^T
+        if (warp == 0 && elect_one()) {
+            if (NT == 1) tc_wait(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);
             tc_fence_after();
-            const uint64_t kq = smem_desc(stage, 16, 1024);
+            const uint64_t kq = smem_desc(rows, 16, 1024);
             issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());
             mma_commit(&bar.g);
         }
         __syncwarp();
+    };
+    RawGates raw = {};
+    if (warp == 7 && chunks > 0) {
+        warp_gates(gates[0], read_gates(a, seq, chunk_start<BWD>(0, chunks), head));
+        if (chunks > 1) raw = read_gates(a, seq, chunk_start<BWD>(1, chunks), head);
+    }
+    if (NT == 1 && chunks > 0) {
+        named_bar_sync(2, kPrepThreads);
+        gram(0);
+    }
+#pragma unroll 1
+    for (int it = 0; it < chunks; ++it) {
+        const ChunkGates &gt = gates[it & 3];
+        const uint32_t p_at = sm32 + L::P_AT + it % PS * L::P_SIZE;
+        if constexpr (NT == 3) {
+            const long long t0 = chunk_start<BWD>(it, chunks);
+            if (it > 0) tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);   // the rows before are done with
+            if (half == 0) load_rows<T, NT, DK, 128>(sm32, 2 * TILE, L::KQ_TERM, a.k, a.sk, seq, t0, kh, a.Dk, ptid);
+            else load_rows<T, NT, DK, 128>(sm32 + TILE, 2 * TILE, L::KQ_TERM, a.q, a.sq, seq, t0, kh, a.Dk, ptid - 128);
+            load_rows<T, NT, 128, kPrepThreads>(sm32 + L::V_AT, TILE, L::V_TERM, third, st3, seq, t0, head, a.Dv, ptid);
+            fence_proxy_async_smem();
+            named_bar_sync(2, kPrepThreads);
+            gram(it);
+        }
         tc_wait_warp(&bar.g, it & 1, gone, a.ctl);
+        tc_wait_warp(&bar.empty[it % PS], ((it / PS) & 1) ^ 1, gone, a.ctl);   // P
         // A row of the Gram product per thread, the 16-column pieces p % 2 == half, with the
         // decays.  Below the warp's 32-row diagonal block D_ts = exp(G_t - G_31) exp(G_31 - G_s),
         // both at most one: no exp per value.
@@ -479,22 +491,30 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const CUtensorMap 
                         store4(tf + t * FLD + s0 + i, make_float4(x[i] * be.x, x[i + 1] * be.y, x[i + 2] * be.z, x[i + 3] * be.w));
                     }
                 } else {
-                    store_terms<PT>(stage + L::P_AT, t, s0 / 8, x);
-                    store_terms<PT>(stage + L::P_AT, t, s0 / 8 + 1, x + 8);
+                    store_terms<PT>(p_at, t, s0 / 8, x);
+                    store_terms<PT>(p_at, t, s0 / 8 + 1, x + 8);
                 }
             }
         }
         tc_fence_before();
         named_bar_sync(2, kPrepThreads);
-        invert_64(tf, yf, ptid, 2);
-        store_inverse(stage + L::T_AT, tf, ptid);
+        if (it + 1 < chunks) {   // the next chunk's gates and Gram products, under way while this one is inverted
+            if (warp == 7) {
+                warp_gates(gates[(it + 1) & 3], raw);
+                if (it + 2 < chunks) raw = read_gates(a, seq, chunk_start<BWD>(it + 2, chunks), head);
+            }
+            if (NT == 1) gram(it + 1);
+        }
+        invert_64(tf, ptid, 2);
+        if (it > 0) tc_wait_warp(&bar.e, (it - 1) & 1, gone, a.ctl);   // the T before has been used
+        store_inverse(sm32 + L::T_AT, tf, ptid);
         fence_proxy_async_smem();
         named_bar_sync(2, kPrepThreads);
-        if (ptid == 0) mbar_arrive(&bar.full[st]);
+        if (ptid == 0) mbar_arrive(&bar.full);
     }
 }
 
-// Sixteen values of the third tensor for value row dv, from step h on (stage at `sm`).
+// Sixteen values of the third tensor for value row dv, from step h on.
 template <int NT>
 __device__ __forceinline__ void third_column(const unsigned char *tiles, int dv, int h, float *v) {
     const unsigned char *p = tiles + dv / 64 * TILE + dv % 8 * 2 + h * 128;
@@ -506,6 +526,35 @@ __device__ __forceinline__ void third_column(const unsigned char *tiles, int dv,
         for (int j = NT - 1; j >= 0; --j)
             v[i] += __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + j * 2 * TILE + i * 128 + (unit ^ (uint32_t)(i % 8 << 4))));
     }
+}
+
+// Stores sixteen steps of a value column per thread (the lanes of a warp hold 32 columns
+// side by side) to rows `step` apart, as far as `left` goes; `out` points at the thread's own
+// column.  bfloat16: four lanes trade their values first, so that each stores four columns
+// of every fourth step (8 bytes; a 2-byte store per step costs four times the instructions).
+// `in`: the thread's column exists (D is a multiple of 8: for four neighbours alike).
+__device__ __forceinline__ void store_columns(float *out, size_t step, int left, bool in, const float *x) {
+    if (in)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < left) out[i * step] = x[i];
+    __syncwarp();
+}
+__device__ __forceinline__ void store_columns(__nv_bfloat16 *out, size_t step, int left, bool in, const float *x) {
+    const int lane = threadIdx.x % 32, odd = lane & 1, far = lane >> 1 & 1, mine = odd + 2 * far;   // the step of four that this lane stores
+    out += mine * step - lane % 4;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        // Two lanes: the even one gets both columns of steps i and i + 2, the odd one of i + 1 and i + 3.
+        const uint32_t a = pack_bf16(x[i], x[i + 1]), b = pack_bf16(x[i + 2], x[i + 3]);
+        const uint32_t oa = __shfl_xor_sync(0xffffffffu, a, 1), ob = __shfl_xor_sync(0xffffffffu, b, 1);
+        const uint32_t p = odd ? __byte_perm(oa, a, 0x7632) : __byte_perm(a, oa, 0x5410);
+        const uint32_t q = odd ? __byte_perm(ob, b, 0x7632) : __byte_perm(b, ob, 0x5410);
+        // Then pairs of lanes: the first keeps the earlier step, the second the later one.
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, far ? p : q, 2);
+        if (in && i + mine < left) *reinterpret_cast<uint2 *>(out + i * step) = far ? make_uint2(o, q) : make_uint2(p, o);
+    }
+    __syncwarp();
 }
 
 // Three terms of sixteen fp32 values, `term` columns apart, eight columns each.

@@ -101,11 +101,10 @@ size_t seg_floats(const DeltaArgs &a) {   // of seg_m, seg_own and seg_map, one 
     return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * ((size_t)a.Dk * a.Dv * 2 + (size_t)a.Dk * a.Dk) : 0;
 }
 
-// A walk over the chunks, one CTA per (sequence, value head) or segment of one.  fp32
-// inputs take three times the space of K and Q: one stage.
+// A walk over the chunks, one CTA per (sequence, value head) or segment of one.
 template <bool BWD, typename T, int NT>
 int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
-    constexpr int STAGES = NT == 1 ? 2 : 1, PT = BWD || NT == 3 ? 3 : 2;
+    constexpr int PT = BWD || NT == 3 ? 3 : 2, PS = !BWD && NT == 1 ? 2 : 1;
     CUtensorMap maps[3];
     if (NT == 1 && a.B * a.S > 0) {
         const qsh::Strides so = {(long long)(a.S * a.Hv * a.Dv), (long long)a.Hv * a.Dv, a.Dv};
@@ -125,13 +124,13 @@ int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
     };
     auto walk = [&](auto sum, long long grid) {
         constexpr bool SUM = decltype(sum)::value;
-        constexpr size_t small = WalkLayout<NT, 64, STAGES, PT>::BYTES, large = WalkLayout<NT, 128, STAGES, PT>::BYTES;
+        constexpr size_t small = WalkLayout<NT, 64, PT, PS>::BYTES, large = WalkLayout<NT, 128, PT, PS>::BYTES;
         if constexpr (BWD)
-            return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, STAGES, SUM>, small, grid)
-                              : go(delta_chain_tc_kernel<T, NT, 128, STAGES, SUM>, large, grid);
+            return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, SUM>, small, grid)
+                              : go(delta_chain_tc_kernel<T, NT, 128, SUM>, large, grid);
         else
-            return a.Dk <= 64 ? go(delta_fwd_tc_kernel<T, NT, 64, STAGES, SUM>, small, grid)
-                              : go(delta_fwd_tc_kernel<T, NT, 128, STAGES, SUM>, large, grid);
+            return a.Dk <= 64 ? go(delta_fwd_tc_kernel<T, NT, 64, SUM>, small, grid)
+                              : go(delta_fwd_tc_kernel<T, NT, 128, SUM>, large, grid);
     };
     const long long pairs = a.N * a.Hv;
     if (a.segs > 1) {
