@@ -45,6 +45,38 @@ __device__ __forceinline__ void store_quads<2, __nv_bfloat16>(__nv_bfloat16 *p, 
     *reinterpret_cast<uint4 *>(p) = make_uint4(a.x, a.y, b.x, b.y);
 }
 
+// N quaternions as they are in memory: loads that run ahead are kept so, because a
+// conversion right behind a load waits for it.
+template <int N, typename T>
+struct RawQuads {
+    float4 r[N];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = __ldg(reinterpret_cast<const float4 *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float4 *v) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = r[i];
+    }
+};
+template <int N>
+struct RawQuads<N, __nv_bfloat16> {
+    uint2 r[N];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        if constexpr (N == 2) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+            r[0] = make_uint2(v.x, v.y), r[1] = make_uint2(v.z, v.w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+        }
+    }
+    __device__ __forceinline__ void get(float4 *v) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = IoBF16::get(r[i]);
+    }
+};
+
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float load1(const float *p) { return __ldg(p); }

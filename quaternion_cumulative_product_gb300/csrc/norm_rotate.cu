@@ -25,6 +25,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// CTAs per SM of the persistent backward, as many as run at once.  It issues about 330
+// instructions per pair of rows and is bound by that, not by its loads: two CTAs of up
+// to 128 registers (two quaternions per lane) take 82 us on 2 x 4099 rows of 32 + 8
+// heads of 96, three of 80 registers 86 us, four with one quaternion per lane 89 us; a
+// second row read ahead gains nothing.
+constexpr int kBwdCtasPerSm = 2;
+
 struct RotateArgs {
     const void *q, *k, *cum;
     const float *wq, *wk;
@@ -103,25 +110,25 @@ __global__ void __launch_bounds__(kThreads, SINGLE ? 6 : 4) rotate_fwd_kernel(co
     if constexpr (SINGLE) {
         row(xq, a.wq, qo);
         row(xk, a.wk, ko);
-        return;
-    }
-    for (unsigned j = 0; j < a.nq; ++j) {
-        float4 nx[V];
+    } else {
+        for (unsigned j = 0; j < a.nq; ++j) {
+            float4 nx[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) nx[i] = qs::q_zero();
-        if (in && j + 1 < a.nq) qs::load_quads<V>(qp + (j + 1) * a.sq.h, nx);
-        row(xq, a.wq, qo + (size_t)j * a.D);
+            for (int i = 0; i < V; ++i) nx[i] = qs::q_zero();
+            if (in && j + 1 < a.nq) qs::load_quads<V>(qp + (j + 1) * a.sq.h, nx);
+            row(xq, a.wq, qo + (size_t)j * a.D);
 #pragma unroll
-        for (int i = 0; i < V; ++i) xq[i] = nx[i];
-    }
-    for (unsigned j = 0; j < a.nk; ++j) {
-        float4 nx[V];
+            for (int i = 0; i < V; ++i) xq[i] = nx[i];
+        }
+        for (unsigned j = 0; j < a.nk; ++j) {
+            float4 nx[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) nx[i] = qs::q_zero();
-        if (in && j + 1 < a.nk) qs::load_quads<V>(kp + (j + 1) * a.sk.h, nx);
-        row(xk, a.wk, ko + (size_t)j * a.D);
+            for (int i = 0; i < V; ++i) nx[i] = qs::q_zero();
+            if (in && j + 1 < a.nk) qs::load_quads<V>(kp + (j + 1) * a.sk.h, nx);
+            row(xk, a.wk, ko + (size_t)j * a.D);
 #pragma unroll
-        for (int i = 0; i < V; ++i) xk[i] = nx[i];
+            for (int i = 0; i < V; ++i) xk[i] = nx[i];
+        }
     }
 }
 
@@ -130,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, SINGLE ? 6 : 4) rotate_fwd_kernel(co
 // groups up in a fixed order and writes one partial row, and
 // rotate_weights_kernel adds the CTAs' partial rows up.
 template <typename T, typename C, int V, int LANES, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 2) rotate_bwd_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) rotate_bwd_kernel(const RotateArgs a) {
     const unsigned groups = kThreads / LANES;
     const unsigned lane = threadIdx.x % LANES, x0 = lane * V * 4;
     const unsigned rounds = (a.items + gridDim.x * groups - 1) / (gridDim.x * groups);
@@ -160,34 +167,31 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 2) rotate_bwd_kernel(co
             for (int i = 0; i < V; ++i)
                 if (turn[i]) c[i] = qs::load4(cp + 4 * i);
 
+        // Lanes past the head read its start (their values count as zero).
+        const unsigned at = in ? x0 : 0;
         auto rows = [&](const void *x_, const void *dz_, void *dx_, const qsh::Strides &st, unsigned n, const float *w,
                         float4 *dw) {
-            const T *xp = static_cast<const T *>(x_) + b * st.b + s * st.s + (long long)h * n * st.h + x0;
-            const T *zp = static_cast<const T *>(dz_) + (size_t)item * n * a.D + x0;
+            const T *xp = static_cast<const T *>(x_) + b * st.b + s * st.s + (long long)h * n * st.h + at;
+            const T *zp = static_cast<const T *>(dz_) + (size_t)(live ? item : 0) * n * a.D + at;
             T *op = static_cast<T *>(dx_) + (size_t)item * n * a.D + x0;
-            float4 x[V], dz[V];
+            float4 ww[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = dz[i] = qs::q_zero();
-            if (in && n) {
-                qs::load_quads<V>(xp, x);
-                qs::load_quads<V>(zp, dz);
-            }
+            for (int i = 0; i < V; ++i) ww[i] = WEIGHTS && w ? qs::load4(w + at + 4 * i) : make_float4(1.f, 1.f, 1.f, 1.f);
+            qs::RawQuads<V, T> nx, nz;   // the next row, as it is in memory
+            if (n) nx.load(xp), nz.load(zp);
             for (unsigned j = 0; j < n; ++j) {
-                float4 nx[V], nz[V];
+                float4 x[V], dz[V];
+                nx.get(x), nz.get(dz);
+                if (j + 1 < n) nx.load(xp + (j + 1) * st.h), nz.load(zp + (size_t)(j + 1) * a.D);
 #pragma unroll
-                for (int i = 0; i < V; ++i) nx[i] = nz[i] = qs::q_zero();
-                if (in && j + 1 < n) {
-                    qs::load_quads<V>(xp + (j + 1) * st.h, nx);
-                    qs::load_quads<V>(zp + (size_t)(j + 1) * a.D, nz);
-                }
+                for (int i = 0; i < V; ++i)
+                    if (!in) x[i] = dz[i] = qs::q_zero();
                 // <dm, x> and sum x^2 need no r: both sums run in one round of shuffles.
-                float4 dn[V], ww[V];
+                float4 dn[V];
                 float sum = 0.f, mix = 0.f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     dn[i] = turn[i] ? qs::q_mul(c[i], dz[i]) : dz[i];
-                    ww[i] = make_float4(1.f, 1.f, 1.f, 1.f);
-                    if (WEIGHTS && w && in) ww[i] = qs::load4(w + x0 + 4 * i);
                     sum += qs::dot4(x[i], x[i]);
                     mix += qs::dot4(make_float4(dn[i].x * ww[i].x, dn[i].y * ww[i].y, dn[i].z * ww[i].z, dn[i].w * ww[i].w), x[i]);
                 }
@@ -213,11 +217,6 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 4 : 2) rotate_bwd_kernel(co
                                         fmaf(x[i].z, back, dn[i].z * ww[i].z * r), fmaf(x[i].w, back, dn[i].w * ww[i].w * r));
                 }
                 if (in) qs::store_quads<V>(op + (size_t)j * a.D, dx);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    x[i] = nx[i];
-                    dz[i] = nz[i];
-                }
             }
         };
         rows(a.q, a.dqo, a.qo, a.sq, a.nq, a.wq, dwq);
@@ -327,12 +326,6 @@ int launched() {
     return QS_OK;
 }
 
-// CTAs per SM that the persistent backward runs, as many as its registers let run at
-// once.  One quaternion per lane (heads up to 128) keeps it at 64 registers, two take
-// twice that: on 2 x 4099 rows with 32 + 8 heads of 96 the first runs in 60% of the
-// second's time, although its bfloat16 accesses are 8 bytes instead of 16.
-constexpr int bwd_ctas_per_sm(int v) { return v == 1 ? 4 : 2; }
-
 }  // namespace
 
 extern "C" int quat_norm_rotate_fwd(int dtype, int cum_dtype, int norm, float eps, const void *q, const void *k,
@@ -420,13 +413,13 @@ extern "C" int quat_norm_rotate_bwd(int dtype, int cum_dtype, int norm, float ep
     a.S = (unsigned)S, a.H = (unsigned)H, a.J = (unsigned)J, a.D = (unsigned)D;
     a.nq = (unsigned)(Hq / H), a.nk = (unsigned)(Hk / H), a.items = (unsigned)(B * S * H);
     a.eps = eps, a.inv_div = norm == QS_NORM_RMS ? 1.f / (float)D : 1.f;
-    const int v = D > 128 ? 2 : 1, lanes = lanes_of(D, v), groups = kThreads / lanes;
+    const int v = D % 8 == 0 ? 2 : 1, lanes = lanes_of(D, v), groups = kThreads / lanes;
     const unsigned all = (a.items + groups - 1) / groups;
     if (!w_q && !w_k) {
         pick<true, false>(dtype, cum_dtype, v, lanes)<<<all, kThreads, 0, stream>>>(a);
         return launched();
     }
-    const unsigned most = (unsigned)(sms * bwd_ctas_per_sm(v)), grid = all < most ? all : most;
+    const unsigned most = (unsigned)(sms * kBwdCtasPerSm), grid = all < most ? all : most;
     unsigned char *ws = nullptr;
     rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)grid * 2 * D * 4, &ws);
     if (rc != QS_OK) return rc;
