@@ -33,7 +33,7 @@ template <typename T, int NT, int DK, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
-    using L = WalkLayout<NT, DK, 3, 1>;
+    using L = WalkLayout<NT, DK, 3>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024u - smem_addr(raw) % 1024u) % 1024u);
     const uint32_t sm32 = smem_addr(sm);
@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
-    const uint32_t tm = walk_setup<L, 3, 1>(bar, sm32);
+    const uint32_t tm = walk_setup<L>(bar, sm32);
 
     if (wg >= 2) {
         const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
-        walk_prep<T, NT, DK, 3, 1, true>(a, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
+        walk_prep<T, NT, DK, 3, true>(a, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of dM per thread
         const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
@@ -82,28 +82,27 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         };
 
         if (NT == 1 && warp == 0 && elect_one())
-            for (int i = 0; i < 3; ++i) fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, i, chunks, head);
+            for (int i = 0; i < L::KS; ++i) fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, i, chunks, head);
         __syncwarp();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int c = chunks - 1 - it;
-            const uint32_t rows = sm32 + it % L::KS * L::ROWS, tile_t = sm32 + L::T_AT, tile_p = sm32 + L::P_AT;
+            const uint32_t rows = sm32 + it % L::KS * L::ROWS, tile_t = sm32 + L::T_AT + it % L::S * L::SLOT, tile_p = tile_t + L::P_IN;
             const ChunkGates &gt = gates[it & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
-            tc_wait_warp(&bar.full, it & 1, gone, a.ctl);
-            if (NT == 1) tc_wait_warp(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);   // (dO is read by all)
+            if (it > 0) {
+                tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
+                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with (prep waits for these before it fills T)
+                    fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, it - 1 + L::KS, chunks, head);
+                __syncwarp();
+            }
+            tc_wait_warp(&bar.full[it % L::S], (it / L::S) & 1, gone, a.ctl);
+            if (NT == 1) tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);   // (dO is read by all)
             if (warp == 0 && elect_one()) {   // R = dO^T P
                 issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(rows + L::V_AT, TILE, 1024), L::V_TERM,
                                             smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
-                mma_commit(&bar.empty[0]);
             }
             __syncwarp();
-            if (it > 0) {
-                tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
-                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with
-                    fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, it + 2, chunks, head);
-                __syncwarp();
-            }
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (it > 0) add_update(p);
@@ -120,13 +119,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.x);
             }
             __syncwarp();
-            if (!SUM && in) {   // while X is under way
+            auto write_ds = [&](int part) {   // dM', half of it behind each of two products
+                if (SUM) return;
                 float *out = a.ds + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
+                if (in)
 #pragma unroll
-                for (int i = 0; i < HALF; ++i, out += a.Dv)
-                    if (col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
-            }
-            __syncwarp();
+                    for (int i = 0; i < HALF; ++i, out += a.Dv)
+                        if (i / (HALF / 2) == part && col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
+                __syncwarp();
+            };
+            write_ds(0);
             tc_wait_warp(&bar.x, it & 1, gone, a.ctl);
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {
@@ -150,8 +152,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.e);
+                mma_commit(&bar.empty[it % L::S]);
             }
             __syncwarp();
+            write_ds(1);
             tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
             if (wg == 0) {
 #pragma unroll 1

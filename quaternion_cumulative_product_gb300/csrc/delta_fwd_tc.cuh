@@ -47,8 +47,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_fwd_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap vmap) {
     constexpr int PT = NT == 1 ? 2 : 3;   // terms of what only o is made of: bfloat16's own rounding is 2^-9
-    constexpr int PS = NT == 1 ? 2 : 1;
-    using L = WalkLayout<NT, DK, PT, PS>;
+    using L = WalkLayout<NT, DK, PT>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024u - smem_addr(raw) % 1024u) % 1024u);
     const uint32_t sm32 = smem_addr(sm);
@@ -63,10 +62,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
-    const uint32_t tm = walk_setup<L, PT, PS>(bar, sm32);
+    const uint32_t tm = walk_setup<L>(bar, sm32);
 
     if (wg >= 2) {
-        walk_prep<T, NT, DK, PT, PS, false>(a, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
+        walk_prep<T, NT, DK, PT, false>(a, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of the state per thread
         constexpr bool kEarly = NT == 1;         // U has a place of its own: the next chunk need not wait for o
@@ -112,17 +111,17 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         };
 
         if (NT == 1 && warp == 0 && elect_one())
-            for (int i = 0; i < 3; ++i) fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, i, chunks, head);
+            for (int i = 0; i < L::KS; ++i) fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, i, chunks, head);
         __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t rows = sm32 + c % L::KS * L::ROWS, tile_t = sm32 + L::T_AT, tile_p = sm32 + L::P_AT + c % PS * L::P_SIZE;
+            const uint32_t rows = sm32 + c % L::KS * L::ROWS, tile_t = sm32 + L::T_AT + c % L::S * L::SLOT, tile_p = tile_t + L::P_IN;
             const ChunkGates &gt = gates[c & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             if (c > 0) {
                 tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
-                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with
-                    fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, c + 2, chunks, head);
+                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with (prep waits for these before it fills T)
+                    fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, c - 1 + L::KS, chunks, head);
                 __syncwarp();
             }
             if (!SUM && !kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
@@ -134,8 +133,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            tc_wait_warp(&bar.full, c & 1, gone, a.ctl);
-            if (NT == 1) tc_wait_warp(&bar.rows[c % 3], (c / 3) & 1, gone, a.ctl);   // (V is read by all)
+            tc_wait_warp(&bar.full[c % L::S], (c / L::S) & 1, gone, a.ctl);
+            if (NT == 1) tc_wait_warp(&bar.rows[c % L::KS], (c / L::KS) & 1, gone, a.ctl);   // (V is read by all)
             whole = gt.whole;
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
@@ -144,14 +143,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.x);
             }
             __syncwarp();
-            // While X and Y are under way: the state that entered the chunk, and the last chunk's o.
-            if (!SUM && a.carries && in) {
+            // While the products run: the state that entered the chunk (half of it now, half behind
+            // the next product), and the last chunk's o.
+            auto write_carry = [&](int part) {
+                if (SUM || !a.carries) return;
                 float *out = a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
+                if (in)
 #pragma unroll
-                for (int i = 0; i < HALF; ++i, out += a.Dv)
-                    if (col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
-            }
-            __syncwarp();
+                    for (int i = 0; i < HALF; ++i, out += a.Dv)
+                        if (i / (HALF / 2) == part && col0 + i < a.Dk) *out = i % 2 ? m[i / 2].y : m[i / 2].x;
+                __syncwarp();
+            };
+            write_carry(0);
             if (!SUM && c > 0) write_o(c - 1);
             tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
 #pragma unroll 1
@@ -194,6 +197,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     tmem_st16(tl + fwd_tmem::O + h, r);
                 }
             }
+            write_carry(1);
             tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
             const int h0 = wg * 32;
             float2 u[16];   // beta e
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(rows, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
                 mma_commit(&bar.s);
-                if (SUM) mma_commit(&bar.empty[c % PS]);
+                if (SUM) mma_commit(&bar.empty[c % L::S]);
             }
             __syncwarp();
             if (!SUM) {   // U, for o
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                                       smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
                                                       KMajor1(), true);
                     mma_commit(&bar.o);
-                    mma_commit(&bar.empty[c % PS]);
+                    mma_commit(&bar.empty[c % L::S]);
                 }
                 __syncwarp();
             }

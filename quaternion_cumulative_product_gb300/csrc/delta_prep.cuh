@@ -8,10 +8,11 @@
 // twice the corner of a block as -T22 N21 T11.  All in fp32; T and P leave as terms.
 //
 // bfloat16 tensors come by TMA (swizzled boxes of 64 steps x 64 values) into a ring of
-// three chunks that the walk refills, and a chunk's Gram products run while the chunk
-// before is inverted: prep's own time per chunk (the decays and the inverse) is what
-// bounds the walks.  fp32 tensors go through registers, which split them, one chunk at
-// a time: their terms take three times the space.
+// chunks that the walk refills: three for D <= 64, where a chunk's Gram products run while
+// the chunk before is inverted (139 instead of 152 us for a segment walk of 1 x 16384 x 16
+// x 64), two for D = 128 (three leave room for a single T: 390 instead of 356 us at 8 x
+// 4096 x 16 x 128).  fp32 tensors go through registers, which split them, one chunk at a time:
+// their terms take three times the space.
 #pragma once
 
 #include <type_traits>
@@ -272,21 +273,20 @@ struct TmemK {     // 8 columns of a left operand in tensor memory
 
 // Barriers and flags of a walk's CTA.
 struct WalkBars {
-    uint64_t full, empty[2], rows[3], x, e, s, o, g;
+    uint64_t full[2], empty[2], rows[3], x, e, s, o, g;
     uint32_t tmem;
     int gone;
 };
 
 // Shared memory of a walk.  KS chunks of rows: K and Q [term][half of D]{K tile, Q tile},
-// the third tensor [term][half of D]; T [3 terms]; PS times P [PT terms].  T is written
-// after the chunk before has used it; P by turns.
-template <int NT, int DK, int PT, int PS>
+// the third tensor [term][half of D]; S slots of T [3 terms] and P [PT terms].
+template <int NT, int DK, int PT>
 struct WalkLayout {
-    static constexpr int KS = NT == 1 ? 3 : 1;
+    static constexpr int KS = NT == 3 ? 1 : DK == 64 ? 3 : 2, S = NT == 3 ? 1 : 2;
     static constexpr int HALVES = DK / 64;
     static constexpr uint32_t KQ_TERM = HALVES * 2 * TILE, V_AT = NT * KQ_TERM, V_TERM = 2 * TILE, ROWS = V_AT + NT * V_TERM;
-    static constexpr uint32_t T_AT = KS * ROWS, P_AT = T_AT + 3 * TILE, P_SIZE = PT * TILE;
-    static constexpr uint32_t F_AT = P_AT + PS * P_SIZE;
+    static constexpr uint32_t T_AT = KS * ROWS, P_IN = 3 * TILE, SLOT = P_IN + PT * TILE;
+    static constexpr uint32_t F_AT = T_AT + S * SLOT;
     static constexpr uint32_t GATES_AT = F_AT + DC * FLD * 4;
     static constexpr uint32_t BARS_AT = GATES_AT + 4 * sizeof(ChunkGates);
     static constexpr uint32_t NEED = BARS_AT + 256 + 1024;            // + alignment of the tiles to 1024 bytes
@@ -342,17 +342,17 @@ struct WalkRow {
 };
 
 // What a walk's CTA sets up before its roles part; returns the tensor memory's base.
-template <typename L, int PT, int PS>
+template <typename L>
 __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32) {
     if (threadIdx.x == 0) {
-        for (uint64_t *b : {&bar.full, &bar.empty[0], &bar.empty[1], &bar.rows[0], &bar.rows[1], &bar.rows[2], &bar.x, &bar.e, &bar.s,
+        for (uint64_t *b : {&bar.full[0], &bar.full[1], &bar.empty[0], &bar.empty[1], &bar.rows[0], &bar.rows[1], &bar.rows[2], &bar.x, &bar.e, &bar.s,
                             &bar.o, &bar.g})
             mbar_init(b, 1);
         *reinterpret_cast<volatile int *>(&bar.gone) = 0;
         fence_mbar_init();
     }
     // T and P are zero above the diagonal blocks, where prep never writes.
-    for (uint32_t i = threadIdx.x; i < (3 + PS * PT) * TILE / 16; i += kWalkThreads) {
+    for (uint32_t i = threadIdx.x; i < L::S * L::SLOT / 16; i += kWalkThreads) {
         const uint32_t z[4] = {0, 0, 0, 0};
         st_shared16(sm32 + L::T_AT + i * 16, z);
     }
@@ -370,13 +370,13 @@ __device__ __forceinline__ long long chunk_start(int it, int chunks) {
 }
 
 // Sends for the rows of the it-th chunk (bfloat16); one thread of the walk, once the
-// chunk three before is done with.
+// chunk KS before is done with.
 template <typename L, bool BWD>
 __device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
                                            WalkBars &bar, unsigned char *sm, const Seq &seq, int it, int chunks, int head) {
     if (it >= chunks) return;
-    unsigned char *dst = sm + it % 3 * L::ROWS;
-    uint64_t *full = &bar.rows[it % 3];
+    unsigned char *dst = sm + it % L::KS * L::ROWS;
+    uint64_t *full = &bar.rows[it % L::KS];
     const int kh = head / (a.Hv / a.Hk), s = (int)(seq.s0 + chunk_start<BWD>(it, chunks)), b = (int)seq.b;
     mbar_arrive_expect_tx(full, (2 * L::HALVES + (a.Dv > 64 ? 2 : 1)) * TILE);
 #pragma unroll
@@ -385,13 +385,22 @@ __device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap
         tma_load_4d(dst + h * 2 * TILE + TILE, qmap, h * 64, kh, s, b, full);
     }
     for (int h = 0; h * 64 < a.Dv; ++h) tma_load_4d(dst + L::V_AT + h * TILE, vmap, h * 64, head, s, b, full);
+    if (L::KS == 2 && it + 1 < chunks) {   // the next ones into L2 meanwhile
+        const int s1 = (int)(seq.s0 + chunk_start<BWD>(it + 1, chunks));
+#pragma unroll
+        for (int h = 0; h < L::HALVES; ++h) {
+            tma_prefetch_4d(kmap, h * 64, kh, s1, b);
+            tma_prefetch_4d(qmap, h * 64, kh, s1, b);
+        }
+        for (int h = 0; h * 64 < a.Dv; ++h) tma_prefetch_4d(vmap, h * 64, head, s1, b);
+    }
 }
 
 // The role of prep's threads (ptid 0 .. 255).  BWD: the backward's order and N.
-template <typename T, int NT, int DK, int PT, int PS, bool BWD>
+template <typename T, int NT, int DK, int PT, bool BWD>
 __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third, const qsh::Strides &st3, WalkBars &bar, unsigned char *sm,
                                           const Seq &seq, int chunks, int head, uint32_t tm, uint32_t gram_at) {
-    using L = WalkLayout<NT, DK, PT, PS>;
+    using L = WalkLayout<NT, DK, PT>;
     const int ptid = threadIdx.x - 256, warp = warp_uniform(ptid / 32), kh = head / (a.Hv / a.Hk), half = ptid / 128;
     const uint32_t sm32 = smem_addr(sm);
     volatile int *gone = &bar.gone;
@@ -405,7 +414,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             const int left = (int)min((long long)DC, seq.len - chunk_start<BWD>(it, chunks));
             // Rows past a packed sequence's end are another sequence's (past S, TMA fills with zeros).
             if (a.offsets && left < DC) {
-                tc_wait_warp(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);
+                tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
                 const uint32_t z[4] = {0, 0, 0, 0};
                 for (int i = ptid; i < (DC - left) * 8; i += kPrepThreads) {
                     const uint32_t at = rows + (left + i / 8) * 128 + i % 8 * 16;
@@ -416,7 +425,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             }
         }
         if (warp == 0 && elect_one()) {
-            if (NT == 1) tc_wait(&bar.rows[it % 3], (it / 3) & 1, gone, a.ctl);
+            if (NT == 1) tc_wait(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
             tc_fence_after();
             const uint64_t kq = smem_desc(rows, 16, 1024);
             issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());
@@ -436,7 +445,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
 #pragma unroll 1
     for (int it = 0; it < chunks; ++it) {
         const ChunkGates &gt = gates[it & 3];
-        const uint32_t p_at = sm32 + L::P_AT + it % PS * L::P_SIZE;
+        const uint32_t slot = sm32 + L::T_AT + it % L::S * L::SLOT, p_at = slot + L::P_IN;
         if constexpr (NT == 3) {
             const long long t0 = chunk_start<BWD>(it, chunks);
             if (it > 0) tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);   // the rows before are done with
@@ -448,7 +457,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             gram(it);
         }
         tc_wait_warp(&bar.g, it & 1, gone, a.ctl);
-        tc_wait_warp(&bar.empty[it % PS], ((it / PS) & 1) ^ 1, gone, a.ctl);   // P
+        tc_wait_warp(&bar.empty[it % L::S], ((it / L::S) & 1) ^ 1, gone, a.ctl);   // the slot of T and P
         // A row of the Gram product per thread, the 16-column pieces p % 2 == half, with the
         // decays.  Below the warp's 32-row diagonal block D_ts = exp(G_t - G_31) exp(G_31 - G_s),
         // both at most one: no exp per value.
@@ -503,14 +512,15 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
                 warp_gates(gates[(it + 1) & 3], raw);
                 if (it + 2 < chunks) raw = read_gates(a, seq, chunk_start<BWD>(it + 2, chunks), head);
             }
-            if (NT == 1) gram(it + 1);
+            if (L::KS > 2) gram(it + 1);
         }
         invert_64(tf, ptid, 2);
-        if (it > 0) tc_wait_warp(&bar.e, (it - 1) & 1, gone, a.ctl);   // the T before has been used
-        store_inverse(sm32 + L::T_AT, tf, ptid);
+        store_inverse(slot, tf, ptid);
         fence_proxy_async_smem();
         named_bar_sync(2, kPrepThreads);
-        if (ptid == 0) mbar_arrive(&bar.full);
+        if (ptid == 0) mbar_arrive(&bar.full[it % L::S]);
+        __syncwarp();
+        if (L::KS == 2 && it + 1 < chunks) gram(it + 1);   // (its rows come only once the walk is a chunk further)
     }
 }
 

@@ -104,7 +104,7 @@ size_t seg_floats(const DeltaArgs &a) {   // of seg_m, seg_own and seg_map, one 
 // A walk over the chunks, one CTA per (sequence, value head) or segment of one.
 template <bool BWD, typename T, int NT>
 int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
-    constexpr int PT = BWD || NT == 3 ? 3 : 2, PS = !BWD && NT == 1 ? 2 : 1;
+    constexpr int PT = BWD || NT == 3 ? 3 : 2;
     CUtensorMap maps[3];
     if (NT == 1 && a.B * a.S > 0) {
         const qsh::Strides so = {(long long)(a.S * a.Hv * a.Dv), (long long)a.Hv * a.Dv, a.Dv};
@@ -124,7 +124,7 @@ int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
     };
     auto walk = [&](auto sum, long long grid) {
         constexpr bool SUM = decltype(sum)::value;
-        constexpr size_t small = WalkLayout<NT, 64, PT, PS>::BYTES, large = WalkLayout<NT, 128, PT, PS>::BYTES;
+        constexpr size_t small = WalkLayout<NT, 64, PT>::BYTES, large = WalkLayout<NT, 128, PT>::BYTES;
         if constexpr (BWD)
             return a.Dk <= 64 ? go(delta_chain_tc_kernel<T, NT, 64, SUM>, small, grid)
                               : go(delta_chain_tc_kernel<T, NT, 128, SUM>, large, grid);
