@@ -65,7 +65,7 @@ constexpr uint32_t I = 0, J = 128;   // over A and S
 }  // namespace bwd_tmem
 
 struct ChunkBars {
-    uint64_t m, s, e, r;
+    uint64_t m, s, e, r, drain;
     uint32_t tmem;
     int gone;
 };
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     const int dvh = a.Dv <= 64 ? 1 : 2;                 // halves of dv in use
 
     if (threadIdx.x == 0) {
-        for (uint64_t *b : {&bar.m, &bar.s, &bar.e, &bar.r}) mbar_init(b, 1);
+        for (uint64_t *b : {&bar.m, &bar.s, &bar.e, &bar.r, &bar.drain}) mbar_init(b, 1);
         *gone = 0;
         fence_mbar_init();
     }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         put_state(sm32 + L::DM_AT, dm, 0);
         fence_proxy_async_smem();
         __syncthreads();
-        if (warp == 0 && elect_one()) {
+        if (warp == 0 && elect_one() && !*gone) {
             tc_fence_after();
             issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 0, dvh, false);
             issue_a(tm + bwd_tmem::S, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, dvh, false);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             put_state(sm32 + L::M_AT, m, round);
             fence_proxy_async_smem();
             __syncthreads();
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, round * 4, min(dvh, L::SH), round > 0);
                 if (round + 1 < rounds) mma_commit(&bar.m);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     };
     uint32_t e_phase = 0;
     if (L::BOTH) {
-        if (warp == 0 && elect_one()) issue_c(0, dvh);
+        if (warp == 0 && elect_one() && !*gone) issue_c(0, dvh);
         __syncwarp();
         tc_wait_warp(&bar.s, 0, gone, a.ctl);
     } else {
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             put_state(sm32 + L::DM_AT, dm, round);
             fence_proxy_async_smem();
             __syncthreads();
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_c(round, min(dvh, L::SH));
             }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && elect_one() && !*gone) {
         tc_fence_after();
         // I: rows of K are the K dimension.  J: [X;Y]'s columns in rows 64 .. 127.
         issue_ss<CT, NT, CT - 1, 4>(tm + bwd_tmem::I, smem_desc(sm32 + L::M_AT, 16, 1024), 2 * TILE,
@@ -431,6 +431,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             if (2 * lane + i < left)
                 store_any(a.dg, a.gate16, (row0 + 2 * lane + i) * a.Hv + head, run + tail - (i ? d[0] : 0.f));
     }
+    if (warp == 0 && elect_one() && *gone) drain_products(&bar.drain, a.ctl);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

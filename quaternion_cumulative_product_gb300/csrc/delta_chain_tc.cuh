@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
             tc_wait_warp(&bar.full[it % L::S], (it / L::S) & 1, gone, a.ctl);
             if (NT == 1) tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);   // (dO is read by all)
-            if (warp == 0 && elect_one()) {   // R = dO^T P
+            if (warp == 0 && elect_one() && !*gone) {   // R = dO^T P
                 issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(rows + L::V_AT, TILE, 1024), L::V_TERM,
                                             smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
             }
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, 64), TmemK(), KMajor());
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64, false, true), TmemK(), MNMajor());
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 const uint32_t id = mma_desc(128, DK, false, true);
                 issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP, 32, smem_desc(rows + TILE, 2 * TILE, 1024), L::KQ_TERM,
@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.d_init[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;
+        if (warp == 0 && elect_one() && *gone) drain_walk<L>(bar, a.ctl);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();

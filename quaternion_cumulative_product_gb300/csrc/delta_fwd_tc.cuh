@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tc_wait_warp(&bar.full[c % L::S], (c / L::S) & 1, gone, a.ctl);
             if (NT == 1) tc_wait_warp(&bar.rows[c % L::KS], (c / L::KS) & 1, gone, a.ctl);   // (V is read by all)
             whole = gt.whole;
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, SUM ? 64 : 128), TmemK(), KMajor());
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64), TmemK(), KMajor1());
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one()) {
+            if (warp == 0 && elect_one() && !*gone) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(rows, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_sync(1, 256);
-                if (warp == 0 && elect_one()) {
+                if (warp == 0 && elect_one() && !*gone) {
                     tc_fence_after();
                     issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
                                                       smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.fin[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;
+        if (warp == 0 && elect_one() && *gone) drain_walk<L>(bar, a.ctl);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();

@@ -273,9 +273,9 @@ struct TmemK {     // 8 columns of a left operand in tensor memory
 
 // Barriers and flags of a walk's CTA.
 struct WalkBars {
-    uint64_t full[2], empty[2], rows[3], x, e, s, o, g;
+    uint64_t full[2], empty[2], rows[3], x, e, s, o, g, drain[2];
     uint32_t tmem;
-    int gone;
+    int gone, fetched;   // chunks whose rows have been sent for
 };
 
 // Shared memory of a walk.  KS chunks of rows: K and Q [term][half of D]{K tile, Q tile},
@@ -346,9 +346,10 @@ template <typename L>
 __device__ __forceinline__ uint32_t walk_setup(WalkBars &bar, uint32_t sm32) {
     if (threadIdx.x == 0) {
         for (uint64_t *b : {&bar.full[0], &bar.full[1], &bar.empty[0], &bar.empty[1], &bar.rows[0], &bar.rows[1], &bar.rows[2], &bar.x, &bar.e, &bar.s,
-                            &bar.o, &bar.g})
+                            &bar.o, &bar.g, &bar.drain[0], &bar.drain[1]})
             mbar_init(b, 1);
         *reinterpret_cast<volatile int *>(&bar.gone) = 0;
+        bar.fetched = 0;
         fence_mbar_init();
     }
     // T and P are zero above the diagonal blocks, where prep never writes.
@@ -374,11 +375,13 @@ __device__ __forceinline__ long long chunk_start(int it, int chunks) {
 template <typename L, bool BWD>
 __device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
                                            WalkBars &bar, unsigned char *sm, const Seq &seq, int it, int chunks, int head) {
-    if (it >= chunks) return;
+    if (it >= chunks || *reinterpret_cast<volatile int *>(&bar.gone)) return;
+    bar.fetched = it + 1;
     unsigned char *dst = sm + it % L::KS * L::ROWS;
     uint64_t *full = &bar.rows[it % L::KS];
     const int kh = head / (a.Hv / a.Hk), s = (int)(seq.s0 + chunk_start<BWD>(it, chunks)), b = (int)seq.b;
-    mbar_arrive_expect_tx(full, (2 * L::HALVES + (a.Dv > 64 ? 2 : 1)) * TILE);
+    // (The test hook makes CTA `stall_tile` expect 16 bytes that never come.)
+    mbar_arrive_expect_tx(full, (2 * L::HALVES + (a.Dv > 64 ? 2 : 1)) * TILE + ((int)blockIdx.x == a.ctl.stall_tile ? 16 : 0));
 #pragma unroll
     for (int h = 0; h < L::HALVES; ++h) {
         tma_load_4d(dst + h * 2 * TILE, kmap, h * 64, kh, s, b, full);
@@ -394,6 +397,15 @@ __device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap
         }
         for (int h = 0; h * 64 < a.Dv; ++h) tma_prefetch_4d(vmap, h * 64, head, s1, b);
     }
+}
+
+// End of a walk that gave up: the thread that issued the walk's products and copies waits
+// for those in flight.
+template <typename L>
+__device__ __forceinline__ void drain_walk(WalkBars &bar, const Control &ctl) {
+    drain_products(&bar.drain[0], ctl);
+    if (L::KS > 1)
+        for (int i = max(0, bar.fetched - L::KS); i < bar.fetched; ++i) drain_wait(&bar.rows[i % L::KS], (i / L::KS) & 1, ctl);
 }
 
 // The role of prep's threads (ptid 0 .. 255).  BWD: the backward's order and N.
@@ -427,9 +439,11 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
         if (warp == 0 && elect_one()) {
             if (NT == 1) tc_wait(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
             tc_fence_after();
-            const uint64_t kq = smem_desc(rows, 16, 1024);
-            issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());
-            mma_commit(&bar.g);
+            if (!*gone) {
+                const uint64_t kq = smem_desc(rows, 16, 1024);
+                issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());
+                mma_commit(&bar.g);
+            }
         }
         __syncwarp();
     };
@@ -522,6 +536,8 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
         __syncwarp();
         if (L::KS == 2 && it + 1 < chunks) gram(it + 1);   // (its rows come only once the walk is a chunk further)
     }
+    if (warp == 0 && elect_one() && *gone) drain_products(&bar.drain[1], a.ctl);
+    __syncwarp();
 }
 
 // Sixteen values of the third tensor for value row dv, from step h on.

@@ -239,7 +239,7 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + seg_floats(a) * 4, &ws);
     if (wc != QS_OK) return wc;
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
-    a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     return dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1>(a, seg, stream) : launch_walks<false, float, 3>(a, seg, stream);
 }
 
@@ -286,7 +286,7 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     unsigned char *p = ws + sizeof(WsHeader);
     a.ds = reinterpret_cast<float *>(p), a.w = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + nds + nw), a.dkh = reinterpret_cast<float *>(p + nds + nw + nh);
-    a.ctl = {reinterpret_cast<WsHeader *>(ws), -1, qsh::timeout_ns()};
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(p + nds + nw + 2 * nh);
     rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1>(a, seg, stream) : launch_walks<true, float, 3>(a, seg, stream);
     if (rc != QS_OK || !some) return rc;

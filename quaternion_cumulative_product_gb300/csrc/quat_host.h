@@ -20,8 +20,9 @@ QS_HIDDEN int device(int *dev, int *sms);
 // qs::WsHeader, which the caller must leave in place.
 QS_HIDDEN int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base);
 
-// Limit of every device-side wait, in nanoseconds.
+// Limit of every device-side wait, in nanoseconds; the CTA that the test hook stalls (-1: none).
 QS_HIDDEN unsigned long long timeout_ns();
+QS_HIDDEN int stall_tile();
 
 inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     if (!a || !b || na == 0 || nb == 0) return false;

@@ -1984,6 +1984,8 @@ int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base) {
 
 unsigned long long timeout_ns() { return g_timeout_ns; }
 
+int stall_tile() { return g_stall_tile; }
+
 int head_map(CUtensorMap *map, const void *p, const Strides &t, int64_t B, int64_t S, int64_t H, int64_t D) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return QS_ERR_CUDA;

@@ -181,9 +181,12 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gm
 
 // ---------------------------------------------------------------------------
 // Waits.  Bounded: a wait that runs out records the error and raises the CTA's
-// `gone` flag, after which no wait of the CTA blocks; the CTA then runs to its
-// end on whatever it holds, frees its tensor memory and returns (its outputs are
-// invalid, and quat_cumprod_status reports QS_ERR_TIMEOUT).
+// `gone` flag.  From then on no wait of the CTA blocks, and its issuing threads send
+// no more products or copies (a copy would arrive on a barrier that still waits for
+// the last one); all threads run on to the CTA's end, through the same barriers, on
+// whatever they hold.  There the issuing threads wait for what is still in flight
+// (drain_*, again with a limit) before the tensor memory is freed.  The outputs are then
+// invalid, and quat_cumprod_status reports QS_ERR_TIMEOUT.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tc_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
     if (mbar_try_wait(bar, parity)) return;
@@ -196,6 +199,19 @@ __device__ __forceinline__ void tc_wait(uint64_t *bar, uint32_t parity, volatile
             return;
         }
     }
+}
+
+// Waits for a phase whatever the flag says, up to the limit.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, const Control &ctl) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 <= ctl.timeout_ns) {
+    }
+}
+
+// The thread that issued the products waits for them on a barrier of its own.
+__device__ __forceinline__ void drain_products(uint64_t *bar, const Control &ctl) {
+    mma_commit(bar);
+    drain_wait(bar, 0, ctl);
 }
 
 // The same for a whole warp, converged afterwards (tensor-memory loads and stores

@@ -387,3 +387,94 @@ def test_zero_sizes(torch):
     w = torch.ones(8, device="cuda")
     d = qs.quat_norm_rotate_bwd(e(1, 0, 2, 8), e(1, 0, 2, 8), e(1, 0, 2, 2, 4), q, k, w, w)
     assert (d[3] == 0).all() and (d[4] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# Autograd, the layer, failures.
+# ---------------------------------------------------------------------------
+def test_autograd_chain(torch):
+    """scan -> rotation -> delta rule through autograd equals the formulas chained by hand."""
+    from quaternion_cumulative_product_gb300 import autograd as ag
+    B, S, H, Hv, D = 1, 70, 2, 4, 64
+    x = delta_inputs(torch, B, S, H, Hv, D, D, "f32", "f32", seed=21)
+    turn = torch.randn(B, S, H, D // 4, 4, device="cuda")
+    turn = turn / turn.norm(dim=-1, keepdim=True)
+    start = turn[:, 0].clone()
+    w = 1 + 0.1 * torch.randn(D, device="cuda")
+    leaves = [t.clone().requires_grad_() for t in (x["q"], x["k"], x["v"], x["g"], x["beta"], x["init"], turn, start, w)]
+    q, k, v, g, beta, init, tu, st, ww = leaves
+    cum = ag.quat_cumprod(tu, st)
+    qo, ko = ag.quat_norm_rotate(q, k, cum, ww, None, norm="l2")
+    o, fin = ag.quat_delta(qo, ko, v, g, beta, init)
+    got = torch.autograd.grad([o, fin], leaves, [x["d_o"], x["d_final"]])
+    n = [wide(t) for t in (x["q"], x["k"], x["v"], x["g"], x["beta"], x["init"], turn, start, w)]
+    c = wide(cum)
+    zq, zk = ref.norm_rotate(n[0], c, n[8], "l2", 1e-6), ref.norm_rotate(n[1], c, None, "l2", 1e-6)
+    d = ref.delta_grad(zq[0], zk[0], n[2][0], n[3][0], n[4][0], n[5][0], D ** -0.5, wide(x["d_o"])[0], wide(x["d_final"])[0])
+    dq, dcq, dw = ref.norm_rotate_grad(n[0], c, n[8], "l2", 1e-6, d[0][None])
+    dk, dck, _ = ref.norm_rotate_grad(n[1], c, None, "l2", 1e-6, d[1][None])
+    import oracle
+    d_turn, d_start = oracle.bwd(n[6], n[7], dcq + dck)
+    # Three operators of the tolerance above and the scan's 1e-4 in a row.
+    for a, b in zip(got, (dq, dk, d[2][None], d[3][None], d[4][None], d[5][None], d_turn, d_start, dw)):
+        assert off(a, b) <= 1e-4 + 3 * TOL["f32"]
+    with torch.no_grad():
+        o2, fin2 = ag.quat_delta(qo, ko, v, g, beta, init)
+    assert torch.equal(o, o2) and torch.equal(fin, fin2)
+
+
+def test_layer_prefill_and_tokens(torch):
+    """The layer's prefill in two parts, then single tokens, gives what one pass over the whole sequence gives."""
+    from quaternion_cumulative_product_gb300.layer import QuatDeltaMixer
+    torch.manual_seed(5)
+    layer = QuatDeltaMixer(96, 2, 64, groups=2, dtype=torch.float32)
+    x = torch.randn(3, 90, 96, device="cuda")
+    with torch.no_grad():
+        whole, end = layer(x)
+        first, cache = layer(x[:, :70])
+        second, cache = layer(x[:, 70:85], cache)
+        tokens = [layer.step(x[:, t : t + 1], cache) for t in range(85, 90)]
+    again = torch.cat([first, second, *tokens], 1)
+    scale = whole.abs().max()
+    assert (again - whole).abs().max() <= 1e-4 * scale   # the scan's tolerance
+    assert (cache.state - end.state).abs().max() <= 1e-4 * end.state.abs().max()
+
+
+def test_layer_learns(torch):
+    from quaternion_cumulative_product_gb300.layer import QuatDeltaMixer
+    torch.manual_seed(6)
+    layer = QuatDeltaMixer(64, 2, 32, groups=1)
+    x = torch.randn(4, 80, 64, device="cuda").bfloat16()
+    want = torch.roll(x, 1, 1)
+    opt = torch.optim.Adam(layer.parameters(), lr=3e-3)
+    losses = []
+    for _ in range(30):
+        loss = (layer(x)[0].float() - want.float()).square().mean()
+        opt.zero_grad()
+        loss.backward()
+        assert all(p.grad is not None and torch.isfinite(p.grad).all() for p in layer.parameters())
+        opt.step()
+        losses.append(loss.item())
+    assert losses[-1] < 0.8 * losses[0]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_delta_stall_is_reported(torch, D):
+    """Rows that never arrive: every wait runs out its limit, the call reports it, and the next one is clean."""
+    lib = qs.load_library()
+    x = delta_inputs(torch, 2, 200, 1, 2, D, D, "bf16", "f32", seed=31)
+    five = [x[n] for n in FIVE]
+    o, fin, carries, errors = qs.quat_delta_fwd_carries(*five, x["init"])
+    try:
+        lib.quat_cumprod_debug_set_timeout_ns(20_000_000)
+        lib.quat_cumprod_debug_stall_tile(1)
+        qs.quat_delta_fwd(*five, x["init"])
+        assert qs.quat_cumprod_status() == qs.QS_ERR_TIMEOUT
+        qs.quat_delta_bwd(*five, carries, errors, x["d_o"], x["d_final"])
+        assert qs.quat_cumprod_status() == qs.QS_ERR_TIMEOUT
+    finally:
+        lib.quat_cumprod_debug_stall_tile(-1)
+        lib.quat_cumprod_debug_set_timeout_ns(0)
+    again = qs.quat_delta_fwd(*five, x["init"])
+    assert qs.quat_cumprod_status() == qs.QS_OK
+    assert torch.equal(again[0], o) and torch.equal(again[1], fin)
