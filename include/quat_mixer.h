@@ -13,6 +13,9 @@
  * quat_cumprod_status(); outputs must not overlap inputs (quat_delta_step's
  * state is updated in place).  Status codes are quat_cumprod.h's.
  *
+ * quat_cumprod_debug_stall_tile(k) makes CTA k of quat_delta_fwd's and _bwd's
+ * bfloat16 walks wait for rows that never come, as it does a tile of the scan.
+ *
  * Element types: QS_F32 or QS_BF16.  All arithmetic, sums, norms and states are
  * fp32; an output in bfloat16 is rounded to nearest even once, when stored.
  *

@@ -1,7 +1,7 @@
 // delta_rule.cu -- the gated delta rule over whole sequences: forward, and
-// backward from the forward's carries and errors.
-#include <cstring>
-
+// backward from the forward's carries and errors.  The kernels are in
+// delta_fwd_tc.cuh (forward walk), delta_chain_tc.cuh (backward: the chain of the
+// states' cotangents) and delta_bwd_tc.cuh (backward: the gradients of each chunk).
 #include "delta_bwd_tc.cuh"
 #include "delta_chain_tc.cuh"
 #include "delta_fwd_tc.cuh"
