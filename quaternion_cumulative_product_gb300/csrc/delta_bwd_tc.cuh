@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     ChunkGates &gt = *reinterpret_cast<ChunkGates *>(sm + L::GATES_AT);
     float *rows = reinterpret_cast<float *>(sm + L::ROWS_AT);   // [4][128] row sums, then 2 x 16 sums of the warps
     volatile int *gone = &bar.gone;
+    bool ok = true;   // none of this thread's waits has run out
 
     const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk);
     Seq seq;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         put_state(sm32 + L::DM_AT, dm, 0);
         fence_proxy_async_smem();
         __syncthreads();
-        if (warp == 0 && elect_one() && !*gone) {
+        if (warp == 0 && elect_one() && ok) {
             tc_fence_after();
             issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, 0, dvh, false);
             issue_a(tm + bwd_tmem::S, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, dvh, false);
@@ -240,11 +241,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     } else {
 #pragma unroll 1
         for (int round = 0; round < rounds; ++round) {
-            if (round) tc_wait_warp(&bar.m, 0, gone, a.ctl);   // the first half of dv is done with
+            if (round) ok &= tc_wait_warp(&bar.m, 0, gone, a.ctl);   // the first half of dv is done with
             put_state(sm32 + L::M_AT, m, round);
             fence_proxy_async_smem();
             __syncthreads();
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, round * 4, min(dvh, L::SH), round > 0);
                 if (round + 1 < rounds) mma_commit(&bar.m);
@@ -283,21 +284,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     };
     uint32_t e_phase = 0;
     if (L::BOTH) {
-        if (warp == 0 && elect_one() && !*gone) issue_c(0, dvh);
+        if (warp == 0 && elect_one() && ok) issue_c(0, dvh);
         __syncwarp();
-        tc_wait_warp(&bar.s, 0, gone, a.ctl);
+        ok &= tc_wait_warp(&bar.s, 0, gone, a.ctl);
     } else {
-        tc_wait_warp(&bar.s, 0, gone, a.ctl);
+        ok &= tc_wait_warp(&bar.s, 0, gone, a.ctl);
 #pragma unroll 1
         for (int round = 0; round < rounds; ++round) {
             if (round) {
-                tc_wait_warp(&bar.e, 0, gone, a.ctl);
+                ok &= tc_wait_warp(&bar.e, 0, gone, a.ctl);
                 e_phase = 1;
             }
             put_state(sm32 + L::DM_AT, dm, round);
             fence_proxy_async_smem();
             __syncthreads();
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_c(round, min(dvh, L::SH));
             }
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             const bool on = s0 + i <= last;
             x[i] = on ? __uint_as_float(g[i]) * (sign * exp2_fast(on ? (mine.hi - o.hi) + (mine.lo - o.lo) : 0.f)) : 0.f;
         }
-        if (!L::BOTH) tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+        if (!L::BOTH) ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             unit_terms<CT>(sm32 + L::M_AT + swizzled(tid, s0 / 8 + i), 2 * TILE, make_float4(x[8 * i], x[8 * i + 1], x[8 * i + 2], x[8 * i + 3]),
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && elect_one() && !*gone) {
+    if (warp == 0 && elect_one() && ok) {
         tc_fence_after();
         // I: rows of K are the K dimension.  J: [X;Y]'s columns in rows 64 .. 127.
         issue_ss<CT, NT, CT - 1, 4>(tm + bwd_tmem::I, smem_desc(sm32 + L::M_AT, 16, 1024), 2 * TILE,
@@ -352,8 +353,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w, f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
         }
     };
-    tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
-    tc_wait_warp(&bar.r, 0, gone, a.ctl);
+    ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+    ok &= tc_wait_warp(&bar.r, 0, gone, a.ctl);
     // dq and dk: rows to tiles in shared memory (every operand is done with), then whole lines out.
     constexpr uint32_t OUT_ROW = DK * 4 + 16;   // padded fp32 rows
     static_assert(L::U_AT + 128 * OUT_ROW <= L::GATES_AT, "the operands' place holds the rows of dq and dk");
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             if (2 * lane + i < left)
                 store_any(a.dg, a.gate16, (row0 + 2 * lane + i) * a.Hv + head, run + tail - (i ? d[0] : 0.f));
     }
-    if (warp == 0 && elect_one() && *gone) drain_products(&bar.drain, a.ctl);
+    if (warp == 0 && elect_one() && (!ok || *gone)) drain_products(&bar.drain, a.ctl);
     __syncwarp();
     tc_fence_before();
     __syncthreads();

@@ -61,8 +61,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const bool in = row.in;
         const size_t state = ((size_t)n * a.Hv + head) * a.Dk * a.Dv + dv, step = (size_t)a.Hv * a.Dv;
         const long long row0 = seq.b * a.S + seq.s0;
+        if (NT == 1 && warp == 0 && elect_one())
+            for (int i = 0; i < L::KS; ++i) fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, i, chunks, head);
+        __syncwarp();
         float2 m[HALF / 2];
         float whole = 0.f;
+        bool ok = true;   // none of this thread's waits has run out
         const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.d_final ? a.d_final + state : nullptr;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
@@ -81,9 +85,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
         };
 
-        if (NT == 1 && warp == 0 && elect_one())
-            for (int i = 0; i < L::KS; ++i) fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, i, chunks, head);
-        __syncwarp();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int c = chunks - 1 - it;
@@ -91,14 +92,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             const ChunkGates &gt = gates[it & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             if (it > 0) {
-                tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
-                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with (prep waits for these before it fills T)
+                ok &= tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);
+                if (NT == 1 && warp == 0 && elect_one() && ok)   // the last chunk's rows are done with (prep waits for these before it fills T)
                     fetch_rows<L, true>(a, &kmap, &qmap, &omap, bar, sm, seq, it - 1 + L::KS, chunks, head);
                 __syncwarp();
             }
-            tc_wait_warp(&bar.full[it % L::S], (it / L::S) & 1, gone, a.ctl);
-            if (NT == 1) tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);   // (dO is read by all)
-            if (warp == 0 && elect_one() && !*gone) {   // R = dO^T P
+            ok &= tc_wait_warp(&bar.full[it % L::S], (it / L::S) & 1, gone, a.ctl);
+            if (NT == 1) ok &= tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);   // (dO is read by all)
+            if (warp == 0 && elect_one() && ok) {   // R = dO^T P
                 issue_ss<NT, 3, 2, DC / 16>(tm + chain_tmem::R, smem_desc(rows + L::V_AT, TILE, 1024), L::V_TERM,
                                             smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64, true, true), MNMajor(), MNMajor());
             }
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, 64), TmemK(), KMajor());
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 __syncwarp();
             };
             write_ds(0);
-            tc_wait_warp(&bar.x, it & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.x, it & 1, gone, a.ctl);
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {
                 uint32_t r[16], y[16];
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64, false, true), TmemK(), MNMajor());
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
             __syncwarp();
             write_ds(1);
-            tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
             if (wg == 0) {
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {   // -exp(G) beta w
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 const uint32_t id = mma_desc(128, DK, false, true);
                 issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP, 32, smem_desc(rows + TILE, 2 * TILE, 1024), L::KQ_TERM,
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
         }
         if (chunks > 0) {
-            tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) add_update(p);
         }
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.d_init[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;
-        if (warp == 0 && elect_one() && *gone) drain_walk<L>(bar, a.ctl);
+        if (warp == 0 && elect_one() && (!ok || *gone)) drain_walk<L>(bar, a.ctl);
         __syncwarp();
     }
     tc_fence_before();

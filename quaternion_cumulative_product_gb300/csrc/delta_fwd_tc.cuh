@@ -75,8 +75,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         const bool in = row.in;
         const size_t state = ((size_t)n * a.Hv + head) * a.Dk * a.Dv + dv, step = (size_t)a.Hv * a.Dv;
         const long long row0 = seq.b * a.S + seq.s0;
+        if (NT == 1 && warp == 0 && elect_one())
+            for (int i = 0; i < L::KS; ++i) fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, i, chunks, head);
+        __syncwarp();
         float2 m[HALF / 2];
         float whole = 0.f;
+        bool ok = true;   // none of this thread's waits has run out
         const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.init ? a.init + state : nullptr;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         };
         // o of chunk c, this warpgroup's half of the steps.
         auto write_o = [&](int c) {
-            tc_wait_warp(&bar.o, c & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.o, c & 1, gone, a.ctl);
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             T *out = static_cast<T *>(a.o) + ((size_t)(row0 + (long long)c * DC + wg * 32) * a.Hv + head) * a.Dv + dv;
 #pragma unroll 1
@@ -110,21 +114,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
         };
 
-        if (NT == 1 && warp == 0 && elect_one())
-            for (int i = 0; i < L::KS; ++i) fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, i, chunks, head);
-        __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const uint32_t rows = sm32 + c % L::KS * L::ROWS, tile_t = sm32 + L::T_AT + c % L::S * L::SLOT, tile_p = tile_t + L::P_IN;
             const ChunkGates &gt = gates[c & 3];
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             if (c > 0) {
-                tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
-                if (NT == 1 && warp == 0 && elect_one())   // the last chunk's rows are done with (prep waits for these before it fills T)
+                ok &= tc_wait_warp(&bar.s, (c - 1) & 1, gone, a.ctl);
+                if (NT == 1 && warp == 0 && elect_one() && ok)   // the last chunk's rows are done with (prep waits for these before it fills T)
                     fetch_rows<L, false>(a, &kmap, &qmap, &vmap, bar, sm, seq, c - 1 + L::KS, chunks, head);
                 __syncwarp();
             }
-            if (!SUM && !kEarly && c > 0) tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
+            if (!SUM && !kEarly && c > 0) ok &= tc_wait_warp(&bar.o, (c - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) {
                 if (c > 0) add_dm(p);
@@ -133,10 +134,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            tc_wait_warp(&bar.full[c % L::S], (c / L::S) & 1, gone, a.ctl);
-            if (NT == 1) tc_wait_warp(&bar.rows[c % L::KS], (c / L::KS) & 1, gone, a.ctl);   // (V is read by all)
+            ok &= tc_wait_warp(&bar.full[c % L::S], (c / L::S) & 1, gone, a.ctl);
+            if (NT == 1) ok &= tc_wait_warp(&bar.rows[c % L::KS], (c / L::KS) & 1, gone, a.ctl);   // (V is read by all)
             whole = gt.whole;
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DK / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, SUM ? 64 : 128), TmemK(), KMajor());
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             };
             write_carry(0);
             if (!SUM && c > 0) write_o(c - 1);
-            tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {   // v - exp(G) X
                 uint32_t r[16];
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, 3, 2, DC / 16>(tm + fwd_tmem::X, tm + fwd_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64), TmemK(), KMajor1());
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
             }
             write_carry(1);
-            tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
             const int h0 = wg * 32;
             float2 u[16];   // beta e
             {
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && !*gone) {
+            if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, NT, 2, DC / 16>(tm + fwd_tmem::D, tm + fwd_tmem::SP + 96, 32, smem_desc(rows, 2 * TILE, 1024), L::KQ_TERM,
                                             mma_desc(128, DK, false, true), TmemK(), MNMajor());
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 named_bar_sync(1, 256);
-                if (warp == 0 && elect_one() && !*gone) {
+                if (warp == 0 && elect_one() && ok) {
                     tc_fence_after();
                     issue_ts<PT, PT, PT - 1, DC / 16>(tm + fwd_tmem::O, tm + (kEarly ? fwd_tmem::X : fwd_tmem::SP), kEarly ? 16 : 32,
                                                       smem_desc(tile_p, 16, 1024), TILE, mma_desc(128, 64), UAt{kEarly},
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
         }
         if (chunks > 0) {
-            tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
+            ok &= tc_wait_warp(&bar.s, (chunks - 1) & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) add_dm(p);
             if (!SUM) write_o(chunks - 1);
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.fin[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;
-        if (warp == 0 && elect_one() && *gone) drain_walk<L>(bar, a.ctl);
+        if (warp == 0 && elect_one() && (!ok || *gone)) drain_walk<L>(bar, a.ctl);
         __syncwarp();
     }
     tc_fence_before();

@@ -375,7 +375,7 @@ __device__ __forceinline__ long long chunk_start(int it, int chunks) {
 template <typename L, bool BWD>
 __device__ __forceinline__ void fetch_rows(const DeltaArgs &a, const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
                                            WalkBars &bar, unsigned char *sm, const Seq &seq, int it, int chunks, int head) {
-    if (it >= chunks || *reinterpret_cast<volatile int *>(&bar.gone)) return;
+    if (it >= chunks) return;
     bar.fetched = it + 1;
     unsigned char *dst = sm + it % L::KS * L::ROWS;
     uint64_t *full = &bar.rows[it % L::KS];
@@ -416,6 +416,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
     const int ptid = threadIdx.x - 256, warp = warp_uniform(ptid / 32), kh = head / (a.Hv / a.Hk), half = ptid / 128;
     const uint32_t sm32 = smem_addr(sm);
     volatile int *gone = &bar.gone;
+    bool ok = true;
     float *tf = reinterpret_cast<float *>(sm + L::F_AT);
     ChunkGates *gates = reinterpret_cast<ChunkGates *>(sm + L::GATES_AT);
     const uint32_t g_at = tm + ((uint32_t)(warp % 4 * 32) << 16) + gram_at;
@@ -426,7 +427,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             const int left = (int)min((long long)DC, seq.len - chunk_start<BWD>(it, chunks));
             // Rows past a packed sequence's end are another sequence's (past S, TMA fills with zeros).
             if (a.offsets && left < DC) {
-                tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
+                ok &= tc_wait_warp(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
                 const uint32_t z[4] = {0, 0, 0, 0};
                 for (int i = ptid; i < (DC - left) * 8; i += kPrepThreads) {
                     const uint32_t at = rows + (left + i / 8) * 128 + i % 8 * 16;
@@ -437,9 +438,9 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             }
         }
         if (warp == 0 && elect_one()) {
-            if (NT == 1) tc_wait(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
+            if (NT == 1) ok &= tc_wait(&bar.rows[it % L::KS], (it / L::KS) & 1, gone, a.ctl);
             tc_fence_after();
-            if (!*gone) {
+            if (ok) {
                 const uint64_t kq = smem_desc(rows, 16, 1024);
                 issue_ss<NT, NT, 2, DK / 16>(tm + gram_at, kq, L::KQ_TERM, kq, L::KQ_TERM, mma_desc(128, 64), KMajor(), KMajor());
                 mma_commit(&bar.g);
@@ -462,7 +463,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
         const uint32_t slot = sm32 + L::T_AT + it % L::S * L::SLOT, p_at = slot + L::P_IN;
         if constexpr (NT == 3) {
             const long long t0 = chunk_start<BWD>(it, chunks);
-            if (it > 0) tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);   // the rows before are done with
+            if (it > 0) ok &= tc_wait_warp(&bar.s, (it - 1) & 1, gone, a.ctl);   // the rows before are done with
             if (half == 0) load_rows<T, NT, DK, 128>(sm32, 2 * TILE, L::KQ_TERM, a.k, a.sk, seq, t0, kh, a.Dk, ptid);
             else load_rows<T, NT, DK, 128>(sm32 + TILE, 2 * TILE, L::KQ_TERM, a.q, a.sq, seq, t0, kh, a.Dk, ptid - 128);
             load_rows<T, NT, 128, kPrepThreads>(sm32 + L::V_AT, TILE, L::V_TERM, third, st3, seq, t0, head, a.Dv, ptid);
@@ -470,8 +471,8 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
             named_bar_sync(2, kPrepThreads);
             gram(it);
         }
-        tc_wait_warp(&bar.g, it & 1, gone, a.ctl);
-        tc_wait_warp(&bar.empty[it % L::S], ((it / L::S) & 1) ^ 1, gone, a.ctl);   // the slot of T and P
+        ok &= tc_wait_warp(&bar.g, it & 1, gone, a.ctl);
+        ok &= tc_wait_warp(&bar.empty[it % L::S], ((it / L::S) & 1) ^ 1, gone, a.ctl);   // the slot of T and P
         // A row of the Gram product per thread, the 16-column pieces p % 2 == half, with the
         // decays.  Below the warp's 32-row diagonal block D_ts = exp(G_t - G_31) exp(G_31 - G_s),
         // both at most one: no exp per value.
@@ -536,7 +537,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
         __syncwarp();
         if (L::KS == 2 && it + 1 < chunks) gram(it + 1);   // (its rows come only once the walk is a chunk further)
     }
-    if (warp == 0 && elect_one() && *gone) drain_products(&bar.drain[1], a.ctl);
+    if (warp == 0 && elect_one() && (!ok || *gone)) drain_products(&bar.drain[1], a.ctl);
     __syncwarp();
 }
 

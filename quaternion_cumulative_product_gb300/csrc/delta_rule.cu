@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const DeltaArgs a, cons
     const int r = threadIdx.x / 2, c = threadIdx.x % 2 * 8, x0 = blockIdx.y * 16 + c;
     const bool in = r < a.Dk && x0 < a.Dv;
     const size_t nh = blockIdx.x, elem = (size_t)r * a.Dv + x0;
+    store4(&m[r][c], q_zero()), store4(&m[r][c + 4], q_zero());   // (rows past Dk stay zero)
     float4 v[2] = {q_zero(), q_zero()};
     if (first && in) {
         const float4 *p = reinterpret_cast<const float4 *>(first + nh * a.Dk * a.Dv + elem);
@@ -51,21 +52,24 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const DeltaArgs a, cons
         }
         if (i + 1 == a.segs) break;
         __syncthreads();
-        store4(&m[r][c], v[0]), store4(&m[r][c + 4], v[1]);
+        if (r < a.Dk) store4(&m[r][c], v[0]), store4(&m[r][c + 4], v[1]);
         __syncthreads();
         v[0] = v[1] = q_zero();
         if (in) {
             const float4 *p = reinterpret_cast<const float4 *>(a.seg_own + at * a.Dk * a.Dv + elem);
             v[0] = __ldg(p), v[1] = __ldg(p + 1);
             const float4 *f = reinterpret_cast<const float4 *>(a.seg_map + (at * a.Dk + r) * a.Dk);
-            for (int j = 0; j < a.Dk; j += 4) {
-                const float4 w4 = __ldg(f + j / 4);
-                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+            for (int j0 = 0; j0 < a.Dk; j0 += 32) {   // eight loads of the map's row at a time (its columns past Dk count as zero)
+                float4 w8[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&m[j + k][c]), y = *reinterpret_cast<const float4 *>(&m[j + k][c + 4]);
-                    v[0] = make_float4(fmaf(w[k], x.x, v[0].x), fmaf(w[k], x.y, v[0].y), fmaf(w[k], x.z, v[0].z), fmaf(w[k], x.w, v[0].w));
-                    v[1] = make_float4(fmaf(w[k], y.x, v[1].x), fmaf(w[k], y.y, v[1].y), fmaf(w[k], y.z, v[1].z), fmaf(w[k], y.w, v[1].w));
+                for (int k = 0; k < 8; ++k) w8[k] = j0 + 4 * k < a.Dk ? __ldg(f + j0 / 4 + k) : q_zero();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float w[4] = {w8[k / 4].x, w8[k / 4].y, w8[k / 4].z, w8[k / 4].w};
+                    const float4 x = *reinterpret_cast<const float4 *>(&m[j0 + k][c]), y = *reinterpret_cast<const float4 *>(&m[j0 + k][c + 4]);
+                    const float f1 = w[k % 4];
+                    v[0] = make_float4(fmaf(f1, x.x, v[0].x), fmaf(f1, x.y, v[0].y), fmaf(f1, x.z, v[0].z), fmaf(f1, x.w, v[0].w));
+                    v[1] = make_float4(fmaf(f1, y.x, v[1].x), fmaf(f1, y.y, v[1].y), fmaf(f1, y.z, v[1].z), fmaf(f1, y.w, v[1].w));
                 }
             }
         }

@@ -174,24 +174,25 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gm
 
 // ---------------------------------------------------------------------------
 // Waits.  Bounded: a wait that runs out records the error and raises the CTA's
-// `gone` flag.  From then on no wait of the CTA blocks, and its issuing threads send
-// no more products or copies (a copy would arrive on a barrier that still waits for
-// the last one); all threads run on to the CTA's end, through the same barriers, on
-// whatever they hold.  There the issuing threads wait for what is still in flight
+// `gone` flag, and from then on no wait of the CTA blocks.  A wait tells whether its phase
+// came; a thread that issues products or copies sends no more once one of its own did
+// not (a copy would arrive on a barrier that still waits for the last one).  All
+// threads run on to the CTA's end, through the same barriers, on whatever they hold.  There the issuing threads wait for what is still in flight
 // (drain_*, again with a limit) before the tensor memory is freed.  The outputs are then
 // invalid, and quat_cumprod_status reports QS_ERR_TIMEOUT.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tc_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
-    if (mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity)) {
-        if (*gone) return;
+        if (*gone) return false;
         if (global_timer_ns() - t0 > ctl.timeout_ns) {
             *gone = 1;
             record_error(ctl.hdr, (int)blockIdx.x);
-            return;
+            return false;
         }
     }
+    return true;
 }
 
 // Waits for a phase whatever the flag says, up to the limit.
@@ -209,10 +210,11 @@ __device__ __forceinline__ void drain_products(uint64_t *bar, const Control &ctl
 
 // The same for a whole warp, converged afterwards (tensor-memory loads and stores
 // want the warp's threads together).
-__device__ __forceinline__ void tc_wait_warp(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
-    tc_wait(bar, parity, gone, ctl);
+__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
+    const bool ok = tc_wait(bar, parity, gone, ctl);
     __syncwarp();
     tc_fence_after();
+    return ok;
 }
 
 }  // namespace qs
