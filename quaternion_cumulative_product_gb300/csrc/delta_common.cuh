@@ -36,6 +36,7 @@
 namespace qs {
 
 constexpr int DC = QS_DELTA_STEPS;   // steps per chunk
+constexpr int kMostOrdered = 128;   // packed sequences that are put in order of length
 
 struct DeltaArgs {
     const void *q, *k, *v, *g, *beta;
@@ -62,6 +63,7 @@ struct DeltaArgs {
     float *seg_own, *seg_map;
     int Hk, Hv, Dk, Dv;
     bool gate16;
+    bool longest_first;   // packed sequences are walked in order of length
     float scale;
     Control ctl;
 };

@@ -305,6 +305,30 @@ struct Walk {
     int head, seg, map_from;
     size_t at;   // (n * Hv + head) * segs + seg
 };
+
+// The sequence of CTA row i where packed sequences are walked longest first: the one that
+// i others come before.  (All threads of the CTA call this.)
+__device__ __forceinline__ unsigned by_length(const DeltaArgs &a, unsigned i) {
+    __shared__ int chunks[kMostOrdered], before[kMostOrdered];
+    __shared__ unsigned mine;
+    const unsigned t = threadIdx.x % kMostOrdered, part = threadIdx.x / kMostOrdered;
+    constexpr unsigned kParts = kWalkThreads / kMostOrdered;
+    if (part == 0) {
+        chunks[t] = t < a.N ? (int)((seq_of(a, t).len + DC - 1) / DC) : -1;
+        before[t] = 0;
+    }
+    __syncthreads();
+    const int c = chunks[t];
+    int n = 0;
+#pragma unroll 8
+    for (unsigned u = part; u < kMostOrdered; u += kParts) n += chunks[u] > c || (chunks[u] == c && u < t);
+    atomicAdd(&before[t], n);   // (whole numbers: their order changes nothing)
+    __syncthreads();
+    if (part == 0 && before[t] == (int)i) mine = t;
+    __syncthreads();
+    return mine;
+}
+
 template <bool SUM, bool BWD>
 __device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
     Walk w;
@@ -323,6 +347,7 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
     w.head = i % a.Hv, i /= a.Hv;
     w.seg = i % segs + (SUM && BWD ? 1 : 0);
     w.n = i / segs;
+    if (!SUM && a.longest_first) w.n = by_length(a, (unsigned)w.n);
     w.at = ((size_t)w.n * a.Hv + w.head) * a.segs + w.seg;
     return w;
 }

@@ -87,8 +87,16 @@ int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 // rule is the cost in chunk steps: waves of CTAs times chunks per segment, a summing
 // walk counted as 0.7 of a real one, a join step as 0.4 of a chunk, the two launches as 3.
 // (1 x 131072 x 16 x 64: 9 segments; 8 x 4096 x 16 x 128 has enough pairs: one.)
+//
+// Packed sequences, whose lengths only the device knows, are walked whole, the longest
+// first where they do not all run at once: a long one that starts last is the call's tail
+// (mean of six draws of lengths, heads of 128, in order and sorted: 17 sequences of 4333
+// steps 122 and 108 us, 64 of 32768 481 and 392, 100 of 65536 838 and 734, 128 of 17000 334
+// and 329).  Sorting costs each CTA about 1 us, which many sequences of under 128 steps,
+// even by themselves, do not win back.
 void cut(DeltaArgs &a, int sms) {
     a.segs = 1, a.seg_chunks = a.NC;
+    a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;
     if (a.offsets || a.NC < 4) return;
     const long long pairs = a.N * a.Hv, kinds = a.Dk <= 64 && a.Dv <= 64 ? 1 : 2;
     double best = (double)a.NC * ((pairs + sms - 1) / sms) * 0.9;   // cut only for a clear gain

@@ -227,6 +227,19 @@ def test_delta_packed(torch, lengths, dt):
     check_delta(x, dt, "f32", offsets=offsets)
 
 
+@pytest.mark.parametrize("N", [80, 128, 129])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_delta_packed_many(torch, N, dt):
+    """More walks than run at once: equal lengths, empty sequences and long ones in any place."""
+    rng = np.random.default_rng(N)
+    lengths = rng.choice([0, 1, 7, 64, 65, 200], N)
+    lengths[[0, N // 2, N - 1]] = [64, 300, 131]
+    lengths[N - 2] += max(0, 130 * N - lengths.sum())
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    x = delta_inputs(torch, 1, int(lengths.sum()), 1, 2, 16, 24, dt, "f32", N=N, seed=N)
+    check_delta(x, dt, "f32", offsets=offsets)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_delta_extreme_gates(torch, dt):
     """Cleared states (-inf), strong and no decay, beta of zero and one, a zero key."""
