@@ -62,6 +62,7 @@ struct DeltaArgs {
     const float *seg_m;
     float *seg_own, *seg_map;
     int Hk, Hv, Dk, Dv;
+    int sms;   // of the device
     bool gate16;
     bool longest_first;   // packed sequences are walked in order of length
     float scale;

@@ -95,7 +95,7 @@ int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 // and 329).  Sorting costs each CTA about 1 us, which many sequences of under 128 steps,
 // even by themselves, do not win back.
 void cut(DeltaArgs &a, int sms) {
-    a.segs = 1, a.seg_chunks = a.NC;
+    a.segs = 1, a.seg_chunks = a.NC, a.sms = sms;
     a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;
     if (a.offsets || a.NC < 4) return;
     const long long pairs = a.N * a.Hv, kinds = a.Dk <= 64 && a.Dv <= 64 ? 1 : 2;
