@@ -27,6 +27,10 @@
 // Bound: the latency of its phases (loads, conversions, five products), one CTA per
 // SM.  Global loads run along the rows (a warp covers whole lines): loads by the
 // thread that owns a row touch 32 lines each, and were half of the kernel's time.
+// Measured at 8 x 4096 x 16 x 128 bfloat16 (8192 CTAs): 732 us with two terms, 868 us with
+// three; of a CTA's 28k clocks about 13k go to the loads and 15k to conversions, products
+// and stores.  2.2 GB, 3.1 TB/s; tensor pipe 21%, issue slots 30%.  M and dM' copied in bulk over
+// the place of their terms, instead of loaded by all threads: 727 us, but 934 with three terms.
 #pragma once
 
 #include "delta_prep.cuh"
@@ -226,6 +230,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
     if (wg == 0 && !keys && live) store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, rows[t]);
 
+    // This warpgroup's quarter of an accumulator's columns: to registers, and added back.
+    auto read_part = [&](uint32_t at, uint32_t *v) {
+#pragma unroll
+        for (int x = 0; x < DK / 4; x += 16) tmem_ld16(tl + at + wg * (DK / 4) + x, v + x);
+        tmem_wait_ld();
+        tc_fence_before();
+    };
+    auto add_part = [&](uint32_t at, const uint32_t *v) {
+#pragma unroll
+        for (int x = 0; x < DK / 4; x += 16) {
+            uint32_t w[16];
+            tmem_ld16(tl + at + wg * (DK / 4) + x, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(v[x + i]));
+            tmem_st8(tl + at + wg * (DK / 4) + x, w);
+            tmem_st8(tl + at + wg * (DK / 4) + x + 8, w + 8);
+        }
+        tmem_wait_st();
+    };
+
     // R and S; then C, dM' beside M or in its place.
     float md = 0.f;
     if (L::BOTH) {
@@ -239,15 +264,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             mma_commit(&bar.s);
         }
     } else {
+        // (A round starts its accumulators anew; the sum over the rounds is taken in registers,
+        // where it rounds once: passes over a full accumulator would cut off its last bit.)
+        uint32_t r0[DK / 4];
 #pragma unroll 1
         for (int round = 0; round < rounds; ++round) {
-            if (round) ok &= tc_wait_warp(&bar.m, 0, gone, a.ctl);   // the first half of dv is done with
+            if (round) {
+                ok &= tc_wait_warp(&bar.m, 0, gone, a.ctl);   // the first half of dv is done with
+                read_part(bwd_tmem::R, r0);
+            }
             put_state(sm32 + L::M_AT, m, round);
             fence_proxy_async_smem();
             __syncthreads();
             if (warp == 0 && elect_one() && ok) {
                 tc_fence_after();
-                issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, round * 4, min(dvh, L::SH), round > 0);
+                issue_a(tm + bwd_tmem::R, sm32 + L::M_AT, L::M_TERM, L::M_HALF, id_dk, round * 4, min(dvh, L::SH), false);
                 if (round + 1 < rounds) mma_commit(&bar.m);
                 else {
                     issue_a(tm + bwd_tmem::S, sm32 + L::U_AT, 2 * TILE, TILE, id_s, 0, dvh, false);
@@ -257,6 +288,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             __syncwarp();
         }
         read_state(a.ds, dm);
+        ok &= tc_wait_warp(&bar.s, 0, gone, a.ctl);
+        if (rounds == 2) add_part(bwd_tmem::R, r0);
     }
     __syncwarp();
 #pragma unroll
@@ -275,7 +308,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
     auto issue_c = [&](int round, int halves) {   // C (+)= U dM'^T, U in rows 64 .. 127
         const uint64_t u = smem_desc(sm32 + L::U_AT - TILE, 16, 1024), d = smem_desc(sm32 + L::DM_AT, 16, 1024);
-        bool add = round > 0;
+        bool add = false;
 #pragma unroll 1
         for (int i = CT - 1; i >= 0; --i)
 #pragma unroll 1
@@ -290,18 +323,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                     }
         mma_commit(&bar.e);
     };
-    uint32_t e_phase = 0;
+    uint32_t e_phase = 0, c0[DK / 4];
     if (L::BOTH) {
         if (warp == 0 && elect_one() && ok) issue_c(0, dvh);
         __syncwarp();
         ok &= tc_wait_warp(&bar.s, 0, gone, a.ctl);
     } else {
-        ok &= tc_wait_warp(&bar.s, 0, gone, a.ctl);
 #pragma unroll 1
         for (int round = 0; round < rounds; ++round) {
             if (round) {
                 ok &= tc_wait_warp(&bar.e, 0, gone, a.ctl);
                 e_phase = 1;
+                read_part(bwd_tmem::C, c0);
             }
             put_state(sm32 + L::DM_AT, dm, round);
             fence_proxy_async_smem();
@@ -330,7 +363,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             const bool on = s0 + i <= last;
             x[i] = on ? __uint_as_float(g[i]) * (sign * exp2_fast(on ? (mine.hi - o.hi) + (mine.lo - o.lo) : 0.f)) : 0.f;
         }
-        if (!L::BOTH) ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+        if (!L::BOTH) {
+            ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+            if (rounds == 2) add_part(bwd_tmem::C, c0);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             unit_terms<CT>(sm32 + L::M_AT + swizzled(tid, s0 / 8 + i), 2 * TILE, make_float4(x[8 * i], x[8 * i + 1], x[8 * i + 2], x[8 * i + 3]),

@@ -239,14 +239,16 @@ __device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint32_t a_term
             }
         }
 }
-// The same with A in tensor memory: terms `a_term` columns apart, K step k at a_at(k).
+// The same with A in tensor memory: terms `a_term` columns apart, K step k at a_at(k).  All
+// pairs of terms, or all but the pair of first terms, or that one.
+enum Pairs { kAllPairs, kSmallPairs, kFirstPair };
 template <int TA, int TB, int LAST, int STEPS, typename Ao, typename Bo>
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t a_term, uint64_t b, uint32_t b_term, uint32_t idesc,
-                                         const Ao &a_at, const Bo &b_at, bool add = false) {
+                                         const Ao &a_at, const Bo &b_at, bool add = false, Pairs pairs = kAllPairs) {
 #pragma unroll 1
-    for (int i = TA - 1; i >= 0; --i)
+    for (int i = pairs == kFirstPair ? 0 : TA - 1; i >= 0; --i)
 #pragma unroll 1
-        for (int j = min(TB - 1, LAST - i); j >= 0; --j) {
+        for (int j = pairs == kFirstPair ? 0 : min(TB - 1, LAST - i); j >= (pairs == kSmallPairs && i == 0 ? 1 : 0); --j) {
             const uint64_t bj = b + ((j * b_term) >> 4);
             const uint32_t ai = a + i * a_term;
 #pragma unroll

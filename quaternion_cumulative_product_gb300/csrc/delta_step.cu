@@ -12,6 +12,11 @@
 // thread.  Splitting the value dimension over CTAs (rather than one CTA per
 // head) is what fills the GPU when there are few sequences; a 32-value row is
 // one full 128-byte line.
+// Measured: 256 sequences x 32 heads x 128 x 128, 9 of them idle, 200 us, 5.2 TB/s (77% of
+// a copy's rate; 105 registers, 15 warps per SM, waiting for the state).  Streaming the state
+// through shared memory with bulk copies took 188 to 236 us depending on the ring, more
+// CTAs per SM 211 to 240 us, whole rows per CTA 255 us.  A call for a single token of one
+// sequence is a launch: 2.8 us on the device.
 #include "mixer_device.cuh"
 #include "quat_host.h"
 #include "quat_mixer.h"
