@@ -87,8 +87,10 @@ int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 // the GPU: a first walk sums every segment but one up as an affine map of its state, the
 // join runs over the segments, and the real walk starts each from its own state.  The
 // rule is the cost in chunk steps: waves of CTAs times chunks per segment, a summing
-// walk counted as 0.7 of a real one, a join step as 0.4 of a chunk, the two launches as 3.
-// (1 x 131072 x 16 x 64: 9 segments; 8 x 4096 x 16 x 128 has enough pairs: one.)
+// walk counted as 0.9 of a real one (139 and 151 us on 1 x 16384 x 16 x 64), a join step as
+// 0.4 of a chunk, the two launches as 3.  (1 x 131072 x 16 x 64: 19 segments, 2.1 instead of
+// 9.8 ms; 1 x 4096 x 48 x 128 whole 363 us, in three segments 419; 8 x 4096 x 16 x 128 has
+// enough pairs: one.)
 //
 // Packed sequences, whose lengths only the device knows, are walked whole, the longest
 // first where they do not all run at once: a long one that starts last is the call's tail
@@ -105,7 +107,7 @@ void cut(DeltaArgs &a, int sms) {
     for (long long want = 2; want <= 64 && want <= a.NC && pairs * want <= 2 * sms; ++want) {
         const long long sc = (a.NC + want - 1) / want, n = (a.NC + sc - 1) / sc;
         if (n < 2) continue;
-        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.7 * (double)((pairs * kinds * (n - 1) + sms - 1) / sms);
+        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.9 * (double)((pairs * kinds * (n - 1) + sms - 1) / sms);
         const double cost = waves * sc + 0.4 * n + 3;
         if (cost < best) best = cost, a.segs = (int)n, a.seg_chunks = sc;
     }
