@@ -16,8 +16,9 @@
  * quat_cumprod_debug_stall_tile(k) makes CTA k of quat_delta_fwd's and _bwd's
  * bfloat16 walks wait for rows that never come, as it does a tile of the scan.
  *
- * Element types: QS_F32 or QS_BF16.  All arithmetic, sums, norms and states are
- * fp32; an output in bfloat16 is rounded to nearest even once, when stored.
+ * Element types: QS_F32 or QS_BF16.  Sums, norms and states are fp32, and products
+ * have fp32 precision, or 16 bits where only bfloat16 outputs are made of them; an
+ * output in bfloat16 is rounded to nearest even once, when stored.
  *
  * Strides: a `strides` argument holds, for each tensor it names, the distances
  * in elements between batch entries, between steps and between heads (three
