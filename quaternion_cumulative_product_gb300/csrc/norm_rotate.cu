@@ -202,8 +202,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) rotate_bwd_kernel(con
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     mix += __shfl_xor_sync(0xffffffffu, mix, o);
                 }
-                const float r = rsqrtf(fmaf(sum, a.inv_div, a.eps));
-                const float back = -r * r * r * mix * a.inv_div;
+                // (A group past the last item has no row: its r would be infinite without eps.  r^3 may be
+                // past fp32 where r^3 <dm, x> x is not: r <dm, x> first.)
+                const float r = live ? rsqrtf(fmaf(sum, a.inv_div, a.eps)) : 0.f;
+                const float back = -(r * (r * (r * mix))) * a.inv_div;
                 float4 dx[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
