@@ -54,7 +54,12 @@
  * which keep no state from one launch to the next (the segmented walks'
  * look-back values are tied to the launch that reads them), so a captured
  * graph may be replayed any number of times; the walks and the
- * short-sequence kernels keep no state either.  Calls on one stream are ordered by the stream; calls on different
+ * short-sequence kernels keep no state either.  A workspace that a capture was
+ * given stays allocated for the life of the process, also when a later call on
+ * the stream outgrows it.  Graphs captured on one stream share that stream's
+ * workspace: replay them one after the other, not at the same time as each
+ * other nor as eager calls on the stream they were captured on.
+ * Calls on one stream are ordered by the stream; calls on different
  * streams use different workspaces and may run concurrently.  A workspace is
  * found by the stream's handle: before destroying a stream, let its work
  * finish, so that a new stream given the same handle cannot meet a launch

@@ -20,7 +20,7 @@ SOURCES = [os.path.join(HERE, "csrc", f) for f in
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("quat_device.cuh", "quat_common.cuh", "quat_tiles.cuh", "quat_chain.cuh", "quat_walk.cuh",
             "quat_segwalk.cuh", "quat_segwalk_ws.cuh", "quat_segwalk_bwd.cuh", "quat_segwalk_tab.cuh",
-            "quat_short.cuh", "quat_host.h", "mixer_device.cuh", "delta_common.cuh", "tensor_core.cuh",
+            "quat_short.cuh", "quat_host.h", "workspace.h", "mixer_device.cuh", "delta_common.cuh", "tensor_core.cuh",
             "delta_prep.cuh", "delta_fwd_tc.cuh", "delta_bwd_tc.cuh", "delta_chain_tc.cuh")]
 DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", f) for f in ("quat_cumprod.h", "quat_mixer.h")]
 LIB = os.path.join(HERE, "libquatscan.so")

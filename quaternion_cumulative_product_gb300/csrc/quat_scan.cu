@@ -62,6 +62,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "quat_cumprod.h"
 #include "quat_chain.cuh"
@@ -72,6 +73,7 @@
 #include "quat_short.cuh"
 #include "quat_tiles.cuh"
 #include "quat_walk.cuh"
+#include "workspace.h"
 
 // ===========================================================================
 // Host side: argument checks, workspace, tensor maps, launches, C ABI.
@@ -462,19 +464,19 @@ struct DevInfo {
 std::map<int, DevInfo> g_dev;
 
 // Library-owned scratch of one (device, stream): status block, then the
-// per-call aggregate and carry arrays.
-struct Workspace {
-    unsigned char *base = nullptr;
-    size_t bytes = 0;
-    uint32_t epoch = 0;   // status words only: last epoch used
-};
-std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
+// per-call aggregate and carry arrays (workspace.h).
+std::map<std::pair<int, uintptr_t>, qsh::Workspace> g_ws;
 // Device -> address of quat_cumprod_bwd_noalloc's fixed scratch array (set up
 // by that call's first use on the device).
 std::map<int, unsigned char *> g_noalloc_ptr;
 // Status words of the chained scan, per (device, stream): an allocation of
 // their own that no other kernel writes, zeroed when allocated.
-std::map<std::pair<int, uintptr_t>, Workspace> g_flags;
+struct StatusWords {
+    unsigned char *base = nullptr;
+    size_t bytes = 0;
+    uint32_t epoch = 0;   // last epoch used
+};
+std::map<std::pair<int, uintptr_t>, StatusWords> g_flags;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -565,45 +567,33 @@ int device_info(DevInfo **out, int *dev_out) {
     return QS_OK;
 }
 
+// The CUDA calls of a workspace (workspace.h): true on success.
+struct ScratchCalls {
+    static bool done(cudaError_t e) {
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess;
+    }
+    static bool capturing(cudaStream_t stream, bool *yes) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        if (!done(cudaStreamIsCapturing(stream, &cs))) return false;
+        *yes = cs != cudaStreamCaptureStatusNone;
+        return true;
+    }
+    static bool synchronize(cudaStream_t stream) { return done(cudaStreamSynchronize(stream)); }
+    static bool allocate(size_t bytes, unsigned char **p) {
+        void *v = nullptr;
+        const bool ok = done(cudaMalloc(&v, bytes));
+        *p = static_cast<unsigned char *>(v);
+        return ok;
+    }
+    static bool clear(unsigned char *p, size_t bytes, cudaStream_t stream) { return done(cudaMemsetAsync(p, 0, bytes, stream)); }
+    static void release(unsigned char *p) { done(cudaFree(p)); }
+};
+
 // Returns the workspace of (device, stream) with at least `need` bytes.
 int ensure_workspace(int dev, cudaStream_t stream, size_t need, unsigned char **out) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
-    if (w.bytes >= need) {
-        *out = w.base;
-        return QS_OK;
-    }
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
-        cudaGetLastError();
-        return QS_ERR_CUDA;
-    }
-    if (cs != cudaStreamCaptureStatusNone) return QS_ERR_NOMEM;
-    if (w.base) {
-        if (cudaStreamSynchronize(stream) != cudaSuccess) {
-            cudaGetLastError();
-            return QS_ERR_CUDA;
-        }
-        cudaFree(w.base);
-        w.base = nullptr;
-        w.bytes = 0;
-    }
-    const size_t bytes = align_up(need + need / 4, 1 << 20);
-    void *p = nullptr;
-    if (cudaMalloc(&p, bytes) != cudaSuccess) {
-        cudaGetLastError();
-        return QS_ERR_NOMEM;
-    }
-    if (cudaMemsetAsync(p, 0, sizeof(qs::WsHeader), stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess) {
-        cudaGetLastError();
-        cudaFree(p);
-        return QS_ERR_CUDA;
-    }
-    w.base = static_cast<unsigned char *>(p);
-    w.bytes = bytes;
-    *out = w.base;
-    return QS_OK;
+    return qsh::ensure<ScratchCalls>(g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}], stream, need, sizeof(qs::WsHeader), out);
 }
 
 // Head of the status-word allocation: the counters of the segmented chained
@@ -722,7 +712,7 @@ int persistent_grid(int dev, const Variant *v, int *grid) {
 // cleared on the stream and the count starts again.
 int chain_flags(int dev, cudaStream_t stream, size_t need, uint32_t **out, uint32_t *epoch) {
     std::lock_guard<std::mutex> lk(g_mu);
-    Workspace &w = g_flags[{dev, reinterpret_cast<uintptr_t>(stream)}];
+    StatusWords &w = g_flags[{dev, reinterpret_cast<uintptr_t>(stream)}];
     if (w.bytes < need) {
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
@@ -1686,15 +1676,19 @@ extern "C" int quat_cumprod_status(void *stream_) {
         cudaGetLastError();
         return QS_ERR_CUDA;
     }
-    // The stream's workspace, and the device's no-alloc scratch (set up by a
-    // quat_cumprod_bwd_noalloc call on this device); neither is allocated here.
-    unsigned char *bases[2] = {nullptr, nullptr};
+    // The stream's workspace (and those it has outgrown, which graphs still use), and the
+    // device's no-alloc scratch (set up by a quat_cumprod_bwd_noalloc call on this device);
+    // none is allocated here.
+    std::vector<unsigned char *> bases;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-        if (it != g_ws.end()) bases[0] = it->second.base;
+        if (it != g_ws.end()) {
+            bases = it->second.kept;
+            bases.push_back(it->second.base);
+        }
         auto na = g_noalloc_ptr.find(dev);
-        if (na != g_noalloc_ptr.end()) bases[1] = na->second;
+        if (na != g_noalloc_ptr.end()) bases.push_back(na->second);
     }
     int status = QS_OK;
     for (unsigned char *base : bases) {

@@ -10,7 +10,7 @@ import pytest
 
 import mixer_reference as ref
 import quaternion_cumulative_product_gb300 as qs
-from test_mixer_gpu import close, rotate_inputs, torch, wide  # noqa: F401  (torch: the fixture)
+from test_mixer_gpu import FIVE, close, delta_inputs, rotate_inputs, torch, wide  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,49 @@ def test_norm_rotate_gradients_without_eps(torch, norm, dims, size):  # noqa: F8
     gk = ref.norm_rotate_grad(n["k"], n["cum"], n["w_k"], norm, 0.0, n["dk"])
     for got, want, what in zip(d, (gq[0], gk[0], gq[1] + gk[1], gq[2], gk[2]), ("d_q", "d_k", "d_cum", "d_w_q", "d_w_k")):
         close(got, want, "f32", what)
+
+
+# ---------------------------------------------------------------------------
+# Scratch shared by the calls of a stream.
+# ---------------------------------------------------------------------------
+def backward_call(torch, S, seed):  # noqa: F811
+    """A delta backward with shared heads and a rotation backward with weights: both hand values over in scratch."""
+    x = delta_inputs(torch, 1, S, 2, 4, 64, 64, "f32", "f32", seed=seed)
+    y = rotate_inputs(torch, 1, S, 2, 4, 2, 64, 16, "f32", "f32", True, seed=seed)
+    five = [x[n] for n in FIVE]
+    _, _, carries, errors = qs.quat_delta_fwd_carries(*five, x["init"])
+
+    def call():
+        return [*qs.quat_delta_bwd(*five, carries, errors, x["d_o"], x["d_final"]),
+                *qs.quat_norm_rotate_bwd(y["q"], y["k"], y["cum"], y["dq"], y["dk"], y["w_q"], y["w_k"])]
+    return call
+
+
+def test_graph_replays_after_its_stream_needed_more(torch):  # noqa: F811
+    """A captured graph keeps its scratch when a larger call on the same stream has grown the stream's."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        small, large = backward_call(torch, 130, 51), backward_call(torch, 9000, 52)
+        want = [t.clone() for t in small()]
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = small()
+    with torch.cuda.stream(s):
+        large()   # more scratch than the first call's
+        second = torch.cuda.CUDAGraph()
+    s.synchronize()
+    with torch.cuda.graph(second, stream=s):
+        large_got = large()
+    with torch.cuda.stream(s):
+        large_want = [t.clone() for t in large()]
+        for t in (*got, *large_got):
+            t.fill_(float("nan"))
+        for g in (graph, second, graph):
+            g.replay()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip(large_got, large_want))
+    with torch.cuda.stream(s):
+        assert qs.quat_cumprod_status() == qs.QS_OK
