@@ -59,7 +59,8 @@
  * the stream outgrows it.  Graphs captured on one stream share that stream's
  * workspace: replay them one after the other, not at the same time as each
  * other nor as eager calls on the stream they were captured on.
- * Calls on one stream are ordered by the stream; calls on different
+ * Calls on one stream are ordered by the stream, whichever host threads make
+ * them (a call's launches are enqueued together); calls on different
  * streams use different workspaces and may run concurrently.  A workspace is
  * found by the stream's handle: before destroying a stream, let its work
  * finish, so that a new stream given the same handle cannot meet a launch

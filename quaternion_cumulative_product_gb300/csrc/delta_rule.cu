@@ -252,7 +252,8 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     unsigned char *ws = nullptr;
     cut(a, sms);
-    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + seg_floats(a) * 4, &ws);
+    qsh::Hold hold;
+    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + seg_floats(a) * 4, &ws, &hold);
     if (wc != QS_OK) return wc;
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
@@ -295,7 +296,8 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     unsigned char *ws = nullptr;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     cut(a, sms);
-    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nds + nw + 2 * nh + seg_floats(a) * 4, &ws);
+    qsh::Hold hold;
+    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nds + nw + 2 * nh + seg_floats(a) * 4, &ws, &hold);
     if (rc != QS_OK) return rc;
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.carries_in = carries, a.errors_in = errors, a.d_o = d_o;
     a.d_final = d_final, a.dq = d_q, a.dk = d_k, a.dv = d_v, a.dg = d_g, a.dbeta = d_beta, a.d_init = d_init;

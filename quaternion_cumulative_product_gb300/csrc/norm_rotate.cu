@@ -425,7 +425,8 @@ extern "C" int quat_norm_rotate_bwd(int dtype, int cum_dtype, int norm, float ep
     }
     const unsigned most = (unsigned)(sms * kBwdCtasPerSm), grid = all < most ? all : most;
     unsigned char *ws = nullptr;
-    rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)grid * 2 * D * 4, &ws);
+    qsh::Hold hold;
+    rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)grid * 2 * D * 4, &ws, &hold);
     if (rc != QS_OK) return rc;
     a.dw_part = reinterpret_cast<float *>(ws + sizeof(qs::WsHeader));
     pick<true, true>(dtype, cum_dtype, v, lanes)<<<grid, kThreads, 0, stream>>>(a);

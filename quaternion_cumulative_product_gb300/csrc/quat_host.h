@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "quat_cumprod.h"
+#include "workspace.h"
 
 #define QS_HIDDEN __attribute__((visibility("hidden")))
 
@@ -17,8 +18,9 @@ namespace qsh {
 QS_HIDDEN int device(int *dev, int *sms);
 
 // The workspace of (device, stream) with at least `need` bytes; it starts with a
-// qs::WsHeader, which the caller must leave in place.
-QS_HIDDEN int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base);
+// qs::WsHeader, which the caller must leave in place.  It is the caller's while `hold` is: until
+// the last launch that uses it is enqueued.
+QS_HIDDEN int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base, Hold *hold);
 
 // Limit of every device-side wait, in nanoseconds; the CTA that the test hook stalls (-1: none).
 QS_HIDDEN unsigned long long timeout_ns();

@@ -463,9 +463,6 @@ struct DevInfo {
 };
 std::map<int, DevInfo> g_dev;
 
-// Library-owned scratch of one (device, stream): status block, then the
-// per-call aggregate and carry arrays (workspace.h).
-std::map<std::pair<int, uintptr_t>, qsh::Workspace> g_ws;
 // Device -> address of quat_cumprod_bwd_noalloc's fixed scratch array (set up
 // by that call's first use on the device).
 std::map<int, unsigned char *> g_noalloc_ptr;
@@ -590,10 +587,14 @@ struct ScratchCalls {
     static void release(unsigned char *p) { done(cudaFree(p)); }
 };
 
-// Returns the workspace of (device, stream) with at least `need` bytes.
-int ensure_workspace(int dev, cudaStream_t stream, size_t need, unsigned char **out) {
-    std::lock_guard<std::mutex> lk(g_mu);
-    return qsh::ensure<ScratchCalls>(g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}], stream, need, sizeof(qs::WsHeader), out);
+// Library-owned scratch of each (device, stream): status block, then the
+// per-call aggregate and carry arrays.
+qsh::Workspaces<ScratchCalls, cudaStream_t> g_ws;
+
+// The workspace of (device, stream) with at least `need` bytes, the caller's while `hold` is.
+// (Taken before g_lbv_launch_mu and g_mu.)
+int ensure_workspace(int dev, cudaStream_t stream, size_t need, unsigned char **out, qsh::Hold *hold) {
+    return g_ws.take(dev, stream, need, sizeof(qs::WsHeader), out, hold);
 }
 
 // Head of the status-word allocation: the counters of the segmented chained
@@ -1165,7 +1166,8 @@ int launch(bool bwd, const void *q, const void *d_cum, void *out, const void *in
     rc = make_plan(bwd, B, S, HJ, di->sms, &pl, mode, bf16, cs != cudaStreamCaptureStatusNone);
     if (rc != QS_OK) return rc;
     unsigned char *ws = nullptr;
-    rc = ensure_workspace(dev, stream, pl.ws_bytes, &ws);
+    qsh::Hold hold;
+    rc = ensure_workspace(dev, stream, pl.ws_bytes, &ws, &hold);
     if (rc != QS_OK) return rc;
     if (pl.v->smax > 0)
         return launch_short(pl, bwd, q, d_cum, out, init, d_init, S, HJ, stream, mode, carries, bf16);
@@ -1679,14 +1681,10 @@ extern "C" int quat_cumprod_status(void *stream_) {
     // The stream's workspace (and those it has outgrown, which graphs still use), and the
     // device's no-alloc scratch (set up by a quat_cumprod_bwd_noalloc call on this device);
     // none is allocated here.
-    std::vector<unsigned char *> bases;
+    qsh::Hold hold;
+    std::vector<unsigned char *> bases = g_ws.bases(dev, stream, &hold);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-        if (it != g_ws.end()) {
-            bases = it->second.kept;
-            bases.push_back(it->second.base);
-        }
         auto na = g_noalloc_ptr.find(dev);
         if (na != g_noalloc_ptr.end()) bases.push_back(na->second);
     }
@@ -1972,8 +1970,8 @@ int device(int *dev, int *sms) {
     return rc;
 }
 
-int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base) {
-    return ensure_workspace(dev, stream, need, base);
+int workspace(int dev, cudaStream_t stream, size_t need, unsigned char **base, Hold *hold) {
+    return ensure_workspace(dev, stream, need, base, hold);
 }
 
 unsigned long long timeout_ns() { return g_timeout_ns; }

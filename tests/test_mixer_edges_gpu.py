@@ -77,3 +77,27 @@ def test_graph_replays_after_its_stream_needed_more(torch):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(large_got, large_want))
     with torch.cuda.stream(s):
         assert qs.quat_cumprod_status() == qs.QS_OK
+
+
+def test_threads_share_a_stream(torch):  # noqa: F811
+    """Host threads whose calls meet on one stream: each gets its own results, whatever the others need of the scratch."""
+    import threading
+    calls = [backward_call(torch, S, 60 + i) for i, S in enumerate((70, 1500, 333))]
+    want = [[t.clone() for t in c()] for c in calls]
+    stream, failed = torch.cuda.Stream(), []   # (a stream without scratch so far)
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                got = calls[i]()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    failed.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed

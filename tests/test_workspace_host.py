@@ -9,10 +9,13 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 FAKE = r"""
+#include <atomic>
+#include <chrono>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <set>
+#include <thread>
 #include "workspace.h"
 #define CHECK(x) do { if (!(x)) { printf("%d: %s\n", __LINE__, #x); return 1; } } while (0)
 struct Gpu {
@@ -77,6 +80,29 @@ CASES = {
         CHECK(ensure<Gpu>(w, 0, 9 * MB, 64, &b) == QS_ERR_NOMEM && !b && !w.base && w.bytes == 0);
         Gpu::full = false;
         CHECK(ensure<Gpu>(w, 0, 1, 64, &b) == QS_OK && b != a && Gpu::live.count(a) && !w.captured);""",
+    # A second thread's call on the stream waits until the first one's launches are enqueued: it
+    # neither comes between them nor frees their scratch.  A call on another stream does not wait.
+    "two threads": """
+        Workspaces<Gpu, int> all;
+        std::atomic<bool> in{false};
+        std::thread second;
+        {
+            Hold hold;
+            CHECK(all.take(0, 1, MB, 64, &a, &hold) == QS_OK && hold.owns_lock());
+            second = std::thread([&] {
+                Hold mine;
+                all.take(0, 1, 50 * MB, 64, &b, &mine);
+                in = true;
+            });
+            Hold other;
+            CHECK(all.take(0, 2, MB, 64, &c, &other) == QS_OK && c != a);
+            std::this_thread::sleep_for(std::chrono::milliseconds(100));
+            CHECK(!in && Gpu::live.count(a));
+        }
+        second.join();
+        Hold last, none;
+        CHECK(in && Gpu::freed.count(a) && all.bases(0, 1, &last)[0] == b && last.owns_lock());
+        CHECK(all.bases(0, 3, &none).empty() && !none.owns_lock());""",
 }
 
 
