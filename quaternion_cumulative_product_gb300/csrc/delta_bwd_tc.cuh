@@ -11,6 +11,7 @@
 //     C = U dM'^T                 the states' part of col (rows 64 .. 127)
 //     I = [X; Y] K                the chunk's part of dq and of row
 //     J = [X; Y]^T [Q; K]         the chunk's part of col
+//     H = [Q; K] K^T              for dg
 //
 // (names as in delta_common.cuh).  I and J have accumulators of their own, and are added
 // to R and C, with the decays of their rows, in registers: adding up on R and C in the
@@ -39,6 +40,16 @@ namespace qs {
 
 constexpr int kChunkThreads = 512;
 
+// Sums in shared memory (floats).
+namespace row_sums {
+constexpr int A = 0;                // [warpgroup][128] a's parts of a query's and a key's row (before that [64] dbeta)
+constexpr int B = A + 4 * 128;      // [warpgroup][64] b's parts
+constexpr int TOTAL = B + 4 * 64;   // [8][64] Z's columns over eight steps each
+constexpr int Z = TOTAL + 8 * 64;   // [2][64] Z's part of dg, by halves of its columns
+constexpr int MD = Z + 2 * 64;      // [16] exp(G_C) <M, dM'> by warps
+constexpr int COUNT = MD + 16;
+}  // namespace row_sums
+
 template <int NT, int CT, int DK>
 struct ChunkLayout {
     static constexpr int HALVES = DK / 64;
@@ -55,7 +66,7 @@ struct ChunkLayout {
     static constexpr uint32_t A_AT = DM_AT;
     static constexpr uint32_t GATES_AT = BOTH ? DM_AT + max2(CT * M_TERM, CT * A_TERM) : M_AT + M_BYTES;
     static constexpr uint32_t ROWS_AT = GATES_AT + sizeof(ChunkGates);
-    static constexpr uint32_t BARS_AT = ROWS_AT + (4 * 128 + 32) * 4;
+    static constexpr uint32_t BARS_AT = ROWS_AT + row_sums::COUNT * 4;
     static constexpr uint32_t NEED = BARS_AT + 256 + 1024;
     static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;     // one CTA per SM: it takes all of the tensor memory
     static_assert(BYTES <= 232448, "227 KB of shared memory");
@@ -67,6 +78,10 @@ constexpr uint32_t S = 192;    // [dO; dV] U^T (64)
 constexpr uint32_t R = 256, C = 384;
 constexpr uint32_t I = 0, J = 128;   // over A and S
 }  // namespace bwd_tmem
+
+// H's columns: beside two terms of A, or over A once that is done with.
+template <int CT>
+constexpr uint32_t kGramAt = CT == 2 ? 128 : 0;
 
 struct ChunkBars {
     uint64_t m, s, e, r, drain;
@@ -96,7 +111,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     const uint32_t sm32 = smem_addr(sm);
     ChunkBars &bar = *reinterpret_cast<ChunkBars *>(sm + L::BARS_AT);
     ChunkGates &gt = *reinterpret_cast<ChunkGates *>(sm + L::GATES_AT);
-    float *rows = reinterpret_cast<float *>(sm + L::ROWS_AT);   // [4][128] row sums, then 2 x 16 sums of the warps
+    float *rows = reinterpret_cast<float *>(sm + L::ROWS_AT);   // row_sums
     volatile int *gone = &bar.gone;
     bool ok = true;   // none of this thread's waits has run out
 
@@ -170,6 +185,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                     }
     };
     const uint32_t id_dk = mma_desc(128, DK), id_s = mma_desc(128, 64);
+    auto issue_h = [&] {
+        issue_ss<NT, NT, 2, DK / 16>(tm + kGramAt<CT>, smem_desc(sm32 + L::QK_AT, 16, 1024), L::QK_TERM,
+                                     smem_desc(sm32 + L::QK_AT + TILE, 16, 1024), L::QK_TERM, id_s, KMajor(), KMajor());
+    };
 
     // Rows: U, [dO; dV] and dbeta = <e, w>, in rounds of SH halves of dv; M alongside.
     const int rounds = (dvh + L::SH - 1) / L::SH;
@@ -223,6 +242,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         }
         if (L::BOTH) put_state(sm32 + L::M_AT, m, 0);   // (elsewhere than the rows on their way)
         tmem_wait_st();
+        if (L::BOTH) fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
     }
@@ -254,6 +274,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     // R and S; then C, dM' beside M or in its place.
     float md = 0.f;
     if (L::BOTH) {
+        if (warp == 0 && elect_one() && ok) {   // (H runs while dM' is converted)
+            tc_fence_after();
+            issue_h();
+        }
+        __syncwarp();
         put_state(sm32 + L::DM_AT, dm, 0);
         fence_proxy_async_smem();
         __syncthreads();
@@ -297,7 +322,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     md *= gt.whole;
 #pragma unroll
     for (int o = 16; o; o /= 2) md += __shfl_xor_sync(0xffffffffu, md, o);
-    if (lane == 0) rows[512 + warp] = md;
+    if (lane == 0) rows[row_sums::MD + warp] = md;
     // The CTAs of a wave run in step: all load, then all compute.  M and dM' of the CTA that
     // likely comes next on this SM go to L2 meanwhile (808 -> 734 us with two terms, 891 -> 872
     // with three; sent for before this CTA's own loads 865, with e's and w's rows 774).
@@ -321,6 +346,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                                d + ((j * L::M_TERM + h * L::M_HALF + k * 32) >> 4), id_dk, add);
                         add = true;
                     }
+        if (!L::BOTH && round + 1 == rounds) issue_h();   // (A is done with: all have waited for R and S)
         mma_commit(&bar.e);
     };
     uint32_t e_phase = 0, c0[DK / 4];
@@ -348,7 +374,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
 
     // X and Y with their decays (16 columns per warpgroup), as tiles over M once its last
-    // reader is done.
+    // reader is done.  Z = X o (Q K^T) + Y o (K K^T) below the diagonal.
+    float z[16];
     {
         const Sum2 mine = gt.sum[t];
         const float sign = keys ? -1.f : a.scale;
@@ -367,6 +394,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
             if (rounds == 2) add_part(bwd_tmem::C, c0);
         }
+        tmem_ld16(tl + kGramAt<CT> + s0, g);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = s0 + i < t ? x[i] * __uint_as_float(g[i]) : 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             unit_terms<CT>(sm32 + L::M_AT + swizzled(tid, s0 / 8 + i), 2 * TILE, make_float4(x[8 * i], x[8 * i + 1], x[8 * i + 2], x[8 * i + 3]),
@@ -386,6 +417,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         mma_commit(&bar.r);
     }
     __syncwarp();
+    // Z's part of dg while the products run: dg_t gathers Z_rs for r >= t > s.  Z goes to U's
+    // place (16-byte units swizzled), a thread takes eight rows of a column and adds them up from below.
+    ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
+    {
+        float *zs = reinterpret_cast<float *>(sm + L::U_AT);
+        static_assert(128 * 64 * 4 <= CT * 2 * TILE, "U's place holds Z's two halves");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store4(zs + tid * 64 + (((wg * 4 + i) ^ (tid & 15)) << 2), make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
+        __syncthreads();
+        const int s = threadIdx.x % 64, part = threadIdx.x / 64;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = part * 8 + j, at = (((s >> 2) ^ (r & 15)) << 2) + (s & 3);
+            v[j] = zs[r * 64 + at] + zs[(64 + r) * 64 + at];
+        }
+#pragma unroll
+        for (int j = 6; j >= 0; --j) v[j] += v[j + 1];
+        rows[row_sums::TOTAL + part * 64 + s] = v[0];
+        __syncthreads();
+        float below = 0.f;
+        for (int q = 7; q > part; --q) below += rows[row_sums::TOTAL + q * 64 + s];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = s < part * 8 + j ? v[j] + below : 0.f;
+        // The warp's 32 columns: each exchange halves the steps that a lane still holds.
+#pragma unroll
+        for (int n = 4, o = 16; n; n /= 2, o /= 2)
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const bool up = lane & o;
+                const float give = up ? v[j] : v[j + n], keep = up ? v[j + n] : v[j];
+                v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if (lane % 4 == 0) rows[row_sums::Z + s / 32 * 64 + part * 8 + lane / 4] = v[0];
+    }
     // Eight values of this thread's row of Q or K, from x0 on.
     auto qk_row = [&](int x0, float *f) {
 #pragma unroll
@@ -397,13 +465,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w, f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
         }
     };
-    ok &= tc_wait_warp(&bar.e, e_phase, gone, a.ctl);
     ok &= tc_wait_warp(&bar.r, 0, gone, a.ctl);
     // dq and dk: rows to tiles in shared memory (every operand is done with), then whole lines out.
     constexpr uint32_t OUT_ROW = DK * 4 + 16;   // padded fp32 rows
     static_assert(L::U_AT + 128 * OUT_ROW <= L::GATES_AT, "the operands' place holds the rows of dq and dk");
     {
-        float sum = 0.f, part = 0.f;   // <q, dq> or <k, row - col>; exp(G_C - G_t) <k_t, dM' u_t>
+        float own = 0.f, part = 0.f;   // a's part of this row, and b's
         const float fr = keys ? -gt.grown[t] : a.scale * gt.grown[t], fc = keys ? gt.left[t] : 0.f;
 #pragma unroll 1
         for (int x0 = wg * DK / 4; x0 < (wg + 1) * DK / 4; x0 += 16) {
@@ -421,21 +488,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
                 qk_row(x0 + 8 * h, f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float w = fmaf(fr, __uint_as_float(r[8 * h + k]), __uint_as_float(i2[8 * h + k]));
+                    const float rs = fr * __uint_as_float(r[8 * h + k]), w = rs + __uint_as_float(i2[8 * h + k]);
                     float cs = 0.f, col = 0.f;   // (a query's rows of C and J hold nothing)
                     if (keys) cs = fc * __uint_as_float(c1[8 * h + k]), col = cs + __uint_as_float(j2[8 * h + k]);
                     part = fmaf(f[k], cs, part);
-                    sum = fmaf(f[k], w - col, sum);
+                    own = fmaf(f[k], rs, own);
                     v[k] = w + col;
                 }
                 store4(out + 8 * h, make_float4(v[0], v[1], v[2], v[3]));
                 store4(out + 8 * h + 4, make_float4(v[4], v[5], v[6], v[7]));
             }
         }
-#pragma unroll
-        for (int o = 16; o; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
-        if (lane == 0) rows[528 + warp] = part;
-        rows[wg * 128 + tid] = sum;
+        rows[row_sums::A + wg * 128 + tid] = own;
+        if (keys) rows[row_sums::B + wg * 64 + t] = part;
     }
     __syncthreads();
     {
@@ -453,28 +518,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             }
         }
     }
-    if (warp == 0) {   // dg: suffix sums of dG, the last step's own part included in all
-        float tail = rows[512 + lane];
+    if (warp == 0) {   // dg: a from the step on, b of the steps before it, Z's part and the state's
+        float whole = lane < 16 ? rows[row_sums::MD + lane] : 0.f;
 #pragma unroll
-        for (int o = 16; o; o /= 2) tail += __shfl_xor_sync(0xffffffffu, tail, o);
-        float d[2];
+        for (int o = 16; o; o /= 2) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+        float d[2], b[2], from = 0.f, upto = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int s = 2 * lane + i;
-            d[i] = 0.f;
+            d[i] = b[i] = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) d[i] += rows[64 * w + s];
+            for (int w = 0; w < 8; ++w) d[i] += rows[row_sums::A + 64 * w + s];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) b[i] += rows[row_sums::B + 64 * w + s];
+            from += d[i], upto += b[i];
         }
-        float run = d[0] + d[1];
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const float other = __shfl_down_sync(0xffffffffu, run, o);
-            if (lane + o < 32) run += other;
+            const float right = __shfl_down_sync(0xffffffffu, from, o), earlier = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane + o < 32) from += right;
+            if (lane >= o) upto += earlier;
         }
+        const float next = __shfl_down_sync(0xffffffffu, from, 1), last = __shfl_up_sync(0xffffffffu, upto, 1);
+        const float after = (lane < 31 ? next : 0.f) + d[1], before = lane ? last : 0.f;   // a from step 2 lane + 1 on; b before step 2 lane
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (2 * lane + i < left)
-                store_any(a.dg, a.gate16, (row0 + 2 * lane + i) * a.Hv + head, run + tail - (i ? d[0] : 0.f));
+        for (int i = 0; i < 2; ++i) {
+            const int s = 2 * lane + i;
+            if (s < left)
+                store_any(a.dg, a.gate16, (row0 + s) * a.Hv + head,
+                          (i ? after : from) + (i ? before + b[0] : before) + (rows[row_sums::Z + s] + rows[row_sums::Z + 64 + s]) + whole);
+        }
     }
     if (warp == 0 && elect_one() && (!ok || *gone)) drain_products(&bar.drain, a.ctl);
     __syncwarp();

@@ -20,10 +20,16 @@
 //     dk_t = row_t + col_t
 //     row_t = -exp(G_t) M dv_t + sum_s Y_ts k_s
 //     col_t = exp(G_C - G_t) dM' u_t + sum_s X_st q_s + sum_s Y_st k_s
-//     dG_t  = <q_t, dq_t> + <k_t, row_t> - <k_t, col_t>   (each vector carries its own decay,
-//             exp(G) where it stands in a row's role, exp(-G) in a column's),
-//     dG_C += exp(G_C) <M, dM'> + sum_t exp(G_C - G_t) <k_t, dM' u_t>
-//     dg_t  = sum_{s>=t} dG_s
+//     dg_t  = sum_{r>=t>s} Z_rs + sum_{r>=t} a_r + sum_{s<t} b_s + exp(G_C) <M, dM'>
+//     Z_rs  = X_rs <q_r, k_s> + Y_rs <k_r, k_s>   (s < r)
+//     a_r   = exp(G_r) (scale <q_r, M do_r> - <k_r, M dv_r>)
+//     b_s   = exp(G_C - G_s) <k_s, dM' u_s>
+//
+// (dg_t holds what crosses step t, from a state or key before it to a query, key or state
+// from it on: each term has the factor exp(g_t), and where that is zero so is dg_t.  The same
+// sum by way of the G's gradients, <q, dq> + <k, row - col> from step t on, adds and takes
+// off every pair inside the rest of the chunk, and what is left of their rounding can be far
+// larger than the gradient of a strong decay.)
 //
 // (w is kept rather than dv, so that beta = 0 loses nothing.)
 #pragma once

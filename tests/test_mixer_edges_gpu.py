@@ -101,3 +101,48 @@ def test_threads_share_a_stream(torch):  # noqa: F811
         t.join()
     torch.cuda.synchronize()
     assert not failed
+
+
+# ---------------------------------------------------------------------------
+# The gates' gradients where decays are strong.
+# ---------------------------------------------------------------------------
+DECAYED = [(1, 150, 1, 2, 64, 64), (2, 129, 2, 2, 128, 128), (1, 90, 2, 4, 24, 104), (1, 64, 1, 2, 96, 40)]
+
+
+@pytest.mark.parametrize("dims", DECAYED)
+@pytest.mark.parametrize("dt,gates", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_delta_gate_gradients_of_decayed_heads(torch, dims, dt, gates):  # noqa: F811
+    """d_g per head, one of them with strong decays only: its gradients are many orders below the chunk's largest products.
+
+    d_g is a sum of products that each hold exp(g): the tolerance is the operators' own, per head.
+    """
+    B, S, Hk, Hv, Dk, Dv = dims
+    x = delta_inputs(torch, *dims, dt, gates, seed=71)
+    x["g"][..., -1] = (-8 - 12 * torch.rand(B, S, device="cuda")).to(x["g"].dtype)   # exp: 3e-4 .. 2e-9
+    five = [x[n] for n in FIVE]
+    _, _, carries, errors = qs.quat_delta_fwd_carries(*five, x["init"])
+    d_g = qs.quat_delta_bwd(*five, carries, errors, x["d_o"], x["d_final"])[3]
+    n = {k: wide(v) for k, v in x.items()}
+    want = np.stack([ref.delta_grad(*[n[k][b] for k in FIVE], n["init"][b], Dk ** -0.5, n["d_o"][b], n["d_final"][b])[3] for b in range(B)])
+    for h in range(Hv):
+        close(d_g[..., h], want[..., h], gates, h)
+
+
+@pytest.mark.parametrize("dt,gates", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_delta_gate_gradients_of_cleared_states(torch, D, dt, gates):  # noqa: F811
+    """Where exp(g) is zero in fp32 nothing depends on g: d_g is exactly zero, and right everywhere else."""
+    x = delta_inputs(torch, 2, 140, 1, 2, D, D, dt, gates, seed=72)
+    cleared = torch.zeros(2, 140, 2, dtype=torch.bool, device="cuda")
+    cleared[0, [0, 17, 63, 64, 139]] = True
+    cleared[1, 30:50, 1] = True
+    x["g"] = torch.where(cleared, torch.full_like(x["g"], -float("inf")), x["g"])
+    x["g"][0, 64] = -300.0
+    five = [x[n] for n in FIVE]
+    _, _, carries, errors = qs.quat_delta_fwd_carries(*five, x["init"])
+    d_g = qs.quat_delta_bwd(*five, carries, errors, x["d_o"], x["d_final"])[3]
+    assert (d_g[cleared] == 0).all()
+    n = {k: wide(v) for k, v in x.items()}
+    want = np.stack([ref.delta_grad(*[n[k][b] for k in FIVE], n["init"][b], D ** -0.5, n["d_o"][b], n["d_final"][b])[3] for b in range(2)])
+    for h in range(2):
+        close(d_g[..., h], want[..., h], gates, h)
