@@ -22,8 +22,8 @@
 // reads), so that a key's row and its col meet in one thread.
 //
 // Terms: CT bfloat16 terms per computed value: three (fp32 precision) where any
-// output is fp32; two (16 bits) where outputs and gates are bfloat16, whose own
-// rounding is 2^-9.
+// output is fp32; two (2^-15 of a product left out at most, rms 2^-17.8) where outputs and
+// gates are bfloat16, whose own rounding is 2^-9.  dg bears it too: no two of its sums cancel.
 //
 // Bound: the latency of its phases (loads, conversions, five products), one CTA per
 // SM.  Global loads run along the rows (a warp covers whole lines): loads by the

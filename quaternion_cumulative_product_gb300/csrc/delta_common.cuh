@@ -128,7 +128,8 @@ __device__ __forceinline__ Sum2 sum2_add(const Sum2 a, const Sum2 b) {   // Knut
 
 // A step's log decay.  Below -256 exp() is zero in fp32 by far, and so is every
 // product of decays <= 1 over it: the clamp makes -inf (a cleared state) finite.
-// In base-2 units, so that a decay is one exp2.
+// In base-2 units, so that a decay is one exp2; the factor log2(e) rounds once, which
+// is 2^-24 of the decay's logarithm, as a rounding of the gate itself would be.
 __device__ __forceinline__ float clamp_gate(float g) { return (g < -256.f ? -256.f : g) * 1.4426950408889634f; }
 
 // 2^x (the instruction: 2^-22 off at most).

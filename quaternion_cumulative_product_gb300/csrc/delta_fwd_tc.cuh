@@ -51,7 +51,7 @@ template <typename T, int NT, int DK, bool SUM>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_fwd_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap vmap) {
-    constexpr int PT = NT == 1 ? 2 : 3;   // terms of what only o is made of: bfloat16's own rounding is 2^-9
+    constexpr int PT = NT == 1 ? 2 : 3;   // terms of what only o is made of: two leave out 2^-15 at most, bfloat16's own rounding is 2^-9
     using L = WalkLayout<NT, DK, PT>;
     extern __shared__ unsigned char raw[];
     unsigned char *sm = raw + ((1024u - smem_addr(raw) % 1024u) % 1024u);

@@ -2,11 +2,14 @@
 // products of fp32 precision, as the delta rule's kernels use them.
 //
 // Precision.  tcgen05.mma multiplies bfloat16 values exactly and adds in fp32.
-// An fp32 value x is carried as three bfloat16 terms x = x0 + x1 + x2 (eight
-// bits each: all 24), a bfloat16 input as itself.
+// An fp32 value x is carried as three bfloat16 terms x = x0 + x1 + x2, each the rounding
+// to nearest of what the ones before it leave (|x1| <= 2^-8, |x2| <= 2^-17 of x's power of
+// two, and nothing is left then), a bfloat16 input as itself.
 // A product of values with terms i and j keeps the pairs i + j <= 2: what is left
-// out is below 2^-24 of the product.  So a product costs 1 (bf16 x bf16), 3 (fp32 x
-// bf16) or 6 (fp32 x fp32) tensor-core passes.
+// out is at most 2^-24 of the product, of either sign (rms 2^-27.4 over normal values).
+// So a product costs 1 (bf16 x bf16), 3 (fp32 x bf16) or 6 (fp32 x fp32) tensor-core passes.
+// Terms that are cut off instead (8 bits each) leave out eight times as much, always with
+// the product's sign.  Two terms and the pairs i + j <= 1 leave out 2^-15 at most, rms 2^-17.8.
 //
 // Layouts.  Operands in shared memory are tiles of 64 values (128 bytes) a row
 // with the 128-byte swizzle: 16-byte unit u of row r sits at unit u ^ (r % 8).
@@ -142,22 +145,15 @@ __device__ __forceinline__ float2 mul2(const float2 a, const float2 b) {
     return r;
 }
 
-// The terms of a pair.  All but the last of two are cut off, not rounded: cutting
-// takes eight bits of the 24 exactly, so three terms hold an fp32 value as it is.
-// (Infinities become NaN, NaNs stay.)
+// The terms of a pair: three hold an fp32 value as it is.  (Infinities become NaN, and so do
+// values that round to one, past 2^128 - 2^119; NaNs stay.)
 template <int TERMS>
 __device__ __forceinline__ void split2(float2 x, uint32_t *t) {
     const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) {
-        if (i == TERMS - 1 && TERMS < 3) {
-            t[i] = pack_bf16(x.x, x.y);
-        } else {
-            t[i] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-            if (i < TERMS - 1)
-                x = fma2(make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)),
-                         minus, x);
-        }
+        t[i] = pack_bf16(x.x, x.y);
+        if (i < TERMS - 1) x = fma2(make_float2(__uint_as_float(t[i] << 16), __uint_as_float(t[i] & 0xffff0000u)), minus, x);
     }
 }
 template <int TERMS>

@@ -146,3 +146,29 @@ def test_delta_gate_gradients_of_cleared_states(torch, D, dt, gates):  # noqa: F
     want = np.stack([ref.delta_grad(*[n[k][b] for k in FIVE], n["init"][b], D ** -0.5, n["d_o"][b], n["d_final"][b])[3] for b in range(2)])
     for h in range(2):
         close(d_g[..., h], want[..., h], gates, h)
+
+
+# ---------------------------------------------------------------------------
+# Products of fp32 precision.
+# ---------------------------------------------------------------------------
+BITS = [0x3f80ffff, 0x3f8080ff, 0x3fffffff, 0x3fff7fff, 0x3f817fff, 0x3faa5555]
+
+
+@pytest.mark.parametrize("low", BITS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_delta_products_keep_fp32(torch, D, low):  # noqa: F811
+    """One step from the zero state: the final state is k v^T, one product per value, like signs and low bits set.
+
+    Tolerance: with these bits the pairs of terms left out are below 0.3 * 2^-24 of the product
+    (terms that are cut off, not rounded: up to 7.9), the sum of the others is cut off by at most
+    2^-23 when the first terms' product comes (and by 2^-8 of that before), and the state rounds
+    once, 2^-24: under 4 * 2^-24 together.
+    """
+    value = float(np.array(low, np.uint32).view(np.float32))
+    full = lambda *s: torch.full(s, value, device="cuda")  # noqa: E731
+    k, v = full(1, 1, 1, D), full(1, 1, 1, D)
+    v[..., ::2] *= -1
+    g, beta = torch.zeros(1, 1, 1, device="cuda"), torch.ones(1, 1, 1, device="cuda")
+    _, fin = qs.quat_delta_fwd(k, k, v, g, beta)
+    want = wide(k)[0, 0, 0][:, None] * wide(v)[0, 0, 0][None]
+    assert (np.abs(wide(fin)[0, 0] - want) <= 4 * 2.0 ** -24 * np.abs(want)).all(), np.abs(wide(fin)[0, 0] / want - 1).max() * 2 ** 24
