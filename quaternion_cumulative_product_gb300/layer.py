@@ -70,7 +70,8 @@ class QuatDeltaMixer(torch.nn.Module):
         cum = quat_cumprod(turn, start, save_carries=True)
         q, k = quat_norm_rotate(q, k, cum, self.w_q, self.w_k)
         o, state = quat_delta(q, k, v, g, beta, None if cache is None else cache.state, scale=1.0)
-        last = cum[:, -1].detach().contiguous() if S else start
+        # A copy: a view would keep all of cum, and step() would write into what autograd has saved.
+        last = (cum[:, -1] if S else start).detach().clone(memory_format=torch.contiguous_format)
         return self.out(o.flatten(2)), MixerCache(last, state.detach())
 
     @torch.no_grad()

@@ -1,0 +1,90 @@
+"""The sequence-mixer layer's cache and the autograd wrappers' bookkeeping, on the CPU.
+
+The operators need a GPU; here plain torch forms stand in for them, so that what the layer
+and the wrappers do around them can be checked.
+"""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from quaternion_cumulative_product_gb300 import layer as mixer_layer  # noqa: E402
+
+
+def mul(a, b):
+    aw, ax, ay, az = a.unbind(-1)
+    bw, bx, by, bz = b.unbind(-1)
+    return torch.stack([aw * bw - ax * bx - ay * by - az * bz, aw * bx + ax * bw + ay * bz - az * by,
+                        aw * by - ax * bz + ay * bw + az * bx, aw * bz + ax * by - ay * bx + az * bw], -1)
+
+
+def plain_cumprod(q, init, **_):
+    out = []
+    for t in range(q.shape[1]):
+        init = mul(q[:, t], init)
+        out.append(init)
+    return torch.stack(out, 1) if out else torch.empty_like(q)
+
+
+def plain_rotate(q, k, cum, w_q=None, w_k=None, **_):
+    conj = cum * torch.tensor([1.0, -1.0, -1.0, -1.0])
+
+    def one(x, w):
+        n = x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w
+        return mul(conj.repeat_interleave(x.shape[2] // cum.shape[2], 2), n.unflatten(-1, (-1, 4))).flatten(-2)
+    return one(q, w_q), one(k, w_k)
+
+
+def plain_delta(q, k, v, g, beta, init=None, scale=1.0, **_):
+    B, S, Hv, Dv = v.shape
+    q, k = (x.repeat_interleave(Hv // x.shape[2], 2) for x in (q, k))
+    m = torch.zeros(B, Hv, q.shape[-1], Dv) if init is None else init + 0
+    out = []
+    for t in range(S):
+        m = m * g[:, t].exp()[..., None, None]
+        e = v[:, t] - torch.einsum("bhk,bhkv->bhv", k[:, t], m)
+        m = m + k[:, t, :, :, None] * (beta[:, t, :, None] * e)[:, :, None]
+        out.append(scale * torch.einsum("bhk,bhkv->bhv", q[:, t], m))
+    return (torch.stack(out, 1) if out else torch.empty_like(v)), m.clone()   # (the library saves no final state)
+
+
+def plain_step(q, k, v, g, beta, state, scale=1.0, **_):
+    o, m = plain_delta(q, k, v, g, beta, state, scale)
+    state.copy_(m)
+    return o
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    for name, fn in (("quat_cumprod", plain_cumprod), ("quat_cumprod_fwd", plain_cumprod), ("quat_norm_rotate", plain_rotate),
+                     ("quat_norm_rotate_fwd", plain_rotate), ("quat_delta", plain_delta), ("quat_delta_step", plain_step)):
+        monkeypatch.setattr(mixer_layer, name, fn)
+    torch.manual_seed(3)
+    return mixer_layer.QuatDeltaMixer(12, 2, 8, groups=2, dtype=torch.float32, device="cpu")
+
+
+@pytest.mark.parametrize("B,S", [(1, 5), (1, 1), (3, 1), (3, 5)])
+def test_cache_owns_its_memory(layer, B, S):
+    """The cache of a prefill holds one step's rotation, and tokens after it leave the prefill's graph as it was."""
+    x = torch.randn(B, S + 2, 12)
+    y, cache = layer(x[:, :S])
+    assert cache.turn.untyped_storage().nbytes() == cache.turn.numel() * 4
+    tokens = [layer.step(x[:, t : t + 1], cache) for t in (S, S + 1)]
+    y.square().sum().backward()   # (an in-place change of what the prefill saved is an error here)
+    assert all(torch.isfinite(p.grad).all() for p in layer.parameters())
+    with torch.no_grad():
+        whole, end = layer(x)
+    assert torch.allclose(torch.cat([y.detach(), *tokens], 1), whole, atol=1e-5)
+    assert torch.allclose(cache.turn, end.turn, atol=1e-5) and torch.allclose(cache.state, end.state, atol=1e-5)
+
+
+def test_empty_prefill_leaves_the_old_cache_alone(layer):
+    x = torch.randn(2, 6, 12)
+    with torch.no_grad():
+        _, old = layer(x[:, :4])
+        kept = old.turn.clone(), old.state.clone()
+        y, new = layer(x[:, :0], old)
+    assert y.shape == (2, 0, 12) and torch.equal(new.turn, kept[0]) and torch.equal(new.state, kept[1])
+    layer.step(x[:, 4:5], new)
+    assert torch.equal(old.turn, kept[0]) and torch.equal(old.state, kept[1])

@@ -172,3 +172,24 @@ def test_delta_products_keep_fp32(torch, D, low):  # noqa: F811
     _, fin = qs.quat_delta_fwd(k, k, v, g, beta)
     want = wide(k)[0, 0, 0][:, None] * wide(v)[0, 0, 0][None]
     assert (np.abs(wide(fin)[0, 0] - want) <= 4 * 2.0 ** -24 * np.abs(want)).all(), np.abs(wide(fin)[0, 0] / want - 1).max() * 2 ** 24
+
+
+# ---------------------------------------------------------------------------
+# The layer.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,S", [(1, 70), (1, 1), (3, 1)])
+def test_layer_cache_of_one_sequence(torch, B, S):  # noqa: F811
+    """Tokens after a prefill neither write into its graph nor keep its rotations."""
+    from quaternion_cumulative_product_gb300.layer import QuatDeltaMixer
+    torch.manual_seed(81)
+    layer = QuatDeltaMixer(96, 2, 64, groups=2, dtype=torch.float32)
+    x = torch.randn(B, S + 2, 96, device="cuda")
+    y, cache = layer(x[:, :S])
+    assert cache.turn.untyped_storage().nbytes() == cache.turn.numel() * 4
+    tokens = [layer.step(x[:, t : t + 1], cache) for t in (S, S + 1)]
+    y.square().sum().backward()
+    assert all(torch.isfinite(p.grad).all() for p in layer.parameters())
+    with torch.no_grad():
+        whole, end = layer(x)
+    assert (torch.cat([y.detach(), *tokens], 1) - whole).abs().max() <= 1e-4 * whole.abs().max()   # the scan's tolerance
+    assert (cache.state - end.state).abs().max() <= 1e-4 * end.state.abs().max()
