@@ -18,11 +18,13 @@ reaches the node already added into ``d_cum[:, S-1]``; the node itself has a
 single output.
 
 ``quat_norm_rotate`` and ``quat_delta`` are the differentiable forms of the
-operators around the scan (:mod:`.mixer`).
+operators around the scan (:mod:`.mixer`).  Their gradients have none of their own: a
+backward through them (``create_graph=True``) raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (
     quat_cumprod_bwd, quat_cumprod_bwd_carries, quat_cumprod_fwd, quat_cumprod_fwd_carries, quat_delta_bwd,
@@ -87,6 +89,7 @@ class QuatNormRotate(torch.autograd.Function):
         return quat_norm_rotate_fwd(q, k, cum, w_q, w_k, norm=norm, eps=eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_q_out, d_k_out):
         q, k, cum, w_q, w_k = ctx.saved_tensors
         d = quat_norm_rotate_bwd(q, k, cum, d_q_out.contiguous(), d_k_out.contiguous(), w_q, w_k,
@@ -105,7 +108,7 @@ class QuatDelta(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, init, scale, offsets, tracked):
         g, beta = g.contiguous(), beta.contiguous()
-        ctx.scale, ctx.has_init = scale, init is not None
+        ctx.scale = scale
         if not tracked:
             return quat_delta_fwd(q, k, v, g, beta, init, scale=scale, offsets=offsets)
         o, final, carries, errors = quat_delta_fwd_carries(q, k, v, g, beta, init, scale=scale, offsets=offsets)
@@ -113,6 +116,7 @@ class QuatDelta(torch.autograd.Function):
         return o, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_final):
         *inputs, offsets = ctx.saved_tensors
         d_final = None if d_final is None else d_final.contiguous()

@@ -9,6 +9,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from quaternion_cumulative_product_gb300 import autograd as ag  # noqa: E402
 from quaternion_cumulative_product_gb300 import layer as mixer_layer  # noqa: E402
 
 
@@ -88,3 +89,59 @@ def test_empty_prefill_leaves_the_old_cache_alone(layer):
     assert y.shape == (2, 0, 12) and torch.equal(new.turn, kept[0]) and torch.equal(new.state, kept[1])
     layer.step(x[:, 4:5], new)
     assert torch.equal(old.turn, kept[0]) and torch.equal(old.state, kept[1])
+
+
+# ---------------------------------------------------------------------------
+# The autograd wrappers.
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def wrapped(monkeypatch):
+    """The wrappers over plain forms; returns the arguments of the delta backward's last call."""
+    seen = {}
+
+    def delta_fwd(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
+        return plain_delta(q, k, v, g, beta, init, scale or 1.0)
+
+    def delta_fwd_carries(*a, **kw):
+        return (*delta_fwd(*a, **kw), torch.zeros(1), torch.zeros(1))
+
+    def delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scale=None, offsets=None):
+        seen.update(q=q, k=k, v=v, d_o=d_o, d_final=d_final)
+        with torch.enable_grad():
+            five = [t.detach().requires_grad_() for t in (q, k, v, g, beta)]
+            o, fin = plain_delta(*five, None, scale or 1.0)
+            outs, cots = ([o, fin], [d_o, d_final]) if d_final is not None else ([o], [d_o])
+            return (*torch.autograd.grad(outs, five, cots), torch.zeros(q.shape[0], v.shape[2], q.shape[3], v.shape[3]))
+
+    def rotate_fwd(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6):
+        return plain_rotate(q, k, cum, w_q, w_k)
+
+    def rotate_bwd(q, k, cum, d_q, d_k, w_q=None, w_k=None, *, norm="rms", eps=1e-6):
+        with torch.enable_grad():
+            five = [t.detach().requires_grad_() for t in (q, k, cum, w_q, w_k)]
+            return torch.autograd.grad(plain_rotate(*five), five, [d_q, d_k])
+
+    for name, fn in (("quat_delta_fwd", delta_fwd), ("quat_delta_fwd_carries", delta_fwd_carries), ("quat_delta_bwd", delta_bwd),
+                     ("quat_norm_rotate_fwd", rotate_fwd), ("quat_norm_rotate_bwd", rotate_bwd)):
+        monkeypatch.setattr(ag, name, fn)
+    return seen
+
+
+def delta_leaves(B=2, S=3, H=1, D=8):
+    torch.manual_seed(4)
+    x = [torch.randn(B, S, H, D), torch.randn(B, S, H, D), torch.randn(B, S, H, D), -torch.rand(B, S, H), torch.rand(B, S, H)]
+    return [t.requires_grad_() for t in x]
+
+
+def test_second_derivatives_are_refused(wrapped):
+    """The gradients carry no graph of their own: asking for theirs is an error, not a silent zero."""
+    x = delta_leaves()
+    o, _ = ag.quat_delta(*x)
+    d_v, = torch.autograd.grad(o.square().sum(), x[2], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        d_v.sum().backward()
+    w = torch.ones(8, requires_grad=True)
+    q, k = ag.quat_norm_rotate(x[0], x[1], torch.randn(2, 3, 1, 2, 4), w, w)
+    d_w, = torch.autograd.grad(q.square().sum() + k.sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        d_w.sum().backward()
