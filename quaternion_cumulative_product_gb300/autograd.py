@@ -109,6 +109,7 @@ class QuatDelta(torch.autograd.Function):
     def forward(ctx, q, k, v, g, beta, init, scale, offsets, tracked):
         g, beta = g.contiguous(), beta.contiguous()
         ctx.scale = scale
+        ctx.set_materialize_grads(False)   # a cotangent that nobody has is None: no zeros are made and read for it
         if not tracked:
             return quat_delta_fwd(q, k, v, g, beta, init, scale=scale, offsets=offsets)
         o, final, carries, errors = quat_delta_fwd_carries(q, k, v, g, beta, init, scale=scale, offsets=offsets)
@@ -119,8 +120,10 @@ class QuatDelta(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_o, d_final):
         *inputs, offsets = ctx.saved_tensors
+        v = inputs[2]
+        d_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if d_o is None else d_o.contiguous()
         d_final = None if d_final is None else d_final.contiguous()
-        d = quat_delta_bwd(*inputs, d_o.contiguous(), d_final, scale=ctx.scale, offsets=offsets)
+        d = quat_delta_bwd(*inputs, d_o, d_final, scale=ctx.scale, offsets=offsets)
         return (*[g if need else None for g, need in zip(d, ctx.needs_input_grad)], None, None, None)
 
 

@@ -145,3 +145,15 @@ def test_second_derivatives_are_refused(wrapped):
     d_w, = torch.autograd.grad(q.square().sum() + k.sum(), w, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         d_w.sum().backward()
+
+
+def test_delta_cotangents_that_nobody_has(wrapped):
+    """A loss of o alone sends no cotangent of the final state; one of the state alone counts o's as zero."""
+    x = delta_leaves()
+    o, fin = ag.quat_delta(*x)
+    want = torch.autograd.grad(plain_delta(*x)[0].square().sum(), x)
+    got = torch.autograd.grad(o.square().sum(), x, retain_graph=True)
+    assert wrapped["d_final"] is None and all(torch.allclose(a, b, atol=1e-5) for a, b in zip(got, want))
+    want = torch.autograd.grad(plain_delta(*x)[1].square().sum(), x[1:])
+    got = torch.autograd.grad(fin.square().sum(), x[1:])
+    assert (wrapped["d_o"] == 0).all() and all(torch.allclose(a, b, atol=1e-5) for a, b in zip(got, want))
