@@ -106,8 +106,8 @@ int quat_norm_rotate_bwd(int dtype, int cum_dtype, int norm, float eps,
  *     carries  fp32 [B, ceil(S/64), Hv, Dk, Dv]; with offsets [S/64 + N, Hv, Dk, Dv],
  *              chunk c of sequence n in slot offsets[n]/64 + n + c
  *     errors   fp32 [B, S, Hv, Dv]
- * `strides` names q, k, v (none may be zero over more than one entry).  Requires
- * Hv a multiple of Hk, Dk and Dv multiples of 8 up to QS_DELTA_MAX_D.
+ * `strides` names q, k, v (in bfloat16 none may be zero over more than one entry).
+ * Requires Hv a multiple of Hk, Dk and Dv multiples of 8 up to QS_DELTA_MAX_D.
  */
 int quat_delta_fwd(int dtype, int gate_dtype, float scale,
                    const void *q, const void *k, const void *v, const void *g, const void *beta, const float *init,

@@ -102,6 +102,12 @@ def quat_norm_rotate(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6):
     return QuatNormRotate.apply(q, k, cum, w_q, w_k, norm, eps)
 
 
+def _own_rows(t):
+    """``t``, or a contiguous copy of an expanded bfloat16 view (whose gradient autograd sums up)."""
+    flat = t.dtype is torch.bfloat16 and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride()))
+    return t.contiguous() if flat else t
+
+
 class QuatDelta(torch.autograd.Function):
     """Gated delta rule over whole sequences; tracked calls keep the carries and the errors."""
 
@@ -128,7 +134,8 @@ class QuatDelta(torch.autograd.Function):
 
 
 def quat_delta(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
-    """Differentiable :func:`quat_delta_fwd`: ``(o, final_state)``."""
+    """Differentiable :func:`quat_delta_fwd`: ``(o, final_state)``.  Expanded bfloat16 inputs are copied."""
+    q, k, v = (_own_rows(t) for t in (q, k, v))
     inputs = [t for t in (q, k, v, g, beta, init) if t is not None]
     tracked = torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
     init = None if init is None else init.contiguous()

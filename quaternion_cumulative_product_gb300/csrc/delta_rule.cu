@@ -215,6 +215,14 @@ void geometry(DeltaArgs &a, const int64_t *strides, const int32_t *offsets, int6
     a.gate16 = gate_dtype == QS_BF16, a.scale = scale;
 }
 
+// Strides that the kernels cannot take.  (bfloat16 rows come by tensor maps, fp32 rows by plain loads.)
+bool bad_layout(const DeltaArgs &a, int dtype) {
+    const int es = dtype == QS_BF16 ? 2 : 4;
+    if (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es)) return true;
+    return dtype == QS_BF16 && (qsh::has_flat_dim(a.sq, a.B, a.S, a.Hk) || qsh::has_flat_dim(a.sk, a.B, a.S, a.Hk) ||
+                                qsh::has_flat_dim(a.sv, a.B, a.S, a.Hv));
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -235,9 +243,7 @@ extern "C" int quat_delta_fwd(int dtype, int gate_dtype, float scale, const void
     const int es = dtype == QS_BF16 ? 2 : 4, ge = gate_dtype == QS_BF16 ? 2 : 4;
     DeltaArgs a{};
     geometry(a, strides, offsets, N, B, S, Hk, Hv, Dk, Dv, gate_dtype, scale);
-    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es) ||
-                    qsh::has_flat_dim(a.sq, B, S, Hk) || qsh::has_flat_dim(a.sk, B, S, Hk) || qsh::has_flat_dim(a.sv, B, S, Hv)))
-        return QS_ERR_MISALIGNED;
+    if (strides && bad_layout(a, dtype)) return QS_ERR_MISALIGNED;
     const size_t gates = (size_t)B * S * Hv * ge, states = (size_t)N * Hv * Dk * Dv * 4, rows = (size_t)B * S * Hv * Dv;
     const Sized ins[] = {{q, qsh::span_bytes(a.sq, B, S, Hk, Dk, es)}, {k, qsh::span_bytes(a.sk, B, S, Hk, Dk, es)},
                          {v, qsh::span_bytes(a.sv, B, S, Hv, Dv, es)}, {g, gates}, {beta, gates}, {init, states},
@@ -278,9 +284,7 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
     const int es = dtype == QS_BF16 ? 2 : 4, ge = gate_dtype == QS_BF16 ? 2 : 4;
     DeltaArgs a{};
     geometry(a, strides, offsets, N, B, S, Hk, Hv, Dk, Dv, gate_dtype, scale);
-    if (strides && (qsh::bad_strides(a.sq, es) || qsh::bad_strides(a.sk, es) || qsh::bad_strides(a.sv, es) ||
-                    qsh::has_flat_dim(a.sq, B, S, Hk) || qsh::has_flat_dim(a.sk, B, S, Hk) || qsh::has_flat_dim(a.sv, B, S, Hv)))
-        return QS_ERR_MISALIGNED;
+    if (strides && bad_layout(a, dtype)) return QS_ERR_MISALIGNED;
     const size_t gates = (size_t)B * S * Hv * ge, states = (size_t)N * Hv * Dk * Dv * 4, rows = (size_t)B * S * Hv * Dv;
     const size_t keys = (size_t)B * S * Hk * Dk, kept = (size_t)a.slots * Hv * Dk * Dv;
     const Sized ins[] = {{q, qsh::span_bytes(a.sq, B, S, Hk, Dk, es)}, {k, qsh::span_bytes(a.sk, B, S, Hk, Dk, es)},

@@ -103,6 +103,13 @@ def _strides(*tensors):
     return (ctypes.c_int64 * len(out))(*out)
 
 
+def _no_expanded(**tensors):
+    """bfloat16 rows of the delta rule come by tensor maps, which hold no stride of zero."""
+    for name, t in tensors.items():
+        if t.dtype is _BF16 and not t.is_contiguous() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+            raise ValueError(f"{name} is an expanded view, which a bfloat16 call does not take: pass {name}.contiguous()")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -232,6 +239,7 @@ def _sequences(offsets, B, S, device):
 
 def _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, keep):
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
+    _no_expanded(q=q, k=k, v=v)
     N, slots = _sequences(offsets, B, S, device)
     if init is not None:
         _need("init", init, (N, Hv, Dk, Dv), device, torch.float32)
@@ -253,7 +261,7 @@ def quat_delta_fwd(q, k, v, g, beta, init=None, *, scale=None, offsets=None, str
     ``M~ = exp(g_t) M_{t-1}``, ``e_t = v_t - M~^T k_t``, ``M_t = M~ + k_t (beta_t e_t)^T``,
     ``o_t = scale * M_t^T q_t`` for each value head, with the key head ``h // (Hv // Hk)``.
     ``q``, ``k`` [B,S,Hk,Dk], ``v`` [B,S,Hv,Dv]: float32 or bfloat16 CUDA (last
-    dimension contiguous; keys are usually unit vectors); ``g`` (log decays, <= 0;
+    dimension contiguous; expanded views in float32 only; keys are usually unit vectors); ``g`` (log decays, <= 0;
     -inf clears the state) and ``beta`` [B,S,Hv]: float32 or bfloat16, both alike.
     ``init`` [N,Hv,Dk,Dv] float32 or None (zeros).  ``scale`` defaults to
     ``Dk ** -0.5``.  ``offsets`` (int32 [N+1] CUDA, from 0 to S): a batch of 1 holds
@@ -277,6 +285,7 @@ def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scal
     ``d_o``: cotangent of ``o`` (contiguous), ``d_final``: of the final state or None.
     """
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
+    _no_expanded(q=q, k=k, v=v)
     N, slots = _sequences(offsets, B, S, device)
     _need("carries", carries, (*slots, Hv, Dk, Dv), device, torch.float32)
     _need("errors", errors, (B, S, Hv, Dv), device, torch.float32)

@@ -10,7 +10,7 @@ import pytest
 
 import mixer_reference as ref
 import quaternion_cumulative_product_gb300 as qs
-from test_mixer_gpu import FIVE, close, delta_inputs, rotate_inputs, torch, wide  # noqa: F401  (torch: the fixture)
+from test_mixer_gpu import FIVE, TOL, close, delta_inputs, rotate_inputs, torch, wide  # noqa: F401  (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,36 @@ def test_layer_cache_of_one_sequence(torch, B, S):  # noqa: F811
         whole, end = layer(x)
     assert (torch.cat([y.detach(), *tokens], 1) - whole).abs().max() <= 1e-4 * whole.abs().max()   # the scan's tolerance
     assert (cache.state - end.state).abs().max() <= 1e-4 * end.state.abs().max()
+
+
+# ---------------------------------------------------------------------------
+# Inputs that are views, heads that are none, streams.
+# ---------------------------------------------------------------------------
+def test_delta_expanded_keys(torch):  # noqa: F811
+    """Queries and keys that all heads or all sequences share, as expanded views in fp32."""
+    x = delta_inputs(torch, 2, 130, 2, 4, 64, 64, "f32", "f32", seed=91)
+    views = dict(x, q=x["q"][:1].expand(2, -1, -1, -1), k=x["k"][:, :, :1].expand(-1, -1, 2, -1), v=x["v"][:, :1].expand(-1, 130, -1, -1))
+    whole = {n: t.contiguous() for n, t in views.items()}
+    out = []
+    for y in (views, whole):
+        five = [y[n] for n in FIVE]
+        o, fin, carries, errors = qs.quat_delta_fwd_carries(*five, y["init"])
+        out.append([o, fin, *qs.quat_delta_bwd(*five, carries, errors, y["d_o"], y["d_final"])])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    with pytest.raises(ValueError, match="k is an expanded view"):   # bfloat16 rows come by tensor maps
+        qs.quat_delta_fwd(*[whole[n].bfloat16() if n != "k" else x["k"].bfloat16()[:, :, :1].expand(-1, -1, 2, -1) for n in FIVE])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_autograd_delta_takes_expanded_inputs(torch, dt):  # noqa: F811
+    """A broadcast input's gradient is the sum over its copies."""
+    from quaternion_cumulative_product_gb300 import autograd as ag
+    x = delta_inputs(torch, 2, 100, 1, 2, 64, 64, dt, "f32", seed=92)
+    k = x["k"][:1].clone().requires_grad_()
+    full = x["k"][:1].repeat(2, 1, 1, 1).requires_grad_()
+    grads = []
+    for leaf, key in ((k, k.expand(2, -1, -1, -1)), (full, full)):
+        o, _ = ag.quat_delta(x["q"], key, x["v"], x["g"], x["beta"])
+        grads.append(torch.autograd.grad(o, leaf, x["d_o"])[0])
+    want = grads[1].float().sum(0, keepdim=True)
+    assert (grads[0].float() - want).abs().max() <= TOL[dt] * want.abs().max()
