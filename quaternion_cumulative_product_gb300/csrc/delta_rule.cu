@@ -186,7 +186,8 @@ int check(int dtype, int gate_dtype, const int32_t *offsets, int64_t N, int64_t 
     if (Hv > 0 && (Hk == 0 || Hv % Hk || Dk == 0 || Dv == 0)) return QS_ERR_DIMS;
     if (offsets ? B != 1 : N != B) return QS_ERR_DIMS;
     const int64_t slots = offsets ? S / DC + N : N * ((S + DC - 1) / DC);
-    if ((__int128)N * Hv >= lim || (__int128)slots * Hv >= lim || (__int128)B * S * Hv >= ((__int128)1 << 40)) return QS_ERR_DIMS;
+    const int64_t heads = Hv > Hk ? Hv : Hk;
+    if ((__int128)N * Hv >= lim || (__int128)slots * Hv >= lim || (__int128)B * S * heads >= ((__int128)1 << 40)) return QS_ERR_DIMS;
     return N * Hv == 0 ? 1 : QS_OK;
 }
 
@@ -272,7 +273,18 @@ extern "C" int quat_delta_bwd(int dtype, int gate_dtype, float scale, const void
                               const int64_t *strides, const int32_t *offsets, int64_t N, int64_t B, int64_t S, int64_t Hk,
                               int64_t Hv, int64_t Dk, int64_t Dv, void *stream_) {
     const int dc = check(dtype, gate_dtype, offsets, N, B, S, Hk, Hv, Dk, Dv);
-    if (dc == 1) return QS_OK;
+    if (dc == 1) {   // keys that no value head uses have zero gradients
+        const size_t bytes = (size_t)B * S * Hk * Dk * (dtype == QS_BF16 ? 2 : 4);
+        for (void *p : {d_q, d_k}) {
+            if (bytes == 0) break;
+            if (!p) return QS_ERR_NULL;
+            if (cudaMemsetAsync(p, 0, bytes, static_cast<cudaStream_t>(stream_)) != cudaSuccess) {
+                cudaGetLastError();
+                return QS_ERR_CUDA;
+            }
+        }
+        return QS_OK;
+    }
     if (dc != QS_OK) return dc;
     const bool some = B * S > 0;
     if (some && (!q || !k || !v || !g || !beta || !carries || !errors || !d_o || !d_q || !d_k || !d_v || !d_g || !d_beta))

@@ -226,3 +226,15 @@ def test_autograd_delta_takes_expanded_inputs(torch, dt):  # noqa: F811
         grads.append(torch.autograd.grad(o, leaf, x["d_o"])[0])
     want = grads[1].float().sum(0, keepdim=True)
     assert (grads[0].float() - want).abs().max() <= TOL[dt] * want.abs().max()
+
+
+def test_delta_gradients_without_value_heads(torch):  # noqa: F811
+    """No value head uses the keys: their gradients are zero, not whatever the memory held."""
+    B, S, Hk, D = 1, 37, 2, 64
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    q = torch.randn(B, S, Hk, D, device="cuda")
+    stale = [torch.full_like(q, float("nan")) for _ in range(4)]
+    del stale   # (the allocator hands this memory out again)
+    d = qs.quat_delta_bwd(q, q, e(B, S, 0, D), e(B, S, 0), e(B, S, 0), e(B, 1, 0, D, D), e(B, S, 0, D), e(B, S, 0, D))
+    assert (d[0] == 0).all() and (d[1] == 0).all()
+    assert d[2].shape == (B, S, 0, D) and d[5].shape == (B, 0, D, D)
