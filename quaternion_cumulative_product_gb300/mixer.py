@@ -10,12 +10,14 @@
 
 As in the rest of the binding, the calls check and marshal arguments only; the
 work runs in the library's CUDA kernels on the current torch stream (or
-``stream``), and there is no CPU path.  The differentiable forms are in
-:mod:`quaternion_cumulative_product_gb300.autograd`.
+``stream``, whose memory the outputs then come from), and there is no CPU path.
+The differentiable forms are in :mod:`quaternion_cumulative_product_gb300.autograd`.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 
 import torch
 
@@ -119,13 +121,35 @@ def _empty(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _run(fn, where, device, stream, *args):
-    """Calls the library with ``stream`` (default: the current one) on ``device``."""
-    if stream is None and _get_device() == device.index:   # the usual call, without a context or a Stream object
+def _with_stream(fn):
+    """Adds the argument ``stream``: the call runs with it as the current stream.
+
+    Outputs are then allocated on it too: from the current stream's memory they could still
+    be in use there when the call writes them, or be handed out again before it has.
+    """
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        q = args[0] if args else kw.get("q")
+        if isinstance(q, torch.Tensor) and q.is_cuda and q.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, expected {q.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    said = inspect.signature(fn)
+    call.__signature__ = said.replace(parameters=[*said.parameters.values(),
+                                                  inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
+    return call
+
+
+def _run(fn, where, device, *args):
+    """Calls the library with the current stream on ``device``."""
+    if _get_device() == device.index:   # the usual call, without a context or a Stream object
         rc = fn(*args, _raw_stream(device.index))
     else:
         with _on_device(device):
-            rc = fn(*args, _stream_handle(stream, device))
+            rc = fn(*args, _stream_handle(None, device))
     if rc != QS_OK:
         raise QuatScanError(rc, where)
 
@@ -156,7 +180,8 @@ def _rotate_args(q, k, cum, w_q, w_k, norm):
     return device, code, cum_code, (B, S, H, J, Hq, Hk, D)
 
 
-def quat_norm_rotate_fwd(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6, q_out=None, k_out=None, stream=None):
+@_with_stream
+def quat_norm_rotate_fwd(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6, q_out=None, k_out=None):
     """Norm of each head of ``q`` and ``k``, then the rotation of its quaternions by ``conj(cum)``.
 
     ``q`` [B,S,Hq,D] and ``k`` [B,S,Hk,D]: float32 or bfloat16 CUDA, the last
@@ -175,13 +200,14 @@ def quat_norm_rotate_fwd(q, k, cum, w_q=None, w_k=None, *, norm="rms", eps=1e-6,
         k_out = _empty(k)
     else:
         _need("k_out", k_out, k.shape, device, k.dtype)
-    _run(_lib().quat_norm_rotate_fwd, "quat_norm_rotate_fwd", device, stream, code, cum_code, _NORMS[norm], eps,
+    _run(_lib().quat_norm_rotate_fwd, "quat_norm_rotate_fwd", device, code, cum_code, _NORMS[norm], eps,
          q.data_ptr(), k.data_ptr(), cum.data_ptr(), _ptr(w_q), _ptr(w_k), q_out.data_ptr(), k_out.data_ptr(),
          _strides(q, k), *dims)
     return q_out, k_out
 
 
-def quat_norm_rotate_bwd(q, k, cum, d_q_out, d_k_out, w_q=None, w_k=None, *, norm="rms", eps=1e-6, stream=None):
+@_with_stream
+def quat_norm_rotate_bwd(q, k, cum, d_q_out, d_k_out, w_q=None, w_k=None, *, norm="rms", eps=1e-6):
     """``(d_q, d_k, d_cum, d_w_q, d_w_k)`` of :func:`quat_norm_rotate_fwd` for cotangents of its outputs.
 
     Recomputed from the inputs.  ``d_cum`` (in ``cum``'s type) sums over the heads
@@ -196,7 +222,7 @@ def quat_norm_rotate_bwd(q, k, cum, d_q_out, d_k_out, w_q=None, w_k=None, *, nor
     d_cum = torch.empty_like(cum)
     d_w_q = None if w_q is None else torch.empty_like(w_q)
     d_w_k = None if w_k is None else torch.empty_like(w_k)
-    _run(_lib().quat_norm_rotate_bwd, "quat_norm_rotate_bwd", device, stream, code, cum_code, _NORMS[norm], eps,
+    _run(_lib().quat_norm_rotate_bwd, "quat_norm_rotate_bwd", device, code, cum_code, _NORMS[norm], eps,
          q.data_ptr(), k.data_ptr(), cum.data_ptr(), _ptr(w_q), _ptr(w_k), d_q_out.data_ptr(), d_k_out.data_ptr(),
          d_q.data_ptr(), d_k.data_ptr(), d_cum.data_ptr(), _ptr(d_w_q), _ptr(d_w_k), _strides(q, k), *dims)
     return d_q, d_k, d_cum, d_w_q, d_w_k
@@ -237,7 +263,7 @@ def _sequences(offsets, B, S, device):
     return N, (S // QS_DELTA_STEPS + N,)
 
 
-def _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, keep):
+def _delta_fwd(q, k, v, g, beta, init, scale, offsets, keep):
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
     _no_expanded(q=q, k=k, v=v)
     N, slots = _sequences(offsets, B, S, device)
@@ -249,13 +275,14 @@ def _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, keep):
     if keep:
         carries = torch.empty((*slots, Hv, Dk, Dv), dtype=torch.float32, device=device)
         errors = torch.empty((B, S, Hv, Dv), dtype=torch.float32, device=device)
-    _run(_lib().quat_delta_fwd, "quat_delta_fwd", device, stream, code, gate, Dk ** -0.5 if scale is None else scale,
+    _run(_lib().quat_delta_fwd, "quat_delta_fwd", device, code, gate, Dk ** -0.5 if scale is None else scale,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(init), o.data_ptr(),
          final.data_ptr(), _ptr(carries), _ptr(errors), _strides(q, k, v), _ptr(offsets), N, B, S, Hk, Hv, Dk, Dv)
     return o, final, carries, errors
 
 
-def quat_delta_fwd(q, k, v, g, beta, init=None, *, scale=None, offsets=None, stream=None):
+@_with_stream
+def quat_delta_fwd(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
     """The gated delta rule over whole sequences: ``(o, final_state)``.
 
     ``M~ = exp(g_t) M_{t-1}``, ``e_t = v_t - M~^T k_t``, ``M_t = M~ + k_t (beta_t e_t)^T``,
@@ -267,19 +294,21 @@ def quat_delta_fwd(q, k, v, g, beta, init=None, *, scale=None, offsets=None, str
     ``Dk ** -0.5``.  ``offsets`` (int32 [N+1] CUDA, from 0 to S): a batch of 1 holds
     N packed sequences, some perhaps empty; else N = B.
     """
-    return _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, False)[:2]
+    return _delta_fwd(q, k, v, g, beta, init, scale, offsets, False)[:2]
 
 
-def quat_delta_fwd_carries(q, k, v, g, beta, init=None, *, scale=None, offsets=None, stream=None):
+@_with_stream
+def quat_delta_fwd_carries(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
     """:func:`quat_delta_fwd` that keeps what the backward needs: ``(o, final_state, carries, errors)``.
 
     ``carries``: the state entering every 64-step chunk, float32 [B,ceil(S/64),Hv,Dk,Dv]
     (packed: [S//64 + N, Hv, Dk, Dv]); ``errors``: the ``e_t``, float32 [B,S,Hv,Dv].
     """
-    return _delta_fwd(q, k, v, g, beta, init, scale, offsets, stream, True)
+    return _delta_fwd(q, k, v, g, beta, init, scale, offsets, True)
 
 
-def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scale=None, offsets=None, stream=None):
+@_with_stream
+def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scale=None, offsets=None):
     """``(d_q, d_k, d_v, d_g, d_beta, d_init)`` from the forward's carries and errors.
 
     ``d_o``: cotangent of ``o`` (contiguous), ``d_final``: of the final state or None.
@@ -296,14 +325,15 @@ def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scal
     d_v = _empty(v)
     d_g, d_beta = torch.empty_like(g), torch.empty_like(beta)
     d_init = torch.empty((N, Hv, Dk, Dv), dtype=torch.float32, device=device)
-    _run(_lib().quat_delta_bwd, "quat_delta_bwd", device, stream, code, gate, Dk ** -0.5 if scale is None else scale,
+    _run(_lib().quat_delta_bwd, "quat_delta_bwd", device, code, gate, Dk ** -0.5 if scale is None else scale,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), carries.data_ptr(), errors.data_ptr(),
          d_o.data_ptr(), _ptr(d_final), d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_g.data_ptr(), d_beta.data_ptr(),
          d_init.data_ptr(), _strides(q, k, v), _ptr(offsets), N, B, S, Hk, Hv, Dk, Dv)
     return d_q, d_k, d_v, d_g, d_beta, d_init
 
 
-def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None, stream=None):
+@_with_stream
+def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None):
     """The gated delta rule for T new tokens (usually one) of N sequences: ``o``; ``state`` is updated in place.
 
     ``q``, ``k`` [N,T,Hk,Dk], ``v`` [N,T,Hv,Dv], ``g``, ``beta`` [N,T,Hv] as for
@@ -323,7 +353,7 @@ def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None, 
         o = _empty(v)
     else:
         _need("o", o, (N, T, Hv, Dv), device, v.dtype)
-    _run(_lib().quat_delta_step, "quat_delta_step", device, stream, code, gate, Dk ** -0.5 if scale is None else scale,
+    _run(_lib().quat_delta_step, "quat_delta_step", device, code, gate, Dk ** -0.5 if scale is None else scale,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
          o.data_ptr(), _strides(q, k, v), P, N, T, Hk, Hv, Dk, Dv)
     return o

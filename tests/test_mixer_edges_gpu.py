@@ -238,3 +238,26 @@ def test_delta_gradients_without_value_heads(torch):  # noqa: F811
     d = qs.quat_delta_bwd(q, q, e(B, S, 0, D), e(B, S, 0), e(B, S, 0), e(B, 1, 0, D, D), e(B, S, 0, D), e(B, S, 0, D))
     assert (d[0] == 0).all() and (d[1] == 0).all()
     assert d[2].shape == (B, S, 0, D) and d[5].shape == (B, 0, D, D)
+
+
+def test_outputs_belong_to_the_call_s_stream(torch):  # noqa: F811
+    """Outputs made for a call on another stream come from that stream's memory: dropped early, they are not handed
+    out to work on the current stream while the call may still write them."""
+    x = delta_inputs(torch, 1, 200, 2, 2, 64, 64, "bf16", "f32", seed=93)
+    y = rotate_inputs(torch, 1, 200, 2, 2, 2, 64, 16, "bf16", "f32", False, seed=93)
+    five, s = [x[n] for n in FIVE], torch.cuda.Stream()
+    states = [x["init"].clone(), x["init"].clone()]
+    s.wait_stream(torch.cuda.current_stream())
+    calls = [lambda st: qs.quat_delta_fwd(*five, x["init"], stream=st)[0], lambda st: qs.quat_norm_rotate_fwd(y["q"], y["k"], y["cum"], stream=st)[0],
+             lambda st: qs.quat_delta_step(*five, states[st is not None], stream=st)]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        out = call(s)
+        s.synchronize()
+        assert torch.equal(out, want)
+        where, shape, dtype = out.data_ptr(), out.shape, out.dtype
+        del out
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != where
+        with torch.cuda.stream(s):
+            assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() == where
