@@ -19,7 +19,7 @@
  * Element types: QS_F32 or QS_BF16.  Sums, norms and states are fp32.  The delta rule's
  * products leave out at most 2^-24 of a product, or, where only bfloat16 outputs are made
  * of them, 2^-15 (rms 2^-17); its decays are off by 2^-22 and by 2^-24 of their logarithm
- * at most.  An output in bfloat16 is rounded to nearest even once, when stored.
+ * at most.  (fp32 values past 2^128 - 2^119 count as infinite there.)  An output in bfloat16 is rounded to nearest even once, when stored.
  *
  * Strides: a `strides` argument holds, for each tensor it names, the distances
  * in elements between batch entries, between steps and between heads (three

@@ -28,10 +28,11 @@
 // Bound: the latency of its phases (loads, conversions, five products), one CTA per
 // SM.  Global loads run along the rows (a warp covers whole lines): loads by the
 // thread that owns a row touch 32 lines each, and were half of the kernel's time.
-// Measured at 8 x 4096 x 16 x 128 bfloat16 (8192 CTAs): 732 us with two terms, 868 us with
-// three; of a CTA's 28k clocks about 13k go to the loads and 15k to conversions, products
-// and stores.  2.2 GB, 3.1 TB/s; tensor pipe 21%, issue slots 30%.  M and dM' copied in bulk over
-// the place of their terms, instead of loaded by all threads: 727 us, but 934 with three terms.
+// Measured at 8 x 4096 x 16 x 128 bfloat16 (8192 CTAs): 777 us with two terms (bfloat16 gates), 904 us
+// with three (fp32 gates); of a CTA's 29k clocks about 13k go to the loads and 16k to conversions,
+// products and stores.  2.2 GB, 2.9 TB/s; tensor pipe 20%, issue slots 32%.  H and Z are 43 and 36 us
+// of that; without them dg cancels (delta_common.cuh).  Without H and Z, M and dM' copied in bulk over
+// the place of their terms, instead of loaded by all threads: 727 against 732 us, but 934 against 868 with three terms.
 #pragma once
 
 #include "delta_prep.cuh"
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     if (lane == 0) rows[row_sums::MD + warp] = md;
     // The CTAs of a wave run in step: all load, then all compute.  M and dM' of the CTA that
     // likely comes next on this SM go to L2 meanwhile (808 -> 734 us with two terms, 891 -> 872
-    // with three; sent for before this CTA's own loads 865, with e's and w's rows 774).
+    // with three; sent for before this CTA's own loads 865, with e's and w's rows 774; all without H and Z).
     if (threadIdx.x == kChunkThreads - 32 && blockIdx.x + a.sms < gridDim.x) {
         const size_t next = (size_t)(blockIdx.x + a.sms) * a.Dk * a.Dv;
         bulk_prefetch(a.ds + next, (uint32_t)(a.Dk * a.Dv) * 4);

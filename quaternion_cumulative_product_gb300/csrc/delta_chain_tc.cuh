@@ -16,7 +16,7 @@
 // T and P are read across their rows (MN-major), dO^T as an MN-major left operand.
 //
 // Bound: the chain's latency, as in the forward (dM = (..) Q - (..) K is one product more).
-// Measured: 8 x 4096 x 16 x 128 bfloat16 475 us, dM' of every chunk and w written (0.8 GB,
+// Measured: 8 x 4096 x 16 x 128 bfloat16 480 us, dM' of every chunk and w written (0.8 GB,
 // 1.7 TB/s); tensor pipe 23%, issue slots 36%.  4 x 1000 x 8 x 64 fp32, in segments:
 // 49 us, and 52 us for the segments' sums.
 #pragma once

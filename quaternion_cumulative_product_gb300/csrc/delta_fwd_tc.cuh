@@ -21,10 +21,10 @@
 // between them.  A product of 64 columns takes the tensor cores as long as one of
 // 128, which is why X and Y are one.  Conversions run in pieces of 16 columns: code
 // that stays in the instruction cache while four roles run, and few registers.
-// Measured (bfloat16): 8 x 4096 x 16 x 128, 128 walks of 64 chunks, 369 us, 5.8 us a
-// chunk (484 us with the states and errors saved: 1.2 GB, 2.9 TB/s); 1 x 131072 x 16 x 64
-// in 9 segments, with their sums and join, 2.08 ms.  Under the profiler the tensor pipe is
-// busy for 22% of the time, issue slots for 35% of the GPU's (42% of an SM with a walk), and
+// Measured (bfloat16): 8 x 4096 x 16 x 128, 128 walks of 64 chunks, 375 us, 5.9 us a
+// chunk (487 us with the states and errors saved: 1.2 GB, 2.5 TB/s); 1 x 131072 x 16 x 64
+// in 19 segments, with their sums and join, 2.11 ms; 8 x 4096 x 16 x 128 fp32 904 us.  Under the
+// profiler the tensor pipe is busy for 22% of the time, issue slots for 35% of the GPU's (43% of an SM with a walk), and
 // stalls are loads from tensor memory, the walk's barriers and the waits for products.
 #pragma once
 
