@@ -119,8 +119,8 @@ int quat_delta_fwd(int dtype, int gate_dtype, float scale,
  * Its vector-Jacobian product from the carries and errors of the forward, for
  * cotangents d_o (contiguous, `dtype`) and d_final (fp32, NULL: zeros): d_q,
  * d_k, d_v (`dtype`; the first two summed over the value heads that share a key
- * head), d_g, d_beta (`gate_dtype`), d_init (fp32, NULL: not written).
- * Sums run in a fixed order.
+ * head), d_g, d_beta (`gate_dtype`), d_init (fp32, NULL: not written).  d_g is
+ * exactly zero where exp(g) is zero in fp32.  Sums run in a fixed order.
  */
 int quat_delta_bwd(int dtype, int gate_dtype, float scale,
                    const void *q, const void *k, const void *v, const void *g, const void *beta,
