@@ -19,8 +19,9 @@ chunk carries between the two), ``quat_cumprod_fwd_bf16`` /
 tensors, copies overlapped with the kernels), ``quat_cumprod_plan`` and
 ``quat_cumprod_status``.  The operators around the scan (norm and rotation of
 queries and keys, the gated delta rule) are in
-:mod:`quaternion_cumulative_product_gb300.mixer` and reached from here too.  The
-autograd wrappers are in :mod:`quaternion_cumulative_product_gb300.autograd`.
+:mod:`quaternion_cumulative_product_gb300.mixer`, those of a residual block (layer
+norm, dropout) in :mod:`quaternion_cumulative_product_gb300.block`; both are reached
+from here too.  The autograd wrappers are in :mod:`quaternion_cumulative_product_gb300.autograd`.
 """
 from __future__ import annotations
 
@@ -40,6 +41,7 @@ __all__ = [
     "QS_DELTA_STEPS", "QS_DELTA_MAX_D", "QS_ROTATE_MAX_D",
     "quat_norm_rotate_fwd", "quat_norm_rotate_bwd", "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd",
     "quat_delta_step",
+    "QS_NORM_MAX_D", "quat_layer_norm_fwd", "quat_layer_norm_bwd", "quat_dropout_fwd", "quat_dropout_bwd",
 ]
 
 QS_OK = 0
@@ -451,9 +453,17 @@ _MIXER = ("QS_DELTA_MAX_D", "QS_DELTA_STEPS", "QS_ROTATE_MAX_D", "quat_delta_bwd
           "quat_delta_fwd_carries", "quat_delta_step", "quat_norm_rotate_bwd", "quat_norm_rotate_fwd")
 
 
+_BLOCK = ("QS_NORM_MAX_D", "quat_dropout_bwd", "quat_dropout_fwd", "quat_layer_norm_bwd", "quat_layer_norm_fwd")
+
+
 def __getattr__(name):
-    if name not in _MIXER:
+    if name in _MIXER:
+        from . import mixer as module
+        names = _MIXER
+    elif name in _BLOCK:
+        from . import block as module
+        names = _BLOCK
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import mixer
-    globals().update({n: getattr(mixer, n) for n in _MIXER})
+    globals().update({n: getattr(module, n) for n in names})
     return globals()[name]

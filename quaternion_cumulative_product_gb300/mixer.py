@@ -131,13 +131,14 @@ def _with_stream(fn):
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        q = args[0] if args else kw.get("q")
+        q = args[0] if args else kw.get(first)
         if isinstance(q, torch.Tensor) and q.is_cuda and q.device != stream.device:
             raise ValueError(f"stream is on {stream.device}, expected {q.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
 
     said = inspect.signature(fn)
+    first = next(iter(said.parameters))
     call.__signature__ = said.replace(parameters=[*said.parameters.values(),
                                                   inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
