@@ -142,6 +142,43 @@ int quat_delta_step(int dtype, int gate_dtype, float scale,
                     float *state, const int32_t *slots, void *o, const int64_t *strides,
                     int64_t P, int64_t N, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, void *stream);
 
+/*
+ * Linear attention with a decay for each head, over whole sequences.  For every
+ * value head h (with key head h / (Hv/Hk)) a state M [Dk,Dv] runs along the sequence:
+ *
+ *     M_t = exp(g_t) M_{t-1} + k_t v_t^T
+ *     o_t = scale * M_t^T q_t
+ *
+ * Tensors, sequences, strides and sizes are those of quat_delta_fwd (without beta);
+ * init NULL: zeros, final_state NULL: not written.  A NaN or infinity at a step
+ * spoils the outputs of its sequence from the start of its chunk (at most 128 steps)
+ * on, never another sequence's.
+ */
+int quat_decay_fwd(int dtype, int gate_dtype, float scale,
+                   const void *q, const void *k, const void *v, const void *g, const float *init,
+                   void *o, float *final_state, const int64_t *strides, const int32_t *offsets, int64_t N,
+                   int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, void *stream);
+
+/*
+ * Its vector-Jacobian product, recomputed from the inputs, for cotangents d_o
+ * (contiguous, `dtype`) and d_final (fp32, NULL: zeros): d_q, d_k (`dtype`; summed over
+ * the value heads that share a key head), d_v (`dtype`), d_g (`gate_dtype`; exactly zero
+ * where exp(g) is zero in fp32), d_init (fp32, NULL: not written).  Sums run in a fixed
+ * order.  Scratch: the states between chunks.
+ */
+int quat_decay_bwd(int dtype, int gate_dtype, float scale,
+                   const void *q, const void *k, const void *v, const void *g, const float *init,
+                   const void *d_o, const float *d_final,
+                   void *d_q, void *d_k, void *d_v, void *d_g, float *d_init,
+                   const int64_t *strides, const int32_t *offsets, int64_t N,
+                   int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, void *stream);
+
+/* The same recurrence for T new tokens (usually one) of each of N sequences, on a pool of states, as quat_delta_step. */
+int quat_decay_step(int dtype, int gate_dtype, float scale,
+                    const void *q, const void *k, const void *v, const void *g,
+                    float *state, const int32_t *slots, void *o, const int64_t *strides,
+                    int64_t P, int64_t N, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,7 +40,7 @@ __all__ = [
     "quat_cumprod_strerror",
     "QS_DELTA_STEPS", "QS_DELTA_MAX_D", "QS_ROTATE_MAX_D",
     "quat_norm_rotate_fwd", "quat_norm_rotate_bwd", "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd",
-    "quat_delta_step",
+    "quat_delta_step", "quat_decay_fwd", "quat_decay_bwd", "quat_decay_step",
     "QS_NORM_MAX_D", "quat_layer_norm_fwd", "quat_layer_norm_bwd", "quat_dropout_fwd", "quat_dropout_bwd",
 ]
 
@@ -449,7 +449,7 @@ def quat_cumprod_status(stream=None, device=None):
 
 
 # The operators around the scan, loaded (with torch) at their first use.
-_MIXER = ("QS_DELTA_MAX_D", "QS_DELTA_STEPS", "QS_ROTATE_MAX_D", "quat_delta_bwd", "quat_delta_fwd",
+_MIXER = ("QS_DELTA_MAX_D", "QS_DELTA_STEPS", "QS_ROTATE_MAX_D", "quat_decay_bwd", "quat_decay_fwd", "quat_decay_step", "quat_delta_bwd", "quat_delta_fwd",
           "quat_delta_fwd_carries", "quat_delta_step", "quat_norm_rotate_bwd", "quat_norm_rotate_fwd")
 
 

@@ -16,12 +16,12 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in
-           ("quat_scan.cu", "norm_rotate.cu", "delta_rule.cu", "delta_step.cu", "layer_norm.cu", "dropout.cu")]
+           ("quat_scan.cu", "norm_rotate.cu", "delta_rule.cu", "delta_step.cu", "decay.cu", "layer_norm.cu", "dropout.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("quat_device.cuh", "quat_common.cuh", "quat_tiles.cuh", "quat_chain.cuh", "quat_walk.cuh",
             "quat_segwalk.cuh", "quat_segwalk_ws.cuh", "quat_segwalk_bwd.cuh", "quat_segwalk_tab.cuh",
             "quat_short.cuh", "quat_host.h", "workspace.h", "mixer_device.cuh", "delta_common.cuh", "tensor_core.cuh",
-            "delta_prep.cuh", "delta_fwd_tc.cuh", "delta_bwd_tc.cuh", "delta_chain_tc.cuh")]
+            "delta_prep.cuh", "delta_fwd_tc.cuh", "delta_bwd_tc.cuh", "delta_chain_tc.cuh", "delta_host.cuh")]
 DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", f) for f in ("quat_cumprod.h", "quat_mixer.h", "quat_block.h")]
 LIB = os.path.join(HERE, "libquatscan.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -104,7 +104,7 @@ __device__ __forceinline__ void unit_terms(uint32_t at, uint32_t term, const flo
 
 __device__ __forceinline__ float4 scaled(const float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
 
-template <typename T, int NT, int CT, int DK>
+template <typename T, int NT, int CT, int DK, bool RULE = true>
 __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const __grid_constant__ DeltaArgs a) {
     using L = ChunkLayout<NT, CT, DK>;
     extern __shared__ unsigned char raw[];
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc_all(&bar.tmem);
-    if (warp == 1) warp_gates(gt, read_gates(a, seq, t0, head));
+    if (warp == 1) warp_gates(gt, read_gates<RULE>(a, seq, t0, head));
     {   // Q by half of the threads, K by the others
         const int w = wg / 2;
         load_rows<T, NT, DK, 256>(sm32 + L::QK_AT + w * TILE, 2 * TILE, L::QK_TERM, w ? a.k : a.q, w ? a.sk : a.sq, seq, t0, kh, a.Dk,
@@ -201,9 +201,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
             const int i = threadIdx.x + kChunkThreads * j, r = i / UNITS, x = i % UNITS * 8 + round * 64, xr = x - round * 64;
             const bool in = r < left && x < a.Dv;
             const size_t at = in ? ((size_t)(row0 + r) * a.Hv + head) * a.Dv + x : 0;
-            const float4 *ep = reinterpret_cast<const float4 *>(a.errors_in + at), *wp = reinterpret_cast<const float4 *>(a.w + at);
-            float4 e0 = __ldg(ep), e1 = __ldg(ep + 1), w0 = __ldg(wp), w1 = __ldg(wp + 1);
-            if (!in) e0 = e1 = w0 = w1 = q_zero();
+            float4 e0 = q_zero(), e1 = q_zero(), w0 = q_zero(), w1 = q_zero();
+            if constexpr (RULE) {
+                const float4 *ep = reinterpret_cast<const float4 *>(a.errors_in + at), *wp = reinterpret_cast<const float4 *>(a.w + at);
+                e0 = __ldg(ep), e1 = __ldg(ep + 1), w0 = __ldg(wp), w1 = __ldg(wp + 1);
+                if (!in) e0 = e1 = w0 = w1 = q_zero();
+            } else if (in) {   // e = v, and no row of keys (w = 0)
+                const T *vp = static_cast<const T *>(a.v) + seq.b * a.sv.b + (seq.s0 + t0 + r) * a.sv.s + (long long)head * a.sv.h + x;
+                e0 = load4(vp), e1 = load4(vp + 4);
+            }
             const uint32_t stage = sm32 + L::A_AT + xr / 64 * L::A_HALF;
             if constexpr (NT == 1) {
                 cp_async16_or_zero(stage + swizzled(r, xr % 64 / 8), static_cast<const T *>(a.d_o) + at, in);
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_tc_kernel(const 
     }
     tc_fence_after();
     const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
-    if (wg == 0 && !keys && live) store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, rows[t]);
+    if (RULE && wg == 0 && !keys && live) store_any(a.dbeta, a.gate16, (row0 + t) * a.Hv + head, rows[t]);
 
     // This warpgroup's quarter of an accumulator's columns: to registers, and added back.
     auto read_part = [&](uint32_t at, uint32_t *v) {

@@ -34,7 +34,7 @@ constexpr uint32_t G = 448;
 }  // namespace chain_tmem
 
 // SUM: sums a segment up (delta_prep.cuh) and writes neither dM' nor w.
-template <typename T, int NT, int DK, bool SUM>
+template <typename T, int NT, int DK, bool SUM, bool RULE = true>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_chain_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
     if (wg >= 2) {
         const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
-        walk_prep<T, NT, DK, 3, true>(a, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
+        walk_prep<T, NT, DK, 3, true, RULE>(a, a.d_o, so, bar, sm, seq, chunks, head, tm, chain_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of dM per thread
         const uint32_t tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 issue_ts<3, NT, 2, DK / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 64, smem_desc(rows, 16, 1024), L::KQ_TERM,
                                             mma_desc(128, 64), TmemK(), KMajor());
                 mma_commit(&bar.x);
+                if (!RULE) mma_commit(&bar.empty[it % L::S]);
             }
             __syncwarp();
             auto write_ds = [&](int part) {   // dM', half of it behind each of two products
@@ -148,12 +149,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     e[i] = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
                                 *reinterpret_cast<const float2 *>(&gt.left[h + 2 * i]),
                                 SUM && row.map ? make_float2(0.f, 0.f) : make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])));
-                put_terms3(tl + chain_tmem::SP + h / 2, 32, e);
+                if constexpr (RULE) {
+                    put_terms3(tl + chain_tmem::SP + h / 2, 32, e);
+                } else {   // w as it is
+                    tmem_st16(tl + chain_tmem::X + h, reinterpret_cast<const uint32_t *>(e));
+                }
             }
             tmem_wait_st();
             tc_fence_before();
             named_bar_sync(1, 256);
-            if (warp == 0 && elect_one() && ok) {
+            if (RULE && warp == 0 && elect_one() && ok) {
                 tc_fence_after();
                 issue_ts<3, 3, 2, DC / 16>(tm + chain_tmem::X, tm + chain_tmem::SP, 32, smem_desc(tile_t, 16, 1024), TILE,
                                            mma_desc(128, 64, false, true), TmemK(), MNMajor());
@@ -162,8 +167,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
             __syncwarp();
             write_ds(1);
-            ok &= tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
+            if (RULE) ok &= tc_wait_warp(&bar.e, it & 1, gone, a.ctl);
+            else tc_fence_after();
             if (wg == 0) {
+              if constexpr (RULE) {
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {   // -exp(G) beta w
                     uint32_t r[16];
@@ -177,6 +184,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                                     *reinterpret_cast<const float2 *>(&gt.grown[h + 2 * i]));
                     put_terms3(tl + chain_tmem::SP + 96 + h / 2, 32, z);
                 }
+              }
             } else {   // scale exp(G) dO, where the terms of X + R were
 #pragma unroll 1
                 for (int h = 0; h < DC; h += 16) {
@@ -199,7 +207,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 // Both products' small terms, then both products' first ones: a pass cuts off the last
                 // bit of what the accumulator holds by then.
 #pragma unroll 1
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; n += RULE ? 1 : 2)
                     issue_ts<3, NT, 2, DC / 16>(tm + chain_tmem::D, tm + chain_tmem::SP + n % 2 * 96, 32,
                                                 smem_desc(n % 2 ? rows : rows + TILE, 2 * TILE, 1024), L::KQ_TERM, id, TmemK(), MNMajor(),
                                                 n > 0, n < 2 ? kSmallPairs : kFirstPair);
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     float x[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
-                    store_columns(wo, step, left - h, in, x);
+                    if (RULE) store_columns(wo, step, left - h, in, x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] *= gt.beta[h + i];
                     store_columns(vo, step, left - h, in, x);

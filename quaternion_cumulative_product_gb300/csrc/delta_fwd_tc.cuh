@@ -47,7 +47,7 @@ struct UAt {   // U's columns: K step k of a term
 };
 
 // SUM: sums a segment up (delta_prep.cuh) and writes no o.
-template <typename T, int NT, int DK, bool SUM>
+template <typename T, int NT, int DK, bool SUM, bool RULE = true>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     delta_fwd_tc_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap vmap) {
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const uint32_t tm = walk_setup<L>(bar, sm32);
 
     if (wg >= 2) {
-        walk_prep<T, NT, DK, PT, false>(a, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
+        walk_prep<T, NT, DK, PT, false, RULE>(a, a.v, a.sv, bar, sm, seq, chunks, head, tm, fwd_tmem::G);
     } else {
         constexpr int HALF = DK / 2;             // columns of the state per thread
         constexpr bool kEarly = NT == 1;         // U has a place of its own: the next chunk need not wait for o
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         };
         // o of chunk c, this warpgroup's half of the steps.
         auto write_o = [&](int c) {
+            if (!RULE && !a.o) return;
             ok &= tc_wait_warp(&bar.o, c & 1, gone, a.ctl);
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             T *out = static_cast<T *>(a.o) + ((size_t)(row0 + (long long)c * DC + wg * 32) * a.Hv + head) * a.Dv + dv;
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             write_carry(0);
             if (!SUM && c > 0) write_o(c - 1);
             ok &= tc_wait_warp(&bar.x, c & 1, gone, a.ctl);
+            if constexpr (RULE) {
 #pragma unroll 1
             for (int h = wg * 32; h < wg * 32 + 32; h += 16) {   // v - exp(G) X
                 uint32_t r[16];
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mma_commit(&bar.e);
             }
             __syncwarp();
+            }
             if (!SUM) {   // Y moves, so that dM can take its place and o add up on it
 #pragma unroll 1
                 for (int h = wg * 32; h < wg * 32 + 32; h += 16) {
@@ -204,17 +207,25 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
             }
             write_carry(1);
-            ok &= tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
+            if (RULE) ok &= tc_wait_warp(&bar.e, c & 1, gone, a.ctl);
             const int h0 = wg * 32;
             float2 u[16];   // beta e
-            {
+            if constexpr (!RULE) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float v[16];
+                    third_column<NT>(sm + c % L::KS * L::ROWS + L::V_AT, dv, h0 + q * 16, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[q * 8 + i] = SUM && row.map ? make_float2(0.f, 0.f) : make_float2(v[2 * i], v[2 * i + 1]);
+                }
+            } else {
                 uint32_t r[32];   // (U takes the place of 32 columns of e: all are read first)
                 tmem_ld32(tl + fwd_tmem::X + h0, r);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) u[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
             }
-            if (!SUM && a.errors && in) {
+            if (RULE && !SUM && a.errors && in) {
                 float *eo = a.errors + ((size_t)(row0 + (long long)c * DC + h0) * a.Hv + head) * a.Dv + dv;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)

@@ -30,16 +30,22 @@ struct __align__(16) ChunkGates {
     float whole;                           // exp(G_C)
 };
 
+// RULE, here and in the kernels: the gated delta rule; else linear attention with a decay,
+// which is the rule without its errors (e = v, no T) and without beta (1).
+
 // A lane's two steps of a chunk's gates as they are read (one warp per chunk).
 struct RawGates {
     float g[2], beta[2];
 };
+template <bool RULE = true>
 __device__ __forceinline__ RawGates read_gates(const DeltaArgs &a, const Seq &seq, long long t0, int head) {
     const int lane = threadIdx.x % 32;
     RawGates r;
     const long long left = seq.len - t0, row = (seq.b * a.S + seq.s0 + t0) * a.Hv + head;
     const int i0 = 2 * lane < left ? 2 * lane : 0, i1 = 2 * lane + 1 < left ? 2 * lane + 1 : 0;
-    if (a.gate16) {
+    if constexpr (!RULE) {
+        r = {{load_any(a.g, a.gate16, row + (long long)i0 * a.Hv), load_any(a.g, a.gate16, row + (long long)i1 * a.Hv)}, {1.f, 1.f}};
+    } else if (a.gate16) {
         const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(a.g) + row, *be = static_cast<const __nv_bfloat16 *>(a.beta) + row;
         const __nv_bfloat16 x = g[(long long)i0 * a.Hv], y = g[(long long)i1 * a.Hv], z = be[(long long)i0 * a.Hv], w = be[(long long)i1 * a.Hv];
         r = {{__bfloat162float(x), __bfloat162float(y)}, {__bfloat162float(z), __bfloat162float(w)}};
@@ -436,7 +442,7 @@ __device__ __forceinline__ void drain_walk(WalkBars &bar, const Control &ctl) {
 }
 
 // The role of prep's threads (ptid 0 .. 255).  BWD: the backward's order and N.
-template <typename T, int NT, int DK, int PT, bool BWD>
+template <typename T, int NT, int DK, int PT, bool BWD, bool RULE = true>
 __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third, const qsh::Strides &st3, WalkBars &bar, unsigned char *sm,
                                           const Seq &seq, int chunks, int head, uint32_t tm, uint32_t gram_at) {
     using L = WalkLayout<NT, DK, PT>;
@@ -477,8 +483,8 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
     };
     RawGates raw = {};
     if (warp == 7 && chunks > 0) {
-        warp_gates(gates[0], read_gates(a, seq, chunk_start<BWD>(0, chunks), head));
-        if (chunks > 1) raw = read_gates(a, seq, chunk_start<BWD>(1, chunks), head);
+        warp_gates(gates[0], read_gates<RULE>(a, seq, chunk_start<BWD>(0, chunks), head));
+        if (chunks > 1) raw = read_gates<RULE>(a, seq, chunk_start<BWD>(1, chunks), head);
     }
     if (NT == 1 && chunks > 0) {
         named_bar_sync(2, kPrepThreads);
@@ -534,6 +540,7 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = x[i] == 0.f ? 0.f : x[i] * __uint_as_float(g[i]);   // (masked places stay 0)
+                if (!RULE && keys) continue;   // (no T)
                 if (keys) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
@@ -552,12 +559,14 @@ __device__ __forceinline__ void walk_prep(const DeltaArgs &a, const void *third,
         if (it + 1 < chunks) {   // the next chunk's gates and Gram products, under way while this one is inverted
             if (warp == 7) {
                 warp_gates(gates[(it + 1) & 3], raw);
-                if (it + 2 < chunks) raw = read_gates(a, seq, chunk_start<BWD>(it + 2, chunks), head);
+                if (it + 2 < chunks) raw = read_gates<RULE>(a, seq, chunk_start<BWD>(it + 2, chunks), head);
             }
             if (L::KS > 2) gram(it + 1);
         }
-        invert_64(tf, ptid, 2);
-        store_inverse(slot, tf, ptid);
+        if (RULE) {
+            invert_64(tf, ptid, 2);
+            store_inverse(slot, tf, ptid);
+        }
         fence_proxy_async_smem();
         named_bar_sync(2, kPrepThreads);
         if (ptid == 0) mbar_arrive(&bar.full[it % L::S]);

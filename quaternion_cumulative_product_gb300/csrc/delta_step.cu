@@ -1,10 +1,11 @@
-// delta_step.cu -- the gated delta rule for single tokens (or a few), on states
-// that stay in a pool.
+// delta_step.cu -- the gated delta rule and linear attention with a decay for single
+// tokens (or a few), on states that stay in a pool.
 //
 // Mathematics.  With a = exp(g), x = M^T k and y = M^T q of the old state M:
 //     e = v - a x,   u = beta e,   M' = a M + k u^T,   o = scale (a y + <q, k> u),
 // so both products with the state are taken in one read of it and one round of
-// sums; the new state follows without a second pass.
+// sums; the new state follows without a second pass.  Linear attention with a decay is
+// the same with u = v and without x.
 //
 // Bound: memory (the state is read and written once: 8 bytes a value against 7
 // operations).  A CTA of 128 threads holds Dk x 32 values of one head's state in
@@ -43,7 +44,8 @@ struct StepArgs {
     float scale;
 };
 
-template <typename T>
+// DELTA: the delta rule; else linear attention with a decay (no beta, u = v).
+template <typename T, bool DELTA>
 __global__ void __launch_bounds__(kThreads, 5) delta_step_kernel(const StepArgs a) {
     __shared__ float part[2][4][3][kCols];   // [token parity][warp][x, y; <q,k>][column]
     const unsigned tile = blockIdx.x % a.tiles, head = (blockIdx.x / a.tiles) % a.Hv;
@@ -89,22 +91,24 @@ __global__ void __launch_bounds__(kThreads, 5) delta_step_kernel(const StepArgs 
             k[i] = on ? qs::load1(kp + (long long)t * a.sk.s + i) : 0.f;
         }
         const long long gi = ((long long)n * a.T + t) * a.Hv + head;
-        const float alpha = expf(qs::load_any(a.g, a.gate16, gi)), beta = qs::load_any(a.beta, a.gate16, gi);
+        const float alpha = expf(qs::load_any(a.g, a.gate16, gi)), beta = DELTA ? qs::load_any(a.beta, a.gate16, gi) : 1.f;
         const float4 v = in ? qs::load4(vp + (long long)t * a.sv.s) : qs::q_zero();
         float4 x = qs::q_zero(), y = qs::q_zero();
         float qk = 0.f;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            x = make_float4(fmaf(k[i], m[i].x, x.x), fmaf(k[i], m[i].y, x.y), fmaf(k[i], m[i].z, x.z), fmaf(k[i], m[i].w, x.w));
+            if (DELTA) x = make_float4(fmaf(k[i], m[i].x, x.x), fmaf(k[i], m[i].y, x.y), fmaf(k[i], m[i].z, x.z), fmaf(k[i], m[i].w, x.w));
             y = make_float4(fmaf(q[i], m[i].x, y.x), fmaf(q[i], m[i].y, y.y), fmaf(q[i], m[i].z, y.z), fmaf(q[i], m[i].w, y.w));
             qk = fmaf(q[i], k[i], qk);
         }
 #pragma unroll
         for (int s = 8; s < 32; s *= 2) {
-            x.x += __shfl_xor_sync(0xffffffffu, x.x, s);
-            x.y += __shfl_xor_sync(0xffffffffu, x.y, s);
-            x.z += __shfl_xor_sync(0xffffffffu, x.z, s);
-            x.w += __shfl_xor_sync(0xffffffffu, x.w, s);
+            if (DELTA) {
+                x.x += __shfl_xor_sync(0xffffffffu, x.x, s);
+                x.y += __shfl_xor_sync(0xffffffffu, x.y, s);
+                x.z += __shfl_xor_sync(0xffffffffu, x.z, s);
+                x.w += __shfl_xor_sync(0xffffffffu, x.w, s);
+            }
             y.x += __shfl_xor_sync(0xffffffffu, y.x, s);
             y.y += __shfl_xor_sync(0xffffffffu, y.y, s);
             y.z += __shfl_xor_sync(0xffffffffu, y.z, s);
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 5) delta_step_kernel(const StepArgs 
         }
         float(*p)[3][kCols] = part[t & 1];
         if (lane < 8) {
-            qs::store4(&p[warp][0][lane * 4], x);
+            if (DELTA) qs::store4(&p[warp][0][lane * 4], x);
             qs::store4(&p[warp][1][lane * 4], y);
             if (lane == 0) p[warp][2][0] = qk;
         }
@@ -123,14 +127,13 @@ __global__ void __launch_bounds__(kThreads, 5) delta_step_kernel(const StepArgs 
         qk = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float4 px = *reinterpret_cast<const float4 *>(&p[w][0][(lane % 8) * 4]);
             const float4 py = *reinterpret_cast<const float4 *>(&p[w][1][(lane % 8) * 4]);
-            x = qs::q_add(x, px);
+            if (DELTA) x = qs::q_add(x, *reinterpret_cast<const float4 *>(&p[w][0][(lane % 8) * 4]));
             y = qs::q_add(y, py);
             qk += p[w][2][0];
         }
-        const float4 u = make_float4(beta * fmaf(-alpha, x.x, v.x), beta * fmaf(-alpha, x.y, v.y),
-                                     beta * fmaf(-alpha, x.z, v.z), beta * fmaf(-alpha, x.w, v.w));
+        const float4 u = DELTA ? make_float4(beta * fmaf(-alpha, x.x, v.x), beta * fmaf(-alpha, x.y, v.y),
+                                             beta * fmaf(-alpha, x.z, v.z), beta * fmaf(-alpha, x.w, v.w)) : v;
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
             m[i] = make_float4(fmaf(alpha, m[i].x, k[i] * u.x), fmaf(alpha, m[i].y, k[i] * u.y),
@@ -145,12 +148,10 @@ __global__ void __launch_bounds__(kThreads, 5) delta_step_kernel(const StepArgs 
         if (in && i < R && row0 + i < a.Dk) qs::store4(st + (size_t)i * a.Dv, m[i]);
 }
 
-}  // namespace
-
-extern "C" int quat_delta_step(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
-                               const void *g, const void *beta, float *state, const int32_t *slots, void *o,
-                               const int64_t *strides, int64_t P, int64_t N, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk,
-                               int64_t Dv, void *stream_) {
+template <bool DELTA>
+int step(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v, const void *g, const void *beta,
+         float *state, const int32_t *slots, void *o, const int64_t *strides, int64_t P, int64_t N, int64_t T, int64_t Hk,
+         int64_t Hv, int64_t Dk, int64_t Dv, void *stream_) {
     if ((dtype != QS_F32 && dtype != QS_BF16) || (gate_dtype != QS_F32 && gate_dtype != QS_BF16)) return QS_ERR_DIMS;
     if (P < 0 || N < 0 || T < 0 || Hk < 0 || Hv < 0 || Dk < 0 || Dv < 0) return QS_ERR_DIMS;
     const int64_t lim = int64_t(1) << 31;
@@ -161,7 +162,7 @@ extern "C" int quat_delta_step(int dtype, int gate_dtype, float scale, const voi
     if (Dk == 0 || (!slots && N > P)) return QS_ERR_DIMS;
     const unsigned tiles = (unsigned)((Dv + kCols - 1) / kCols);
     if ((__int128)N * Hv * tiles >= lim || (__int128)N * T * Hv >= ((__int128)1 << 40)) return QS_ERR_DIMS;
-    if (!q || !k || !v || !g || !beta || !o || (P && !state)) return QS_ERR_NULL;
+    if (!q || !k || !v || !g || (DELTA && !beta) || !o || (P && !state)) return QS_ERR_NULL;
     const int es = dtype == QS_BF16 ? 2 : 4, ge = gate_dtype == QS_BF16 ? 2 : 4;
     for (const void *p : {q, k, v, g, beta, (const void *)state, (const void *)slots, (const void *)o})
         if (qsh::misaligned(p)) return QS_ERR_MISALIGNED;
@@ -185,7 +186,22 @@ extern "C" int quat_delta_step(int dtype, int gate_dtype, float scale, const voi
     a.gate16 = gate_dtype == QS_BF16, a.scale = scale;
     const unsigned grid = (unsigned)(N * Hv * tiles);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (dtype == QS_BF16) delta_step_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else delta_step_kernel<float><<<grid, kThreads, 0, stream>>>(a);
+    if (dtype == QS_BF16) delta_step_kernel<__nv_bfloat16, DELTA><<<grid, kThreads, 0, stream>>>(a);
+    else delta_step_kernel<float, DELTA><<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int quat_delta_step(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
+                               const void *g, const void *beta, float *state, const int32_t *slots, void *o,
+                               const int64_t *strides, int64_t P, int64_t N, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk,
+                               int64_t Dv, void *stream) {
+    return step<true>(dtype, gate_dtype, scale, q, k, v, g, beta, state, slots, o, strides, P, N, T, Hk, Hv, Dk, Dv, stream);
+}
+
+extern "C" int quat_decay_step(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v,
+                               const void *g, float *state, const int32_t *slots, void *o, const int64_t *strides, int64_t P,
+                               int64_t N, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, void *stream) {
+    return step<false>(dtype, gate_dtype, scale, q, k, v, g, nullptr, state, slots, o, strides, P, N, T, Hk, Hv, Dk, Dv, stream);
 }

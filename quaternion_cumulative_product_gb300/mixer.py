@@ -6,7 +6,9 @@
   gated delta rule over whole sequences (equal or packed), and its backward from
   the forward's carries and errors;
 * :func:`quat_delta_step`: the gated delta rule for single tokens, on a pool of states
-  updated in place.
+  updated in place;
+* :func:`quat_decay_fwd`, :func:`quat_decay_bwd`, :func:`quat_decay_step`: the same three for
+  linear attention with a decay for each head (whose backward recomputes from the inputs).
 
 As in the rest of the binding, the calls check and marshal arguments only; the
 work runs in the library's CUDA kernels on the current torch stream (or
@@ -24,7 +26,8 @@ import torch
 from . import QS_OK, QuatScanError, _on_device, _stream_handle, load_library
 
 __all__ = ["QS_DELTA_STEPS", "QS_DELTA_MAX_D", "QS_ROTATE_MAX_D", "quat_norm_rotate_fwd", "quat_norm_rotate_bwd",
-           "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd", "quat_delta_step"]
+           "quat_delta_fwd", "quat_delta_fwd_carries", "quat_delta_bwd", "quat_delta_step",
+           "quat_decay_fwd", "quat_decay_bwd", "quat_decay_step"]
 
 QS_DELTA_STEPS = 64     # steps per chunk of the delta rule's carries
 QS_DELTA_MAX_D = 128    # largest head dimensions of the delta rule
@@ -49,7 +52,10 @@ def _lib():
                                             ("quat_norm_rotate_bwd", [c_int, c_int, c_int, f32], 13, 7),
                                             ("quat_delta_fwd", [c_int, c_int, f32], 12, 7),
                                             ("quat_delta_bwd", [c_int, c_int, f32], 17, 7),
-                                            ("quat_delta_step", [c_int, c_int, f32], 9, 7)):
+                                            ("quat_delta_step", [c_int, c_int, f32], 9, 7),
+                                            ("quat_decay_fwd", [c_int, c_int, f32], 9, 7),
+                                            ("quat_decay_bwd", [c_int, c_int, f32], 14, 7),
+                                            ("quat_decay_step", [c_int, c_int, f32], 8, 7)):
             fn = getattr(lib, name)
             fn.argtypes = head + [vp] * pointers + [i64] * sizes + [vp]
             fn.restype = c_int
@@ -232,7 +238,7 @@ def quat_norm_rotate_bwd(q, k, cum, d_q_out, d_k_out, w_q=None, w_k=None, *, nor
 # ---------------------------------------------------------------------------
 # The gated delta rule.
 # ---------------------------------------------------------------------------
-def _delta_args(q, k, v, g, beta):
+def _delta_args(q, k, v, g, beta=None):
     device = _first("q", q, 4)
     _first("v", v, 4)
     B, S, Hk, Dk = q.shape
@@ -242,7 +248,8 @@ def _delta_args(q, k, v, g, beta):
     _need("v", v, (B, S, Hv, Dv), device, q.dtype, contiguous=False)
     gate = _code(g, "g")
     _need("g", g, (B, S, Hv), device, g.dtype)
-    _need("beta", beta, (B, S, Hv), device, g.dtype)
+    if beta is not None:
+        _need("beta", beta, (B, S, Hv), device, g.dtype)
     if Hk == 0 or Hv % Hk:
         raise ValueError(f"the heads of v ({Hv}) must be a multiple of those of q and k ({Hk})")
     for name, d in (("q and k", Dk), ("v", Dv)):
@@ -333,6 +340,21 @@ def quat_delta_bwd(q, k, v, g, beta, carries, errors, d_o, d_final=None, *, scal
     return d_q, d_k, d_v, d_g, d_beta, d_init
 
 
+def _step_args(state, slots, o, v, device, N, T, Hv, Dk, Dv):
+    """Checks a pool of states and its slots; returns the output."""
+    _first("state", state, 4)
+    P = state.shape[0]
+    _need("state", state, (P, Hv, Dk, Dv), device, torch.float32)
+    if slots is not None:
+        _need("slots", slots, (N,), device, torch.int32)
+    elif N > P:
+        raise ValueError(f"{N} rows without slots need as many states, got {P}")
+    if o is None:
+        return _empty(v)
+    _need("o", o, (N, T, Hv, Dv), device, v.dtype)
+    return o
+
+
 @_with_stream
 def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None):
     """The gated delta rule for T new tokens (usually one) of N sequences: ``o``; ``state`` is updated in place.
@@ -343,18 +365,70 @@ def quat_delta_step(q, k, v, g, beta, state, *, slots=None, scale=None, o=None):
     (-1) marks an idle row, whose output is zero.  No two rows may share a slot.
     """
     device, code, gate, (N, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g, beta)
-    _first("state", state, 4)
-    P = state.shape[0]
-    _need("state", state, (P, Hv, Dk, Dv), device, torch.float32)
-    if slots is not None:
-        _need("slots", slots, (N,), device, torch.int32)
-    elif N > P:
-        raise ValueError(f"{N} rows without slots need as many states, got {P}")
-    if o is None:
-        o = _empty(v)
-    else:
-        _need("o", o, (N, T, Hv, Dv), device, v.dtype)
+    o = _step_args(state, slots, o, v, device, N, T, Hv, Dk, Dv)
     _run(_lib().quat_delta_step, "quat_delta_step", device, code, gate, Dk ** -0.5 if scale is None else scale,
          q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots),
-         o.data_ptr(), _strides(q, k, v), P, N, T, Hk, Hv, Dk, Dv)
+         o.data_ptr(), _strides(q, k, v), state.shape[0], N, T, Hk, Hv, Dk, Dv)
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head.
+# ---------------------------------------------------------------------------
+@_with_stream
+def quat_decay_fwd(q, k, v, g, init=None, *, scale=None, offsets=None):
+    """Linear attention with a decay for each head, over whole sequences: ``(o, final_state)``.
+
+    ``M_t = exp(g_t) M_{t-1} + k_t v_t^T``, ``o_t = scale * M_t^T q_t`` for each value head,
+    with the key head ``h // (Hv // Hk)``.  Tensors, ``init``, ``scale`` and ``offsets`` are
+    those of :func:`quat_delta_fwd`, without ``beta`` (a write strength is a factor of ``v``).
+    """
+    device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g)
+    _no_expanded(q=q, k=k, v=v)
+    N = _sequences(offsets, B, S, device)[0]
+    if init is not None:
+        _need("init", init, (N, Hv, Dk, Dv), device, torch.float32)
+    o = _empty(v)
+    final = torch.empty((N, Hv, Dk, Dv), dtype=torch.float32, device=device)
+    _run(_lib().quat_decay_fwd, "quat_decay_fwd", device, code, gate, Dk ** -0.5 if scale is None else scale,
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(init), o.data_ptr(), final.data_ptr(),
+         _strides(q, k, v), _ptr(offsets), N, B, S, Hk, Hv, Dk, Dv)
+    return o, final
+
+
+@_with_stream
+def quat_decay_bwd(q, k, v, g, d_o, d_final=None, init=None, *, scale=None, offsets=None):
+    """``(d_q, d_k, d_v, d_g, d_init)`` of :func:`quat_decay_fwd`, recomputed from its inputs.
+
+    ``d_o``: cotangent of ``o`` (contiguous), ``d_final``: of the final state or None;
+    ``init``: the forward's.
+    """
+    device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g)
+    _no_expanded(q=q, k=k, v=v)
+    N = _sequences(offsets, B, S, device)[0]
+    _need("d_o", d_o, (B, S, Hv, Dv), device, v.dtype)
+    for name, t in (("d_final", d_final), ("init", init)):
+        if t is not None:
+            _need(name, t, (N, Hv, Dk, Dv), device, torch.float32)
+    d_q, d_k, d_v, d_g = _empty(q), _empty(k), _empty(v), torch.empty_like(g)
+    d_init = torch.empty((N, Hv, Dk, Dv), dtype=torch.float32, device=device)
+    _run(_lib().quat_decay_bwd, "quat_decay_bwd", device, code, gate, Dk ** -0.5 if scale is None else scale,
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(init), d_o.data_ptr(), _ptr(d_final),
+         d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), d_g.data_ptr(), d_init.data_ptr(),
+         _strides(q, k, v), _ptr(offsets), N, B, S, Hk, Hv, Dk, Dv)
+    return d_q, d_k, d_v, d_g, d_init
+
+
+@_with_stream
+def quat_decay_step(q, k, v, g, state, *, slots=None, scale=None, o=None):
+    """:func:`quat_decay_fwd` for T new tokens (usually one) of N sequences: ``o``; ``state`` is updated in place.
+
+    ``q``, ``k`` [N,T,Hk,Dk], ``v`` [N,T,Hv,Dv], ``g`` [N,T,Hv]; ``state`` and ``slots`` as for
+    :func:`quat_delta_step`.
+    """
+    device, code, gate, (N, T, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g)
+    o = _step_args(state, slots, o, v, device, N, T, Hv, Dk, Dv)
+    _run(_lib().quat_decay_step, "quat_decay_step", device, code, gate, Dk ** -0.5 if scale is None else scale,
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), _ptr(slots),
+         o.data_ptr(), _strides(q, k, v), state.shape[0], N, T, Hk, Hv, Dk, Dv)
     return o
