@@ -1,11 +1,103 @@
 // decay.cu -- linear attention with a decay for each head over whole sequences: forward and
 // backward.
 //
-// Mathematics: the delta rule's chunked form (delta_common.cuh) with e_t = v_t and beta = 1,
-// so that no step of a chunk waits for another.
+// bfloat16: the walk of decay_walk.cuh.  fp32, whose values are three terms each and take
+// three times the room: the delta rule's kernels without its errors (RULE, delta_prep.cuh).
+#include "decay_walk.cuh"
 #include "delta_host.cuh"
 
 using namespace qs;
+
+namespace {
+
+// Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
+// sums up every segment but one, the join hands the states on, and the real walk starts each
+// segment from its own.
+void cut_walks(DecayArgs &a, int sms) {
+    a.segs = 1, a.seg_chunks = a.NC;
+    a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv * a.roles > sms && a.S >= 128 * a.N;
+    if (a.offsets || a.NC < 4) return;
+    const long long pairs = a.N * a.Hv * a.roles;
+    double best = (double)a.NC * ((pairs + sms - 1) / sms) * 0.9;   // cut only for a clear gain
+    for (long long want = 2; want <= 64 && want <= a.NC && pairs * want <= 4 * sms; ++want) {
+        const long long sc = (a.NC + want - 1) / want, n = (a.NC + sc - 1) / sc;
+        if (n < 2) continue;
+        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.6 * (double)((pairs * (n - 1) + sms - 1) / sms);
+        const double cost = waves * sc + 0.1 * n + 3;
+        if (cost < best) best = cost, a.segs = (int)n, a.seg_chunks = sc;
+    }
+}
+
+size_t walk_floats(const DecayArgs &a, int D) {   // of seg_m, seg_own and seg_decay of every role
+    return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * a.roles * (2 * (size_t)D * D + 4) : 0;
+}
+
+template <int D>
+int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
+    auto go = [&](auto kernel, size_t smem, long long grid) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return (int)QS_ERR_CUDA;
+        }
+        kernel<<<(unsigned)grid, kDecayThreads, smem, stream>>>(a);
+        return launched();
+    };
+    const long long pairs = a.N * a.Hv;
+    if (a.segs > 1) {
+        const size_t n = (size_t)pairs * a.segs;
+        for (int r = 0; r < a.roles; ++r, seg += n * (2 * (size_t)D * D + 4))
+            a.role[r].seg_m = seg, a.role[r].seg_own = seg + n * D * D, a.role[r].seg_decay = seg + 2 * n * D * D;
+        int rc = go(decay_walk_kernel<D, true>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1) * a.roles);
+        if (rc != QS_OK) return rc;
+        decay_join_kernel<D><<<dim3(D * D / 1024, (unsigned)pairs, (unsigned)a.roles), 256, 0, stream>>>(a);
+        rc = launched();
+        if (rc != QS_OK) return rc;
+    }
+    return go(decay_walk_kernel<D, false>, DecayLayout<D, false>::BYTES, pairs * a.segs * a.roles);
+}
+
+// A tensor [B, S, H, D] that a walk reads.
+struct Rows {
+    const void *p;
+    qsh::Strides st;
+    int64_t H, D;
+};
+
+int set_role(DecayRole &r, const DecayArgs &a, const Rows &x, const Rows &y, const Rows &z) {
+    r.gx = (int)(a.Hv / x.H), r.gy = (int)(a.Hv / y.H), r.gz = (int)(a.Hv / z.H);
+    r.dk = (int)x.D, r.dv = (int)z.D;
+    if (a.B * a.S == 0) return QS_OK;
+    int rc = qsh::head_map(&r.x, x.p, x.st, a.B, a.S, x.H, x.D);
+    if (rc == QS_OK) rc = qsh::head_map(&r.y, y.p, y.st, a.B, a.S, y.H, y.D);
+    if (rc == QS_OK) rc = qsh::head_map(&r.z, z.p, z.st, a.B, a.S, z.H, z.D);
+    return rc;
+}
+
+void set_walks(DecayArgs &a, const DeltaArgs &d) {
+    a.g = d.g, a.offsets = d.offsets, a.B = d.B, a.S = d.S, a.N = d.N, a.NC = (d.S + WC - 1) / WC, a.Hv = d.Hv;
+    a.gate16 = d.gate16, a.scale = d.scale;
+}
+
+int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
+    DecayArgs a{};
+    set_walks(a, d);
+    a.roles = 1;
+    DecayRole &r = a.role[0];
+    const int rc = set_role(r, a, {d.q, d.sq, d.Hk, d.Dk}, {d.k, d.sk, d.Hk, d.Dk}, {d.v, d.sv, d.Hv, d.Dv});
+    if (rc != QS_OK) return rc;
+    r.out = d.o, r.init = d.init, r.fin = d.fin, r.lane = 1, r.col = d.Dv;
+    cut_walks(a, sms);
+    const int D = d.Dk <= 64 && d.Dv <= 64 ? 64 : 128;
+    unsigned char *ws = nullptr;
+    qsh::Hold hold;
+    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + walk_floats(a, D) * 4, &ws, &hold);
+    if (wc != QS_OK) return wc;
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
+    float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
+    return D == 64 ? launch_decay<64>(a, seg, stream) : launch_decay<128>(a, seg, stream);
+}
+
+}  // namespace
 
 extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v, const void *g,
                               const float *init, void *o, float *final_state, const int64_t *strides, const int32_t *offsets,
@@ -31,6 +123,7 @@ extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void
     if (rc != QS_OK) return rc;
     a.q = q, a.k = k, a.v = v, a.g = g, a.init = init, a.o = o, a.fin = final_state;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (dtype == QS_BF16) return forward16(a, dev, sms, stream);
     unsigned char *ws = nullptr;
     cut(a, sms);
     qsh::Hold hold;
@@ -38,8 +131,7 @@ extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void
     if (wc != QS_OK) return wc;
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    return dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1, false>(a, seg, stream)
-                            : launch_walks<false, float, 3, false>(a, seg, stream);
+    return launch_walks<false, float, 3, false>(a, seg, stream);
 }
 
 extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v, const void *g,

@@ -1,0 +1,647 @@
+// decay_walk.cuh -- linear attention with a decay on the tensor cores, bfloat16: one walk over
+// the chunks of a (sequence, head) that serves the forward and all three products of the backward.
+//
+// A walk takes "queries" x, "keys" y [.., dk] and "values" z [.., dv] and computes
+//
+//     out_t = scale sum_s D_ts <x_t, y_s> z_s,      D_ts = exp(|G_t - G_s|'s decay between s and t)
+//
+// over the steps s <= t (forward in time) or s >= t (backward in time):
+//
+//     o  = (q, k, v) forward          dq = (dO, v, k) forward
+//     dv = (k, q, dO) backward        dk = (v, dO, q) backward
+//
+// Chunks hold C = 128 steps.  With the state M [dk][dv] that enters a chunk (from earlier steps
+// forward, later ones backward) and the decay sums G_t = g_0 + .. + g_t inside the chunk:
+//
+//     out = scale f (x M) + P z,       P_ts = scale D_ts <x_t, y_s>,     f_t = exp(G_t) | exp(G_C - G_t)
+//     M'  = exp(G_C) M + y^T (h z),                                      h_s = exp(G_C - G_s) | exp(G_s)
+//
+// (forward | backward in time).  Nothing but M' = exp(G_C) M + .. links two chunks, and that is a
+// sum in registers: the tensor cores are kept busy across chunks by roles that run at the same time:
+//
+//     state    two warpgroups: M^T [dv][dk] in fp32 registers, one value row per thread, half of dk
+//              each; M's terms to shared memory; the scaling of x M; out to memory
+//     convert  two warpgroups: P from S = x y^T (in place, in tensor memory), h z as three terms
+//     one warp each: products, copies (TMA into a ring of tiles), gates
+//
+// Per chunk, in the order of issue: Y = x M (2 terms of M), dM += (h z)^T y for the first 64
+// steps, out = f Y + P z (2 terms of P), dM for the other 64, and the next chunk's S.  The
+// product that waits for a conversion always has another one running before it.
+//
+// Terms (tensor_core.cuh): h z in three, so that states have fp32 precision; M and P, of which
+// only bfloat16 outputs are made, in two (2^-15 of a product left out at most).
+//
+// Bound: the tensor cores (8 products of 128 x 128 x 128 a chunk, 64 clocks each 16 of K: 2.1 us
+// at 1.9 GHz) and memory (131 KB a chunk) alike.
+#pragma once
+
+#include "delta_prep.cuh"
+
+namespace qs {
+
+constexpr int WC = 128;              // steps per chunk
+constexpr int kDecayThreads = 640;   // five warpgroups
+
+struct DecayRole {
+    CUtensorMap x, y, z;
+    void *out;               // [B, S, Hv, dv], bfloat16 or (out32) fp32
+    const void *beside;      // dots: <beside_t, scale f Y_t>, bfloat16, or NULL
+    float *dots;             // [2][B, S, Hv] by halves of the columns
+    const float *init;       // state that enters (first chunk of a walk) [N, Hv, ..], or NULL
+    float *fin;              // state that leaves, or NULL
+    float *dump;             // state that enters each chunk [slots, Hv, D * D], or NULL
+    const float *other;      // another walk's states at the same places: cross = exp(G_C) <other, M>
+    float *cross;            // [slots, Hv]
+    const float *seg_m;      // state that enters each segment
+    float *seg_own, *seg_decay;
+    qsh::Strides sb;         // of `beside`
+    int gx, gy, gz, gb;      // value heads that share a head of x, y, z, beside
+    int dk, dv;              // values of a row of x and y; of z and out
+    int lane, col;           // distances in init and fin of the state's dv and dk
+    bool rev, out32;
+};
+
+struct DecayArgs {
+    DecayRole role[3];
+    const void *g;
+    const int *offsets;
+    long long B, S, N, NC, seg_chunks;   // NC: chunks per sequence without offsets
+    int Hv, segs, roles;
+    bool gate16, longest_first;
+    float scale;
+    Control ctl;
+};
+
+// The state as the walks keep it between kernels: D * D floats, float4 j of (warpgroup, lane).
+template <int D>
+__device__ __forceinline__ size_t state_at(int j4, int wg, int lane) {
+    return ((size_t)j4 * 2 * D + wg * D + lane) * 4;
+}
+
+struct WalkGates {
+    Sum2 sum[WC];          // G_t
+    float h[WC], mid[WC];  // h_s; decay between s and the end of its 32 steps that faces the others
+    float whole;           // exp(G_C)
+    float pad[3];
+};
+
+struct DecayBars {
+    uint64_t full[8], empty[8], aux, gfull[2], gfree[2];
+    uint64_t s, p, y, scaled, out, ofree, vl, dm0, dm, m, drain;
+    uint32_t tmem;
+    int gone;
+};
+
+template <int D, bool SUM>
+struct DecayLayout {
+    static constexpr int HALVES = D / 64, PER = SUM ? 2 : 3;               // tiles per chunk
+    static constexpr uint32_t HALF = WC * 128, TILE_BYTES = HALVES * HALF;  // tile: [half of D][128 steps][64 values]
+    static constexpr int SLOTS = D == 64 ? 6 : 5;
+    static constexpr int GB = D == 64 ? 2 : 1;                              // chunks of gates
+    static constexpr uint32_t M_HALF = D * 128, M_TERM = HALVES * M_HALF;   // M: [term][half of dk][dv rows][64]
+    static constexpr uint32_t M_AT = SLOTS * TILE_BYTES, GATES_AT = M_AT + 2 * M_TERM;
+    static constexpr uint32_t BARS_AT = GATES_AT + GB * sizeof(WalkGates), NEED = BARS_AT + sizeof(DecayBars);
+    static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;        // one CTA per SM: it takes all of the tensor memory
+    static_assert(BYTES <= 232448, "227 KB of shared memory");
+};
+
+namespace decay_tmem {
+constexpr uint32_t S = 0;     // x y^T (128), then P: each 32 columns give way to their two terms
+constexpr uint32_t O = 128;   // x M, scaled, then out
+constexpr uint32_t DM = 256;  // the chunk's part of M'^T
+constexpr uint32_t VL = 384;  // terms of h z, 64 steps (3 x 32)
+}  // namespace decay_tmem
+
+// Arrives on a barrier that counts warps.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+// One warp: the gates of a chunk from its log decays (four steps per lane, zeros past the end).
+__device__ __forceinline__ void walk_gates(WalkGates &s, const float *raw, bool rev) {
+    const int lane = threadIdx.x % 32;
+    Sum2 in[4], run = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in[i] = run = sum2_add(run, {clamp_gate(raw[i]), 0.f});
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const Sum2 other = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+        if (lane >= o) run = sum2_add(other, run);
+    }
+    Sum2 before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Sum2 end = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+    // Lanes 8b .. 8b+7 hold block b: its last sum, and the one before its first.
+    const int edge = rev ? lane / 8 * 8 : lane / 8 * 8 + 7;
+    const Sum2 face = {__shfl_sync(0xffffffffu, rev ? before.hi : run.hi, edge), __shfl_sync(0xffffffffu, rev ? before.lo : run.lo, edge)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const Sum2 g = i < 3 ? sum2_add(before, in[i]) : run;
+        s.sum[4 * lane + i] = g;
+        s.h[4 * lane + i] = rev ? decay(g, {0.f, 0.f}) : decay(end, g);
+        s.mid[4 * lane + i] = rev ? decay(g, face) : decay(face, g);
+    }
+    if (lane == 31) s.whole = decay(end, {0.f, 0.f});
+}
+
+__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const uint32_t *r, int n, bool wide) {   // 16 values, n of them exist
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    if (wide && n >= 16) {   // 32 bytes: a whole sector
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), QS_W8(p, 0) : "memory");
+        return;
+    }
+    if (n >= 8) *reinterpret_cast<uint4 *>(out) = make_uint4(p[0], p[1], p[2], p[3]);
+    if (n >= 16) *reinterpret_cast<uint4 *>(out + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+}
+__device__ __forceinline__ void store_row(float *out, const uint32_t *r, int n) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        if (i < n) *reinterpret_cast<uint4 *>(out + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+}
+
+// SUM: the state that a segment adds up from zero, and its decay; no out.
+template <int D, bool SUM>
+__global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __grid_constant__ DecayArgs a) {
+    using L = DecayLayout<D, SUM>;
+    namespace tmem = decay_tmem;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t sm32 = smem_addr(sm);   // (1024-byte aligned: the kernel has no other shared memory)
+    DecayBars &bar = *reinterpret_cast<DecayBars *>(sm + L::BARS_AT);
+    WalkGates *gates = reinterpret_cast<WalkGates *>(sm + L::GATES_AT);
+    volatile int *gone = &bar.gone;
+
+    // Which walk: role, sequence, segment, head.
+    const int segs = SUM ? a.segs - 1 : a.segs;
+    const unsigned per = (unsigned)(a.N * segs * a.Hv);
+    const DecayRole &ro = a.role[blockIdx.x / per];
+    unsigned id = blockIdx.x % per;
+    const int head = id % a.Hv;
+    id /= a.Hv;
+    const int seg = id % segs + (SUM && ro.rev ? 1 : 0);
+    long long n = id / segs;
+    if (!SUM && a.longest_first) {
+        int *scratch = reinterpret_cast<int *>(sm);
+        n = by_length<kDecayThreads>(a.offsets, a.N, a.S, (unsigned)n, scratch, scratch + kMostOrdered, reinterpret_cast<unsigned *>(scratch + 2 * kMostOrdered));
+        __syncthreads();   // (all have read it before the tiles come)
+    }
+    long long b = n, s0 = 0, len = a.S, slot0 = n * a.NC;
+    if (a.offsets) {
+        const Seq seq = seq_of(a.offsets, a.S, n);
+        b = 0, s0 = seq.s0, len = seq.len, slot0 = s0 / WC + n;
+    }
+    if (a.segs > 1) {
+        const long long off = seg * a.seg_chunks * WC, left = len > off ? len - off : 0, most = a.seg_chunks * WC;
+        s0 += off, slot0 += seg * a.seg_chunks, len = left < most ? left : most;
+    }
+    const int chunks = (int)((len + WC - 1) / WC);
+    const size_t pair = (size_t)n * a.Hv + head, seg_at = pair * a.segs + seg;
+    const bool rev = ro.rev;
+    auto chunk_at = [&](int it) { return rev ? chunks - 1 - it : it; };   // the it-th chunk that the walk comes to
+    const int wg = warp_uniform(threadIdx.x / 128), warp = warp_uniform(threadIdx.x / 32), tid = threadIdx.x % 128;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 8; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
+        for (uint64_t *x : {&bar.aux, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
+        for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.vl, &bar.m}) mbar_init(x, 8);   // two warpgroups' warps
+        mbar_init(&bar.gfree[0], 16), mbar_init(&bar.gfree[1], 16);
+        *gone = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc_all(&bar.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = (uint32_t)warp_uniform((int)bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
+    bool ok = true;   // none of this thread's waits has run out
+    // Tiles come in the order x, y, z of each chunk (SUM: y, z); tile i is in slot i % SLOTS.
+    auto tile = [&](int it, int which) { return L::PER * it + which - (SUM ? 1 : 0); };
+    auto slot = [&](int i) { return (uint32_t)(i % L::SLOTS) * L::TILE_BYTES; };
+    // Waits of the warps that issue: whole warps go on or stop together.
+    auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, tc_wait_warp(x, parity, gone, a.ctl)) != 0; };
+    auto wait_tile = [&](int i) { return tc_wait_warp(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, gone, a.ctl); };
+
+    if (wg < 2) {
+        // ------------------------------------------------------------------ state, out
+        constexpr int HALF = D / 2;   // of dk: this thread's columns of M^T; of dv: its columns of out
+        const int col0 = wg * HALF;
+        const bool in = tid < ro.dv;
+        const size_t outside = pair * ro.dk * ro.dv + (size_t)tid * ro.lane;
+        float2 m[HALF / 2];
+        float whole = 0.f;
+#pragma unroll
+        for (int i = 0; i < HALF / 2; ++i) m[i] = make_float2(0.f, 0.f);
+        if (!SUM && a.segs > 1 && tid < D) {
+#pragma unroll
+            for (int j = 0; j < HALF / 4; ++j) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.seg_m + seg_at * D * D + state_at<D>(j, wg, tid)));
+                m[2 * j] = make_float2(v.x, v.y), m[2 * j + 1] = make_float2(v.z, v.w);
+            }
+        } else if (!SUM && ro.init && in) {
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                const float v = col0 + i < ro.dk ? __ldg(ro.init + outside + (size_t)(col0 + i) * ro.col) : 0.f;
+                if (i % 2) m[i / 2].y = v;
+                else m[i / 2].x = v;
+            }
+        }
+        // Terms of M: row tid of [term][half of dk][D rows][64].
+        auto put_m = [&](int p) {   // columns 16p ..
+            if (D == 64 && tid >= 64) return;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t t[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2<2>(m[p * 8 + u * 4 + i], t[i]);
+                const int c = col0 + p * 16 + u * 8;
+                const uint32_t at = sm32 + L::M_AT + (uint32_t)(c / 64) * L::M_HALF + swizzled(tid, c % 64 / 8);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t v[4] = {t[0][j], t[1][j], t[2][j], t[3][j]};
+                    st_shared16(at + j * L::M_TERM, v);
+                }
+            }
+        };
+        auto give_m = [&] {   // M's terms are there (SUM: dM has been read)
+            if (!SUM) fence_proxy_async_smem();
+            tc_fence_before();
+            warp_arrive(&bar.m);
+        };
+        if (!SUM) {
+#pragma unroll
+            for (int p = 0; p < HALF / 16; ++p) put_m(p);
+        }
+        give_m();
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            const int c = chunk_at(it), gb = it % L::GB;
+            const long long t0 = (long long)c * WC;
+            const WalkGates &gt = gates[gb];
+            const int left = (int)min((long long)WC, len - t0);
+            const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
+            ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+            whole = gt.whole;
+            const float f = a.scale * (rev ? decay(gt.sum[WC - 1], gt.sum[tid]) : decay(gt.sum[tid], {0.f, 0.f}));
+            warp_arrive(&bar.gfree[gb]);
+            if constexpr (!SUM) {
+                const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
+                if (ro.dump && tid < D)
+#pragma unroll
+                    for (int j = 0; j < HALF / 4; ++j)
+                        *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
+                if (ro.other) {
+                    float2 dot = make_float2(0.f, 0.f);
+                    if (tid < D)
+#pragma unroll
+                        for (int j = 0; j < HALF / 4; ++j) {
+                            const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid)));
+                            dot = fma2(m[2 * j], make_float2(v.x, v.y), dot);
+                            dot = fma2(m[2 * j + 1], make_float2(v.z, v.w), dot);
+                        }
+                    float sum = (dot.x + dot.y) * whole;
+                    __syncwarp();
+#pragma unroll
+                    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
+                }
+                uint4 be[HALF / 8];   // this row of `beside`, on its way while Y is made
+                if (ro.dots) {
+                    const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + tid) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + col0;
+#pragma unroll
+                    for (int j = 0; j < HALF / 8; ++j)
+                        be[j] = tid < left && col0 + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(p) + j) : make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+                ok &= tc_wait_warp(&bar.y, it & 1, gone, a.ctl);
+                float dot = 0.f;
+#pragma unroll
+                for (int p = 0; p < HALF / 16; ++p) {   // f Y
+                    uint32_t r[16];
+                    tmem_ld16(tl + tmem::O + col0 + p * 16, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f));
+                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
+                    }
+                    tmem_st16(tl + tmem::O + col0 + p * 16, r);
+                    if (ro.dots)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 &q = be[p * 2 + i / 4];
+                            const uint32_t w = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+                            dot = fmaf(__uint_as_float(r[2 * i]), __uint_as_float(w << 16), dot);
+                            dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
+                        }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.scaled);
+                if (ro.dots && tid < left) ro.dots[(size_t)wg * a.B * a.S * a.Hv + row] = dot;
+                __syncwarp();
+                ok &= tc_wait_warp(&bar.out, it & 1, gone, a.ctl);
+#pragma unroll
+                for (int p = 0; p < HALF / 16; ++p) {
+                    uint32_t r[16];
+                    tmem_ld16(tl + tmem::O + col0 + p * 16, r);
+                    tmem_wait_ld();
+                    const size_t at = row * ro.dv + col0 + p * 16;
+                    const int cols = tid < left ? ro.dv - col0 - p * 16 : 0;
+                    if (ro.out32) store_row(static_cast<float *>(ro.out) + at, r, cols);
+                    else store_row(static_cast<__nv_bfloat16 *>(ro.out) + at, r, cols, ro.dv % 16 == 0);
+                    __syncwarp();
+                }
+                tc_fence_before();
+                warp_arrive(&bar.ofree);
+            }
+            ok &= tc_wait_warp(&bar.dm, it & 1, gone, a.ctl);
+#pragma unroll
+            for (int p = 0; p < HALF / 16; ++p) {
+                uint32_t r[16];
+                tmem_ld16(tl + tmem::DM + col0 + p * 16, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+                if (!SUM) put_m(p);
+                __syncwarp();
+            }
+            give_m();
+        }
+        if (SUM) {
+            if (tid < D)
+#pragma unroll
+                for (int j = 0; j < HALF / 4; ++j)
+                    *reinterpret_cast<float4 *>(ro.seg_own + seg_at * D * D + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
+        } else if (ro.fin && in && seg == (rev ? 0 : a.segs - 1)) {
+#pragma unroll
+            for (int i = 0; i < HALF; ++i)
+                if (col0 + i < ro.dk) ro.fin[outside + (size_t)(col0 + i) * ro.col] = i % 2 ? m[i / 2].y : m[i / 2].x;
+        }
+        __syncwarp();
+    } else if (wg < 4) {
+        // ------------------------------------------------------------------ convert
+        const int part = wg - 2, rb = warp % 4;   // every other 32 columns of P; this warp's 32 rows
+        const unsigned char *column = sm + (D == 128 ? tid / 64 : 0) * L::HALF + tid % 8 * 2;
+        const uint32_t unit = (uint32_t)(tid % 64 / 8) << 4;
+        auto values = [&](int it, int h) {   // h z of the chunk's steps 64h ..
+            const unsigned char *p = column + slot(tile(it, 2)) + (h * 64 + part * 32) * 128;
+            const float *f = &gates[it % L::GB].h[h * 64 + part * 32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float2 e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = q * 16 + 2 * i;
+                    const float lo = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + r * 128 + (unit ^ (uint32_t)(r % 8 << 4))));
+                    const float hi = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + (r + 1) * 128 + (unit ^ (uint32_t)((r + 1) % 8 << 4))));
+                    e[i] = mul2(make_float2(lo, hi), *reinterpret_cast<const float2 *>(f + r));
+                }
+                put_terms3(tl + tmem::VL + (part * 32 + q * 16) / 2, 32, e);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar.vl);
+        };
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            const int gb = it % L::GB;
+            const WalkGates &gt = gates[gb];
+            ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+            ok &= wait_tile(tile(it, 2));
+            if (it > 0) ok &= tc_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);
+            values(it, 0);
+            if constexpr (!SUM) {
+                ok &= tc_wait_warp(&bar.s, it & 1, gone, a.ctl);
+                const Sum2 mine = gt.sum[rb * 32 + threadIdx.x % 32];
+#pragma unroll 1
+                for (int cb = part; cb < 4; cb += 2) {   // 32 columns of P
+                    const uint32_t at = tl + tmem::S + cb * 32;
+                    if (rev ? cb < rb : cb > rb) {
+                        const uint32_t z[16] = {};
+                        tmem_st16(at, z), tmem_st16(at + 16, z);
+                        continue;
+                    }
+                    uint32_t r[32];
+                    tmem_ld32(at, r);
+                    const bool diagonal = cb == rb;
+                    const float row = diagonal ? 0.f : a.scale * (rev ? decay(gt.sum[cb * 32 - 1], mine) : decay(mine, gt.sum[cb * 32 + 31]));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float2 w[8];
+                        if (diagonal) {
+                            const int t = threadIdx.x % 32;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const Sum2 o = gt.sum[cb * 32 + q * 16 + i];
+                                const bool on = rev ? q * 16 + i >= t : q * 16 + i <= t;
+                                const float d = (mine.hi - o.hi) + (mine.lo - o.lo);
+                                const float e = on ? a.scale * exp2_fast(rev ? -d : d) : 0.f;
+                                if (i % 2) w[i / 2].y = e;
+                                else w[i / 2].x = e;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = mul2(*reinterpret_cast<const float2 *>(&gt.mid[cb * 32 + q * 16 + 2 * i]), make_float2(row, row));
+                        }
+                        uint32_t t0[8], t1[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = make_float2(__uint_as_float(r[q * 16 + 2 * i]), __uint_as_float(r[q * 16 + 2 * i + 1]));
+                            float2 x = mul2(w[i], g);
+                            if (w[i].x == 0.f) x.x = 0.f;   // (masked places stay 0, whatever x y^T holds there)
+                            if (w[i].y == 0.f) x.y = 0.f;
+                            uint32_t t[2];
+                            split2<2>(x, t);
+                            t0[i] = t[0], t1[i] = t[1];
+                        }
+                        tmem_st8(at + q * 8, t0);
+                        tmem_st8(at + 16 + q * 8, t1);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.p);
+            }
+            ok &= tc_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
+            values(it, 1);
+            warp_arrive(&bar.gfree[gb]);
+        }
+    } else if (warp == 16) {
+        // ------------------------------------------------------------------ products
+        const uint32_t id_s = mma_desc(128, 128), id_y = mma_desc(128, D), id_mn = mma_desc(128, D, false, true);
+        auto k_major = [](int k) { return (uint32_t)((k / 4) * L::HALF + (k % 4) * 32) >> 4; };
+        auto all_tile = [&](int i) { return all_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1); };
+        auto scores = [&](int it) {   // S = x y^T
+            ok &= all_tile(tile(it, 0));
+            ok &= all_tile(tile(it, 1));
+            if (elect_one() && ok) {
+                const uint64_t x = smem_desc(sm32 + slot(tile(it, 0)), 16, 1024), y = smem_desc(sm32 + slot(tile(it, 1)), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::S, x + k_major(k), y + k_major(k), id_s, k > 0);
+                mma_commit(&bar.s);
+            }
+            __syncwarp();
+        };
+        if (!SUM && chunks > 0) scores(0);
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            if constexpr (!SUM) {   // Y = x M
+                ok &= all_wait(&bar.m, it & 1);
+                if (it > 0) ok &= all_wait(&bar.ofree, (it - 1) & 1);
+                if (elect_one() && ok) {
+                    const uint64_t x = smem_desc(sm32 + slot(tile(it, 0)), 16, 1024), y = smem_desc(sm32 + L::M_AT, 16, 1024);
+#pragma unroll 1
+                    for (int j = 1; j >= 0; --j)   // the small term first
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j == 0 || k > 0);
+                    mma_commit(&bar.y);
+                    mma_commit(&bar.empty[tile(it, 0) % L::SLOTS]);
+                }
+                __syncwarp();
+            } else {
+                ok &= all_wait(&bar.m, it & 1);   // dM has been read
+                ok &= all_tile(tile(it, 1));
+            }
+            auto update = [&](int h) {   // dM += (h z)^T y over 64 steps
+                ok &= all_wait(&bar.vl, h);
+                if (elect_one() && ok) {
+                    const uint64_t y = smem_desc(sm32 + slot(tile(it, 1)) + h * 64 * 128, L::HALF, 1024);
+#pragma unroll 1
+                    for (int j = 2; j >= 0; --j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(tm + tmem::DM, tm + tmem::VL + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
+                    mma_commit(h ? &bar.dm : &bar.dm0);
+                    if (h) mma_commit(&bar.empty[tile(it, 1) % L::SLOTS]), mma_commit(&bar.empty[tile(it, 2) % L::SLOTS]);
+                }
+                __syncwarp();
+            };
+            update(0);
+            if constexpr (!SUM) {   // out = f Y + P z
+                ok &= all_wait(&bar.p, it & 1);
+                ok &= all_wait(&bar.scaled, it & 1);
+                ok &= all_tile(tile(it, 2));
+                if (elect_one() && ok) {
+                    const uint64_t z = smem_desc(sm32 + slot(tile(it, 2)), L::HALF, 1024);
+#pragma unroll 1
+                    for (int j = 1; j >= 0; --j)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + j * 16 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
+                    mma_commit(&bar.out);
+                }
+                __syncwarp();
+            }
+            update(1);
+            if (!SUM && it + 1 < chunks) scores(it + 1);
+        }
+        if (elect_one() && (!ok || *gone)) drain_products(&bar.drain, a.ctl);
+        __syncwarp();
+    } else if (warp == 17) {
+        // ------------------------------------------------------------------ copies
+        // (Only in a packed batch a walk's last rows may be another sequence's; past S, TMA fills with zeros.)
+        int aux = 0, sent = 0;
+        const int tiles = L::PER * chunks;
+#pragma unroll 1
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int it = i / L::PER, which = i % L::PER + (SUM ? 1 : 0), sl = i % L::SLOTS;
+            ok &= all_wait(&bar.empty[sl], ((i / L::SLOTS) & 1) ^ 1);
+            if (!ok) break;
+            const long long t0 = (long long)chunk_at(it) * WC;
+            const int left = (int)min((long long)WC, len - t0);
+            const bool clear = a.offsets && which > 0 && left < WC;   // rows of y and z past the end count as zero
+            unsigned char *dst = sm + slot(i);
+            if (elect_one()) {
+                const CUtensorMap *map = which == 0 ? &ro.x : which == 1 ? &ro.y : &ro.z;
+                const int h = head / (which == 0 ? ro.gx : which == 1 ? ro.gy : ro.gz), s = (int)(s0 + t0);
+                uint64_t *on = clear ? &bar.aux : &bar.full[sl];
+                // (The test hook makes CTA `stall_tile` expect 16 bytes that never come.)
+                mbar_arrive_expect_tx(on, L::TILE_BYTES + ((int)blockIdx.x == a.ctl.stall_tile ? 16 : 0));
+#pragma unroll
+                for (int x = 0; x < L::HALVES; ++x) {
+                    tma_load_4d(dst + x * L::HALF, map, x * 64, h, s, (int)b, on);
+                    tma_load_4d(dst + x * L::HALF + 8192, map, x * 64, h, s + 64, (int)b, on);
+                }
+            }
+            __syncwarp();
+            sent = i + 1;
+            if (clear) {
+                ok &= all_wait(&bar.aux, aux++ & 1);
+                const uint32_t z[4] = {0, 0, 0, 0};
+                for (int k = threadIdx.x % 32; k < (WC - left) * 8; k += 32)
+#pragma unroll
+                    for (int x = 0; x < L::HALVES; ++x) st_shared16(sm32 + slot(i) + x * L::HALF + (left + k / 8) * 128 + k % 8 * 16, z);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one() && ok) mbar_arrive(&bar.full[sl]);
+                __syncwarp();
+            }
+        }
+        if (elect_one() && (!ok || *gone)) {   // copies still in flight
+            for (int i = max(0, sent - L::SLOTS); i < sent; ++i) drain_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, a.ctl);
+            if (aux) drain_wait(&bar.aux, (aux - 1) & 1, a.ctl);
+        }
+        __syncwarp();
+    } else if (warp == 18) {
+        // ------------------------------------------------------------------ gates
+        const int lane = threadIdx.x % 32;
+        float raw[4];
+        Sum2 all = {0.f, 0.f};
+        auto read = [&](int it) {
+            const long long t0 = (long long)chunk_at(it) * WC + 4 * lane, row = (b * a.S + s0 + t0) * a.Hv + head;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = t0 + i < len ? load_any(a.g, a.gate16, row + (long long)i * a.Hv) : 0.f;
+        };
+        if (chunks > 0) read(0);
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            const int gb = it % L::GB;
+            ok &= all_wait(&bar.gfree[gb], ((it / L::GB) & 1) ^ 1);
+            walk_gates(gates[gb], raw, rev);
+            __syncwarp();
+            if (SUM) all = sum2_add(all, gates[gb].sum[WC - 1]);
+            warp_arrive(&bar.gfull[gb]);
+            if (it + 1 < chunks) read(it + 1);
+        }
+        if (SUM && lane == 0) ro.seg_decay[seg_at] = decay(all, {0.f, 0.f});
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_free_all(tm);
+}
+
+// The state that enters each segment, from the state that enters the first in walking order:
+// m' = decay m + own.  A thread per four values of a (role, sequence, head).
+template <int D>
+__global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DecayArgs a) {
+    const DecayRole &ro = a.role[blockIdx.z];
+    const size_t pair = blockIdx.y;
+    const int i = blockIdx.x * 256 + threadIdx.x, j4 = i / (2 * D), wg = i / D % 2, dv = i % D;   // as state_at
+    float4 m = q_zero();
+    if (ro.init && dv < ro.dv) {
+        const float *p = ro.init + pair * ro.dk * ro.dv + (size_t)dv * ro.lane;
+        float *f = &m.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = wg * (D / 2) + j4 * 4 + k;
+            f[k] = c < ro.dk ? __ldg(p + (size_t)c * ro.col) : 0.f;
+        }
+    }
+    float *enter = const_cast<float *>(ro.seg_m);
+    for (int s = 0; s < a.segs; ++s) {
+        const size_t at = pair * a.segs + (ro.rev ? a.segs - 1 - s : s);
+        *reinterpret_cast<float4 *>(enter + at * D * D + (size_t)i * 4) = m;
+        if (s + 1 == a.segs) break;
+        const float4 own = __ldg(reinterpret_cast<const float4 *>(ro.seg_own + at * D * D + (size_t)i * 4));
+        const float d = __ldg(ro.seg_decay + at);
+        m = make_float4(fmaf(d, m.x, own.x), fmaf(d, m.y, own.y), fmaf(d, m.z, own.z), fmaf(d, m.w, own.w));
+    }
+}
+
+}  // namespace qs

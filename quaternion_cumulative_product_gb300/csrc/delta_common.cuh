@@ -80,12 +80,14 @@ struct Seq {
     long long b, s0, len, slot0;
 };
 
-__device__ __forceinline__ Seq seq_of(const DeltaArgs &a, long long n) {
-    if (!a.offsets) return {n, 0, a.S, n * a.NC};
-    const long long lo = a.offsets[n], hi = a.offsets[n + 1];
-    const long long s0 = lo < 0 ? 0 : lo > a.S ? a.S : lo;
-    const long long s1 = hi < s0 ? s0 : hi > a.S ? a.S : hi;
+__device__ __forceinline__ Seq seq_of(const int *offsets, long long S, long long n) {   // packed
+    const long long lo = offsets[n], hi = offsets[n + 1];
+    const long long s0 = lo < 0 ? 0 : lo > S ? S : lo;
+    const long long s1 = hi < s0 ? s0 : hi > S ? S : hi;
     return {0, s0, s1 - s0, s0 / DC + n};
+}
+__device__ __forceinline__ Seq seq_of(const DeltaArgs &a, long long n) {
+    return a.offsets ? seq_of(a.offsets, a.S, n) : Seq{n, 0, a.S, n * a.NC};
 }
 
 // Segment `seg` of a sequence.

@@ -316,13 +316,13 @@ struct Walk {
 
 // The sequence of CTA row i where packed sequences are walked longest first: the one that
 // i others come before.  (All threads of the CTA call this.)
-__device__ __forceinline__ unsigned by_length(const DeltaArgs &a, unsigned i) {
-    __shared__ int chunks[kMostOrdered], before[kMostOrdered];
-    __shared__ unsigned mine;
+template <int THREADS>
+__device__ __forceinline__ unsigned by_length(const int *offsets, long long N, long long S, unsigned i, int *chunks, int *before,
+                                              volatile unsigned *mine) {   // (the last three: shared memory)
     const unsigned t = threadIdx.x % kMostOrdered, part = threadIdx.x / kMostOrdered;
-    constexpr unsigned kParts = kWalkThreads / kMostOrdered;
+    constexpr unsigned kParts = THREADS / kMostOrdered;
     if (part == 0) {
-        chunks[t] = t < a.N ? (int)((seq_of(a, t).len + DC - 1) / DC) : -1;
+        chunks[t] = t < N ? (int)((seq_of(offsets, S, t).len + DC - 1) / DC) : -1;
         before[t] = 0;
     }
     __syncthreads();
@@ -332,9 +332,9 @@ __device__ __forceinline__ unsigned by_length(const DeltaArgs &a, unsigned i) {
     for (unsigned u = part; u < kMostOrdered; u += kParts) n += chunks[u] > c || (chunks[u] == c && u < t);
     atomicAdd(&before[t], n);   // (whole numbers: their order changes nothing)
     __syncthreads();
-    if (part == 0 && before[t] == (int)i) mine = t;
+    if (part == 0 && before[t] == (int)i) *mine = t;
     __syncthreads();
-    return mine;
+    return *mine;
 }
 
 template <bool SUM, bool BWD>
@@ -355,7 +355,9 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
     w.head = i % a.Hv, i /= a.Hv;
     w.seg = i % segs + (SUM && BWD ? 1 : 0);
     w.n = i / segs;
-    if (!SUM && a.longest_first) w.n = by_length(a, (unsigned)w.n);
+    __shared__ int lengths[2][kMostOrdered];
+    __shared__ unsigned mine;
+    if (!SUM && a.longest_first) w.n = by_length<kWalkThreads>(a.offsets, a.N, a.S, (unsigned)w.n, lengths[0], lengths[1], &mine);
     w.at = ((size_t)w.n * a.Hv + w.head) * a.segs + w.seg;
     return w;
 }
