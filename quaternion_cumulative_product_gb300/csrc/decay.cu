@@ -32,7 +32,7 @@ size_t walk_floats(const DecayArgs &a, int D) {   // of seg_m, seg_own and seg_d
     return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * a.roles * (2 * (size_t)D * D + 4) : 0;
 }
 
-template <int D>
+template <int D, bool BWD>
 int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
     auto go = [&](auto kernel, size_t smem, long long grid) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
@@ -47,13 +47,13 @@ int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
         const size_t n = (size_t)pairs * a.segs;
         for (int r = 0; r < a.roles; ++r, seg += n * (2 * (size_t)D * D + 4))
             a.role[r].seg_m = seg, a.role[r].seg_own = seg + n * D * D, a.role[r].seg_decay = seg + 2 * n * D * D;
-        int rc = go(decay_walk_kernel<D, true>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1) * a.roles);
+        int rc = go(decay_walk_kernel<D, true, false>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1) * a.roles);
         if (rc != QS_OK) return rc;
         decay_join_kernel<D><<<dim3(D * D / 1024, (unsigned)pairs, (unsigned)a.roles), 256, 0, stream>>>(a);
         rc = launched();
         if (rc != QS_OK) return rc;
     }
-    return go(decay_walk_kernel<D, false>, DecayLayout<D, false>::BYTES, pairs * a.segs * a.roles);
+    return go(decay_walk_kernel<D, false, BWD>, DecayLayout<D, false>::BYTES, pairs * a.segs * a.roles);
 }
 
 // A tensor [B, S, H, D] that a walk reads.
@@ -85,6 +85,11 @@ int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     DecayRole &r = a.role[0];
     const int rc = set_role(r, a, {d.q, d.sq, d.Hk, d.Dk}, {d.k, d.sk, d.Hk, d.Dk}, {d.v, d.sv, d.Hv, d.Dv});
     if (rc != QS_OK) return rc;
+    if (d.B * d.S > 0) {
+        const qsh::Strides so = {(long long)(d.S * d.Hv * d.Dv), (long long)d.Hv * d.Dv, d.Dv};
+        const int oc = qsh::head_map(&r.o, d.o, so, d.B, d.S, d.Hv, d.Dv);
+        if (oc != QS_OK) return oc;
+    }
     r.out = d.o, r.init = d.init, r.fin = d.fin, r.lane = 1, r.col = d.Dv;
     cut_walks(a, sms);
     const int D = d.Dk <= 64 && d.Dv <= 64 ? 64 : 128;
@@ -94,7 +99,7 @@ int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     if (wc != QS_OK) return wc;
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
-    return D == 64 ? launch_decay<64>(a, seg, stream) : launch_decay<128>(a, seg, stream);
+    return D == 64 ? launch_decay<64, false>(a, seg, stream) : launch_decay<128, false>(a, seg, stream);
 }
 
 }  // namespace

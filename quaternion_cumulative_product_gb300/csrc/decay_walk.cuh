@@ -35,15 +35,18 @@
 // at 1.9 GHz) and memory (131 KB a chunk) alike.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "delta_prep.cuh"
 
 namespace qs {
 
 constexpr int WC = 128;              // steps per chunk
+enum { TILE_Y, TILE_Z, TILE_X };     // a chunk's tiles, in the order in which they come
 constexpr int kDecayThreads = 640;   // five warpgroups
 
 struct DecayRole {
-    CUtensorMap x, y, z;
+    CUtensorMap x, y, z, o;  // (o: of out, bfloat16)
     void *out;               // [B, S, Hv, dv], bfloat16 or (out32) fp32
     const void *beside;      // dots: <beside_t, scale f Y_t>, bfloat16, or NULL
     float *dots;             // [2][B, S, Hv] by halves of the columns
@@ -78,16 +81,17 @@ __device__ __forceinline__ size_t state_at(int j4, int wg, int lane) {
     return ((size_t)j4 * 2 * D + wg * D + lane) * 4;
 }
 
-struct WalkGates {
-    Sum2 sum[WC];          // G_t
-    float h[WC], mid[WC];  // h_s; decay between s and the end of its 32 steps that faces the others
-    float whole;           // exp(G_C)
-    float pad[3];
+struct __align__(16) WalkGates {
+    float hi[WC];      // G_t = hi + lo, in base-2 units
+    float mid[WC];     // decay between s and the end of its 32 steps that faces the others: h_s = mid_s edge_{s/32}
+    __half lo[WC];     // (at most half an ulp of hi: 11 bits of it leave out 2^-36 of G)
+    float edge[4], whole;   // decay between the blocks' faces and where the chunk's state is; exp(G_C)
+    __device__ __forceinline__ Sum2 sum(int t) const { return {hi[t], __half2float(lo[t])}; }
 };
 
 struct DecayBars {
     uint64_t full[8], empty[8], aux, gfull[2], gfree[2];
-    uint64_t s, p, y, scaled, out, ofree, vl, dm0, dm, m, drain;
+    uint64_t s, p, y, scaled, out, ofree, staged, vl, dm0, dm, m, drain;
     uint32_t tmem;
     int gone;
 };
@@ -97,7 +101,7 @@ struct DecayLayout {
     static constexpr int HALVES = D / 64, PER = SUM ? 2 : 3;               // tiles per chunk
     static constexpr uint32_t HALF = WC * 128, TILE_BYTES = HALVES * HALF;  // tile: [half of D][128 steps][64 values]
     static constexpr int SLOTS = D == 64 ? 6 : 5;
-    static constexpr int GB = D == 64 ? 2 : 1;                              // chunks of gates
+    static constexpr int GB = 2;                                            // chunks of gates
     static constexpr uint32_t M_HALF = D * 128, M_TERM = HALVES * M_HALF;   // M: [term][half of dk][dv rows][64]
     static constexpr uint32_t M_AT = SLOTS * TILE_BYTES, GATES_AT = M_AT + 2 * M_TERM;
     static constexpr uint32_t BARS_AT = GATES_AT + GB * sizeof(WalkGates), NEED = BARS_AT + sizeof(DecayBars);
@@ -111,6 +115,13 @@ constexpr uint32_t O = 128;   // x M, scaled, then out
 constexpr uint32_t DM = 256;  // the chunk's part of M'^T
 constexpr uint32_t VL = 384;  // terms of h z, 64 steps (3 x 32)
 }  // namespace decay_tmem
+
+// A warpgroup's share of the registers: 640 x 96 at launch are 2 x 128 x 128 + 2 x 128 x 88 + 128 x 48.
+template <bool MORE, int N>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Arrives on a barrier that counts warps.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -138,21 +149,18 @@ __device__ __forceinline__ void walk_gates(WalkGates &s, const float *raw, bool 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const Sum2 g = i < 3 ? sum2_add(before, in[i]) : run;
-        s.sum[4 * lane + i] = g;
-        s.h[4 * lane + i] = rev ? decay(g, {0.f, 0.f}) : decay(end, g);
+        s.hi[4 * lane + i] = g.hi, s.lo[4 * lane + i] = __float2half_rn(g.lo);
         s.mid[4 * lane + i] = rev ? decay(g, face) : decay(face, g);
     }
+    if (lane % 8 == 0) s.edge[lane / 8] = rev ? decay(face, {0.f, 0.f}) : decay(end, face);
     if (lane == 31) s.whole = decay(end, {0.f, 0.f});
 }
 
-__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const uint32_t *r, int n, bool wide) {   // 16 values, n of them exist
+// Sixteen values of a row, n of them exist (a multiple of 8).
+__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const uint32_t *r, int n) {
     uint32_t p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-    if (wide && n >= 16) {   // 32 bytes: a whole sector
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), QS_W8(p, 0) : "memory");
-        return;
-    }
     if (n >= 8) *reinterpret_cast<uint4 *>(out) = make_uint4(p[0], p[1], p[2], p[3]);
     if (n >= 16) *reinterpret_cast<uint4 *>(out + 8) = make_uint4(p[4], p[5], p[6], p[7]);
 }
@@ -162,8 +170,11 @@ __device__ __forceinline__ void store_row(float *out, const uint32_t *r, int n) 
         if (i < n) *reinterpret_cast<uint4 *>(out + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
 }
 
-// SUM: the state that a segment adds up from zero, and its decay; no out.
-template <int D, bool SUM>
+// SUM: the state that a segment adds up from zero, and its decay; no out.  BWD: with what
+// d_g needs (dump, dots, cross).  Loops are kept rolled where registers allow: five roles
+// share the instruction cache (unrolled, warps waited for instructions 3.6 times as long as
+// they issued, and a chunk took 5.6 us instead of XXX).
+template <int D, bool SUM, bool BWD>
 __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __grid_constant__ DecayArgs a) {
     using L = DecayLayout<D, SUM>;
     namespace tmem = decay_tmem;
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
         for (uint64_t *x : {&bar.aux, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
-        for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.vl, &bar.m}) mbar_init(x, 8);   // two warpgroups' warps
+        for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.staged, &bar.vl, &bar.m}) mbar_init(x, 8);   // two warpgroups' warps
         mbar_init(&bar.gfree[0], 16), mbar_init(&bar.gfree[1], 16);
         *gone = 0;
         fence_mbar_init();
@@ -216,14 +227,16 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     tc_fence_after();
     const uint32_t tm = (uint32_t)warp_uniform((int)bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
     bool ok = true;   // none of this thread's waits has run out
-    // Tiles come in the order x, y, z of each chunk (SUM: y, z); tile i is in slot i % SLOTS.
-    auto tile = [&](int it, int which) { return L::PER * it + which - (SUM ? 1 : 0); };
+    // Tiles come in the order y, z, x of each chunk (SUM: y, z): so the slot that one takes is
+    // that of a tile which is done with early enough.  Tile i is in slot i % SLOTS.
+    auto tile = [&](int it, int which) { return L::PER * it + which; };   // `which`: Y, Z, X
     auto slot = [&](int i) { return (uint32_t)(i % L::SLOTS) * L::TILE_BYTES; };
     // Waits of the warps that issue: whole warps go on or stop together.
     auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, tc_wait_warp(x, parity, gone, a.ctl)) != 0; };
     auto wait_tile = [&](int i) { return tc_wait_warp(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, gone, a.ctl); };
 
     if (wg < 2) {
+        set_registers<true, 128>();
         // ------------------------------------------------------------------ state, out
         constexpr int HALF = D / 2;   // of dk: this thread's columns of M^T; of dv: its columns of out
         const int col0 = wg * HALF;
@@ -283,15 +296,15 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
             ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
-            const float f = a.scale * (rev ? decay(gt.sum[WC - 1], gt.sum[tid]) : decay(gt.sum[tid], {0.f, 0.f}));
+            const float f = a.scale * (rev ? decay(gt.sum(WC - 1), gt.sum(tid)) : decay(gt.sum(tid), {0.f, 0.f}));
             warp_arrive(&bar.gfree[gb]);
             if constexpr (!SUM) {
                 const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
-                if (ro.dump && tid < D)
+                if (BWD && ro.dump && tid < D)
 #pragma unroll
                     for (int j = 0; j < HALF / 4; ++j)
                         *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
-                if (ro.other) {
+                if (BWD && ro.other) {
                     float2 dot = make_float2(0.f, 0.f);
                     if (tid < D)
 #pragma unroll
@@ -306,32 +319,31 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
                 }
-                uint4 be[HALF / 8];   // this row of `beside`, on its way while Y is made
-                if (ro.dots) {
-                    const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + tid) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + col0;
-#pragma unroll
-                    for (int j = 0; j < HALF / 8; ++j)
-                        be[j] = tid < left && col0 + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(p) + j) : make_uint4(0, 0, 0, 0);
-                }
+                const __nv_bfloat16 *be = nullptr;
+                if (BWD && ro.dots)
+                    be = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(tid, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + col0;
                 __syncwarp();
                 ok &= tc_wait_warp(&bar.y, it & 1, gone, a.ctl);
                 float dot = 0.f;
-#pragma unroll
-                for (int p = 0; p < HALF / 16; ++p) {   // f Y
+#pragma unroll 1
+                for (int p = 0; p < HALF; p += 16) {   // f Y
                     uint32_t r[16];
-                    tmem_ld16(tl + tmem::O + col0 + p * 16, r);
+                    uint4 q[2];
+                    if (BWD && be)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) q[j] = col0 + p + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(be + p) + j) : make_uint4(0, 0, 0, 0);
+                    tmem_ld16(tl + tmem::O + col0 + p, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f));
                         r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
                     }
-                    tmem_st16(tl + tmem::O + col0 + p * 16, r);
-                    if (ro.dots)
+                    tmem_st16(tl + tmem::O + col0 + p, r);
+                    if (BWD && be)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint4 &q = be[p * 2 + i / 4];
-                            const uint32_t w = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+                            const uint32_t w = i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w;
                             dot = fmaf(__uint_as_float(r[2 * i]), __uint_as_float(w << 16), dot);
                             dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
                         }
@@ -339,36 +351,61 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.scaled);
-                if (ro.dots && tid < left) ro.dots[(size_t)wg * a.B * a.S * a.Hv + row] = dot;
+                if (BWD && ro.dots && tid < left) ro.dots[(size_t)wg * a.B * a.S * a.Hv + row] = dot;
                 __syncwarp();
-                ok &= tc_wait_warp(&bar.out, it & 1, gone, a.ctl);
-#pragma unroll
-                for (int p = 0; p < HALF / 16; ++p) {
-                    uint32_t r[16];
-                    tmem_ld16(tl + tmem::O + col0 + p * 16, r);
-                    tmem_wait_ld();
-                    const size_t at = row * ro.dv + col0 + p * 16;
-                    const int cols = tid < left ? ro.dv - col0 - p * 16 : 0;
-                    if (ro.out32) store_row(static_cast<float *>(ro.out) + at, r, cols);
-                    else store_row(static_cast<__nv_bfloat16 *>(ro.out) + at, r, cols, ro.dv % 16 == 0);
-                    __syncwarp();
-                }
-                tc_fence_before();
-                warp_arrive(&bar.ofree);
             }
             ok &= tc_wait_warp(&bar.dm, it & 1, gone, a.ctl);
 #pragma unroll
-            for (int p = 0; p < HALF / 16; ++p) {
-                uint32_t r[16];
-                tmem_ld16(tl + tmem::DM + col0 + p * 16, r);
+            for (int p = 0; p < HALF / 16; p += 2) {
+                uint32_t r[32];
+                tmem_ld32(tl + tmem::DM + col0 + p * 16, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 16; ++i)
                     m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
-                if (!SUM) put_m(p);
+                if (!SUM) put_m(p), put_m(p + 1);
                 __syncwarp();
             }
             give_m();
+            if constexpr (!SUM) {
+                ok &= tc_wait_warp(&bar.out, it & 1, gone, a.ctl);
+                // Whole chunks leave by TMA, from x's place, which is done with.
+                if (ro.out32 || (a.offsets && left < WC)) {
+#pragma unroll 1
+                    for (int p = 0; p < HALF / 16; ++p) {
+                        uint32_t r[16];
+                        tmem_ld16(tl + tmem::O + col0 + p * 16, r);
+                        tmem_wait_ld();
+                        const size_t at = row * ro.dv + col0 + p * 16;
+                        const int cols = tid < left ? ro.dv - col0 - p * 16 : 0;
+                        if (ro.out32) store_row(static_cast<float *>(ro.out) + at, r, cols);
+                        else store_row(static_cast<__nv_bfloat16 *>(ro.out) + at, r, cols);
+                        __syncwarp();
+                    }
+                    tc_fence_before();
+                    warp_arrive(&bar.ofree);
+                } else {
+                    const uint32_t stage = sm32 + slot(tile(it, TILE_X));
+#pragma unroll 1
+                    for (int p = 0; p < HALF; p += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(tl + tmem::O + col0 + p, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = pack_bf16(__uint_as_float(r[u * 8 + 2 * i]), __uint_as_float(r[u * 8 + 2 * i + 1]));
+                            const int c = col0 + p + u * 8;
+                            st_shared16(stage + (uint32_t)(c / 64) * L::HALF + swizzled(tid, c % 64 / 8), v);
+                        }
+                    }
+                    tc_fence_before();
+                    warp_arrive(&bar.ofree);
+                    fence_proxy_async_smem();
+                }
+                warp_arrive(&bar.staged);
+            }
         }
         if (SUM) {
             if (tid < D)
@@ -382,22 +419,23 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         }
         __syncwarp();
     } else if (wg < 4) {
+        set_registers<false, 88>();
         // ------------------------------------------------------------------ convert
         const int part = wg - 2, rb = warp % 4;   // every other 32 columns of P; this warp's 32 rows
         const unsigned char *column = sm + (D == 128 ? tid / 64 : 0) * L::HALF + tid % 8 * 2;
         const uint32_t unit = (uint32_t)(tid % 64 / 8) << 4;
         auto values = [&](int it, int h) {   // h z of the chunk's steps 64h ..
-            const unsigned char *p = column + slot(tile(it, 2)) + (h * 64 + part * 32) * 128;
-            const float *f = &gates[it % L::GB].h[h * 64 + part * 32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            const unsigned char *p = column + slot(tile(it, TILE_Z)) + (h * 64 + part * 32) * 128;
+            const float *f = &gates[it % L::GB].mid[h * 64 + part * 32], edge = gates[it % L::GB].edge[h * 2 + part];
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q, p += 16 * 128, f += 16) {
                 float2 e[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int r = q * 16 + 2 * i;
+                    const int r = 2 * i;
                     const float lo = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + r * 128 + (unit ^ (uint32_t)(r % 8 << 4))));
                     const float hi = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + (r + 1) * 128 + (unit ^ (uint32_t)((r + 1) % 8 << 4))));
-                    e[i] = mul2(make_float2(lo, hi), *reinterpret_cast<const float2 *>(f + r));
+                    e[i] = mul2(make_float2(lo, hi), mul2(*reinterpret_cast<const float2 *>(f + r), make_float2(edge, edge)));
                 }
                 put_terms3(tl + tmem::VL + (part * 32 + q * 16) / 2, 32, e);
             }
@@ -410,135 +448,139 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const int gb = it % L::GB;
             const WalkGates &gt = gates[gb];
             ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
-            ok &= wait_tile(tile(it, 2));
-            if (it > 0) ok &= tc_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);
-            values(it, 0);
-            if constexpr (!SUM) {
-                ok &= tc_wait_warp(&bar.s, it & 1, gone, a.ctl);
-                const Sum2 mine = gt.sum[rb * 32 + threadIdx.x % 32];
+            ok &= wait_tile(tile(it, TILE_Z));
+            const Sum2 mine = gt.sum(rb * 32 + threadIdx.x % 32);
 #pragma unroll 1
-                for (int cb = part; cb < 4; cb += 2) {   // 32 columns of P
-                    const uint32_t at = tl + tmem::S + cb * 32;
-                    if (rev ? cb < rb : cb > rb) {
-                        const uint32_t z[16] = {};
-                        tmem_st16(at, z), tmem_st16(at + 16, z);
-                        continue;
-                    }
+            for (int h = 0; h < 2; ++h) {
+                // h z of a half of the steps, once the last half's product is done with its place
+                if (h) ok &= tc_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
+                else if (it > 0) ok &= tc_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);
+                values(it, h);
+                if constexpr (SUM) continue;
+                if (h == 0) ok &= tc_wait_warp(&bar.s, it & 1, gone, a.ctl);
+                // 32 columns of P
+                const int cb = part + 2 * h;
+                const uint32_t at = tl + tmem::S + cb * 32;
+                if (rev ? cb < rb : cb > rb) {
+                    const uint32_t z[16] = {};
+                    tmem_st16(at, z), tmem_st16(at + 16, z);
+                } else {
+                    const bool diagonal = cb == rb;
+                    const float row = diagonal ? 0.f : a.scale * (rev ? decay(gt.sum(cb * 32 - 1), mine) : decay(mine, gt.sum(cb * 32 + 31)));
                     uint32_t r[32];
                     tmem_ld32(at, r);
-                    const bool diagonal = cb == rb;
-                    const float row = diagonal ? 0.f : a.scale * (rev ? decay(gt.sum[cb * 32 - 1], mine) : decay(mine, gt.sum[cb * 32 + 31]));
                     tmem_wait_ld();
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float2 w[8];
                         if (diagonal) {
-                            const int t = threadIdx.x % 32;
+                            const int t = threadIdx.x % 32 - q * 16;
+                            const float *oh = &gt.hi[cb * 32 + q * 16];
+                            const __half2 *ol = reinterpret_cast<const __half2 *>(&gt.lo[cb * 32 + q * 16]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const Sum2 o = gt.sum[cb * 32 + q * 16 + i];
-                                const bool on = rev ? q * 16 + i >= t : q * 16 + i <= t;
-                                const float d = (mine.hi - o.hi) + (mine.lo - o.lo);
-                                const float e = on ? a.scale * exp2_fast(rev ? -d : d) : 0.f;
-                                if (i % 2) w[i / 2].y = e;
-                                else w[i / 2].x = e;
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 lo = __half22float2(ol[i / 2]);
+                                const float d0 = (mine.hi - oh[i]) + (mine.lo - lo.x), d1 = (mine.hi - oh[i + 1]) + (mine.lo - lo.y);
+                                w[i / 2] = make_float2((rev ? i >= t : i <= t) ? a.scale * exp2_fast(rev ? -d0 : d0) : 0.f,
+                                                       (rev ? i + 1 >= t : i + 1 <= t) ? a.scale * exp2_fast(rev ? -d1 : d1) : 0.f);
                             }
                         } else {
+                            const float *o = &gt.mid[cb * 32 + q * 16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) w[i] = mul2(*reinterpret_cast<const float2 *>(&gt.mid[cb * 32 + q * 16 + 2 * i]), make_float2(row, row));
+                            for (int i = 0; i < 8; ++i) w[i] = mul2(*reinterpret_cast<const float2 *>(o + 2 * i), make_float2(row, row));
                         }
                         uint32_t t0[8], t1[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float2 g = make_float2(__uint_as_float(r[q * 16 + 2 * i]), __uint_as_float(r[q * 16 + 2 * i + 1]));
-                            float2 x = mul2(w[i], g);
-                            if (w[i].x == 0.f) x.x = 0.f;   // (masked places stay 0, whatever x y^T holds there)
-                            if (w[i].y == 0.f) x.y = 0.f;
                             uint32_t t[2];
-                            split2<2>(x, t);
+                            split2<2>(mul2(w[i], make_float2(__uint_as_float(r[q * 16 + 2 * i]), __uint_as_float(r[q * 16 + 2 * i + 1]))), t);
                             t0[i] = t[0], t1[i] = t[1];
                         }
                         tmem_st8(at + q * 8, t0);
                         tmem_st8(at + 16 + q * 8, t1);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar.p);
+                if (h) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&bar.p);
+                }
             }
-            ok &= tc_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
-            values(it, 1);
             warp_arrive(&bar.gfree[gb]);
         }
-    } else if (warp == 16) {
+    } else {
+        set_registers<false, 48>();
+    if (warp == 16) {
         // ------------------------------------------------------------------ products
         const uint32_t id_s = mma_desc(128, 128), id_y = mma_desc(128, D), id_mn = mma_desc(128, D, false, true);
         auto k_major = [](int k) { return (uint32_t)((k / 4) * L::HALF + (k % 4) * 32) >> 4; };
         auto all_tile = [&](int i) { return all_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1); };
         auto scores = [&](int it) {   // S = x y^T
-            ok &= all_tile(tile(it, 0));
-            ok &= all_tile(tile(it, 1));
+            ok &= all_tile(tile(it, TILE_Y));
+            ok &= all_tile(tile(it, TILE_X));
             if (elect_one() && ok) {
-                const uint64_t x = smem_desc(sm32 + slot(tile(it, 0)), 16, 1024), y = smem_desc(sm32 + slot(tile(it, 1)), 16, 1024);
+                const uint64_t x = smem_desc(sm32 + slot(tile(it, TILE_X)), 16, 1024), y = smem_desc(sm32 + slot(tile(it, TILE_Y)), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::S, x + k_major(k), y + k_major(k), id_s, k > 0);
                 mma_commit(&bar.s);
             }
             __syncwarp();
         };
-        if (!SUM && chunks > 0) scores(0);
+        auto update = [&](int it, int h) {   // dM += (h z)^T y over 64 steps
+            ok &= all_wait(&bar.vl, h);
+            if (elect_one() && ok) {
+                const uint64_t y = smem_desc(sm32 + slot(tile(it, TILE_Y)) + h * 64 * 128, L::HALF, 1024);
+#pragma unroll 1
+                for (int j = 2; j >= 0; --j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tm + tmem::DM, tm + tmem::VL + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
+                mma_commit(h ? &bar.dm : &bar.dm0);
+                if (h) mma_commit(&bar.empty[tile(it, TILE_Y) % L::SLOTS]);
+                if (h && SUM) mma_commit(&bar.empty[tile(it, TILE_Z) % L::SLOTS]);
+            }
+            __syncwarp();
+        };
+        // What a chunk begins with: its scores and the first half of its dM (behind the last chunk's out).
+        auto begin = [&](int it) {
+            if (!SUM) scores(it);
+            else ok &= all_tile(tile(it, TILE_Y));
+            ok &= all_wait(&bar.m, it & 1);   // dM has been read (and M's terms are there)
+            update(it, 0);
+        };
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
+            begin(it);
             if constexpr (!SUM) {   // Y = x M
-                ok &= all_wait(&bar.m, it & 1);
                 if (it > 0) ok &= all_wait(&bar.ofree, (it - 1) & 1);
                 if (elect_one() && ok) {
-                    const uint64_t x = smem_desc(sm32 + slot(tile(it, 0)), 16, 1024), y = smem_desc(sm32 + L::M_AT, 16, 1024);
+                    const uint64_t x = smem_desc(sm32 + slot(tile(it, TILE_X)), 16, 1024), y = smem_desc(sm32 + L::M_AT, 16, 1024);
 #pragma unroll 1
                     for (int j = 1; j >= 0; --j)   // the small term first
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j == 0 || k > 0);
                     mma_commit(&bar.y);
-                    mma_commit(&bar.empty[tile(it, 0) % L::SLOTS]);
                 }
                 __syncwarp();
-            } else {
-                ok &= all_wait(&bar.m, it & 1);   // dM has been read
-                ok &= all_tile(tile(it, 1));
             }
-            auto update = [&](int h) {   // dM += (h z)^T y over 64 steps
-                ok &= all_wait(&bar.vl, h);
-                if (elect_one() && ok) {
-                    const uint64_t y = smem_desc(sm32 + slot(tile(it, 1)) + h * 64 * 128, L::HALF, 1024);
-#pragma unroll 1
-                    for (int j = 2; j >= 0; --j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ts(tm + tmem::DM, tm + tmem::VL + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
-                    mma_commit(h ? &bar.dm : &bar.dm0);
-                    if (h) mma_commit(&bar.empty[tile(it, 1) % L::SLOTS]), mma_commit(&bar.empty[tile(it, 2) % L::SLOTS]);
-                }
-                __syncwarp();
-            };
-            update(0);
+            update(it, 1);
             if constexpr (!SUM) {   // out = f Y + P z
                 ok &= all_wait(&bar.p, it & 1);
                 ok &= all_wait(&bar.scaled, it & 1);
-                ok &= all_tile(tile(it, 2));
+                ok &= all_tile(tile(it, TILE_Z));
                 if (elect_one() && ok) {
-                    const uint64_t z = smem_desc(sm32 + slot(tile(it, 2)), L::HALF, 1024);
+                    const uint64_t z = smem_desc(sm32 + slot(tile(it, TILE_Z)), L::HALF, 1024);
 #pragma unroll 1
                     for (int j = 1; j >= 0; --j)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + j * 16 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
                     mma_commit(&bar.out);
+                    mma_commit(&bar.empty[tile(it, TILE_Z) % L::SLOTS]);
                 }
                 __syncwarp();
             }
-            update(1);
-            if (!SUM && it + 1 < chunks) scores(it + 1);
         }
         if (elect_one() && (!ok || *gone)) drain_products(&bar.drain, a.ctl);
         __syncwarp();
@@ -549,16 +591,16 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         const int tiles = L::PER * chunks;
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
-            const int it = i / L::PER, which = i % L::PER + (SUM ? 1 : 0), sl = i % L::SLOTS;
+            const int it = i / L::PER, which = i % L::PER, sl = i % L::SLOTS;
             ok &= all_wait(&bar.empty[sl], ((i / L::SLOTS) & 1) ^ 1);
             if (!ok) break;
             const long long t0 = (long long)chunk_at(it) * WC;
             const int left = (int)min((long long)WC, len - t0);
-            const bool clear = a.offsets && which > 0 && left < WC;   // rows of y and z past the end count as zero
+            const bool clear = a.offsets && which != TILE_X && left < WC;   // rows of y and z past the end count as zero
             unsigned char *dst = sm + slot(i);
             if (elect_one()) {
-                const CUtensorMap *map = which == 0 ? &ro.x : which == 1 ? &ro.y : &ro.z;
-                const int h = head / (which == 0 ? ro.gx : which == 1 ? ro.gy : ro.gz), s = (int)(s0 + t0);
+                const CUtensorMap *map = which == TILE_X ? &ro.x : which == TILE_Y ? &ro.y : &ro.z;
+                const int h = head / (which == TILE_X ? ro.gx : which == TILE_Y ? ro.gy : ro.gz), s = (int)(s0 + t0);
                 uint64_t *on = clear ? &bar.aux : &bar.full[sl];
                 // (The test hook makes CTA `stall_tile` expect 16 bytes that never come.)
                 mbar_arrive_expect_tx(on, L::TILE_BYTES + ((int)blockIdx.x == a.ctl.stall_tile ? 16 : 0));
@@ -566,6 +608,14 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 for (int x = 0; x < L::HALVES; ++x) {
                     tma_load_4d(dst + x * L::HALF, map, x * 64, h, s, (int)b, on);
                     tma_load_4d(dst + x * L::HALF + 8192, map, x * 64, h, s + 64, (int)b, on);
+                }
+                if (it + 1 < chunks) {   // and the next chunk's tile into L2
+                    const int s1 = (int)(s0 + (long long)chunk_at(it + 1) * WC);
+#pragma unroll
+                    for (int x = 0; x < L::HALVES; ++x) {
+                        tma_prefetch_4d(map, x * 64, h, s1, (int)b);
+                        tma_prefetch_4d(map, x * 64, h, s1 + 64, (int)b);
+                    }
                 }
             }
             __syncwarp();
@@ -604,11 +654,37 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             ok &= all_wait(&bar.gfree[gb], ((it / L::GB) & 1) ^ 1);
             walk_gates(gates[gb], raw, rev);
             __syncwarp();
-            if (SUM) all = sum2_add(all, gates[gb].sum[WC - 1]);
+            if (SUM) all = sum2_add(all, gates[gb].sum(WC - 1));
             warp_arrive(&bar.gfull[gb]);
             if (it + 1 < chunks) read(it + 1);
         }
         if (SUM && lane == 0) ro.seg_decay[seg_at] = decay(all, {0.f, 0.f});
+    } else if (!SUM) {
+        // ------------------------------------------------------------------ out to memory
+        bool some = false;
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            ok &= all_wait(&bar.staged, it & 1);
+            const long long t0 = (long long)chunk_at(it) * WC;
+            const int left = (int)min((long long)WC, len - t0), i = tile(it, TILE_X);
+            const bool staged = !ro.out32 && !(a.offsets && left < WC);
+            if (elect_one() && ok) {
+                if (staged) {
+#pragma unroll
+                    for (int x = 0; x < 2 * L::HALVES; ++x)
+                        if (x / 2 * 64 < ro.dv && (x % 2 == 0 || left > 64))
+                            tma_store_4d(&ro.o, sm + slot(i) + x / 2 * L::HALF + x % 2 * 8192, x / 2 * 64, head, (int)(s0 + t0) + x % 2 * 64, (int)b);
+                    bulk_commit_group();
+                    bulk_wait_group_read<0>();
+                    some = true;
+                }
+                mbar_arrive(&bar.empty[i % L::SLOTS]);
+            }
+            __syncwarp();
+        }
+        if (some) bulk_wait_group_all();
+        __syncwarp();
+    }
     }
     tc_fence_before();
     __syncthreads();
