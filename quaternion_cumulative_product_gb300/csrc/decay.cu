@@ -3,7 +3,7 @@
 //
 // bfloat16: the walk of decay_walk.cuh.  fp32, whose values are three terms each and take
 // three times the room: the delta rule's kernels without its errors (RULE, delta_prep.cuh).
-#include "decay_walk.cuh"
+#include "decay_gate.cuh"
 #include "delta_host.cuh"
 
 using namespace qs;
@@ -78,28 +78,96 @@ void set_walks(DecayArgs &a, const DeltaArgs &d) {
     a.gate16 = d.gate16, a.scale = d.scale;
 }
 
+// `out` [B, S, Hv, dv] of a role, bfloat16 (by TMA) or fp32.
+int set_out(DecayRole &r, const DecayArgs &a, void *out, int64_t dv, bool fp32) {
+    r.out = out, r.out32 = fp32;
+    if (fp32 || a.B * a.S == 0) return QS_OK;
+    return qsh::head_map(&r.o, out, {(long long)(a.S * a.Hv * dv), (long long)a.Hv * dv, (long long)dv}, a.B, a.S, a.Hv, dv);
+}
+
 int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     DecayArgs a{};
     set_walks(a, d);
     a.roles = 1;
     DecayRole &r = a.role[0];
-    const int rc = set_role(r, a, {d.q, d.sq, d.Hk, d.Dk}, {d.k, d.sk, d.Hk, d.Dk}, {d.v, d.sv, d.Hv, d.Dv});
+    int rc = set_role(r, a, {d.q, d.sq, d.Hk, d.Dk}, {d.k, d.sk, d.Hk, d.Dk}, {d.v, d.sv, d.Hv, d.Dv});
+    if (rc == QS_OK) rc = set_out(r, a, d.o, d.Dv, false);
     if (rc != QS_OK) return rc;
-    if (d.B * d.S > 0) {
-        const qsh::Strides so = {(long long)(d.S * d.Hv * d.Dv), (long long)d.Hv * d.Dv, d.Dv};
-        const int oc = qsh::head_map(&r.o, d.o, so, d.B, d.S, d.Hv, d.Dv);
-        if (oc != QS_OK) return oc;
-    }
-    r.out = d.o, r.init = d.init, r.fin = d.fin, r.lane = 1, r.col = d.Dv;
+    r.init = d.init, r.fin = d.fin, r.lane = 1, r.col = d.Dv;
     cut_walks(a, sms);
     const int D = d.Dk <= 64 && d.Dv <= 64 ? 64 : 128;
     unsigned char *ws = nullptr;
     qsh::Hold hold;
-    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + walk_floats(a, D) * 4, &ws, &hold);
-    if (wc != QS_OK) return wc;
+    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + walk_floats(a, D) * 4, &ws, &hold);
+    if (rc != QS_OK) return rc;
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     return D == 64 ? launch_decay<64, false>(a, seg, stream) : launch_decay<128, false>(a, seg, stream);
+}
+
+template <int D>
+int launch_gates(const GateArgs &a, cudaStream_t stream) {
+    constexpr int smem = GateLayout<D>::BYTES;
+    if (cudaFuncSetAttribute(decay_gate_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return QS_ERR_CUDA;
+    }
+    decay_gate_kernel<D><<<(unsigned)(a.slots * a.Hv), kGateThreads, smem, stream>>>(a);
+    return launched();
+}
+
+// dq and (with the states that it leaves) dk and dv are walks, dg a kernel of its own.
+int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
+    DecayArgs one{}, two{};
+    set_walks(one, d), set_walks(two, d);
+    const qsh::Strides so = {(long long)(d.S * d.Hv * d.Dv), (long long)d.Hv * d.Dv, d.Dv};
+    const Rows q = {d.q, d.sq, d.Hk, d.Dk}, k = {d.k, d.sk, d.Hk, d.Dk}, v = {d.v, d.sv, d.Hv, d.Dv}, o = {d.d_o, so, d.Hv, d.Dv};
+    const int D = d.Dk <= 64 && d.Dv <= 64 ? 64 : 128, group = d.Hv / d.Hk;
+    const bool shared = d.Hv != d.Hk;
+    const long long slots = d.offsets ? d.S / WC + d.N : d.N * one.NC;
+    one.roles = 1, two.roles = 2;
+    cut_walks(one, sms), cut_walks(two, sms);
+    const size_t rows = (size_t)d.B * d.S * d.Hv, nstate = align256((size_t)slots * d.Hv * D * D * 4), ndots = align256(2 * rows * 4),
+                 ncross = align256((size_t)slots * d.Hv * 8 * 4), nh = shared ? align256(rows * d.Dk * 4) : 0;
+    const size_t nseg = walk_floats(one, D) > walk_floats(two, D) ? walk_floats(one, D) : walk_floats(two, D);
+    unsigned char *ws = nullptr;
+    qsh::Hold hold;
+    int rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nstate + 2 * ndots + ncross + 2 * nh + nseg * 4, &ws, &hold);
+    if (rc != QS_OK) return rc;
+    unsigned char *p = ws + sizeof(WsHeader);
+    auto part = [&](size_t n) {
+        float *at = reinterpret_cast<float *>(p);
+        p += n;
+        return at;
+    };
+    float *states = part(nstate), *dota = part(ndots), *dotb = part(ndots), *cross = part(ncross), *dqh = part(nh), *dkh = part(nh), *seg = part(nseg * 4);
+    one.ctl = two.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
+    DecayRole &rq = one.role[0], &rk = two.role[0], &rv = two.role[1];
+    rc = set_role(rq, one, o, v, k);
+    if (rc == QS_OK) rc = set_out(rq, one, shared ? dqh : d.dq, d.Dk, shared);
+    if (rc == QS_OK) rc = set_role(rk, two, v, o, q);
+    if (rc == QS_OK) rc = set_out(rk, two, shared ? dkh : d.dk, d.Dk, shared);
+    if (rc == QS_OK) rc = set_role(rv, two, k, q, o);
+    if (rc == QS_OK) rc = set_out(rv, two, d.dv, d.Dv, false);
+    if (rc != QS_OK) return rc;
+    rq.beside = d.q, rq.sb = d.sq, rq.gb = group, rq.dots = dota, rq.init = d.init, rq.dump = states, rq.lane = d.Dv, rq.col = 1;
+    rk.beside = d.k, rk.sb = d.sk, rk.gb = group, rk.dots = dotb, rk.init = d.d_final, rk.other = states, rk.cross = cross, rk.lane = d.Dv, rk.col = 1;
+    rv.init = d.d_final, rv.fin = d.d_init, rv.lane = 1, rv.col = d.Dv;
+    rk.rev = rv.rev = true;
+    rc = D == 64 ? launch_decay<64, true>(one, seg, stream) : launch_decay<128, true>(one, seg, stream);
+    if (rc == QS_OK) rc = D == 64 ? launch_decay<64, true>(two, seg, stream) : launch_decay<128, true>(two, seg, stream);
+    if (rc != QS_OK || d.B * d.S == 0) return rc;
+    GateArgs g{};
+    g.q = rv.y, g.k = rq.z, g.v = rq.y, g.o = rq.x;
+    g.g = d.g, g.dg = d.dg, g.a = dota, g.b = dotb, g.cross = cross, g.offsets = d.offsets;
+    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = one.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = one.ctl;
+    rc = D == 64 ? launch_gates<64>(g, stream) : launch_gates<128>(g, stream);
+    if (rc != QS_OK || !shared) return rc;
+    DeltaArgs sum = d;
+    sum.dqh = dqh, sum.dkh = dkh;
+    const long long quads = d.B * d.S * d.Hk * d.Dk / 4;
+    delta_shared_kernel<__nv_bfloat16><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(sum, quads);
+    return launched();
 }
 
 }  // namespace
@@ -177,6 +245,9 @@ extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void
     int dev = 0, sms = 0;
     int rc = qsh::device(&dev, &sms);
     if (rc != QS_OK) return rc;
+    a.q = q, a.k = k, a.v = v, a.g = g, a.init = init, a.d_o = d_o, a.d_final = d_final;
+    a.dq = d_q, a.dk = d_k, a.dv = d_v, a.dg = d_g, a.d_init = d_init;
+    if (dtype == QS_BF16) return backward16(a, dev, sms, stream);
     const bool shared = Hv != Hk;
     const size_t nds = align256(kept * 4), nh = shared ? align256((size_t)B * S * Hv * Dk * 4) : 0;
     unsigned char *ws = nullptr;
@@ -185,26 +256,17 @@ extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void
     rc = qsh::workspace(dev, stream, sizeof(WsHeader) + 2 * nds + 2 * nh + seg_floats(a) * 4, &ws, &hold);
     if (rc != QS_OK) return rc;
     unsigned char *p = ws + sizeof(WsHeader);
-    a.q = q, a.k = k, a.v = v, a.g = g, a.init = init, a.d_o = d_o, a.d_final = d_final;
-    a.dq = d_q, a.dk = d_k, a.dv = d_v, a.dg = d_g, a.d_init = d_init;
     a.carries = reinterpret_cast<float *>(p), a.carries_in = a.carries;
     a.ds = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + 2 * nds), a.dkh = reinterpret_cast<float *>(p + 2 * nds + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(p + 2 * nds + 2 * nh);
-    if (some)   // the states that enter the chunks
-        rc = dtype == QS_BF16 ? launch_walks<false, __nv_bfloat16, 1, false>(a, seg, stream)
-                              : launch_walks<false, float, 3, false>(a, seg, stream);
-    if (rc != QS_OK) return rc;
-    rc = dtype == QS_BF16 ? launch_walks<true, __nv_bfloat16, 1, false>(a, seg, stream)
-                          : launch_walks<true, float, 3, false>(a, seg, stream);
+    if (some) rc = launch_walks<false, float, 3, false>(a, seg, stream);   // the states that enter the chunks
+    if (rc == QS_OK) rc = launch_walks<true, float, 3, false>(a, seg, stream);
     if (rc != QS_OK || !some) return rc;
-    if (dtype != QS_BF16) rc = launch_chunks<float, 3, 3, false>(a, stream);
-    else rc = gate_dtype == QS_BF16 ? launch_chunks<__nv_bfloat16, 1, 2, false>(a, stream) : launch_chunks<__nv_bfloat16, 1, 3, false>(a, stream);
+    rc = launch_chunks<float, 3, 3, false>(a, stream);
     if (rc != QS_OK || !shared) return rc;
     const long long quads = B * S * Hk * Dk / 4;
-    const unsigned grid = (unsigned)((quads + 255) / 256);
-    if (dtype == QS_BF16) delta_shared_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, quads);
-    else delta_shared_kernel<float><<<grid, 256, 0, stream>>>(a, quads);
+    delta_shared_kernel<float><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(a, quads);
     return launched();
 }

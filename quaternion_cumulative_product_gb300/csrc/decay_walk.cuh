@@ -13,10 +13,10 @@
 // Chunks hold C = 128 steps.  With the state M [dk][dv] that enters a chunk (from earlier steps
 // forward, later ones backward) and the decay sums G_t = g_0 + .. + g_t inside the chunk:
 //
-//     out = scale f (x M) + P z,       P_ts = scale D_ts <x_t, y_s>,     f_t = exp(G_t) | exp(G_C - G_t)
-//     M'  = exp(G_C) M + y^T (h z),                                      h_s = exp(G_C - G_s) | exp(G_s)
+//     out = f (x M) + P z,            P_ts = scale D_ts <x_t, y_s>,     f_t = scale exp(G_t) | exp(G_C - G_t)
+//     M'  = exp(G_C) M + y^T (h z),                                     h_s = exp(G_C - G_s) | scale exp(G_s)
 //
-// (forward | backward in time).  Nothing but M' = exp(G_C) M + .. links two chunks, and that is a
+// (forward | backward in time: backward, M is the state's cotangent).  Nothing but M' = exp(G_C) M + .. links two chunks, and that is a
 // sum in registers: the tensor cores are kept busy across chunks by roles that run at the same time:
 //
 //     state    two warpgroups: M^T [dv][dk] in fp32 registers, one value row per thread, half of dk
@@ -48,7 +48,7 @@ constexpr int kDecayThreads = 640;   // five warpgroups
 struct DecayRole {
     CUtensorMap x, y, z, o;  // (o: of out, bfloat16)
     void *out;               // [B, S, Hv, dv], bfloat16 or (out32) fp32
-    const void *beside;      // dots: <beside_t, scale f Y_t>, bfloat16, or NULL
+    const void *beside;      // dots: <beside_t, f Y_t>, bfloat16, or NULL
     float *dots;             // [2][B, S, Hv] by halves of the columns
     const float *init;       // state that enters (first chunk of a walk) [N, Hv, ..], or NULL
     float *fin;              // state that leaves, or NULL
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
             ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
-            const float f = a.scale * (rev ? decay(gt.sum(WC - 1), gt.sum(tid)) : decay(gt.sum(tid), {0.f, 0.f}));
+            const float f = rev ? decay(gt.sum(WC - 1), gt.sum(tid)) : a.scale * decay(gt.sum(tid), {0.f, 0.f});
             warp_arrive(&bar.gfree[gb]);
             if constexpr (!SUM) {
                 const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         const uint32_t unit = (uint32_t)(tid % 64 / 8) << 4;
         auto values = [&](int it, int h) {   // h z of the chunk's steps 64h ..
             const unsigned char *p = column + slot(tile(it, TILE_Z)) + (h * 64 + part * 32) * 128;
-            const float *f = &gates[it % L::GB].mid[h * 64 + part * 32], edge = gates[it % L::GB].edge[h * 2 + part];
+            const float *f = &gates[it % L::GB].mid[h * 64 + part * 32], edge = gates[it % L::GB].edge[h * 2 + part] * (rev ? a.scale : 1.f);
 #pragma unroll 1
             for (int q = 0; q < 2; ++q, p += 16 * 128, f += 16) {
                 float2 e[8];
