@@ -24,15 +24,18 @@
 //     convert  two warpgroups: P from S = x y^T (in place, in tensor memory), h z as three terms
 //     one warp each: products, copies (TMA into a ring of tiles), gates
 //
-// Per chunk, in the order of issue: Y = x M (2 terms of M), dM += (h z)^T y for the first 64
-// steps, out = f Y + P z (2 terms of P), dM for the other 64, and the next chunk's S.  The
-// product that waits for a conversion always has another one running before it.
+// Per chunk, in the order of issue: S, dM = (h z)^T y over the first 64 steps, Y = x M, dM over the
+// other 64, out = f Y + P z.
 //
-// Terms (tensor_core.cuh): h z in three, so that states have fp32 precision; M and P, of which
-// only bfloat16 outputs are made, in two (2^-15 of a product left out at most).
+// Terms (tensor_core.cuh): h z in three, so that states have fp32 precision (they add up rounded
+// once a chunk).  P and the M of Y, of which only bfloat16 outputs are made, in one: rounded to
+// nearest, their errors are as large as the output's own rounding and independent of it (measured
+// against 64 bits: 1.2 times its error alone; two terms of each took XXX).  Where Y goes into d_g
+// as well (dots), M has two terms.
 //
-// Bound: the tensor cores (8 products of 128 x 128 x 128 a chunk, 64 clocks each 16 of K: 2.1 us
-// at 1.9 GHz) and memory (131 KB a chunk) alike.
+// Bound: shared memory.  The tensor cores read 64 KB (S) + 64 KB (Y) + 32 KB (P z) + 96 KB (dM) of
+// operands a chunk, the copies write 96 KB and read 32 KB, conversions write M (32 KB) and out (32 KB)
+// and read h z's columns two bytes a lane.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -123,6 +126,52 @@ __device__ __forceinline__ void set_registers() {
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// tc_wait and tc_wait_warp (tensor_core.cuh) that sleep in the barrier for up to 0.1 ms at a time:
+// polls read shared memory, which is what bounds this kernel.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool walk_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
+    if (mbar_sleep(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_sleep(bar, parity)) {
+        if (*gone) return false;
+        if (global_timer_ns() - t0 > ctl.timeout_ns) {
+            *gone = 1;
+            record_error(ctl.hdr, (int)blockIdx.x);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool walk_wait_warp(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
+    const bool ok = walk_wait(bar, parity, gone, ctl);
+    __syncwarp();
+    tc_fence_after();
+    return ok;
+}
+
+// Four 8 x 8 matrices of bfloat16 (rows of 16 bytes, one address per lane), each transposed:
+// lane t gets rows 2 (t % 4) and + 1 of column t / 4.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t at, uint32_t *v) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+// Sixteen tensor-memory lanes x 8 columns: lane t holds column t % 4 of rows t / 4 (a) and t / 4 + 8 (b), and column 4 + t % 4 (c, d).
+__device__ __forceinline__ void tmem_st16x128b2(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // Arrives on a barrier that counts warps.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
@@ -207,7 +256,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         const long long off = seg * a.seg_chunks * WC, left = len > off ? len - off : 0, most = a.seg_chunks * WC;
         s0 += off, slot0 += seg * a.seg_chunks, len = left < most ? left : most;
     }
-    const int chunks = (int)((len + WC - 1) / WC);
+    const int chunks = __reduce_min_sync(0xffffffffu, (int)((len + WC - 1) / WC));   // (in a uniform register, as the loops over it then are)
     const size_t pair = (size_t)n * a.Hv + head, seg_at = pair * a.segs + seg;
     const bool rev = ro.rev;
     auto chunk_at = [&](int it) { return rev ? chunks - 1 - it : it; };   // the it-th chunk that the walk comes to
@@ -225,15 +274,45 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = (uint32_t)warp_uniform((int)bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
+    const uint32_t tm = __reduce_min_sync(0xffffffffu, bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
+    const int terms = BWD && ro.dots ? 2 : 1;   // of M
     bool ok = true;   // none of this thread's waits has run out
     // Tiles come in the order y, z, x of each chunk (SUM: y, z): so the slot that one takes is
     // that of a tile which is done with early enough.  Tile i is in slot i % SLOTS.
     auto tile = [&](int it, int which) { return L::PER * it + which; };   // `which`: Y, Z, X
     auto slot = [&](int i) { return (uint32_t)(i % L::SLOTS) * L::TILE_BYTES; };
     // Waits of the warps that issue: whole warps go on or stop together.
-    auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, tc_wait_warp(x, parity, gone, a.ctl)) != 0; };
-    auto wait_tile = [&](int i) { return tc_wait_warp(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, gone, a.ctl); };
+    auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, walk_wait_warp(x, parity, gone, a.ctl)) != 0; };
+    auto wait_tile = [&](int i) { return walk_wait_warp(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, gone, a.ctl); };
+
+    // Terms of h z, 32 of the chunk's steps 64h .. (the first half by `convert`, the second by `state`):
+    // 16 steps at a time, transposed by the loads, so that a register holds two steps of value
+    // row lane / 4 (+ 8, 16, 24), which is how the 16-lane stores to tensor memory want them.
+    auto values = [&](int it, int h) {
+        const int lane = threadIdx.x % 32, step0 = h * 64 + wg % 2 * 32, row0 = warp % 4 * 32 % D;
+        uint32_t at = sm32 + slot(tile(it, TILE_Z)) + (uint32_t)(row0 / 64) * L::HALF + (uint32_t)(step0 + lane / 8 % 2 * 8 + lane % 8) * 128 +
+                      (uint32_t)(((row0 % 64 / 8 + lane / 16) ^ (lane % 8)) << 4);
+        const float *f = &gates[it % L::GB].mid[step0 + lane % 4 * 2], edge = gates[it % L::GB].edge[h * 2 + wg % 2] * (rev ? a.scale : 1.f);
+        uint32_t to = tl + tmem::VL + wg % 2 * 16;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q, at += 16 * 128, f += 16, to += 8) {
+            const float2 lo = mul2(*reinterpret_cast<const float2 *>(f), make_float2(edge, edge));        // h of steps 0 .. 7
+            const float2 hi = mul2(*reinterpret_cast<const float2 *>(f + 8), make_float2(edge, edge));    // and 8 .. 15
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {   // 16 value rows
+                uint32_t v[4], t[4][3];
+                ldmatrix4_trans(x ? at ^ 32 : at, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    split2<3>(mul2(make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u)), i % 2 ? hi : lo), t[i]);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) tmem_st16x128b2(to + (x << 20) + j * 32, t[0][j], t[2][j], t[1][j], t[3][j]);
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&bar.vl);
+    };
 
     if (wg < 2) {
         set_registers<true, 128>();
@@ -265,16 +344,20 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             if (D == 64 && tid >= 64) return;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint32_t t[4][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split2<2>(m[p * 8 + u * 4 + i], t[i]);
                 const int c = col0 + p * 16 + u * 8;
                 const uint32_t at = sm32 + L::M_AT + (uint32_t)(c / 64) * L::M_HALF + swizzled(tid, c % 64 / 8);
+                uint32_t t[4][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t v[4] = {t[0][j], t[1][j], t[2][j], t[3][j]};
-                    st_shared16(at + j * L::M_TERM, v);
+                for (int i = 0; i < 4; ++i) {
+                    if (terms == 2) split2<2>(m[p * 8 + u * 4 + i], t[i]);
+                    else split2<1>(m[p * 8 + u * 4 + i], t[i]);
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (j < terms) {
+                        const uint32_t v[4] = {t[0][j], t[1][j], t[2][j], t[3][j]};
+                        st_shared16(at + j * L::M_TERM, v);
+                    }
             }
         };
         auto give_m = [&] {   // M's terms are there (SUM: dM has been read)
@@ -294,10 +377,10 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const WalkGates &gt = gates[gb];
             const int left = (int)min((long long)WC, len - t0);
             const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
-            ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+            ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
             const float f = rev ? decay(gt.sum(WC - 1), gt.sum(tid)) : a.scale * decay(gt.sum(tid), {0.f, 0.f});
-            warp_arrive(&bar.gfree[gb]);
+            __syncwarp();
             if constexpr (!SUM) {
                 const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
                 if (BWD && ro.dump && tid < D)
@@ -319,11 +402,17 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
                 }
+            }
+            ok &= wait_tile(tile(it, TILE_Z));
+            ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
+            values(it, 1);
+            warp_arrive(&bar.gfree[gb]);
+            if constexpr (!SUM) {
                 const __nv_bfloat16 *be = nullptr;
                 if (BWD && ro.dots)
                     be = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(tid, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + col0;
                 __syncwarp();
-                ok &= tc_wait_warp(&bar.y, it & 1, gone, a.ctl);
+                ok &= walk_wait_warp(&bar.y, it & 1, gone, a.ctl);
                 float dot = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < HALF; p += 16) {   // f Y
@@ -354,7 +443,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 if (BWD && ro.dots && tid < left) ro.dots[(size_t)wg * a.B * a.S * a.Hv + row] = dot;
                 __syncwarp();
             }
-            ok &= tc_wait_warp(&bar.dm, it & 1, gone, a.ctl);
+            ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);
 #pragma unroll
             for (int p = 0; p < HALF / 16; p += 2) {
                 uint32_t r[32];
@@ -368,7 +457,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             }
             give_m();
             if constexpr (!SUM) {
-                ok &= tc_wait_warp(&bar.out, it & 1, gone, a.ctl);
+                ok &= walk_wait_warp(&bar.out, it & 1, gone, a.ctl);
                 // Whole chunks leave by TMA, from x's place, which is done with.
                 if (ro.out32 || (a.offsets && left < WC)) {
 #pragma unroll 1
@@ -422,89 +511,68 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         set_registers<false, 88>();
         // ------------------------------------------------------------------ convert
         const int part = wg - 2, rb = warp % 4;   // every other 32 columns of P; this warp's 32 rows
-        const unsigned char *column = sm + (D == 128 ? tid / 64 : 0) * L::HALF + tid % 8 * 2;
-        const uint32_t unit = (uint32_t)(tid % 64 / 8) << 4;
-        auto values = [&](int it, int h) {   // h z of the chunk's steps 64h ..
-            const unsigned char *p = column + slot(tile(it, TILE_Z)) + (h * 64 + part * 32) * 128;
-            const float *f = &gates[it % L::GB].mid[h * 64 + part * 32], edge = gates[it % L::GB].edge[h * 2 + part] * (rev ? a.scale : 1.f);
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q, p += 16 * 128, f += 16) {
-                float2 e[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 2 * i;
-                    const float lo = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + r * 128 + (unit ^ (uint32_t)(r % 8 << 4))));
-                    const float hi = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + (r + 1) * 128 + (unit ^ (uint32_t)((r + 1) % 8 << 4))));
-                    e[i] = mul2(make_float2(lo, hi), mul2(*reinterpret_cast<const float2 *>(f + r), make_float2(edge, edge)));
-                }
-                put_terms3(tl + tmem::VL + (part * 32 + q * 16) / 2, 32, e);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&bar.vl);
-        };
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int gb = it % L::GB;
             const WalkGates &gt = gates[gb];
-            ok &= tc_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+            ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             ok &= wait_tile(tile(it, TILE_Z));
-            const Sum2 mine = gt.sum(rb * 32 + threadIdx.x % 32);
+            if (it > 0) ok &= walk_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);   // the last half's terms are done with
+            values(it, 0);
+            if constexpr (!SUM) {
+                const Sum2 mine = gt.sum(rb * 32 + threadIdx.x % 32);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                // h z of a half of the steps, once the last half's product is done with its place
-                if (h) ok &= tc_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
-                else if (it > 0) ok &= tc_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);
-                values(it, h);
-                if constexpr (SUM) continue;
-                if (h == 0) ok &= tc_wait_warp(&bar.s, it & 1, gone, a.ctl);
-                // 32 columns of P
-                const int cb = part + 2 * h;
-                const uint32_t at = tl + tmem::S + cb * 32;
-                if (rev ? cb < rb : cb > rb) {
-                    const uint32_t z[16] = {};
-                    tmem_st16(at, z), tmem_st16(at + 16, z);
-                } else {
-                    const bool diagonal = cb == rb;
-                    const float row = diagonal ? 0.f : a.scale * (rev ? decay(gt.sum(cb * 32 - 1), mine) : decay(mine, gt.sum(cb * 32 + 31)));
-                    uint32_t r[32];
-                    tmem_ld32(at, r);
-                    tmem_wait_ld();
+                for (int h = 0; h < 2; ++h) {   // 32 columns of P
+                    const int cb = part + 2 * h;
+                    const uint32_t at = tl + tmem::S + cb * 32;
+                    const bool none = rev ? cb < rb : cb > rb, diagonal = cb == rb;
+                    float2 w[16];   // scale D, while x y^T is made
+                    // D_ts = mid_s row, the second factor at most 1 off the diagonal; on it the other way
+                    // round, as long as the block's decay is no more than 2^-60, else one exp2 a value.
+                    const Sum2 face = rev ? cb ? gt.sum(cb * 32 - 1) : Sum2{0.f, 0.f} : gt.sum(cb * 32 + 31);
+                    const int t = threadIdx.x % 32;
+                    if (diagonal && fabsf(face.hi - gt.hi[cb * 32 + (rev ? 31 : 0)]) > 60.f) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float2 w[8];
-                        if (diagonal) {
-                            const int t = threadIdx.x % 32 - q * 16;
-                            const float *oh = &gt.hi[cb * 32 + q * 16];
-                            const __half2 *ol = reinterpret_cast<const __half2 *>(&gt.lo[cb * 32 + q * 16]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&gt.lo[cb * 32 + 2 * i]));
+                            const float d0 = (mine.hi - gt.hi[cb * 32 + 2 * i]) + (mine.lo - lo.x), d1 = (mine.hi - gt.hi[cb * 32 + 2 * i + 1]) + (mine.lo - lo.y);
+                            w[i] = make_float2((rev ? 2 * i >= t : 2 * i <= t) ? a.scale * exp2_fast(rev ? -d0 : d0) : 0.f,
+                                               (rev ? 2 * i + 1 >= t : 2 * i + 1 <= t) ? a.scale * exp2_fast(rev ? -d1 : d1) : 0.f);
+                        }
+                    } else if (!none) {
+                        const float row = a.scale * (rev ? decay(face, mine) : decay(mine, face));
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 lo = __half22float2(ol[i / 2]);
-                                const float d0 = (mine.hi - oh[i]) + (mine.lo - lo.x), d1 = (mine.hi - oh[i + 1]) + (mine.lo - lo.y);
-                                w[i / 2] = make_float2((rev ? i >= t : i <= t) ? a.scale * exp2_fast(rev ? -d0 : d0) : 0.f,
-                                                       (rev ? i + 1 >= t : i + 1 <= t) ? a.scale * exp2_fast(rev ? -d1 : d1) : 0.f);
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 o = *reinterpret_cast<const float4 *>(&gt.mid[cb * 32 + i]);
+                            w[i / 2] = mul2(make_float2(o.x, o.y), make_float2(row, row)), w[i / 2 + 1] = mul2(make_float2(o.z, o.w), make_float2(row, row));
+                        }
+                        if (diagonal)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                if (rev ? 2 * i < t : 2 * i > t) w[i].x = 0.f;
+                                if (rev ? 2 * i + 1 < t : 2 * i + 1 > t) w[i].y = 0.f;
                             }
-                        } else {
-                            const float *o = &gt.mid[cb * 32 + q * 16];
+                    }
+                    __syncwarp();
+                    if (h == 0) ok &= walk_wait_warp(&bar.s, it & 1, gone, a.ctl);
+                    if (none) {
+                        const uint32_t z[16] = {};
+                        tmem_st16(at, z);
+                    } else {
+                        uint32_t r[32];
+                        tmem_ld32(at, r);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) w[i] = mul2(*reinterpret_cast<const float2 *>(o + 2 * i), make_float2(row, row));
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = mul2(w[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+                            r[i] = pack_bf16(x.x, x.y);
                         }
-                        uint32_t t0[8], t1[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t t[2];
-                            split2<2>(mul2(w[i], make_float2(__uint_as_float(r[q * 16 + 2 * i]), __uint_as_float(r[q * 16 + 2 * i + 1]))), t);
-                            t0[i] = t[0], t1[i] = t[1];
-                        }
-                        tmem_st8(at + q * 8, t0);
-                        tmem_st8(at + 16 + q * 8, t1);
+                        tmem_st16(at, r);
                     }
                 }
-                if (h) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    warp_arrive(&bar.p);
-                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.p);
             }
             warp_arrive(&bar.gfree[gb]);
         }
@@ -514,12 +582,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         // ------------------------------------------------------------------ products
         const uint32_t id_s = mma_desc(128, 128), id_y = mma_desc(128, D), id_mn = mma_desc(128, D, false, true);
         auto k_major = [](int k) { return (uint32_t)((k / 4) * L::HALF + (k % 4) * 32) >> 4; };
+        auto tile_at = [&](int i) { return __reduce_min_sync(0xffffffffu, sm32 + slot(i)); };   // (uniform descriptors: tensor_core.cuh)
         auto all_tile = [&](int i) { return all_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1); };
         auto scores = [&](int it) {   // S = x y^T
             ok &= all_tile(tile(it, TILE_Y));
             ok &= all_tile(tile(it, TILE_X));
+            const uint64_t x = smem_desc(tile_at(tile(it, TILE_X)), 16, 1024), y = smem_desc(tile_at(tile(it, TILE_Y)), 16, 1024);
             if (elect_one() && ok) {
-                const uint64_t x = smem_desc(sm32 + slot(tile(it, TILE_X)), 16, 1024), y = smem_desc(sm32 + slot(tile(it, TILE_Y)), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::S, x + k_major(k), y + k_major(k), id_s, k > 0);
                 mma_commit(&bar.s);
@@ -528,8 +597,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         };
         auto update = [&](int it, int h) {   // dM += (h z)^T y over 64 steps
             ok &= all_wait(&bar.vl, h);
+            const uint64_t y = smem_desc(tile_at(tile(it, TILE_Y)) + h * 64 * 128, L::HALF, 1024);
             if (elect_one() && ok) {
-                const uint64_t y = smem_desc(sm32 + slot(tile(it, TILE_Y)) + h * 64 * 128, L::HALF, 1024);
 #pragma unroll 1
                 for (int j = 2; j >= 0; --j)
 #pragma unroll
@@ -553,13 +622,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             begin(it);
             if constexpr (!SUM) {   // Y = x M
                 if (it > 0) ok &= all_wait(&bar.ofree, (it - 1) & 1);
+                const uint64_t x = smem_desc(tile_at(tile(it, TILE_X)), 16, 1024), y = smem_desc(__reduce_min_sync(0xffffffffu, sm32 + L::M_AT), 16, 1024);
                 if (elect_one() && ok) {
-                    const uint64_t x = smem_desc(sm32 + slot(tile(it, TILE_X)), 16, 1024), y = smem_desc(sm32 + L::M_AT, 16, 1024);
 #pragma unroll 1
-                    for (int j = 1; j >= 0; --j)   // the small term first
+                    for (int j = terms - 1; j >= 0; --j)   // the small term first
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j == 0 || k > 0);
+                            mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j < terms - 1 || k > 0);
                     mma_commit(&bar.y);
                 }
                 __syncwarp();
@@ -569,13 +638,10 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 ok &= all_wait(&bar.p, it & 1);
                 ok &= all_wait(&bar.scaled, it & 1);
                 ok &= all_tile(tile(it, TILE_Z));
+                const uint64_t z = smem_desc(tile_at(tile(it, TILE_Z)), L::HALF, 1024);
                 if (elect_one() && ok) {
-                    const uint64_t z = smem_desc(sm32 + slot(tile(it, TILE_Z)), L::HALF, 1024);
-#pragma unroll 1
-                    for (int j = 1; j >= 0; --j)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + j * 16 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
+                    for (int k = 0; k < 8; ++k) mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
                     mma_commit(&bar.out);
                     mma_commit(&bar.empty[tile(it, TILE_Z) % L::SLOTS]);
                 }
