@@ -7,7 +7,8 @@
 // Values are selected, not multiplied: a dropped NaN is gone.
 //
 // Bound: memory (4 to 6 bytes a value in bfloat16) against about 15 instructions a value
-// (two 32 x 32 -> 64 bit products a round for four values).
+// (two 32 x 32 -> 64 bit products a round for four values).  CTAs are persistent: a thread
+// makes the rounds' keys once, and its next piece is on its way while one is worked on.
 #include <cmath>
 
 #include "mixer_device.cuh"
@@ -16,7 +17,7 @@
 
 namespace {
 
-constexpr int kThreads = 256, kPer = 2;   // pieces of VEC values per thread
+constexpr int kThreads = 256;
 
 struct DropArgs {
     const long long *key;
@@ -29,72 +30,89 @@ struct DropArgs {
 };
 
 struct Philox {
-    uint32_t k0, k1, o0, o1;
+    uint32_t k0[10], k1[10], o1, low, high;   // low, high: the first round's product with the offset
     __device__ __forceinline__ explicit Philox(const long long *key) {
         const unsigned long long seed = (unsigned long long)__ldg(key), offset = (unsigned long long)__ldg(key + 1);
-        k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32), o0 = (uint32_t)offset, o1 = (uint32_t)(offset >> 32);
+        k0[0] = (uint32_t)seed, k1[0] = (uint32_t)(seed >> 32), o1 = (uint32_t)(offset >> 32);
+        const unsigned long long q = (offset & 0xffffffffull) * 0xCD9E8D57u;
+        low = (uint32_t)q, high = (uint32_t)(q >> 32);
+#pragma unroll
+        for (int i = 1; i < 10; ++i) k0[i] = k0[i - 1] + 0x9E3779B9u, k1[i] = k1[i - 1] + 0xBB67AE85u;
     }
     __device__ __forceinline__ uint4 words(unsigned long long block) const {
-        uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = o0, c3 = o1, a = k0, b = k1;
+        const unsigned long long first = (block & 0xffffffffull) * 0xD2511F53u;
+        uint32_t c0 = high ^ (uint32_t)(block >> 32) ^ k0[0], c1 = low, c2 = (uint32_t)(first >> 32) ^ o1 ^ k1[0], c3 = (uint32_t)first;
 #pragma unroll
-        for (int i = 0; i < 10; ++i) {
+        for (int i = 1; i < 10; ++i) {
             const unsigned long long p = (unsigned long long)c0 * 0xD2511F53u, q = (unsigned long long)c2 * 0xCD9E8D57u;
-            c0 = (uint32_t)(q >> 32) ^ c1 ^ a, c1 = (uint32_t)q;
-            c2 = (uint32_t)(p >> 32) ^ c3 ^ b, c3 = (uint32_t)p;
-            a += 0x9E3779B9u, b += 0xBB67AE85u;
+            c0 = (uint32_t)(q >> 32) ^ c1 ^ k0[i], c1 = (uint32_t)q;
+            c2 = (uint32_t)(p >> 32) ^ c3 ^ k1[i], c3 = (uint32_t)p;
         }
         return make_uint4(c0, c1, c2, c3);
     }
 };
 
-// VEC values at a time: 8 of bfloat16 or 4 of fp32 in one access (all pointers 16-byte
-// aligned), or 4 one by one.
-template <typename T, int VEC, bool WIDE>
+// VEC values at a time: 8 in one access of bfloat16 or two of fp32 (all pointers 16-byte
+// aligned; what is left of the last piece one by one), or 4 one by one.
+template <typename T, int VEC, bool WIDE, bool RES>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     T *y = static_cast<T *>(a.y);
+    const long long step = (long long)gridDim.x * kThreads * VEC;
+    long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * VEC;
+    struct Piece {
+        qs::RawQuads<VEC / 4, T> v;
+    } px, pr;
+    auto whole = [&](long long at) { return WIDE && at + VEC <= a.n; };
+    auto fetch = [&](long long at) {
+        if (!whole(at)) return;
+        px.v.load(x + at);
+        if (RES) pr.v.load(res + at);
+    };
+    fetch(i);
     const Philox gen(a.key);
-    const long long first = ((long long)blockIdx.x * kPer * kThreads + threadIdx.x) * VEC;
-    float4 v[kPer][VEC / 4], r[kPer][VEC / 4];
+    for (; i < a.n; i += step) {
+        float4 v[VEC / 4], r[VEC / 4];
+        if (whole(i)) {
+            px.v.get(v);
+            if (RES) pr.v.get(r);
+        } else {
+            float *f = reinterpret_cast<float *>(v), *g = reinterpret_cast<float *>(r);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const long long i = first + (long long)j * kThreads * VEC;
-#pragma unroll
-        for (int k = 0; k < VEC / 4; ++k) v[j][k] = r[j][k] = qs::q_zero();
-        if (WIDE && i + VEC <= a.n) {
-            qs::load_quads<VEC / 4>(x + i, v[j]);
-            if (res) qs::load_quads<VEC / 4>(res + i, r[j]);
-        } else if (i < a.n) {
-            float *f = reinterpret_cast<float *>(v[j]), *g = reinterpret_cast<float *>(r[j]);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                if (i + k < a.n) {
-                    f[k] = qs::load1(x + i + k);
-                    if (res) g[k] = qs::load1(res + i + k);
-                }
+            for (int k = 0; k < VEC; ++k) {
+                f[k] = i + k < a.n ? qs::load1(x + i + k) : 0.f;
+                g[k] = RES && i + k < a.n ? qs::load1(res + i + k) : 0.f;
+            }
         }
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const long long i = first + (long long)j * kThreads * VEC;
-        if (i >= a.n) return;
+        fetch(i + step);
 #pragma unroll
         for (int k = 0; k < VEC / 4; ++k) {
             const uint4 w = gen.words((unsigned long long)i / 4 + k);
-            v[j][k].x = r[j][k].x + (w.x > a.least || a.all ? v[j][k].x * a.scale : 0.f);
-            v[j][k].y = r[j][k].y + (w.y > a.least || a.all ? v[j][k].y * a.scale : 0.f);
-            v[j][k].z = r[j][k].z + (w.z > a.least || a.all ? v[j][k].z * a.scale : 0.f);
-            v[j][k].w = r[j][k].w + (w.w > a.least || a.all ? v[j][k].w * a.scale : 0.f);
+            v[k].x = w.x > a.least || a.all ? v[k].x * a.scale : 0.f;
+            v[k].y = w.y > a.least || a.all ? v[k].y * a.scale : 0.f;
+            v[k].z = w.z > a.least || a.all ? v[k].z * a.scale : 0.f;
+            v[k].w = w.w > a.least || a.all ? v[k].w * a.scale : 0.f;
+            if (RES) v[k] = qs::q_add(r[k], v[k]);
         }
-        if (WIDE && i + VEC <= a.n) {
-            qs::store_quads<VEC / 4>(y + i, v[j]);
+        if (whole(i)) {
+            qs::store_quads<VEC / 4>(y + i, v);
         } else {
-            const float *f = reinterpret_cast<const float *>(v[j]);
+            const float *f = reinterpret_cast<const float *>(v);
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
                 if (i + k < a.n) qs::store1(y + i + k, f[k]);
         }
     }
+}
+
+template <typename T, int VEC, bool WIDE>
+int launch(const DropArgs &a, int sms, cudaStream_t stream) {
+    auto go = [&](auto kernel) {
+        const long long all = (a.n + (long long)VEC * kThreads - 1) / ((long long)VEC * kThreads), most = (long long)sms * (2048 / kThreads);
+        kernel<<<(unsigned)(all < most ? all : most), kThreads, 0, stream>>>(a);
+        return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+    };
+    return a.res ? go(dropout_kernel<T, VEC, WIDE, true>) : go(dropout_kernel<T, VEC, WIDE, false>);
 }
 
 int run(int dtype, double p, const int64_t *key, const void *x, const void *res, void *y, int64_t n, void *stream_) {
@@ -115,17 +133,9 @@ int run(int dtype, double p, const int64_t *key, const void *x, const void *res,
     a.all = drop == 0, a.least = a.all ? 0u : (uint32_t)(drop - 1);
     a.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
     const bool wide = !qsh::misaligned(x) && !qsh::misaligned(res) && !qsh::misaligned(y);
-    const int vec = wide && dtype == QS_BF16 ? 8 : 4;
-    const unsigned grid = (unsigned)((n + (int64_t)vec * kPer * kThreads - 1) / ((int64_t)vec * kPer * kThreads));
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (dtype == QS_BF16) {
-        if (wide) dropout_kernel<__nv_bfloat16, 8, true><<<grid, kThreads, 0, stream>>>(a);
-        else dropout_kernel<__nv_bfloat16, 4, false><<<grid, kThreads, 0, stream>>>(a);
-    } else {
-        if (wide) dropout_kernel<float, 4, true><<<grid, kThreads, 0, stream>>>(a);
-        else dropout_kernel<float, 4, false><<<grid, kThreads, 0, stream>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+    if (dtype == QS_BF16) return wide ? launch<__nv_bfloat16, 8, true>(a, sms, stream) : launch<__nv_bfloat16, 4, false>(a, sms, stream);
+    return wide ? launch<float, 8, true>(a, sms, stream) : launch<float, 4, false>(a, sms, stream);
 }
 
 }  // namespace
