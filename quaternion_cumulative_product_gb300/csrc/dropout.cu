@@ -6,9 +6,10 @@
 // depend on the key and i alone, so the gradient makes them again and no mask is stored.
 // Values are selected, not multiplied: a dropped NaN is gone.
 //
-// Bound: memory (4 to 6 bytes a value in bfloat16) against about 15 instructions a value
-// (two 32 x 32 -> 64 bit products a round for four values).  CTAs are persistent: a thread
-// makes the rounds' keys once, and its next piece is on its way while one is worked on.
+// Bound: fp32, memory (8 or 12 bytes a value: 60 us with a residual, 44 us without at 32 M values,
+// 0.99 and 0.91 of a copy's rate); bfloat16, the generator (two 32 x 32 -> 64 bit products a
+// round for four values: 87 and 70 us at 64 M values, 0.68 and 0.56).  CTAs are persistent: a
+// thread makes the rounds' keys once, and its next piece is on its way while one is worked on.
 #include <cmath>
 
 #include "mixer_device.cuh"
@@ -17,7 +18,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kCtas = 5, kResCtas = 4;   // CTAs per SM, what their registers allow
 
 struct DropArgs {
     const long long *key;
@@ -55,7 +56,7 @@ struct Philox {
 // VEC values at a time: 8 in one access of bfloat16 or two of fp32 (all pointers 16-byte
 // aligned; what is left of the last piece one by one), or 4 one by one.
 template <typename T, int VEC, bool WIDE, bool RES>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
+__global__ void __launch_bounds__(kThreads, RES ? kResCtas : kCtas) dropout_kernel(const DropArgs a) {
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     T *y = static_cast<T *>(a.y);
     const long long step = (long long)gridDim.x * kThreads * VEC;
@@ -107,12 +108,12 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
 
 template <typename T, int VEC, bool WIDE>
 int launch(const DropArgs &a, int sms, cudaStream_t stream) {
-    auto go = [&](auto kernel) {
-        const long long all = (a.n + (long long)VEC * kThreads - 1) / ((long long)VEC * kThreads), most = (long long)sms * (2048 / kThreads);
+    auto go = [&](auto kernel, int ctas) {
+        const long long all = (a.n + (long long)VEC * kThreads - 1) / ((long long)VEC * kThreads), most = (long long)sms * ctas;
         kernel<<<(unsigned)(all < most ? all : most), kThreads, 0, stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
     };
-    return a.res ? go(dropout_kernel<T, VEC, WIDE, true>) : go(dropout_kernel<T, VEC, WIDE, false>);
+    return a.res ? go(dropout_kernel<T, VEC, WIDE, true>, kResCtas) : go(dropout_kernel<T, VEC, WIDE, false>, kCtas);
 }
 
 int run(int dtype, double p, const int64_t *key, const void *x, const void *res, void *y, int64_t n, void *stream_) {
