@@ -17,8 +17,9 @@ slice of ``cum``.  As in the page's module documentation, its cotangent then
 reaches the node already added into ``d_cum[:, S-1]``; the node itself has a
 single output.
 
-``quat_norm_rotate`` and ``quat_delta`` are the differentiable forms of the
-operators around the scan (:mod:`.mixer`).  Their gradients have none of their own: a
+``quat_norm_rotate``, ``quat_delta`` and ``quat_decay`` are the differentiable forms of
+the operators around the scan (:mod:`.mixer`), ``quat_layer_norm`` and ``quat_dropout`` those
+of a residual block (:mod:`.block`).  Their gradients have none of their own: a
 backward through them (``create_graph=True``) raises.
 """
 from __future__ import annotations
@@ -27,11 +28,14 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (
-    quat_cumprod_bwd, quat_cumprod_bwd_carries, quat_cumprod_fwd, quat_cumprod_fwd_carries, quat_delta_bwd,
-    quat_delta_fwd, quat_delta_fwd_carries, quat_norm_rotate_bwd, quat_norm_rotate_fwd)
+    quat_cumprod_bwd, quat_cumprod_bwd_carries, quat_cumprod_fwd, quat_cumprod_fwd_carries, quat_decay_bwd,
+    quat_decay_fwd, quat_delta_bwd, quat_delta_fwd, quat_delta_fwd_carries, quat_dropout_bwd, quat_dropout_fwd,
+    quat_layer_norm_bwd, quat_layer_norm_fwd, quat_norm_rotate_bwd, quat_norm_rotate_fwd)
+from .block import _rows
 
 __all__ = ["QuatCumprod", "quat_cumprod", "quat_cumprod_recalculated", "QuatNormRotate", "quat_norm_rotate",
-           "QuatDelta", "quat_delta"]
+           "QuatDelta", "quat_delta", "QuatDecay", "quat_decay", "QuatLayerNorm", "quat_layer_norm", "QuatDropout",
+           "quat_dropout"]
 
 
 class QuatCumprod(torch.autograd.Function):
@@ -140,3 +144,84 @@ def quat_delta(q, k, v, g, beta, init=None, *, scale=None, offsets=None):
     tracked = torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
     init = None if init is None else init.contiguous()
     return QuatDelta.apply(q, k, v, g, beta, init, scale, offsets, tracked)
+
+
+class QuatDecay(torch.autograd.Function):
+    """Linear attention with a decay for each head; the backward recomputes from the inputs."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, init, scale, offsets):
+        g = g.contiguous()
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)   # a cotangent that nobody has is None: no zeros are made and read for it
+        ctx.save_for_backward(q, k, v, g, init, offsets)
+        return quat_decay_fwd(q, k, v, g, init, scale=scale, offsets=offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_o, d_final):
+        q, k, v, g, init, offsets = ctx.saved_tensors
+        d_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if d_o is None else d_o.contiguous()
+        d_final = None if d_final is None else d_final.contiguous()
+        d = quat_decay_bwd(q, k, v, g, d_o, d_final, init, scale=ctx.scale, offsets=offsets)
+        return (*[t if need else None for t, need in zip(d, ctx.needs_input_grad)], None, None)
+
+
+def quat_decay(q, k, v, g, init=None, *, scale=None, offsets=None):
+    """Differentiable :func:`quat_decay_fwd`: ``(o, final_state)``.  Expanded bfloat16 inputs are copied."""
+    q, k, v = (_own_rows(t) for t in (q, k, v))
+    init = None if init is None else init.contiguous()
+    return QuatDecay.apply(q, k, v, g, init, scale, offsets)
+
+
+class QuatLayerNorm(torch.autograd.Function):
+    """Layer norm over the last dimension; the backward recomputes from the input."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        ctx.eps = eps
+        ctx.save_for_backward(x, w, b)
+        return quat_layer_norm_fwd(x, w, b, eps=eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        x, w, b = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        d = quat_layer_norm_bwd(x, d_y.contiguous(), w, b, eps=ctx.eps)
+        return (*[t if n else None for t, n in zip(d, need)], None)
+
+
+def quat_layer_norm(x, w=None, b=None, *, eps=1e-5):
+    """Differentiable :func:`quat_layer_norm_fwd`.  A view whose rows lie at no single distance is copied."""
+    try:
+        _rows(x)
+    except ValueError:
+        x = x.contiguous()
+    return QuatLayerNorm.apply(x, w, b, eps)
+
+
+class QuatDropout(torch.autograd.Function):
+    """Dropout from a counter-based generator, added on a residual; the backward makes the mask again."""
+
+    @staticmethod
+    def forward(ctx, x, key, p, residual, tracked):
+        ctx.p = p
+        if tracked:
+            ctx.save_for_backward(key.clone())   # (the program counts the key up in place)
+        return quat_dropout_fwd(x, key, p, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        need = ctx.needs_input_grad
+        d_x = quat_dropout_bwd(d_y.contiguous(), *ctx.saved_tensors, ctx.p) if need[0] else None
+        return d_x, None, None, d_y if need[3] else None, None
+
+
+def quat_dropout(x, key, p, residual=None):
+    """Differentiable :func:`quat_dropout_fwd`: ``residual + dropout(x)``.  The key is copied for the backward."""
+    x = x.contiguous()
+    residual = None if residual is None else residual.contiguous()
+    tracked = torch.is_grad_enabled() and x.requires_grad
+    return QuatDropout.apply(x, key, p, residual, tracked)

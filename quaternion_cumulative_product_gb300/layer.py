@@ -7,6 +7,10 @@ and keys (:func:`.autograd.quat_norm_rotate`) and the gated delta rule
 (:func:`.autograd.quat_delta`) follow, and an output projection.  The same layer
 trains on whole sequences, prefills a cache and continues it token by token
 (:func:`.quat_delta_step` on the cache's states in place).
+
+:class:`QuatDecayMixer` is the same layer with linear attention with a decay
+(:func:`.autograd.quat_decay`, :func:`.quat_decay_step`) in place of the delta rule, and
+:class:`QuatMixerBlock` the residual block around either: ``x + dropout(mixer(layer_norm(x)))``.
 """
 from __future__ import annotations
 
@@ -14,10 +18,10 @@ import dataclasses
 
 import torch
 
-from . import quat_cumprod_fwd, quat_delta_step, quat_norm_rotate_fwd
-from .autograd import quat_cumprod, quat_delta, quat_norm_rotate
+from . import quat_cumprod_fwd, quat_decay_step, quat_delta_step, quat_layer_norm_fwd, quat_norm_rotate_fwd
+from .autograd import quat_cumprod, quat_decay, quat_delta, quat_dropout, quat_layer_norm, quat_norm_rotate
 
-__all__ = ["QuatDeltaMixer", "MixerCache"]
+__all__ = ["QuatDeltaMixer", "QuatDecayMixer", "QuatMixerBlock", "MixerCache"]
 
 
 @dataclasses.dataclass
@@ -30,6 +34,8 @@ class MixerCache:
 class QuatDeltaMixer(torch.nn.Module):
     """``width`` -> ``width``, with ``heads`` key heads of ``dim`` values shared by ``groups`` value heads each."""
 
+    gates_per_head = 2
+
     def __init__(self, width, heads, dim, groups=1, dtype=torch.bfloat16, device="cuda"):
         super().__init__()
         if dim % 8:
@@ -39,23 +45,33 @@ class QuatDeltaMixer(torch.nn.Module):
         kw = {"bias": False, "dtype": dtype, "device": device}
         self.qkv = torch.nn.Linear(width, (2 * heads + hv) * dim, **kw)
         self.turn = torch.nn.Linear(width, heads * dim, **kw)
-        self.gates = torch.nn.Linear(width, 2 * hv, **kw)
+        self.gates = torch.nn.Linear(width, self.gates_per_head * hv, **kw)
         self.out = torch.nn.Linear(hv * dim, width, **kw)
         self.w_q = torch.nn.Parameter(torch.full((dim,), dim ** -0.5, device=device))   # unit vectors to start from
         self.w_k = torch.nn.Parameter(torch.full((dim,), dim ** -0.5, device=device))
         self.rate = torch.nn.Parameter(torch.linspace(-4.0, 0.0, hv, device=device))
 
     def _project(self, x):
-        """q, k, v (views of one projection), log decays, beta, unit quaternions near the identity."""
+        """q, k, v (views of one projection), the rule's gates, unit quaternions near the identity."""
         B, S, _ = x.shape
         H, hv = self.heads, self.heads * self.groups
         q, k, v = self.qkv(x).view(B, S, 2 * H + hv, self.dim).split([H, H, hv], dim=2)
-        a, b = self.gates(x).float().chunk(2, dim=-1)
-        g = -self.rate.exp() * torch.nn.functional.softplus(a)
+        gates = self._gates(self.gates(x).float())
         turn = self.turn(x).float().view(B, S, H, self.dim // 4, 4)
         turn = torch.cat([1 + 0.1 * turn[..., :1], 0.1 * turn[..., 1:]], -1)
         turn = turn / turn.norm(dim=-1, keepdim=True)
-        return q, k, v, g.contiguous(), torch.sigmoid(b).contiguous(), turn.contiguous()
+        return q, k, v, gates, turn.contiguous()
+
+    def _gates(self, t):
+        """Log decays and beta."""
+        a, b = t.chunk(2, dim=-1)
+        return (-self.rate.exp() * torch.nn.functional.softplus(a)).contiguous(), torch.sigmoid(b).contiguous()
+
+    def _attend(self, q, k, v, gates, state):
+        return quat_delta(q, k, v, *gates, state, scale=1.0)
+
+    def _attend_step(self, q, k, v, gates, state):
+        return quat_delta_step(q, k, v, *gates, state, scale=1.0)
 
     def _identity(self, B, device):
         turn = torch.zeros(B, self.heads, self.dim // 4, 4, device=device)
@@ -65,11 +81,11 @@ class QuatDeltaMixer(torch.nn.Module):
     def forward(self, x, cache: MixerCache | None = None):
         """``x`` [B,S,width] -> (y [B,S,width], cache): training, or prefill after ``cache``."""
         B, S, _ = x.shape
-        q, k, v, g, beta, turn = self._project(x)
+        q, k, v, gates, turn = self._project(x)
         start = self._identity(B, x.device) if cache is None else cache.turn
         cum = quat_cumprod(turn, start, save_carries=True)
         q, k = quat_norm_rotate(q, k, cum, self.w_q, self.w_k)
-        o, state = quat_delta(q, k, v, g, beta, None if cache is None else cache.state, scale=1.0)
+        o, state = self._attend(q, k, v, gates, None if cache is None else cache.state)
         # A copy: a view would keep all of cum, and step() would write into what autograd has saved.
         last = (cum[:, -1] if S else start).detach().clone(memory_format=torch.contiguous_format)
         return self.out(o.flatten(2)), MixerCache(last, state.detach())
@@ -77,9 +93,54 @@ class QuatDeltaMixer(torch.nn.Module):
     @torch.no_grad()
     def step(self, x, cache: MixerCache):
         """One token per sequence: ``x`` [B,1,width] -> y [B,1,width]; ``cache`` moves on in place."""
-        q, k, v, g, beta, turn = self._project(x)
+        q, k, v, gates, turn = self._project(x)
         cum = quat_cumprod_fwd(turn, cache.turn)
         cache.turn.copy_(cum[:, -1])
         q, k = quat_norm_rotate_fwd(q, k, cum, self.w_q, self.w_k)
-        o = quat_delta_step(q, k, v, g, beta, cache.state, scale=1.0)
+        o = self._attend_step(q, k, v, gates, cache.state)
         return self.out(o.flatten(2))
+
+
+class QuatDecayMixer(QuatDeltaMixer):
+    """The same with linear attention with a decay for each head: no beta, states that only add up."""
+
+    gates_per_head = 1
+
+    def _gates(self, t):
+        """Log decays."""
+        return ((-self.rate.exp() * torch.nn.functional.softplus(t)).contiguous(),)
+
+    def _attend(self, q, k, v, gates, state):
+        return quat_decay(q, k, v, *gates, state, scale=1.0)
+
+    def _attend_step(self, q, k, v, gates, state):
+        return quat_decay_step(q, k, v, *gates, state, scale=1.0)
+
+
+class QuatMixerBlock(torch.nn.Module):
+    """``x + dropout(mixer(layer_norm(x)))`` around a mixer of ``width``.
+
+    ``key`` (a buffer: seed, offset) draws the dropout's mask; its offset is counted up by one
+    each time the block trains, on the device, so that a captured step draws anew too.
+    """
+
+    def __init__(self, mixer, width, p=0.0, eps=1e-5, seed=0, device="cuda"):
+        super().__init__()
+        self.mixer, self.p, self.eps = mixer, p, eps
+        self.w = torch.nn.Parameter(torch.ones(width, device=device))
+        self.b = torch.nn.Parameter(torch.zeros(width, device=device))
+        self.register_buffer("key", torch.tensor([seed, 0], dtype=torch.int64, device=device))
+
+    def forward(self, x, cache: MixerCache | None = None):
+        """``x`` [B,S,width] -> (y [B,S,width], cache), as the mixer's."""
+        y, cache = self.mixer(quat_layer_norm(x, self.w, self.b, eps=self.eps), cache)
+        if not self.training or self.p == 0:
+            return x + y, cache
+        y = quat_dropout(y, self.key, self.p, x)
+        self.key[1] += 1
+        return y, cache
+
+    @torch.no_grad()
+    def step(self, x, cache: MixerCache):
+        """One token per sequence: ``x`` [B,1,width] -> y [B,1,width]; ``cache`` moves on in place."""
+        return x + self.mixer.step(quat_layer_norm_fwd(x, self.w, self.b, eps=self.eps), cache)
