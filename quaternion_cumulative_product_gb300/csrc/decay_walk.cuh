@@ -379,7 +379,6 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
             ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
-            const float f = rev ? decay(gt.sum(WC - 1), gt.sum(tid)) : a.scale * decay(gt.sum(tid), {0.f, 0.f});
             __syncwarp();
             if constexpr (!SUM) {
                 const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
@@ -407,43 +406,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
             values(it, 1);
             warp_arrive(&bar.gfree[gb]);
-            if constexpr (!SUM) {
-                const __nv_bfloat16 *be = nullptr;
-                if (BWD && ro.dots)
-                    be = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(tid, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + col0;
-                __syncwarp();
-                ok &= walk_wait_warp(&bar.y, it & 1, gone, a.ctl);
-                float dot = 0.f;
-#pragma unroll 1
-                for (int p = 0; p < HALF; p += 16) {   // f Y
-                    uint32_t r[16];
-                    uint4 q[2];
-                    if (BWD && be)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) q[j] = col0 + p + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(be + p) + j) : make_uint4(0, 0, 0, 0);
-                    tmem_ld16(tl + tmem::O + col0 + p, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f));
-                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
-                    }
-                    tmem_st16(tl + tmem::O + col0 + p, r);
-                    if (BWD && be)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t w = i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w;
-                            dot = fmaf(__uint_as_float(r[2 * i]), __uint_as_float(w << 16), dot);
-                            dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
-                        }
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar.scaled);
-                if (BWD && ro.dots && tid < left) ro.dots[(size_t)wg * a.B * a.S * a.Hv + row] = dot;
-                __syncwarp();
-            }
-            ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);
+            ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
 #pragma unroll
             for (int p = 0; p < HALF / 16; p += 2) {
                 uint32_t r[32];
@@ -510,6 +473,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     } else if (wg < 4) {
         set_registers<false, 88>();
         // ------------------------------------------------------------------ convert
+        constexpr int HALF = D / 2;   // columns of Y that this warpgroup scales
         const int part = wg - 2, rb = warp % 4;   // every other 32 columns of P; this warp's 32 rows
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
@@ -573,6 +537,50 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.p);
+                // f Y in place, and its product with the row of `beside`, which is on its way while Y is made.
+                const long long t0 = (long long)chunk_at(it) * WC;
+                const int left = (int)min((long long)WC, len - t0), row = rb * 32 + threadIdx.x % 32;
+                const float f = rev ? decay(gt.sum(WC - 1), mine) : a.scale * decay(mine, {0.f, 0.f});
+                uint4 be[HALF / 8];
+                const bool dots = BWD && ro.dots;
+                if (dots) {
+                    const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(row, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + part * HALF;
+#pragma unroll
+                    for (int j = 0; j < HALF / 8; ++j) be[j] = part * HALF + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(p) + j) : make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+                ok &= walk_wait_warp(&bar.y, it & 1, gone, a.ctl);
+                float dot = 0.f;
+                auto scale = [&](int p, const uint4 *q) {   // 16 columns
+                    uint32_t r[16];
+                    tmem_ld16(tl + tmem::O + part * HALF + p, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f));
+                        r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
+                    }
+                    tmem_st16(tl + tmem::O + part * HALF + p, r);
+                    if (q)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t w = i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w;
+                            dot = fmaf(__uint_as_float(r[2 * i]), __uint_as_float(w << 16), dot);
+                            dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
+                        }
+                };
+                if (dots) {
+#pragma unroll
+                    for (int p = 0; p < HALF; p += 16) scale(p, be + p / 8);
+                } else {
+#pragma unroll 1
+                    for (int p = 0; p < HALF; p += 16) scale(p, nullptr);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.scaled);
+                if (dots && row < left) ro.dots[(size_t)part * a.B * a.S * a.Hv + (size_t)(b * a.S + s0 + t0 + row) * a.Hv + head] = dot;
+                __syncwarp();
             }
             warp_arrive(&bar.gfree[gb]);
         }
@@ -722,7 +730,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             __syncwarp();
             if (SUM) all = sum2_add(all, gates[gb].sum(WC - 1));
             warp_arrive(&bar.gfull[gb]);
-            if (it + 1 < chunks) read(it + 1);
+            if (it + 1 < chunks) {
+                read(it + 1);
+                if (BWD && ro.other && lane == 0)   // and the states that the next chunk's are compared with, into L2
+                    bulk_prefetch(ro.other + ((size_t)(slot0 + chunk_at(it + 1)) * a.Hv + head) * D * D, D * D * 4);
+            }
         }
         if (SUM && lane == 0) ro.seg_decay[seg_at] = decay(all, {0.f, 0.f});
     } else if (!SUM) {
