@@ -15,9 +15,9 @@ namespace {
 // segment from its own.
 void cut_walks(DecayArgs &a, int sms) {
     a.segs = 1, a.seg_chunks = a.NC;
-    a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv * a.roles > sms && a.S >= 128 * a.N;
+    a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;
     if (a.offsets || a.NC < 4) return;
-    const long long pairs = a.N * a.Hv * a.roles;
+    const long long pairs = a.N * a.Hv;
     double best = (double)a.NC * ((pairs + sms - 1) / sms) * 0.9;   // cut only for a clear gain
     for (long long want = 2; want <= 64 && want <= a.NC && pairs * want <= 4 * sms; ++want) {
         const long long sc = (a.NC + want - 1) / want, n = (a.NC + sc - 1) / sc;
@@ -28,12 +28,14 @@ void cut_walks(DecayArgs &a, int sms) {
     }
 }
 
-size_t walk_floats(const DecayArgs &a, int D) {   // of seg_m, seg_own and seg_decay of every role
-    return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * a.roles * (2 * (size_t)D * D + 4) : 0;
+size_t walk_floats(const DecayArgs &a, int D) {   // of seg_m, seg_own and seg_decay
+    return a.segs > 1 ? (size_t)(a.N * a.Hv) * a.segs * (2 * (size_t)D * D + 4) : 0;
 }
 
-template <int D, bool BWD>
+// A walk of KIND, in segments with their sums and the join before it.
+template <int D, WalkKind KIND>
 int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
+    constexpr bool REV = KIND == WALK_DK || KIND == WALK_DV;
     auto go = [&](auto kernel, size_t smem, long long grid) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
             cudaGetLastError();
@@ -45,15 +47,19 @@ int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
     const long long pairs = a.N * a.Hv;
     if (a.segs > 1) {
         const size_t n = (size_t)pairs * a.segs;
-        for (int r = 0; r < a.roles; ++r, seg += n * (2 * (size_t)D * D + 4))
-            a.role[r].seg_m = seg, a.role[r].seg_own = seg + n * D * D, a.role[r].seg_decay = seg + 2 * n * D * D;
-        int rc = go(decay_walk_kernel<D, true, false>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1) * a.roles);
+        DecayRole &r = a.role;
+        r.seg_m = seg, r.seg_own = seg + n * D * D, r.seg_decay = seg + 2 * n * D * D;
+        int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1));
         if (rc != QS_OK) return rc;
-        decay_join_kernel<D><<<dim3(D * D / 1024, (unsigned)pairs, (unsigned)a.roles), 256, 0, stream>>>(a);
+        decay_join_kernel<D, REV><<<dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream>>>(a);
         rc = launched();
         if (rc != QS_OK) return rc;
     }
-    return go(decay_walk_kernel<D, false, BWD>, DecayLayout<D, false>::BYTES, pairs * a.segs * a.roles);
+    return go(decay_walk_kernel<D, KIND>, DecayLayout<D, false>::BYTES, pairs * a.segs);
+}
+template <WalkKind KIND>
+int launch_walk(DecayArgs &a, int D, float *seg, cudaStream_t stream) {
+    return D == 64 ? launch_decay<64, KIND>(a, seg, stream) : launch_decay<128, KIND>(a, seg, stream);
 }
 
 // A tensor [B, S, H, D] that a walk reads.
@@ -88,8 +94,7 @@ int set_out(DecayRole &r, const DecayArgs &a, void *out, int64_t dv, bool fp32) 
 int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     DecayArgs a{};
     set_walks(a, d);
-    a.roles = 1;
-    DecayRole &r = a.role[0];
+    DecayRole &r = a.role;
     int rc = set_role(r, a, {d.q, d.sq, d.Hk, d.Dk}, {d.k, d.sk, d.Hk, d.Dk}, {d.v, d.sv, d.Hv, d.Dv});
     if (rc == QS_OK) rc = set_out(r, a, d.o, d.Dv, false);
     if (rc != QS_OK) return rc;
@@ -102,7 +107,7 @@ int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     if (rc != QS_OK) return rc;
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
-    return D == 64 ? launch_decay<64, false>(a, seg, stream) : launch_decay<128, false>(a, seg, stream);
+    return launch_walk<WALK_OUT>(a, D, seg, stream);
 }
 
 template <int D>
@@ -118,21 +123,19 @@ int launch_gates(const GateArgs &a, cudaStream_t stream) {
 
 // dq and (with the states that it leaves) dk and dv are walks, dg a kernel of its own.
 int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
-    DecayArgs one{}, two{};
-    set_walks(one, d), set_walks(two, d);
+    DecayArgs a{};
+    set_walks(a, d);
+    cut_walks(a, sms);
     const qsh::Strides so = {(long long)(d.S * d.Hv * d.Dv), (long long)d.Hv * d.Dv, d.Dv};
     const Rows q = {d.q, d.sq, d.Hk, d.Dk}, k = {d.k, d.sk, d.Hk, d.Dk}, v = {d.v, d.sv, d.Hv, d.Dv}, o = {d.d_o, so, d.Hv, d.Dv};
     const int D = d.Dk <= 64 && d.Dv <= 64 ? 64 : 128, group = d.Hv / d.Hk;
     const bool shared = d.Hv != d.Hk;
-    const long long slots = d.offsets ? d.S / WC + d.N : d.N * one.NC;
-    one.roles = 1, two.roles = 2;
-    cut_walks(one, sms), cut_walks(two, sms);
+    const long long slots = d.offsets ? d.S / WC + d.N : d.N * a.NC;
     const size_t rows = (size_t)d.B * d.S * d.Hv, nstate = align256((size_t)slots * d.Hv * D * D * 4), ndots = align256(2 * rows * 4),
                  ncross = align256((size_t)slots * d.Hv * 8 * 4), nh = shared ? align256(rows * d.Dk * 4) : 0;
-    const size_t nseg = walk_floats(one, D) > walk_floats(two, D) ? walk_floats(one, D) : walk_floats(two, D);
     unsigned char *ws = nullptr;
     qsh::Hold hold;
-    int rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nstate + 2 * ndots + ncross + 2 * nh + nseg * 4, &ws, &hold);
+    int rc = qsh::workspace(dev, stream, sizeof(WsHeader) + nstate + 2 * ndots + ncross + 2 * nh + walk_floats(a, D) * 4, &ws, &hold);
     if (rc != QS_OK) return rc;
     unsigned char *p = ws + sizeof(WsHeader);
     auto part = [&](size_t n) {
@@ -140,27 +143,32 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
         p += n;
         return at;
     };
-    float *states = part(nstate), *dota = part(ndots), *dotb = part(ndots), *cross = part(ncross), *dqh = part(nh), *dkh = part(nh), *seg = part(nseg * 4);
-    one.ctl = two.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    DecayRole &rq = one.role[0], &rk = two.role[0], &rv = two.role[1];
-    rc = set_role(rq, one, o, v, k);
-    if (rc == QS_OK) rc = set_out(rq, one, shared ? dqh : d.dq, d.Dk, shared);
-    if (rc == QS_OK) rc = set_role(rk, two, v, o, q);
-    if (rc == QS_OK) rc = set_out(rk, two, shared ? dkh : d.dk, d.Dk, shared);
-    if (rc == QS_OK) rc = set_role(rv, two, k, q, o);
-    if (rc == QS_OK) rc = set_out(rv, two, d.dv, d.Dv, false);
-    if (rc != QS_OK) return rc;
-    rq.beside = d.q, rq.sb = d.sq, rq.gb = group, rq.dots = dota, rq.init = d.init, rq.dump = states, rq.lane = d.Dv, rq.col = 1;
-    rk.beside = d.k, rk.sb = d.sk, rk.gb = group, rk.dots = dotb, rk.init = d.d_final, rk.other = states, rk.cross = cross, rk.lane = d.Dv, rk.col = 1;
-    rv.init = d.d_final, rv.fin = d.d_init, rv.lane = 1, rv.col = d.Dv;
-    rk.rev = rv.rev = true;
-    rc = D == 64 ? launch_decay<64, true>(one, seg, stream) : launch_decay<128, true>(one, seg, stream);
-    if (rc == QS_OK) rc = D == 64 ? launch_decay<64, true>(two, seg, stream) : launch_decay<128, true>(two, seg, stream);
-    if (rc != QS_OK || d.B * d.S == 0) return rc;
+    float *states = part(nstate), *dota = part(ndots), *dotb = part(ndots), *cross = part(ncross), *dqh = part(nh), *dkh = part(nh), *seg = part(0);
+    a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     GateArgs g{};
-    g.q = rv.y, g.k = rq.z, g.v = rq.y, g.o = rq.x;
+    DecayRole &r = a.role;
+    rc = set_role(r, a, o, v, k);
+    if (rc == QS_OK) rc = set_out(r, a, shared ? dqh : d.dq, d.Dk, shared);
+    if (rc != QS_OK) return rc;
+    r.beside = d.q, r.sb = d.sq, r.gb = group, r.dots = dota, r.init = d.init, r.dump = states, r.lane = d.Dv, r.col = 1;
+    g.o = r.x, g.v = r.y, g.k = r.z;
+    rc = launch_walk<WALK_DQ>(a, D, seg, stream);
+    r = DecayRole{};
+    if (rc == QS_OK) rc = set_role(r, a, v, o, q);
+    if (rc == QS_OK) rc = set_out(r, a, shared ? dkh : d.dk, d.Dk, shared);
+    if (rc != QS_OK) return rc;
+    r.beside = d.k, r.sb = d.sk, r.gb = group, r.dots = dotb, r.init = d.d_final, r.other = states, r.cross = cross, r.lane = d.Dv, r.col = 1;
+    g.q = r.z;
+    rc = launch_walk<WALK_DK>(a, D, seg, stream);
+    r = DecayRole{};
+    if (rc == QS_OK) rc = set_role(r, a, k, q, o);
+    if (rc == QS_OK) rc = set_out(r, a, d.dv, d.Dv, false);
+    if (rc != QS_OK) return rc;
+    r.init = d.d_final, r.fin = d.d_init, r.lane = 1, r.col = d.Dv;
+    rc = launch_walk<WALK_DV>(a, D, seg, stream);
+    if (rc != QS_OK || d.B * d.S == 0) return rc;
     g.g = d.g, g.dg = d.dg, g.a = dota, g.b = dotb, g.cross = cross, g.offsets = d.offsets;
-    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = one.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = one.ctl;
+    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
     rc = D == 64 ? launch_gates<64>(g, stream) : launch_gates<128>(g, stream);
     if (rc != QS_OK || !shared) return rc;
     DeltaArgs sum = d;

@@ -64,15 +64,15 @@ struct DecayRole {
     int gx, gy, gz, gb;      // value heads that share a head of x, y, z, beside
     int dk, dv;              // values of a row of x and y; of z and out
     int lane, col;           // distances in init and fin of the state's dv and dk
-    bool rev, out32;
+    bool out32;
 };
 
 struct DecayArgs {
-    DecayRole role[3];
+    DecayRole role;
     const void *g;
     const int *offsets;
     long long B, S, N, NC, seg_chunks;   // NC: chunks per sequence without offsets
-    int Hv, segs, roles;
+    int Hv, segs;
     bool gate16, longest_first;
     float scale;
     Control ctl;
@@ -145,8 +145,7 @@ __device__ __forceinline__ bool walk_wait(uint64_t *bar, uint32_t parity, volati
     while (!mbar_sleep(bar, parity)) {
         if (*gone) return false;
         if (global_timer_ns() - t0 > ctl.timeout_ns) {
-            *gone = 1;
-            record_error(ctl.hdr, (int)blockIdx.x);
+            *gone = 1;   // (recorded once, at the kernel's end: the code of each wait stays short)
             return false;
         }
     }
@@ -219,12 +218,16 @@ __device__ __forceinline__ void store_row(float *out, const uint32_t *r, int n) 
         if (i < n) *reinterpret_cast<uint4 *>(out + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
 }
 
-// SUM: the state that a segment adds up from zero, and its decay; no out.  BWD: with what
-// d_g needs (dump, dots, cross).  Loops are kept rolled where registers allow: five roles
-// share the instruction cache (unrolled, warps waited for instructions 3.6 times as long as
-// they issued, and a chunk took 5.6 us instead of XXX).
-template <int D, bool SUM, bool BWD>
+// SUM: the state that a segment adds up from zero, and its decay; no out.  dq and dk also make
+// what d_g needs (dots, dump, cross).  Loops are kept rolled where registers allow, and kinds are
+// kernels of their own: five roles share the instruction cache (unrolled, warps waited for
+// instructions 3.6 times as long as they issued, and a chunk took 5.6 us instead of XXX).
+enum WalkKind { WALK_OUT, WALK_DQ, WALK_DK, WALK_DV, WALK_SUM, WALK_SUM_REV };
+
+template <int D, WalkKind KIND>
 __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __grid_constant__ DecayArgs a) {
+    constexpr bool SUM = KIND == WALK_SUM || KIND == WALK_SUM_REV, rev = KIND == WALK_DK || KIND == WALK_DV || KIND == WALK_SUM_REV;
+    constexpr bool dots = KIND == WALK_DQ || KIND == WALK_DK, dump = KIND == WALK_DQ, cross = KIND == WALK_DK;
     using L = DecayLayout<D, SUM>;
     namespace tmem = decay_tmem;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -233,14 +236,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     WalkGates *gates = reinterpret_cast<WalkGates *>(sm + L::GATES_AT);
     volatile int *gone = &bar.gone;
 
-    // Which walk: role, sequence, segment, head.
+    // Which walk: sequence, segment, head.
     const int segs = SUM ? a.segs - 1 : a.segs;
-    const unsigned per = (unsigned)(a.N * segs * a.Hv);
-    const DecayRole &ro = a.role[blockIdx.x / per];
-    unsigned id = blockIdx.x % per;
+    const DecayRole &ro = a.role;
+    unsigned id = blockIdx.x;
     const int head = id % a.Hv;
     id /= a.Hv;
-    const int seg = id % segs + (SUM && ro.rev ? 1 : 0);
+    const int seg = id % segs + (SUM && rev ? 1 : 0);
     long long n = id / segs;
     if (!SUM && a.longest_first) {
         int *scratch = reinterpret_cast<int *>(sm);
@@ -258,7 +260,6 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     }
     const int chunks = __reduce_min_sync(0xffffffffu, (int)((len + WC - 1) / WC));   // (in a uniform register, as the loops over it then are)
     const size_t pair = (size_t)n * a.Hv + head, seg_at = pair * a.segs + seg;
-    const bool rev = ro.rev;
     auto chunk_at = [&](int it) { return rev ? chunks - 1 - it : it; };   // the it-th chunk that the walk comes to
     const int wg = warp_uniform(threadIdx.x / 128), warp = warp_uniform(threadIdx.x / 32), tid = threadIdx.x % 128;
 
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = __reduce_min_sync(0xffffffffu, bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
-    const int terms = BWD && ro.dots ? 2 : 1;   // of M
+    constexpr int terms = dots ? 2 : 1;   // of M
     bool ok = true;   // none of this thread's waits has run out
     // Tiles come in the order y, z, x of each chunk (SUM: y, z): so the slot that one takes is
     // that of a tile which is done with early enough.  Tile i is in slot i % SLOTS.
@@ -382,11 +383,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             __syncwarp();
             if constexpr (!SUM) {
                 const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
-                if (BWD && ro.dump && tid < D)
+                if (dump && tid < D)
 #pragma unroll
                     for (int j = 0; j < HALF / 4; ++j)
                         *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
-                if (BWD && ro.other) {
+                if constexpr (cross) {
                     float2 dot = make_float2(0.f, 0.f);
                     if (tid < D)
 #pragma unroll
@@ -541,9 +542,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 const long long t0 = (long long)chunk_at(it) * WC;
                 const int left = (int)min((long long)WC, len - t0), row = rb * 32 + threadIdx.x % 32;
                 const float f = rev ? decay(gt.sum(WC - 1), mine) : a.scale * decay(mine, {0.f, 0.f});
-                uint4 be[HALF / 8];
-                const bool dots = BWD && ro.dots;
-                if (dots) {
+                uint4 be[dots ? HALF / 8 : 1];
+                if constexpr (dots) {
                     const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(row, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + part * HALF;
 #pragma unroll
                     for (int j = 0; j < HALF / 8; ++j) be[j] = part * HALF + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(p) + j) : make_uint4(0, 0, 0, 0);
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                             dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
                         }
                 };
-                if (dots) {
+                if constexpr (dots) {
 #pragma unroll
                     for (int p = 0; p < HALF; p += 16) scale(p, be + p / 8);
                 } else {
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             warp_arrive(&bar.gfull[gb]);
             if (it + 1 < chunks) {
                 read(it + 1);
-                if (BWD && ro.other && lane == 0)   // and the states that the next chunk's are compared with, into L2
+                if (cross && lane == 0)   // and the states that the next chunk's are compared with, into L2
                     bulk_prefetch(ro.other + ((size_t)(slot0 + chunk_at(it + 1)) * a.Hv + head) * D * D, D * D * 4);
             }
         }
@@ -768,13 +768,14 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_free_all(tm);
+    if (threadIdx.x == 0 && *gone) record_error(a.ctl.hdr, (int)blockIdx.x);
 }
 
 // The state that enters each segment, from the state that enters the first in walking order:
 // m' = decay m + own.  A thread per four values of a (role, sequence, head).
-template <int D>
+template <int D, bool REV>
 __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DecayArgs a) {
-    const DecayRole &ro = a.role[blockIdx.z];
+    const DecayRole &ro = a.role;
     const size_t pair = blockIdx.y;
     const int i = blockIdx.x * 256 + threadIdx.x, j4 = i / (2 * D), wg = i / D % 2, dv = i % D;   // as state_at
     float4 m = q_zero();
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
     }
     float *enter = const_cast<float *>(ro.seg_m);
     for (int s = 0; s < a.segs; ++s) {
-        const size_t at = pair * a.segs + (ro.rev ? a.segs - 1 - s : s);
+        const size_t at = pair * a.segs + (REV ? a.segs - 1 - s : s);
         *reinterpret_cast<float4 *>(enter + at * D * D + (size_t)i * 4) = m;
         if (s + 1 == a.segs) break;
         const float4 own = __ldg(reinterpret_cast<const float4 *>(ro.seg_own + at * D * D + (size_t)i * 4));
