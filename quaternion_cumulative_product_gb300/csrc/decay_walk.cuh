@@ -486,54 +486,54 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             values(it, 0);
             if constexpr (!SUM) {
                 const Sum2 mine = gt.sum(rb * 32 + threadIdx.x % 32);
+                ok &= walk_wait_warp(&bar.s, it & 1, gone, a.ctl);
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {   // 32 columns of P
-                    const int cb = part + 2 * h;
-                    const uint32_t at = tl + tmem::S + cb * 32;
-                    const bool none = rev ? cb < rb : cb > rb, diagonal = cb == rb;
-                    float2 w[16];   // scale D, while x y^T is made
+                for (int h = 0; h < 4; ++h) {   // 16 columns of P: every other block of 32, half of it at a time
+                    const int cb = part + h / 2 * 2, c0 = cb * 32 + h % 2 * 16;
+                    const uint32_t from = tl + tmem::S + c0, to = tl + tmem::S + cb * 32 + h % 2 * 8;
+                    uint32_t r[16];
+                    if (rev ? cb < rb : cb > rb) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r[i] = 0;
+                        tmem_st8(to, r);
+                        continue;
+                    }
+                    tmem_ld16(from, r);
                     // D_ts = mid_s row, the second factor at most 1 off the diagonal; on it the other way
                     // round, as long as the block's decay is no more than 2^-60, else one exp2 a value.
                     const Sum2 face = rev ? cb ? gt.sum(cb * 32 - 1) : Sum2{0.f, 0.f} : gt.sum(cb * 32 + 31);
-                    const int t = threadIdx.x % 32;
-                    if (diagonal && fabsf(face.hi - gt.hi[cb * 32 + (rev ? 31 : 0)]) > 60.f) {
+                    const bool diagonal = cb == rb;
+                    const int t = threadIdx.x % 32 - h % 2 * 16;   // the diagonal's column
+                    const float row = a.scale * (rev ? decay(face, mine) : decay(mine, face));
+                    float2 w[8];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&gt.lo[cb * 32 + 2 * i]));
-                            const float d0 = (mine.hi - gt.hi[cb * 32 + 2 * i]) + (mine.lo - lo.x), d1 = (mine.hi - gt.hi[cb * 32 + 2 * i + 1]) + (mine.lo - lo.y);
-                            w[i] = make_float2((rev ? 2 * i >= t : 2 * i <= t) ? a.scale * exp2_fast(rev ? -d0 : d0) : 0.f,
-                                               (rev ? 2 * i + 1 >= t : 2 * i + 1 <= t) ? a.scale * exp2_fast(rev ? -d1 : d1) : 0.f);
-                        }
-                    } else if (!none) {
-                        const float row = a.scale * (rev ? decay(face, mine) : decay(mine, face));
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 o = *reinterpret_cast<const float4 *>(&gt.mid[c0 + 4 * i]);
+                        w[2 * i] = mul2(make_float2(o.x, o.y), make_float2(row, row)), w[2 * i + 1] = mul2(make_float2(o.z, o.w), make_float2(row, row));
+                    }
+                    if (diagonal) {
+                        if (fabsf(face.hi - gt.hi[cb * 32 + (rev ? 31 : 0)]) > 60.f) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 o = *reinterpret_cast<const float4 *>(&gt.mid[cb * 32 + i]);
-                            w[i / 2] = mul2(make_float2(o.x, o.y), make_float2(row, row)), w[i / 2 + 1] = mul2(make_float2(o.z, o.w), make_float2(row, row));
-                        }
-                        if (diagonal)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                if (rev ? 2 * i < t : 2 * i > t) w[i].x = 0.f;
-                                if (rev ? 2 * i + 1 < t : 2 * i + 1 > t) w[i].y = 0.f;
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&gt.lo[c0 + 2 * i])), hi = *reinterpret_cast<const float2 *>(&gt.hi[c0 + 2 * i]);
+                                const float d0 = (mine.hi - hi.x) + (mine.lo - lo.x), d1 = (mine.hi - hi.y) + (mine.lo - lo.y);
+                                w[i] = make_float2(a.scale * exp2_fast(fminf(rev ? -d0 : d0, 0.f)), a.scale * exp2_fast(fminf(rev ? -d1 : d1, 0.f)));
                             }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (rev ? 2 * i < t : 2 * i > t) w[i].x = 0.f;
+                            if (rev ? 2 * i + 1 < t : 2 * i + 1 > t) w[i].y = 0.f;
+                        }
                     }
                     __syncwarp();
-                    if (h == 0) ok &= walk_wait_warp(&bar.s, it & 1, gone, a.ctl);
-                    if (none) {
-                        const uint32_t z[16] = {};
-                        tmem_st16(at, z);
-                    } else {
-                        uint32_t r[32];
-                        tmem_ld32(at, r);
-                        tmem_wait_ld();
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = mul2(w[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
-                            r[i] = pack_bf16(x.x, x.y);
-                        }
-                        tmem_st16(at, r);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 x = mul2(w[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+                        r[i] = pack_bf16(x.x, x.y);
                     }
+                    tmem_st8(to, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
