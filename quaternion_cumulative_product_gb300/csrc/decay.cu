@@ -49,13 +49,13 @@ int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
         const size_t n = (size_t)pairs * a.segs;
         DecayRole &r = a.role;
         r.seg_m = seg, r.seg_own = seg + n * D * D, r.seg_decay = seg + 2 * n * D * D;
-        int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true>::BYTES, pairs * (a.segs - 1));
+        int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true, false>::BYTES, pairs * (a.segs - 1));
         if (rc != QS_OK) return rc;
         decay_join_kernel<D, REV><<<dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream>>>(a);
         rc = launched();
         if (rc != QS_OK) return rc;
     }
-    return go(decay_walk_kernel<D, KIND>, DecayLayout<D, false>::BYTES, pairs * a.segs);
+    return go(decay_walk_kernel<D, KIND>, DecayLayout<D, false, KIND == WALK_DQ || KIND == WALK_DK>::BYTES, pairs * a.segs);
 }
 template <WalkKind KIND>
 int launch_walk(DecayArgs &a, int D, float *seg, cudaStream_t stream) {
@@ -150,14 +150,18 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     rc = set_role(r, a, o, v, k);
     if (rc == QS_OK) rc = set_out(r, a, shared ? dqh : d.dq, d.Dk, shared);
     if (rc != QS_OK) return rc;
-    r.beside = d.q, r.sb = d.sq, r.gb = group, r.dots = dota, r.init = d.init, r.dump = states, r.lane = d.Dv, r.col = 1;
+    if (d.B * d.S > 0) rc = qsh::head_map(&r.b, d.q, d.sq, d.B, d.S, d.Hk, d.Dk);
+    if (rc != QS_OK) return rc;
+    r.gb = group, r.dots = dota, r.init = d.init, r.dump = states, r.lane = d.Dv, r.col = 1;
     g.o = r.x, g.v = r.y, g.k = r.z;
     rc = launch_walk<WALK_DQ>(a, D, seg, stream);
     r = DecayRole{};
     if (rc == QS_OK) rc = set_role(r, a, v, o, q);
     if (rc == QS_OK) rc = set_out(r, a, shared ? dkh : d.dk, d.Dk, shared);
     if (rc != QS_OK) return rc;
-    r.beside = d.k, r.sb = d.sk, r.gb = group, r.dots = dotb, r.init = d.d_final, r.other = states, r.cross = cross, r.lane = d.Dv, r.col = 1;
+    if (d.B * d.S > 0) rc = qsh::head_map(&r.b, d.k, d.sk, d.B, d.S, d.Hk, d.Dk);
+    if (rc != QS_OK) return rc;
+    r.gb = group, r.dots = dotb, r.init = d.d_final, r.other = states, r.cross = cross, r.lane = d.Dv, r.col = 1;
     g.q = r.z;
     rc = launch_walk<WALK_DK>(a, D, seg, stream);
     r = DecayRole{};

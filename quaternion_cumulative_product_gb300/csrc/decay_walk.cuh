@@ -45,14 +45,12 @@
 namespace qs {
 
 constexpr int WC = 128;              // steps per chunk
-enum { TILE_Y, TILE_Z, TILE_X };     // a chunk's tiles, in the order in which they come
 constexpr int kDecayThreads = 640;   // five warpgroups
 
 struct DecayRole {
-    CUtensorMap x, y, z, o;  // (o: of out, bfloat16)
+    CUtensorMap x, y, z, o, b;   // (o: of out, bfloat16; b: of `beside`)
     void *out;               // [B, S, Hv, dv], bfloat16 or (out32) fp32
-    const void *beside;      // dots: <beside_t, f Y_t>, bfloat16, or NULL
-    float *dots;             // [2][B, S, Hv] by halves of the columns
+    float *dots;             // <beside_t, f Y_t> [2][B, S, Hv] by halves of the columns
     const float *init;       // state that enters (first chunk of a walk) [N, Hv, ..], or NULL
     float *fin;              // state that leaves, or NULL
     float *dump;             // state that enters each chunk [slots, Hv, D * D], or NULL
@@ -60,7 +58,6 @@ struct DecayRole {
     float *cross;            // [slots, Hv]
     const float *seg_m;      // state that enters each segment
     float *seg_own, *seg_decay;
-    qsh::Strides sb;         // of `beside`
     int gx, gy, gz, gb;      // value heads that share a head of x, y, z, beside
     int dk, dv;              // values of a row of x and y; of z and out
     int lane, col;           // distances in init and fin of the state's dv and dk
@@ -93,20 +90,24 @@ struct __align__(16) WalkGates {
 };
 
 struct DecayBars {
-    uint64_t full[8], empty[8], aux, gfull[2], gfree[2];
+    uint64_t full[8], empty[8], aux, beside, gfull[2], gfree[2];
     uint64_t s, p, y, scaled, out, ofree, staged, vl, dm0, dm, m, drain;
     uint32_t tmem;
     int gone;
 };
 
-template <int D, bool SUM>
+template <int D, bool SUM, bool DOTS>
 struct DecayLayout {
     static constexpr int HALVES = D / 64, PER = SUM ? 2 : 3;               // tiles per chunk
     static constexpr uint32_t HALF = WC * 128, TILE_BYTES = HALVES * HALF;  // tile: [half of D][128 steps][64 values]
-    static constexpr int SLOTS = D == 64 ? 6 : 5;
+    // Room for five tiles (six of 64 values), of which one is `beside`'s and, later in the chunk, out's.
+    static constexpr int ROOM = D == 64 ? 6 : 5, SLOTS = DOTS ? ROOM - 1 : ROOM;
+    // The order in which a chunk's tiles come, so that the slot that one takes is that of a tile
+    // which is done with early enough: y after dM, x after Y (or, where out leaves from its place, after that), z after out.
+    static constexpr int Y = 0, X = DOTS ? 1 : 2, Z = DOTS ? 2 : 1;
     static constexpr int GB = 2;                                            // chunks of gates
     static constexpr uint32_t M_HALF = D * 128, M_TERM = HALVES * M_HALF;   // M: [term][half of dk][dv rows][64]
-    static constexpr uint32_t M_AT = SLOTS * TILE_BYTES, GATES_AT = M_AT + 2 * M_TERM;
+    static constexpr uint32_t M_AT = ROOM * TILE_BYTES, GATES_AT = M_AT + 2 * M_TERM;
     static constexpr uint32_t BARS_AT = GATES_AT + GB * sizeof(WalkGates), NEED = BARS_AT + sizeof(DecayBars);
     static constexpr uint32_t BYTES = NEED > 117760 ? NEED : 117760;        // one CTA per SM: it takes all of the tensor memory
     static_assert(BYTES <= 232448, "227 KB of shared memory");
@@ -228,7 +229,7 @@ template <int D, WalkKind KIND>
 __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __grid_constant__ DecayArgs a) {
     constexpr bool SUM = KIND == WALK_SUM || KIND == WALK_SUM_REV, rev = KIND == WALK_DK || KIND == WALK_DV || KIND == WALK_SUM_REV;
     constexpr bool dots = KIND == WALK_DQ || KIND == WALK_DK, dump = KIND == WALK_DQ, cross = KIND == WALK_DK;
-    using L = DecayLayout<D, SUM>;
+    using L = DecayLayout<D, SUM, dots>;
     namespace tmem = decay_tmem;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t sm32 = smem_addr(sm);   // (1024-byte aligned: the kernel has no other shared memory)
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
-        for (uint64_t *x : {&bar.aux, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
+        for (uint64_t *x : {&bar.aux, &bar.beside, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
         for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.staged, &bar.vl, &bar.m}) mbar_init(x, 8);   // two warpgroups' warps
         mbar_init(&bar.gfree[0], 16), mbar_init(&bar.gfree[1], 16);
         *gone = 0;
@@ -278,9 +279,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     const uint32_t tm = __reduce_min_sync(0xffffffffu, bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
     constexpr int terms = dots ? 2 : 1;   // of M
     bool ok = true;   // none of this thread's waits has run out
-    // Tiles come in the order y, z, x of each chunk (SUM: y, z): so the slot that one takes is
-    // that of a tile which is done with early enough.  Tile i is in slot i % SLOTS.
-    auto tile = [&](int it, int which) { return L::PER * it + which; };   // `which`: Y, Z, X
+    auto tile = [&](int it, int which) { return L::PER * it + which; };   // the it-th chunk's; tile i is in slot i % SLOTS
+    auto stage_at = [&](int it) { return dots ? (uint32_t)(L::ROOM - 1) * L::TILE_BYTES : (uint32_t)(tile(it, L::X) % L::SLOTS) * L::TILE_BYTES; };
     auto slot = [&](int i) { return (uint32_t)(i % L::SLOTS) * L::TILE_BYTES; };
     // Waits of the warps that issue: whole warps go on or stop together.
     auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, walk_wait_warp(x, parity, gone, a.ctl)) != 0; };
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     // row lane / 4 (+ 8, 16, 24), which is how the 16-lane stores to tensor memory want them.
     auto values = [&](int it, int h) {
         const int lane = threadIdx.x % 32, step0 = h * 64 + wg % 2 * 32, row0 = warp % 4 * 32 % D;
-        uint32_t at = sm32 + slot(tile(it, TILE_Z)) + (uint32_t)(row0 / 64) * L::HALF + (uint32_t)(step0 + lane / 8 % 2 * 8 + lane % 8) * 128 +
+        uint32_t at = sm32 + slot(tile(it, L::Z)) + (uint32_t)(row0 / 64) * L::HALF + (uint32_t)(step0 + lane / 8 % 2 * 8 + lane % 8) * 128 +
                       (uint32_t)(((row0 % 64 / 8 + lane / 16) ^ (lane % 8)) << 4);
         const float *f = &gates[it % L::GB].mid[step0 + lane % 4 * 2], edge = gates[it % L::GB].edge[h * 2 + wg % 2] * (rev ? a.scale : 1.f);
         uint32_t to = tl + tmem::VL + wg % 2 * 16;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
                 }
             }
-            ok &= wait_tile(tile(it, TILE_Z));
+            ok &= wait_tile(tile(it, L::Z));
             ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
             values(it, 1);
             warp_arrive(&bar.gfree[gb]);
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             give_m();
             if constexpr (!SUM) {
                 ok &= walk_wait_warp(&bar.out, it & 1, gone, a.ctl);
-                // Whole chunks leave by TMA, from x's place, which is done with.
+                // Whole chunks leave by TMA, from x's place (dots: from `beside`'s), which is done with.
                 if (ro.out32 || (a.offsets && left < WC)) {
 #pragma unroll 1
                     for (int p = 0; p < HALF / 16; ++p) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     tc_fence_before();
                     warp_arrive(&bar.ofree);
                 } else {
-                    const uint32_t stage = sm32 + slot(tile(it, TILE_X));
+                    const uint32_t stage = sm32 + stage_at(it);
 #pragma unroll 1
                     for (int p = 0; p < HALF; p += 16) {
                         uint32_t r[16];
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const int gb = it % L::GB;
             const WalkGates &gt = gates[gb];
             ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
-            ok &= wait_tile(tile(it, TILE_Z));
+            ok &= wait_tile(tile(it, L::Z));
             if (it > 0) ok &= walk_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);   // the last half's terms are done with
             values(it, 0);
             if constexpr (!SUM) {
@@ -538,49 +538,41 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.p);
-                // f Y in place, and its product with the row of `beside`, which is on its way while Y is made.
-                const long long t0 = (long long)chunk_at(it) * WC;
-                const int left = (int)min((long long)WC, len - t0), row = rb * 32 + threadIdx.x % 32;
+                // f Y in place, and its product with the row of `beside`.
                 const float f = rev ? decay(gt.sum(WC - 1), mine) : a.scale * decay(mine, {0.f, 0.f});
-                uint4 be[dots ? HALF / 8 : 1];
-                if constexpr (dots) {
-                    const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(ro.beside) + b * ro.sb.b + (s0 + t0 + min(row, left - 1)) * ro.sb.s + (long long)(head / ro.gb) * ro.sb.h + part * HALF;
-#pragma unroll
-                    for (int j = 0; j < HALF / 8; ++j) be[j] = part * HALF + 8 * j < ro.dv ? __ldg(reinterpret_cast<const uint4 *>(p) + j) : make_uint4(0, 0, 0, 0);
-                }
-                __syncwarp();
+                const int row = rb * 32 + threadIdx.x % 32;
+                const unsigned char *be = sm + (L::ROOM - 1) * L::TILE_BYTES;
+                if (dots) ok &= walk_wait_warp(&bar.beside, it & 1, gone, a.ctl);
                 ok &= walk_wait_warp(&bar.y, it & 1, gone, a.ctl);
-                float dot = 0.f;
-                auto scale = [&](int p, const uint4 *q) {   // 16 columns
+                float2 dot = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int c = part * HALF; c < part * HALF + HALF; c += 16) {
                     uint32_t r[16];
-                    tmem_ld16(tl + tmem::O + part * HALF + p, r);
+                    tmem_ld16(tl + tmem::O + c, r);
+                    uint4 q[2];
+                    if (dots)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) q[j] = *reinterpret_cast<const uint4 *>(be + c / 64 * L::HALF + swizzled(row, c % 64 / 8 + j));
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 y = mul2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), make_float2(f, f));
                         r[2 * i] = __float_as_uint(y.x), r[2 * i + 1] = __float_as_uint(y.y);
-                    }
-                    tmem_st16(tl + tmem::O + part * HALF + p, r);
-                    if (q)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        if (dots) {
                             const uint32_t w = i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w;
-                            dot = fmaf(__uint_as_float(r[2 * i]), __uint_as_float(w << 16), dot);
-                            dot = fmaf(__uint_as_float(r[2 * i + 1]), __uint_as_float(w & 0xffff0000u), dot);
+                            dot = fma2(y, make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), dot);
                         }
-                };
-                if constexpr (dots) {
-#pragma unroll
-                    for (int p = 0; p < HALF; p += 16) scale(p, be + p / 8);
-                } else {
-#pragma unroll 1
-                    for (int p = 0; p < HALF; p += 16) scale(p, nullptr);
+                    }
+                    tmem_st16(tl + tmem::O + c, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.scaled);
-                if (dots && row < left) ro.dots[(size_t)part * a.B * a.S * a.Hv + (size_t)(b * a.S + s0 + t0 + row) * a.Hv + head] = dot;
-                __syncwarp();
+                if (dots) {
+                    const long long t = (long long)chunk_at(it) * WC + row;
+                    if (t < len) ro.dots[(size_t)part * a.B * a.S * a.Hv + (size_t)(b * a.S + s0 + t) * a.Hv + head] = dot.x + dot.y;
+                    __syncwarp();
+                }
             }
             warp_arrive(&bar.gfree[gb]);
         }
@@ -593,9 +585,9 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         auto tile_at = [&](int i) { return __reduce_min_sync(0xffffffffu, sm32 + slot(i)); };   // (uniform descriptors: tensor_core.cuh)
         auto all_tile = [&](int i) { return all_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1); };
         auto scores = [&](int it) {   // S = x y^T
-            ok &= all_tile(tile(it, TILE_Y));
-            ok &= all_tile(tile(it, TILE_X));
-            const uint64_t x = smem_desc(tile_at(tile(it, TILE_X)), 16, 1024), y = smem_desc(tile_at(tile(it, TILE_Y)), 16, 1024);
+            ok &= all_tile(tile(it, L::Y));
+            ok &= all_tile(tile(it, L::X));
+            const uint64_t x = smem_desc(tile_at(tile(it, L::X)), 16, 1024), y = smem_desc(tile_at(tile(it, L::Y)), 16, 1024);
             if (elect_one() && ok) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::S, x + k_major(k), y + k_major(k), id_s, k > 0);
@@ -605,7 +597,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         };
         auto update = [&](int it, int h) {   // dM += (h z)^T y over 64 steps
             ok &= all_wait(&bar.vl, h);
-            const uint64_t y = smem_desc(tile_at(tile(it, TILE_Y)) + h * 64 * 128, L::HALF, 1024);
+            const uint64_t y = smem_desc(tile_at(tile(it, L::Y)) + h * 64 * 128, L::HALF, 1024);
             if (elect_one() && ok) {
 #pragma unroll 1
                 for (int j = 2; j >= 0; --j)
@@ -613,15 +605,15 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     for (int k = 0; k < 4; ++k)
                         mma_ts(tm + tmem::DM, tm + tmem::VL + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
                 mma_commit(h ? &bar.dm : &bar.dm0);
-                if (h) mma_commit(&bar.empty[tile(it, TILE_Y) % L::SLOTS]);
-                if (h && SUM) mma_commit(&bar.empty[tile(it, TILE_Z) % L::SLOTS]);
+                if (h) mma_commit(&bar.empty[tile(it, L::Y) % L::SLOTS]);
+                if (h && SUM) mma_commit(&bar.empty[tile(it, L::Z) % L::SLOTS]);
             }
             __syncwarp();
         };
         // What a chunk begins with: its scores and the first half of its dM (behind the last chunk's out).
         auto begin = [&](int it) {
             if (!SUM) scores(it);
-            else ok &= all_tile(tile(it, TILE_Y));
+            else ok &= all_tile(tile(it, L::Y));
             ok &= all_wait(&bar.m, it & 1);   // dM has been read (and M's terms are there)
             update(it, 0);
         };
@@ -630,7 +622,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             begin(it);
             if constexpr (!SUM) {   // Y = x M
                 if (it > 0) ok &= all_wait(&bar.ofree, (it - 1) & 1);
-                const uint64_t x = smem_desc(tile_at(tile(it, TILE_X)), 16, 1024), y = smem_desc(__reduce_min_sync(0xffffffffu, sm32 + L::M_AT), 16, 1024);
+                const uint64_t x = smem_desc(tile_at(tile(it, L::X)), 16, 1024), y = smem_desc(__reduce_min_sync(0xffffffffu, sm32 + L::M_AT), 16, 1024);
                 if (elect_one() && ok) {
 #pragma unroll 1
                     for (int j = terms - 1; j >= 0; --j)   // the small term first
@@ -638,6 +630,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                         for (int k = 0; k < D / 16; ++k)
                             mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j < terms - 1 || k > 0);
                     mma_commit(&bar.y);
+                    if (dots) mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
                 }
                 __syncwarp();
             }
@@ -645,13 +638,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             if constexpr (!SUM) {   // out = f Y + P z
                 ok &= all_wait(&bar.p, it & 1);
                 ok &= all_wait(&bar.scaled, it & 1);
-                ok &= all_tile(tile(it, TILE_Z));
-                const uint64_t z = smem_desc(tile_at(tile(it, TILE_Z)), L::HALF, 1024);
+                ok &= all_tile(tile(it, L::Z));
+                const uint64_t z = smem_desc(tile_at(tile(it, L::Z)), L::HALF, 1024);
                 if (elect_one() && ok) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
                     mma_commit(&bar.out);
-                    mma_commit(&bar.empty[tile(it, TILE_Z) % L::SLOTS]);
+                    mma_commit(&bar.empty[tile(it, L::Z) % L::SLOTS]);
                 }
                 __syncwarp();
             }
@@ -670,11 +663,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             if (!ok) break;
             const long long t0 = (long long)chunk_at(it) * WC;
             const int left = (int)min((long long)WC, len - t0);
-            const bool clear = a.offsets && which != TILE_X && left < WC;   // rows of y and z past the end count as zero
+            const bool clear = a.offsets && which != L::X && left < WC;   // rows of y and z past the end count as zero
             unsigned char *dst = sm + slot(i);
             if (elect_one()) {
-                const CUtensorMap *map = which == TILE_X ? &ro.x : which == TILE_Y ? &ro.y : &ro.z;
-                const int h = head / (which == TILE_X ? ro.gx : which == TILE_Y ? ro.gy : ro.gz), s = (int)(s0 + t0);
+                const CUtensorMap *map = which == L::X ? &ro.x : which == L::Y ? &ro.y : &ro.z;
+                const int h = head / (which == L::X ? ro.gx : which == L::Y ? ro.gy : ro.gz), s = (int)(s0 + t0);
                 uint64_t *on = clear ? &bar.aux : &bar.full[sl];
                 // (The test hook makes CTA `stall_tile` expect 16 bytes that never come.)
                 mbar_arrive_expect_tx(on, L::TILE_BYTES + ((int)blockIdx.x == a.ctl.stall_tile ? 16 : 0));
@@ -740,26 +733,47 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     } else if (!SUM) {
         // ------------------------------------------------------------------ out to memory
         bool some = false;
+        int asked = 0;   // tiles of `beside`
+        auto beside = [&](int it) {
+            if (!dots || it >= chunks || !ok) return;
+            if (elect_one()) {
+                const int s = (int)(s0 + (long long)chunk_at(it) * WC), h = head / ro.gb;
+                unsigned char *dst = sm + (L::ROOM - 1) * L::TILE_BYTES;
+                mbar_arrive_expect_tx(&bar.beside, L::TILE_BYTES);
+#pragma unroll
+                for (int x = 0; x < L::HALVES; ++x) {
+                    tma_load_4d(dst + x * L::HALF, &ro.b, x * 64, h, s, (int)b, &bar.beside);
+                    tma_load_4d(dst + x * L::HALF + 8192, &ro.b, x * 64, h, s + 64, (int)b, &bar.beside);
+                }
+            }
+            __syncwarp();
+            asked = it + 1;
+        };
+        beside(0);
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             ok &= all_wait(&bar.staged, it & 1);
             const long long t0 = (long long)chunk_at(it) * WC;
-            const int left = (int)min((long long)WC, len - t0), i = tile(it, TILE_X);
+            const int left = (int)min((long long)WC, len - t0);
             const bool staged = !ro.out32 && !(a.offsets && left < WC);
             if (elect_one() && ok) {
                 if (staged) {
+                    const unsigned char *src = sm + stage_at(it);
 #pragma unroll
                     for (int x = 0; x < 2 * L::HALVES; ++x)
                         if (x / 2 * 64 < ro.dv && (x % 2 == 0 || left > 64))
-                            tma_store_4d(&ro.o, sm + slot(i) + x / 2 * L::HALF + x % 2 * 8192, x / 2 * 64, head, (int)(s0 + t0) + x % 2 * 64, (int)b);
+                            tma_store_4d(&ro.o, src + x / 2 * L::HALF + x % 2 * 8192, x / 2 * 64, head, (int)(s0 + t0) + x % 2 * 64, (int)b);
                     bulk_commit_group();
                     bulk_wait_group_read<0>();
                     some = true;
                 }
-                mbar_arrive(&bar.empty[i % L::SLOTS]);
+                if (!dots) mbar_arrive(&bar.empty[tile(it, L::X) % L::SLOTS]);
             }
             __syncwarp();
+            beside(it + 1);
         }
+        if (dots && elect_one() && (!ok || *gone) && asked) drain_wait(&bar.beside, (asked - 1) & 1, a.ctl);
+        __syncwarp();
         if (some) bulk_wait_group_all();
         __syncwarp();
     }
