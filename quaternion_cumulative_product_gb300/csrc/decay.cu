@@ -172,7 +172,7 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     rc = launch_walk<WALK_DV>(a, D, seg, stream);
     if (rc != QS_OK || d.B * d.S == 0) return rc;
     g.g = d.g, g.dg = d.dg, g.a = dota, g.b = dotb, g.cross = cross, g.offsets = d.offsets;
-    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
+    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.ahead = 2 * (unsigned)sms, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
     rc = D == 64 ? launch_gates<64>(g, stream) : launch_gates<128>(g, stream);
     if (rc != QS_OK || !shared) return rc;
     DeltaArgs sum = d;

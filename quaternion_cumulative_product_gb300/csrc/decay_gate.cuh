@@ -22,7 +22,7 @@
 
 namespace qs {
 
-constexpr int kGateThreads = 256;
+constexpr int kGateThreads = 512;
 
 struct GateArgs {
     CUtensorMap q, k, v, o;       // o: dO
@@ -32,6 +32,7 @@ struct GateArgs {
     const int *offsets;
     long long B, S, N, NC, slots;
     int Hv, shared;               // value heads that share a key head
+    unsigned ahead;               // CTAs that run at once
     bool gate16;
     float scale;
     Control ctl;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
     tc_fence_after();
     const uint32_t tm = (uint32_t)warp_uniform((int)sh.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);
     bool ok = true;
-    if (warp == 7) {   // products: Q, K and V come first, dO in Q's place once S is made
+    if (warp == 12) {   // products (a warp without a piece of Z, as the gates' one): Q, K and V come first, dO in Q's place once S is made
         auto load = [&](const CUtensorMap *map, int at, int h, uint64_t *on) {
             mbar_arrive_expect_tx(on, L::TILE_BYTES);
 #pragma unroll
@@ -115,7 +116,22 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
             mma_commit(done);
         };
         const int kh = head / a.shared;
-        if (elect_one()) load(&a.q, 0, kh, &sh.q), load(&a.k, 1, kh, &sh.k), load(&a.v, 2, head, &sh.v);
+        if (elect_one()) {
+            load(&a.q, 0, kh, &sh.q), load(&a.k, 1, kh, &sh.k), load(&a.v, 2, head, &sh.v);
+#pragma unroll
+            for (int x = 0; x < 2 * L::HALVES; ++x) tma_prefetch_4d(&a.o, x / 2 * 64, head, (int)(s0 + t0) + x % 2 * 64, (int)b);
+            // The CTA that likely comes next on this SM: its tiles into L2 meanwhile.
+            const unsigned next = blockIdx.x + a.ahead;
+            if (!a.offsets && next < gridDim.x) {
+                const int h = next % a.Hv, s = (int)(next / a.Hv % a.NC) * WC, nb = (int)(next / a.Hv / a.NC);
+#pragma unroll
+                for (int x = 0; x < 2 * L::HALVES; ++x) {
+                    tma_prefetch_4d(&a.q, x / 2 * 64, h / a.shared, s + x % 2 * 64, nb);
+                    tma_prefetch_4d(&a.k, x / 2 * 64, h / a.shared, s + x % 2 * 64, nb);
+                    tma_prefetch_4d(&a.v, x / 2 * 64, h, s + x % 2 * 64, nb);
+                }
+            }
+        }
         __syncwarp();
         auto both = [&](uint64_t *x) { ok &= __all_sync(0xffffffffu, tc_wait_warp(x, 0, gone, a.ctl)) != 0; };
         both(&sh.q), both(&sh.k);
@@ -135,7 +151,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
         }
         __syncwarp();
     }
-    if (warp == 6) {
+    if (warp == 8) {
         float raw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = 4 * lane + i < left ? load_any(a.g, a.gate16, row0 + (size_t)(4 * lane + i) * a.Hv) : 0.f;
@@ -149,8 +165,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
     const int rb = warp % 4, t = rb * 32 + lane;
     const Sum2 mine = gt.sum(t);
     const bool live = t < left;
-#pragma unroll 1
-    for (int cb = warp / 4; cb <= rb; cb += 2) {
+    const int cb = warp / 4;
+    if (cb <= rb) {
         const bool diagonal = cb == rb;
         const float row = diagonal ? 0.f : a.scale * decay(mine, gt.sum(cb * 32 + 31));
         float z[32], sum = 0.f;
