@@ -83,7 +83,14 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
     const int left = (int)min((long long)WC, len - t0);
     const size_t row0 = (size_t)(b * a.S + s0 + t0) * a.Hv + head;
 
-    if (threadIdx.x == 0) {
+    // What the walks have left, for the last step's warps (step u = warp * 32 + lane); on its way meanwhile.
+    float fa = 0.f, fb = 0.f, whole = 0.f;
+    if (warp < 4) {
+        const size_t half = (size_t)a.B * a.S * a.Hv, at = row0 + (size_t)(warp * 32 + lane) * a.Hv;
+        if (warp * 32 + lane < left) fa = a.a[at] + a.a[half + at], fb = a.b[at] + a.b[half + at];
+        if (lane < 8) whole = a.cross[((size_t)slot * a.Hv + head) * 8 + lane];
+    }
+    if (threadIdx.x == 32) {
         for (uint64_t *x : {&sh.q, &sh.k, &sh.v, &sh.o, &sh.s, &sh.e, &sh.drain}) mbar_init(x, 1);
         *gone = 0;
         fence_mbar_init();
@@ -206,10 +213,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
     if (warp >= 4) return;
     // A warp takes the 32 steps u of block `warp`.
     const int u = warp * 32 + lane;
-    const size_t half = (size_t)a.B * a.S * a.Hv, at = row0 + (size_t)u * a.Hv;
-    const float fa = u < left ? a.a[at] + a.a[half + at] : 0.f, fb = u < left ? a.b[at] + a.b[half + at] : 0.f;
-    float d = 0.f, below = 0.f, here = 0.f, whole = 0.f;
-    if (lane < 8) whole = a.cross[((size_t)slot * a.Hv + head) * 8 + lane];
+    float d = 0.f, below = 0.f, here = 0.f;
     for (int r = warp; r < 4; ++r) d += sh.columns[r][u];
     // Rows' sums over the blocks before this one: of the rows below, whole; of its own, from step u on.
     for (int cb = 0; cb < warp; ++cb) {
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
     if (lane == 0) before = 0.f;
     for (int r = 0; r < warp; ++r) before += sh.sumb[r];
     for (int r = warp + 1; r < 4; ++r) from += sh.suma[r];
-    if (u < left) store_any(a.dg, a.gate16, at, d + below + from + before + whole);
+    if (u < left) store_any(a.dg, a.gate16, row0 + (size_t)u * a.Hv, d + below + from + before + whole);
 }
 
 }  // namespace qs

@@ -381,32 +381,30 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
             __syncwarp();
-            if constexpr (!SUM) {
-                const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
-                if (dump && tid < D)
+            const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
+            if constexpr (cross) {   // (before the chunk's products are asked for: 204 us; behind h z's second half 221)
+                float2 dot = make_float2(0.f, 0.f);
+                if (tid < D)
 #pragma unroll
-                    for (int j = 0; j < HALF / 4; ++j)
-                        *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
-                if constexpr (cross) {
-                    float2 dot = make_float2(0.f, 0.f);
-                    if (tid < D)
+                    for (int j = 0; j < HALF / 4; ++j) {
+                        const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid)));
+                        dot = fma2(m[2 * j], make_float2(v.x, v.y), dot);
+                        dot = fma2(m[2 * j + 1], make_float2(v.z, v.w), dot);
+                    }
+                float sum = (dot.x + dot.y) * whole;
+                __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < HALF / 4; ++j) {
-                            const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid)));
-                            dot = fma2(m[2 * j], make_float2(v.x, v.y), dot);
-                            dot = fma2(m[2 * j + 1], make_float2(v.z, v.w), dot);
-                        }
-                    float sum = (dot.x + dot.y) * whole;
-                    __syncwarp();
-#pragma unroll
-                    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
-                }
+                for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
             }
             ok &= wait_tile(tile(it, L::Z));
             ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
             values(it, 1);
             warp_arrive(&bar.gfree[gb]);
+            if (dump && tid < D)   // while Y and the rest of dM are made (175 us before them, 156 here)
+#pragma unroll
+                for (int j = 0; j < HALF / 4; ++j)
+                    *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
             ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
 #pragma unroll
             for (int p = 0; p < HALF / 16; p += 2) {
