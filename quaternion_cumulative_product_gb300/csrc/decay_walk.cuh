@@ -289,7 +289,12 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     // Terms of h z, 32 of the chunk's steps 64h .. (the first half by `convert`, the second by `state`):
     // 16 steps at a time, transposed by the loads, so that a register holds two steps of value
     // row lane / 4 (+ 8, 16, 24), which is how the 16-lane stores to tensor memory want them.
+    const bool rows = D == 128 || warp % 4 < 2;   // this warp's value rows exist
     auto values = [&](int it, int h) {
+        if (!rows) {
+            warp_arrive(&bar.vl);
+            return;
+        }
         const int lane = threadIdx.x % 32, step0 = h * 64 + wg % 2 * 32, row0 = warp % 4 * 32 % D;
         uint32_t at = sm32 + slot(tile(it, L::Z)) + (uint32_t)(row0 / 64) * L::HALF + (uint32_t)(step0 + lane / 8 % 2 * 8 + lane % 8) * 128 +
                       (uint32_t)(((row0 % 64 / 8 + lane / 16) ^ (lane % 8)) << 4);
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         }
         // Terms of M: row tid of [term][half of dk][D rows][64].
         auto put_m = [&](int p) {   // columns 16p ..
-            if (D == 64 && tid >= 64) return;
+            if (!rows) return;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int c = col0 + p * 16 + u * 8;
@@ -406,6 +411,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 for (int j = 0; j < HALF / 4; ++j)
                     *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
             ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
+            if (rows)
 #pragma unroll
             for (int p = 0; p < HALF / 16; p += 2) {
                 uint32_t r[32];
