@@ -21,7 +21,7 @@ HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("quat_device.cuh", "quat_common.cuh", "quat_tiles.cuh", "quat_chain.cuh", "quat_walk.cuh",
             "quat_segwalk.cuh", "quat_segwalk_ws.cuh", "quat_segwalk_bwd.cuh", "quat_segwalk_tab.cuh",
             "quat_short.cuh", "quat_host.h", "workspace.h", "mixer_device.cuh", "delta_common.cuh", "tensor_core.cuh",
-            "delta_prep.cuh", "delta_fwd_tc.cuh", "delta_bwd_tc.cuh", "delta_chain_tc.cuh", "delta_host.cuh", "decay_walk.cuh", "decay_gate.cuh")]
+            "delta_prep.cuh", "delta_fwd_tc.cuh", "delta_bwd_tc.cuh", "delta_chain_tc.cuh", "delta_host.cuh", "decay_walk.cuh", "decay_gate.cuh", "decay_states.cuh")]
 DEPS = SOURCES + HEADERS + [os.path.join(ROOT, "include", f) for f in ("quat_cumprod.h", "quat_mixer.h", "quat_block.h")]
 LIB = os.path.join(HERE, "libquatscan.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

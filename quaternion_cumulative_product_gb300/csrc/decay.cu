@@ -4,11 +4,43 @@
 // bfloat16: the walk of decay_walk.cuh.  fp32, whose values are three terms each and take
 // three times the room: the delta rule's kernels without its errors (RULE, delta_prep.cuh).
 #include "decay_gate.cuh"
+#include "decay_states.cuh"
 #include "delta_host.cuh"
 
 using namespace qs;
 
 namespace {
+
+// fp32: cuts sequences into as many segments as fill the GPU (their states come from all chunks at once).
+void cut_states(DeltaArgs &a, int sms) {
+    a.segs = 1, a.seg_chunks = a.NC, a.sms = sms;
+    a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;
+    const long long pairs = a.N * a.Hv, want = pairs ? sms / pairs : 0;
+    if (a.offsets || want < 2 || a.NC < 2) return;
+    a.seg_chunks = (a.NC + want - 1) / want, a.segs = (int)((a.NC + a.seg_chunks - 1) / a.seg_chunks);
+}
+
+template <bool REV>
+int launch_states(const DeltaArgs &d, float *states, float *whole, const float *first, float *last, cudaStream_t stream) {
+    const StateArgs s = {d, states, whole, first, last};
+    auto own = [&](auto kernel, int D) {
+        const int smem = 2 * DC * D * 4;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return (int)QS_ERR_CUDA;
+        }
+        kernel<<<(unsigned)(d.slots * d.Hv), kOwnThreads, smem, stream>>>(s);
+        return launched();
+    };
+    if (d.slots > 0) {
+        const int rc = d.Dk <= 64 && d.Dv <= 64 ? own(decay_own_kernel<64, REV>, 64) : own(decay_own_kernel<128, REV>, 128);
+        if (rc != QS_OK) return rc;
+    }
+    const long long parts = (d.Dk * d.Dv / 4 + 255) / 256;
+    if (d.N * d.Hv * parts >= 1ll << 31) return QS_ERR_DIMS;
+    decay_run_kernel<REV><<<(unsigned)(d.N * d.Hv * parts), 256, 0, stream>>>(s, (unsigned)parts);
+    return launched();
+}
 
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
 // sums up every segment but one, the join hands the states on, and the real walk starts each
@@ -210,13 +242,17 @@ extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (dtype == QS_BF16) return forward16(a, dev, sms, stream);
     unsigned char *ws = nullptr;
-    cut(a, sms);
+    cut_states(a, sms);
+    const size_t kept = a.segs > 1 ? (size_t)a.slots * Hv * Dk * Dv : 0, wholes = a.segs > 1 ? (size_t)a.slots * Hv : 0;
     qsh::Hold hold;
-    const int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + seg_floats(a) * 4, &ws, &hold);
+    int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + (kept + wholes) * 4, &ws, &hold);
     if (wc != QS_OK) return wc;
-    float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
+    float *carries = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    return launch_walks<false, float, 3, false>(a, seg, stream);
+    if (a.segs > 1) wc = launch_states<false>(a, carries, carries + kept, init, nullptr, stream);
+    if (wc != QS_OK) return wc;
+    a.carries_in = carries;
+    return launch_walks<false, float, 3, false>(a, nullptr, stream);
 }
 
 extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void *q, const void *k, const void *v, const void *g,
@@ -261,22 +297,23 @@ extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void
     a.dq = d_q, a.dk = d_k, a.dv = d_v, a.dg = d_g, a.d_init = d_init;
     if (dtype == QS_BF16) return backward16(a, dev, sms, stream);
     const bool shared = Hv != Hk;
-    const size_t nds = align256(kept * 4), nh = shared ? align256((size_t)B * S * Hv * Dk * 4) : 0;
+    const size_t nds = align256(kept * 4), nh = shared ? align256((size_t)B * S * Hv * Dk * 4) : 0, nwhole = align256((size_t)a.slots * Hv * 4);
     unsigned char *ws = nullptr;
-    cut(a, sms);
+    cut_states(a, sms);
     qsh::Hold hold;
-    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + 2 * nds + 2 * nh + seg_floats(a) * 4, &ws, &hold);
+    rc = qsh::workspace(dev, stream, sizeof(WsHeader) + 2 * nds + 2 * nh + nwhole, &ws, &hold);
     if (rc != QS_OK) return rc;
     unsigned char *p = ws + sizeof(WsHeader);
-    a.carries = reinterpret_cast<float *>(p), a.carries_in = a.carries;
+    float *carries = reinterpret_cast<float *>(p), *whole = reinterpret_cast<float *>(p + 2 * nds + 2 * nh);
     a.ds = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + 2 * nds), a.dkh = reinterpret_cast<float *>(p + 2 * nds + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    float *seg = reinterpret_cast<float *>(p + 2 * nds + 2 * nh);
-    if (some) rc = launch_walks<false, float, 3, false>(a, seg, stream);   // the states that enter the chunks
-    if (rc == QS_OK) rc = launch_walks<true, float, 3, false>(a, seg, stream);
+    rc = launch_states<true>(a, a.ds, whole, d_final, d_init, stream);   // (without steps: d_init is d_final, or zeros)
     if (rc != QS_OK || !some) return rc;
-    rc = launch_chunks<float, 3, 3, false>(a, stream);
+    rc = launch_states<false>(a, carries, whole, init, nullptr, stream);
+    a.carries_in = carries, a.d_init = nullptr;
+    if (rc == QS_OK) rc = launch_walks<true, float, 3, false>(a, nullptr, stream);   // dv
+    if (rc == QS_OK) rc = launch_chunks<float, 3, 3, false>(a, stream);
     if (rc != QS_OK || !shared) return rc;
     const long long quads = B * S * Hk * Dk / 4;
     delta_shared_kernel<float><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(a, quads);

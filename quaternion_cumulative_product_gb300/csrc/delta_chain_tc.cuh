@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float2 m[HALF / 2];
         float whole = 0.f;
         bool ok = true;   // none of this thread's waits has run out
-        const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.d_final ? a.d_final + state : nullptr;
+        const float *from = a.d_final ? a.d_final + state : nullptr;
+        if (a.segs > 1) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.ds + ((size_t)(seq.slot0 + max(chunks - 1, 0)) * a.Hv + head) * a.Dk * a.Dv) + dv;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
             float v;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             }
             __syncwarp();
             auto write_ds = [&](int part) {   // dM', half of it behind each of two products
-                if (SUM) return;
+                if (!RULE || SUM) return;
                 float *out = a.ds + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
                 if (in)
 #pragma unroll

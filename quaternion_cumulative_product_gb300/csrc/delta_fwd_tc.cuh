@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float2 m[HALF / 2];
         float whole = 0.f;
         bool ok = true;   // none of this thread's waits has run out
-        const float *from = a.segs > 1 ? a.seg_m + walk.at * a.Dk * a.Dv + dv : a.init ? a.init + state : nullptr;
+        const float *from = a.init ? a.init + state : nullptr;
+        if (a.segs > 1) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.carries_in + ((size_t)seq.slot0 * a.Hv + head) * a.Dk * a.Dv) + dv;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
             float v;
@@ -107,7 +108,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         };
         // o of chunk c, this warpgroup's half of the steps.
         auto write_o = [&](int c) {
-            if (!RULE && !a.o) return;
             ok &= tc_wait_warp(&bar.o, c & 1, gone, a.ctl);
             const int left = (int)min((long long)DC, seq.len - (long long)c * DC);
             T *out = static_cast<T *>(a.o) + ((size_t)(row0 + (long long)c * DC + wg * 32) * a.Hv + head) * a.Dv + dv;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             // While the products run: the state that entered the chunk (half of it now, half behind
             // the next product), and the last chunk's o.
             auto write_carry = [&](int part) {
-                if (SUM || !a.carries) return;
+                if (!RULE || SUM || !a.carries) return;
                 float *out = a.carries + ((size_t)(seq.slot0 + c) * a.Hv + head) * a.Dk * a.Dv + (size_t)col0 * a.Dv + dv;
                 if (in)
 #pragma unroll

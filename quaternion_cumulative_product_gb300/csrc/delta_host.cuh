@@ -151,10 +151,11 @@ int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
                               : go(delta_fwd_tc_kernel<T, NT, 128, SUM, RULE>, large, grid);
     };
     const long long pairs = a.N * a.Hv;
-    if (a.segs > 1) {
+    if (RULE && a.segs > 1) {
         const size_t states = (size_t)pairs * a.segs * a.Dk * a.Dv;
         a.seg_m = seg, a.seg_own = seg + states, a.seg_map = seg + 2 * states;
-        int rc = walk(std::true_type(), pairs * (a.segs - 1) * (a.Dk <= 64 && a.Dv <= 64 ? 1 : 2));
+        int rc = QS_OK;
+        if constexpr (RULE) rc = walk(std::true_type(), pairs * (a.segs - 1) * (a.Dk <= 64 && a.Dv <= 64 ? 1 : 2));
         if (rc != QS_OK) return rc;
         delta_join_kernel<BWD><<<dim3((unsigned)pairs, (unsigned)(a.Dv + 15) / 16), 256, 0, stream>>>(a, BWD ? a.d_final : a.init, seg);
         rc = launched();
