@@ -1,8 +1,11 @@
 // decay.cu -- linear attention with a decay for each head over whole sequences: forward and
 // backward.
 //
-// bfloat16: the walk of decay_walk.cuh.  fp32, whose values are three terms each and take
-// three times the room: the delta rule's kernels without its errors (RULE, delta_prep.cuh).
+// bfloat16: the walk of decay_walk.cuh; backward three of them (dq, dk, dv) and decay_gate.cuh.
+// fp32, whose values are three terms each and take three times the room: the states of all chunks
+// at once (decay_states.cuh), then the delta rule's kernels without its errors (RULE,
+// delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 201 us; with the states walked,
+// twice where sequences are cut, 326 us.
 #include "decay_gate.cuh"
 #include "decay_states.cuh"
 #include "delta_host.cuh"

@@ -15,7 +15,9 @@
 // pieces of Z: prefix sums along its rows, sums down the columns by exchanges that halve the columns
 // a lane still holds; sums of whole rows carry over to the pieces on the right.
 //
-// Bound: memory (the four tensors once more).
+// Bound: memory (the four tensors once more) and the latency of a CTA's steps: 142 us at
+// 8 x 4096 x 16 x 128, 537 MB, 3.8 TB/s (180 us with eight warps instead of sixteen and without the
+// next CTA's tiles in L2).
 #pragma once
 
 #include "decay_walk.cuh"

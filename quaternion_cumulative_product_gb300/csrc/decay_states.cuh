@@ -8,7 +8,8 @@
 // of each (sequence, head), element by element.  (The delta rule's states have to be walked.)
 //
 // Bound: own, fp32 arithmetic (64 x 128 x 128 a chunk; 8 x 8 values of a product per thread, two
-// 16-byte reads of shared memory a side for 64 multiply-adds); the run, memory.
+// 16-byte reads of shared memory a side for 64 multiply-adds: 127 us for 2048 chunks of 128, 45% of
+// the fp32 rate); the run, memory (36 us there, 268 MB, 7.4 TB/s).
 #pragma once
 
 #include "delta_prep.cuh"

@@ -74,7 +74,8 @@ def check_norm(torch, x, w, b, dy, dt, eps=1e-5):
 
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (2, 3, 32), (1, 2048), (8, 1, 2048), (300, 2048), (17, 1001), (33, 4096), (700, 96), (2, 2, 2, 40),
-          (5000, 64), (4, 8192), (3, 8191), (2, 16384), (3, 16383), (9000, 33), (64,), (40, 520), (1300, 1544)]
+          (5000, 64), (4, 8192), (3, 8191), (2, 16384), (3, 16383), (9000, 33), (64,), (40, 520), (1300, 1544),
+          (5003, 520), (4900, 1024), (2600, 1100), (2451, 2048), (1301, 4096), (650, 8192)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -88,6 +89,26 @@ def test_layer_norm(torch, shape, dt):
 def test_layer_norm_of_a_slice(torch, dt, D, left, right):
     x, w, b, dy = norm_inputs(torch, (3, 21, left + D + right), dt, True)
     check_norm(torch, x[..., left: left + D], w[left: left + D].clone(), b[left: left + D].clone(), dy[..., :D].contiguous(), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("R,D,right", [(5001, 520, 80), (2500, 2048, 8)])
+def test_layer_norm_of_many_rows_of_a_slice(torch, dt, R, D, right):
+    x, w, b, dy = norm_inputs(torch, (R, D + right), dt, True)
+    check_norm(torch, x[:, :D], w[:D].clone(), b[:D].clone(), dy[:, :D].contiguous(), dt)
+
+
+def test_layer_norm_bwd_without_bias_or_weight(torch):
+    """Each gradient is made where its parameter is given, whatever else is."""
+    for R in (40, 5000):
+        x, w, b, dy = norm_inputs(torch, (R, 512), "bf16", True)
+        both = qs.quat_layer_norm_bwd(x, dy, w, b)
+        one = qs.quat_layer_norm_bwd(x, dy, w)
+        assert one[2] is None and torch.equal(one[0], both[0]) and torch.equal(one[1], both[1])
+        ones = torch.ones_like(w)
+        flat, plain = qs.quat_layer_norm_bwd(x, dy, None, b), qs.quat_layer_norm_bwd(x, dy, ones, b)
+        assert flat[1] is None and torch.equal(flat[0], plain[0]) and torch.equal(flat[2], plain[2])
+        assert torch.equal(qs.quat_layer_norm_bwd(x, dy)[0], plain[0])
 
 
 def test_layer_norm_rows_elsewhere(torch):

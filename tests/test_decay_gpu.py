@@ -311,3 +311,37 @@ def test_another_stream(torch):
     s.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_stall_is_reported(torch, D):
+    """Rows that never arrive: every wait runs out its limit, the call reports it, and the next one is clean."""
+    lib = qs.load_library()
+    x = inputs(torch, 2, 300, 1, 2, D, D, "bf16", seed=31)
+    args = (x["q"], x["k"], x["v"], x["g"])
+    want = qs.quat_decay_fwd(*args, x["init"])
+    back = qs.quat_decay_bwd(*args, x["d_o"], x["d_final"], x["init"])
+    try:
+        lib.quat_cumprod_debug_set_timeout_ns(20_000_000)
+        lib.quat_cumprod_debug_stall_tile(1)
+        qs.quat_decay_fwd(*args, x["init"])
+        assert qs.quat_cumprod_status() == qs.QS_ERR_TIMEOUT
+        qs.quat_decay_bwd(*args, x["d_o"], x["d_final"], x["init"])
+        assert qs.quat_cumprod_status() == qs.QS_ERR_TIMEOUT
+    finally:
+        lib.quat_cumprod_debug_stall_tile(-1)
+        lib.quat_cumprod_debug_set_timeout_ns(0)
+    for a, b in zip(qs.quat_decay_fwd(*args, x["init"]), want):
+        assert torch.equal(a, b)
+    for a, b in zip(qs.quat_decay_bwd(*args, x["d_o"], x["d_final"], x["init"]), back):
+        assert torch.equal(a, b)
+
+
+def test_many_packed_sequences(torch):
+    """More sequences than are put in order, and more walks than run at once."""
+    for N, most in ((150, 9), (60, 40)):
+        gen = np.random.default_rng(N)
+        offsets = [0, *np.cumsum(gen.integers(0, most, N)).tolist()]
+        check(torch, inputs(torch, 1, offsets[-1], 2, 4, 64, 64, "bf16", N=N), offsets=offsets)
+    offsets = [0, 700, 710, 1400, 1500, 2700]
+    check(torch, inputs(torch, 1, 2700, 1, 32, 16, 16, "bf16", N=5), offsets=offsets)
