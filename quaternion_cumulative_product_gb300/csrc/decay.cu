@@ -14,6 +14,11 @@ using namespace qs;
 
 namespace {
 
+int early(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
 // fp32: cuts sequences into as many segments as fill the GPU (their states come from all chunks at once).
 void cut_states(DeltaArgs &a, int sms) {
     a.segs = 1, a.seg_chunks = a.NC, a.sms = sms;
@@ -41,8 +46,7 @@ int launch_states(const DeltaArgs &d, float *states, float *whole, const float *
     }
     const long long parts = (d.Dk * d.Dv / 4 + 255) / 256;
     if (d.N * d.Hv * parts >= 1ll << 31) return QS_ERR_DIMS;
-    decay_run_kernel<REV><<<(unsigned)(d.N * d.Hv * parts), 256, 0, stream>>>(s, (unsigned)parts);
-    return launched();
+    return early(qsh::launch_next(decay_run_kernel<REV>, (unsigned)(d.N * d.Hv * parts), 256, 0, stream, s, (unsigned)parts));
 }
 
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
@@ -68,14 +72,16 @@ size_t walk_floats(const DecayArgs &a, int D) {   // of seg_m, seg_own and seg_d
 }
 
 // A walk of KIND, in segments with their sums and the join before it.
+// `next`: not the call's first launch.
 template <int D, WalkKind KIND>
-int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
+int launch_decay(DecayArgs &a, float *seg, bool next, cudaStream_t stream) {
     constexpr bool REV = KIND == WALK_DK || KIND == WALK_DV;
     auto go = [&](auto kernel, size_t smem, long long grid) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
             cudaGetLastError();
             return (int)QS_ERR_CUDA;
         }
+        if (next) return early(qsh::launch_next(kernel, (unsigned)grid, kDecayThreads, smem, stream, a));
         kernel<<<(unsigned)grid, kDecayThreads, smem, stream>>>(a);
         return launched();
     };
@@ -86,15 +92,15 @@ int launch_decay(DecayArgs &a, float *seg, cudaStream_t stream) {
         r.seg_m = seg, r.seg_own = seg + n * D * D, r.seg_decay = seg + 2 * n * D * D;
         int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true, false>::BYTES, pairs * (a.segs - 1));
         if (rc != QS_OK) return rc;
-        decay_join_kernel<D, REV><<<dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream>>>(a);
-        rc = launched();
+        rc = early(qsh::launch_next(decay_join_kernel<D, REV>, dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream, a));
         if (rc != QS_OK) return rc;
+        next = true;
     }
     return go(decay_walk_kernel<D, KIND>, DecayLayout<D, false, KIND == WALK_DQ || KIND == WALK_DK>::BYTES, pairs * a.segs);
 }
 template <WalkKind KIND>
-int launch_walk(DecayArgs &a, int D, float *seg, cudaStream_t stream) {
-    return D == 64 ? launch_decay<64, KIND>(a, seg, stream) : launch_decay<128, KIND>(a, seg, stream);
+int launch_walk(DecayArgs &a, int D, float *seg, bool next, cudaStream_t stream) {
+    return D == 64 ? launch_decay<64, KIND>(a, seg, next, stream) : launch_decay<128, KIND>(a, seg, next, stream);
 }
 
 // A tensor [B, S, H, D] that a walk reads.
@@ -142,7 +148,7 @@ int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     if (rc != QS_OK) return rc;
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
     float *seg = reinterpret_cast<float *>(ws + sizeof(WsHeader));
-    return launch_walk<WALK_OUT>(a, D, seg, stream);
+    return launch_walk<WALK_OUT>(a, D, seg, false, stream);
 }
 
 template <int D>
@@ -152,8 +158,7 @@ int launch_gates(const GateArgs &a, cudaStream_t stream) {
         cudaGetLastError();
         return QS_ERR_CUDA;
     }
-    decay_gate_kernel<D><<<(unsigned)(a.slots * a.Hv), kGateThreads, smem, stream>>>(a);
-    return launched();
+    return early(qsh::launch_next(decay_gate_kernel<D>, (unsigned)(a.slots * a.Hv), kGateThreads, smem, stream, a));
 }
 
 // dq and (with the states that it leaves) dk and dv are walks, dg a kernel of its own.
@@ -189,7 +194,7 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     if (rc != QS_OK) return rc;
     r.gb = group, r.dots = dota, r.init = d.init, r.dump = states, r.lane = d.Dv, r.col = 1;
     g.o = r.x, g.v = r.y, g.k = r.z;
-    rc = launch_walk<WALK_DQ>(a, D, seg, stream);
+    rc = launch_walk<WALK_DQ>(a, D, seg, false, stream);
     r = DecayRole{};
     if (rc == QS_OK) rc = set_role(r, a, v, o, q);
     if (rc == QS_OK) rc = set_out(r, a, shared ? dkh : d.dk, d.Dk, shared);
@@ -198,13 +203,13 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     if (rc != QS_OK) return rc;
     r.gb = group, r.dots = dotb, r.init = d.d_final, r.other = states, r.cross = cross, r.lane = d.Dv, r.col = 1;
     g.q = r.z;
-    rc = launch_walk<WALK_DK>(a, D, seg, stream);
+    rc = launch_walk<WALK_DK>(a, D, seg, true, stream);
     r = DecayRole{};
     if (rc == QS_OK) rc = set_role(r, a, k, q, o);
     if (rc == QS_OK) rc = set_out(r, a, d.dv, d.Dv, false);
     if (rc != QS_OK) return rc;
     r.init = d.d_final, r.fin = d.d_init, r.lane = 1, r.col = d.Dv;
-    rc = launch_walk<WALK_DV>(a, D, seg, stream);
+    rc = launch_walk<WALK_DV>(a, D, seg, true, stream);
     if (rc != QS_OK || d.B * d.S == 0) return rc;
     g.g = d.g, g.dg = d.dg, g.a = dota, g.b = dotb, g.cross = cross, g.offsets = d.offsets;
     g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.ahead = 2 * (unsigned)sms, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
@@ -213,8 +218,7 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     DeltaArgs sum = d;
     sum.dqh = dqh, sum.dkh = dkh;
     const long long quads = d.B * d.S * d.Hk * d.Dk / 4;
-    delta_shared_kernel<__nv_bfloat16><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(sum, quads);
-    return launched();
+    return early(qsh::launch_next(delta_shared_kernel<__nv_bfloat16>, (unsigned)((quads + 255) / 256), 256, 0, stream, sum, quads));
 }
 
 }  // namespace

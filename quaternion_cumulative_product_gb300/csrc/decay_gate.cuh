@@ -87,7 +87,9 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
 
     // What the walks have left, for the last step's warps (step u = warp * 32 + lane); on its way meanwhile.
     float fa = 0.f, fb = 0.f, whole = 0.f;
+    let_next_start();
     if (warp < 4) {
+        wait_for_last();
         const size_t half = (size_t)a.B * a.S * a.Hv, at = row0 + (size_t)(warp * 32 + lane) * a.Hv;
         if (warp * 32 + lane < left) fa = a.a[at] + a.a[half + at], fb = a.b[at] + a.b[half + at];
         if (lane < 8) whole = a.cross[((size_t)slot * a.Hv + head) * 8 + lane];

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
     extern __shared__ __align__(16) float rows[];   // [64][D] k (q), [64][D] v (dO)
     __shared__ ChunkGates gt;
     const DeltaArgs &a = s.d;
+    let_next_start();
     const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk), tid = threadIdx.x;
     const long long slot = blockIdx.x / a.Hv;
     Seq seq;
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
 template <bool REV>
 __global__ void __launch_bounds__(256) decay_run_kernel(const __grid_constant__ StateArgs s, unsigned parts) {
     const DeltaArgs &a = s.d;
+    wait_for_last();
     const size_t size = (size_t)a.Dk * a.Dv, e = ((size_t)(blockIdx.x % parts) * 256 + threadIdx.x) * 4, nh = blockIdx.x / parts;
     if (e >= size) return;
     const Seq seq = seq_of(a, (long long)(nh / a.Hv));

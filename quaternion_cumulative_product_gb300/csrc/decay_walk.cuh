@@ -324,8 +324,10 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         warp_arrive(&bar.vl);
     };
 
+    let_next_start();
     if (wg < 2) {
         set_registers<true, 128>();
+        wait_for_last();   // (the other roles touch the call's own inputs and outputs alone)
         // ------------------------------------------------------------------ state, out
         constexpr int HALF = D / 2;   // of dk: this thread's columns of M^T; of dv: its columns of out
         const int col0 = wg * HALF;
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         if (!SUM && a.segs > 1 && tid < D) {
 #pragma unroll
             for (int j = 0; j < HALF / 4; ++j) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.seg_m + seg_at * D * D + state_at<D>(j, wg, tid)));
+                const float4 v = *reinterpret_cast<const float4 *>(ro.seg_m + seg_at * D * D + state_at<D>(j, wg, tid));
                 m[2 * j] = make_float2(v.x, v.y), m[2 * j + 1] = make_float2(v.z, v.w);
             }
         } else if (!SUM && ro.init && in) {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 if (tid < D)
 #pragma unroll
                     for (int j = 0; j < HALF / 4; ++j) {
-                        const float4 v = __ldg(reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid)));
+                        const float4 v = *reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid));
                         dot = fma2(m[2 * j], make_float2(v.x, v.y), dot);
                         dot = fma2(m[2 * j + 1], make_float2(v.z, v.w), dot);
                     }
@@ -799,6 +801,8 @@ template <int D, bool REV>
 __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DecayArgs a) {
     const DecayRole &ro = a.role;
     const size_t pair = blockIdx.y;
+    let_next_start();
+    wait_for_last();
     const int i = blockIdx.x * 256 + threadIdx.x, j4 = i / (2 * D), wg = i / D % 2, dv = i % D;   // as state_at
     float4 m = q_zero();
     if (ro.init && dv < ro.dv) {
@@ -815,8 +819,8 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
         const size_t at = pair * a.segs + (REV ? a.segs - 1 - s : s);
         *reinterpret_cast<float4 *>(enter + at * D * D + (size_t)i * 4) = m;
         if (s + 1 == a.segs) break;
-        const float4 own = __ldg(reinterpret_cast<const float4 *>(ro.seg_own + at * D * D + (size_t)i * 4));
-        const float d = __ldg(ro.seg_decay + at);
+        const float4 own = *reinterpret_cast<const float4 *>(ro.seg_own + at * D * D + (size_t)i * 4);
+        const float d = ro.seg_decay[at];
         m = make_float4(fmaf(d, m.x, own.x), fmaf(d, m.y, own.y), fmaf(d, m.z, own.z), fmaf(d, m.w, own.w));
     }
 }

@@ -15,6 +15,7 @@ using namespace qs;
 // dq, dk of a key head: the sum over the value heads that share it.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, long long quads) {
+    wait_for_last();   // (linear attention launches it early)
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= quads) return;
     const int dq = a.Dk / 4, G = a.Hv / a.Hk;
@@ -23,8 +24,8 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, lo
     float4 q = q_zero(), k = q_zero();
     for (int j = 0; j < G; ++j) {
         const size_t at = ((size_t)row * a.Hv + h * G + j) * a.Dk + x;
-        q = q_add(q, load4(a.dqh + at));
-        k = q_add(k, load4(a.dkh + at));
+        q = q_add(q, *reinterpret_cast<const float4 *>(a.dqh + at));   // (no load that may move before the wait)
+        k = q_add(k, *reinterpret_cast<const float4 *>(a.dkh + at));
     }
     const size_t out = ((size_t)row * a.Hk + h) * a.Dk + x;
     store4(static_cast<T *>(a.dq) + out, q);

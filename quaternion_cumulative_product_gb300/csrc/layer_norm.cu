@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_kernel(const NormArgs a) {
     __shared__ float slots[kMostWide][64][2];
     const long long stride = (long long)gridDim.x * blockDim.y;
     const int lanes = blockDim.x;
+    if (BWD) qs::let_next_start();
     Vals<VEC> w[PER], b[PER], dw[PER];   // backward: b holds db
     Raw<T, VEC> rx[PER], rd[PER];
     bool on[PER];
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) norm_tile_kernel(const NormAr
     const long long tiles = (a.R + RT - 1) / RT;
     bool ok = true;
     int sent = 0, seen = 0;
+    qs::let_next_start();
     auto send = [&](long long tile) {   // thread 0
         if (tile >= tiles || !ok) return;
         unsigned char *to = dynamic + (size_t)(sent % kTileStages) * stageb;
@@ -521,6 +523,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) norm_tile_kernel(const NormAr
 // dw and db: the sum of the CTAs' parts, 32 columns and 32 groups of parts per CTA.
 __global__ void __launch_bounds__(1024) norm_weights_kernel(const float *part, float *dw, float *db, unsigned parts, unsigned D) {
     __shared__ float sums[32][33];
+    qs::wait_for_last();
     const unsigned x = threadIdx.x % 32, y = threadIdx.x / 32, col = blockIdx.x * 32 + x;
     float s = 0.f;
     if (col < 2 * D)
@@ -577,6 +580,13 @@ bool skew(const void *p, int m) { return reinterpret_cast<uintptr_t>(p) % m != 0
 
 int launched() { return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA; }
 
+int weights(const NormArgs &a, float *d_w, float *d_b, unsigned parts, cudaStream_t stream) {
+    const float *part = a.part;
+    if (qsh::launch_next(norm_weights_kernel, (unsigned)(2 * a.D + 31) / 32, 1024, 0, stream, part, d_w, d_b, parts, (unsigned)a.D) == cudaSuccess) return QS_OK;
+    cudaGetLastError();
+    return QS_ERR_CUDA;
+}
+
 template <bool BWD>
 int launch(NormArgs &a, int dtype, bool wide, long long units, int sms, float *d_w, float *d_b, int dev, cudaStream_t stream) {
     const int vec = wide ? dtype == QS_BF16 ? 8 : 4 : 1, most = vec == 8 ? 2 : vec == 4 ? (BWD ? 2 : 4) : (BWD ? 8 : 16);
@@ -603,8 +613,7 @@ int launch(NormArgs &a, int dtype, bool wide, long long units, int sms, float *d
     fn<<<grid, dim3(lanes, rows), smem, stream>>>(a);
     const int rc = launched();
     if (rc != QS_OK || !a.part) return rc;
-    norm_weights_kernel<<<(unsigned)(2 * a.D + 31) / 32, 1024, 0, stream>>>(a.part, d_w, d_b, grid, (unsigned)a.D);
-    return launched();
+    return weights(a, d_w, d_b, grid, stream);
 }
 
 }  // namespace
@@ -688,8 +697,7 @@ extern "C" int quat_layer_norm_bwd(int dtype, float eps, const void *x, const fl
             kernel<<<(unsigned)sms, kTileThreads, smem, stream>>>(a);
             rc = launched();
             if (rc != QS_OK || !a.part) return rc;
-            norm_weights_kernel<<<(unsigned)(2 * D + 31) / 32, 1024, 0, stream>>>(a.part, d_w, d_b, (unsigned)sms, (unsigned)D);
-            return launched();
+            return weights(a, d_w, d_b, (unsigned)sms, stream);
         };
         using B = __nv_bfloat16;
         if (dtype == QS_BF16)

@@ -84,6 +84,13 @@ __device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Kernels of one call in a row: the next one's CTAs may start (where there is room) once all of
+// this one's have said so, and its threads wait, before they touch what this one reads or
+// writes, until it is done (qsh::launch_next).  What this one writes is then read by plain loads:
+// read-only ones (__ldg) may move before the wait.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One value of an array whose element type is known at run time only.
 __device__ __forceinline__ float load_any(const void *p, bool bf16, long long i) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];

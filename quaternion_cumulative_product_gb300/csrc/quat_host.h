@@ -26,6 +26,19 @@ QS_HIDDEN int workspace(int dev, cudaStream_t stream, size_t need, unsigned char
 QS_HIDDEN unsigned long long timeout_ns();
 QS_HIDDEN int stall_tile();
 
+// Launches a kernel whose CTAs may start before the kernel launched last on the stream is done: a
+// kernel of the same call, which says so (qs::let_next_start), and for whose end this one waits by
+// itself (qs::wait_for_last).
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid, c.blockDim = block, c.dynamicSmemBytes = smem, c.stream = stream, c.attrs = &early, c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     if (!a || !b || na == 0 || nb == 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
