@@ -542,6 +542,9 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const float *part, f
 
 using Kernel = void (*)(NormArgs);
 
+// Dynamic shared memory of norm_kernel, at most: one limit for all sizes, which calls at once on several threads do not take from each other.
+constexpr int kMostSums = QS_NORM_MAX_D * 2 * (int)sizeof(float);
+
 // Values per thread, 16 forward and 8 backward (16 of bfloat16, whose next row waits packed):
 // what the registers of 512 threads hold.  THREADS: rows of more than that many threads have 1024.
 template <typename T, int VEC, bool BWD>
@@ -551,7 +554,9 @@ template <typename T, int VEC, bool BWD>
 Kernel pick_per(int per, int threads) {
     constexpr int MOST = kPer<T, VEC, BWD>, FEW = VEC == 1 ? MOST / 4 : 1;
     if (threads <= 512) return per <= FEW ? norm_kernel<T, VEC, FEW, 512, BWD> : norm_kernel<T, VEC, MOST, 512, BWD>;
-    return per <= MOST ? norm_kernel<T, VEC, MOST, 1024, BWD> : norm_kernel<T, VEC, 2 * MOST, 1024, BWD>;
+    if constexpr (1024 * VEC * MOST < QS_NORM_MAX_D)   // (else 1024 threads hold the longest row)
+        if (per > MOST) return norm_kernel<T, VEC, 2 * MOST, 1024, BWD>;
+    return norm_kernel<T, VEC, MOST, 1024, BWD>;
 }
 template <bool BWD>
 Kernel pick(int dtype, bool wide, int per, int threads, int *slots) {
@@ -597,7 +602,7 @@ int launch(NormArgs &a, int dtype, bool wide, long long units, int sms, float *d
     int slots = 0, fit = 1;
     const Kernel fn = pick<BWD>(dtype, wide, (int)((units + lanes - 1) / lanes), lanes * rows, &slots);
     const size_t smem = d_w || d_b ? (size_t)lanes * slots * vec * 2 * sizeof(float) : 0;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return cudaGetLastError(), QS_ERR_CUDA;
+    if (smem && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSums) != cudaSuccess) return cudaGetLastError(), QS_ERR_CUDA;
     unsigned grid = (unsigned)all;
     if (all > sms) {   // as many CTAs as run at once
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, lanes * rows, smem) != cudaSuccess || fit < 1) return cudaGetLastError(), QS_ERR_CUDA;
@@ -687,7 +692,7 @@ extern "C" int quat_layer_norm_bwd(int dtype, float eps, const void *x, const fl
     if (wide && D >= 256 && D <= 8 * cols && R >= 32 * (int64_t)sms / wpr) {
         auto go = [&](auto kernel) {
             const size_t smem = (size_t)kTileStages * 2 * (16 / wpr) * D * es;
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return cudaGetLastError(), (int)QS_ERR_CUDA;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileStages * 2 * 16 * 32 * kTileUnits * 16) != cudaSuccess) return cudaGetLastError(), (int)QS_ERR_CUDA;
             unsigned char *ws = nullptr;
             qsh::Hold hold;
             int rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)sms * 2 * D * 4, &ws, &hold);

@@ -263,3 +263,37 @@ def test_dropout_captured(torch):
         s.synchronize()
     for i, got in enumerate(seen):
         assert torch.equal(got, qs.quat_dropout_fwd(x, torch.tensor([9, i], device="cuda"), 0.5))
+
+
+@pytest.mark.parametrize("R", [40, 6000])
+def test_layer_norm_bwd_on_threads(torch, R):
+    """Rows of different lengths on several host threads at once (the limits of a kernel's shared memory are the process's)."""
+    import threading
+
+    widths = (256, 1024, 2000)
+    sets = []
+    for D in widths:
+        gen = torch.Generator(device="cuda").manual_seed(D)
+        x, d = (torch.randn(R, D, generator=gen, device="cuda") for _ in range(2))
+        w = torch.randn(D, generator=gen, device="cuda")
+        sets.append((x, d, w, qs.quat_layer_norm_bwd(x, d, w, w)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        x, d, w, want = sets[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            try:
+                for _ in range(100):
+                    got = qs.quat_layer_norm_bwd(x, d, w, w)
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    wrong.append(widths[i])
+            except Exception as e:  # noqa: BLE001
+                wrong.append((widths[i], repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(widths))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
