@@ -81,7 +81,10 @@ __global__ void __launch_bounds__(kGateThreads, 2) decay_gate_kernel(const __gri
         b = slot / a.NC, s0 = 0, len = a.S, c = slot % a.NC;
     }
     const long long t0 = c * WC;
-    if (c < 0 || t0 >= len) return;   // (a slot that holds no chunk)
+    if (c < 0 || t0 >= len) {   // (a slot that holds no chunk; what comes after this kernel takes its end for that of the walks, too)
+        wait_for_last();
+        return;
+    }
     const int left = (int)min((long long)WC, len - t0);
     const size_t row0 = (size_t)(b * a.S + s0 + t0) * a.Hv + head;
 

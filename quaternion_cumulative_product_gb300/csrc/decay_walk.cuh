@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     let_next_start();
     if (wg < 2) {
         set_registers<true, 128>();
-        wait_for_last();   // (the other roles touch the call's own inputs and outputs alone)
+        wait_for_last();   // (the other roles touch the call's inputs and outputs, dots that nothing reads yet, and what waits by itself)
         // ------------------------------------------------------------------ state, out
         constexpr int HALF = D / 2;   // of dk: this thread's columns of M^T; of dv: its columns of out
         const int col0 = wg * HALF;
@@ -739,7 +739,10 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     bulk_prefetch(ro.other + ((size_t)(slot0 + chunk_at(it + 1)) * a.Hv + head) * D * D, D * D * 4);
             }
         }
-        if (SUM && lane == 0) ro.seg_decay[seg_at] = decay(all, {0.f, 0.f});
+        if (SUM) {
+            wait_for_last();   // (the join of the walk before may not have read its own yet)
+            if (lane == 0) ro.seg_decay[seg_at] = decay(all, {0.f, 0.f});
+        }
     } else if (!SUM) {
         // ------------------------------------------------------------------ out to memory
         bool some = false;

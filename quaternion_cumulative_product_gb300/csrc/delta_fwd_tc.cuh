@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     float v[16];
                     third_column<NT>(sm + c % L::KS * L::ROWS + L::V_AT, dv, h0 + q * 16, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[q * 8 + i] = SUM && row.map ? make_float2(0.f, 0.f) : make_float2(v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 8; ++i) u[q * 8 + i] = make_float2(v[2 * i], v[2 * i + 1]);
                 }
             } else {
                 uint32_t r[32];   // (U takes the place of 32 columns of e: all are read first)

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) delta_shared_kernel(const DeltaArgs a, lo
     if (i >= quads) return;
     const int dq = a.Dk / 4, G = a.Hv / a.Hk;
     const long long row = i / dq / a.Hk;
+    if (a.offsets && row >= a.offsets[a.N]) return;   // rows behind the last sequence are left as they were
     const int x = (int)(i % dq) * 4, h = (int)(i / dq % a.Hk);
     float4 q = q_zero(), k = q_zero();
     for (int j = 0; j < G; ++j) {

@@ -345,3 +345,35 @@ def test_many_packed_sequences(torch):
         check(torch, inputs(torch, 1, offsets[-1], 2, 4, 64, 64, "bf16", N=N), offsets=offsets)
     offsets = [0, 700, 710, 1400, 1500, 2700]
     check(torch, inputs(torch, 1, 2700, 1, 32, 16, 16, "bf16", N=5), offsets=offsets)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_behind_the_last_sequence(torch, dt):
+    """Packed sequences that end before S: what stands behind them in the outputs stays."""
+    import ctypes
+
+    from quaternion_cumulative_product_gb300 import mixer
+
+    S, end, Hk, Hv, D = 420, 333, 2, 4, 64
+    x = inputs(torch, 1, S, Hk, Hv, D, D, dt, N=2, seed=17)
+    for n in ("q", "k", "v", "d_o"):
+        x[n][:, end:] = float("nan")
+    offsets = torch.tensor([0, 130, end], dtype=torch.int32, device="cuda")
+    sizes = [2, 1, S, Hk, Hv, D, D]
+    code = 0 if dt == "f32" else 1
+    gate = 0 if x["g"].dtype == torch.float32 else 1
+    lib, stream = mixer._lib(), torch.cuda.current_stream().cuda_stream
+    o = torch.full_like(x["v"], 7.0)
+    final = torch.zeros(2, Hv, D, D, device="cuda")
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (x["q"], x["k"], x["v"], x["g"], x["init"])]
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert lib.quat_decay_fwd(code, gate, 0.125, *p, ptr(o), ptr(final), None, ptr(offsets), *sizes, stream) == 0
+    out = [torch.full_like(x[n], 7.0) for n in ("q", "k", "v", "g")] + [torch.zeros_like(x["init"])]
+    assert lib.quat_decay_bwd(code, gate, 0.125, *p, ptr(x["d_o"]), None, *map(ptr, out), None, ptr(offsets), *sizes, stream) == 0
+    whole = {n: x[n][:, :end].contiguous() if n in ("q", "k", "v", "g", "d_o") else x[n] for n in x}
+    want_o, want_final = qs.quat_decay_fwd(whole["q"], whole["k"], whole["v"], whole["g"], whole["init"], scale=0.125, offsets=offsets)
+    want = qs.quat_decay_bwd(whole["q"], whole["k"], whole["v"], whole["g"], whole["d_o"], None, whole["init"], scale=0.125, offsets=offsets)
+    assert torch.equal(final, want_final) and torch.equal(out[4], want[4])
+    for got, w in zip([o] + out[:4], (want_o, *want[:4])):
+        assert torch.equal(got[:, :end], w)
+        assert (got[:, end:] == 7.0).all()
