@@ -6,6 +6,8 @@
 // at once (decay_states.cuh), then the delta rule's kernels without its errors (RULE,
 // delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 201 us; with the states walked,
 // twice where sequences are cut, 326 us.
+#include <algorithm>
+
 #include "decay_gate.cuh"
 #include "decay_states.cuh"
 #include "delta_host.cuh"
@@ -90,11 +92,13 @@ int launch_decay(DecayArgs &a, float *seg, bool next, cudaStream_t stream) {
         const size_t n = (size_t)pairs * a.segs;
         DecayRole &r = a.role;
         r.seg_m = seg, r.seg_own = seg + n * D * D, r.seg_decay = seg + 2 * n * D * D;
-        int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true, false>::BYTES, pairs * (a.segs - 1));
-        if (rc != QS_OK) return rc;
-        rc = early(qsh::launch_next(decay_join_kernel<D, REV>, dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream, a));
-        if (rc != QS_OK) return rc;
-        next = true;
+        if constexpr (KIND != WALK_DV) {   // (which takes the states of dk, just walked: the same, transposed)
+            int rc = go(decay_walk_kernel<D, REV ? WALK_SUM_REV : WALK_SUM>, DecayLayout<D, true, false>::BYTES, pairs * (a.segs - 1));
+            if (rc != QS_OK) return rc;
+            rc = early(qsh::launch_next(decay_join_kernel<D, REV>, dim3(D * D / 1024, (unsigned)pairs), 256, 0, stream, a));
+            if (rc != QS_OK) return rc;
+            next = true;
+        }
     }
     return go(decay_walk_kernel<D, KIND>, DecayLayout<D, false, KIND == WALK_DQ || KIND == WALK_DK>::BYTES, pairs * a.segs);
 }
@@ -152,13 +156,13 @@ int forward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
 }
 
 template <int D>
-int launch_gates(const GateArgs &a, cudaStream_t stream) {
+int launch_gates(const GateArgs &a, int sms, cudaStream_t stream) {
     constexpr int smem = GateLayout<D>::BYTES;
     if (cudaFuncSetAttribute(decay_gate_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return QS_ERR_CUDA;
     }
-    return early(qsh::launch_next(decay_gate_kernel<D>, (unsigned)(a.slots * a.Hv), kGateThreads, smem, stream, a));
+    return early(qsh::launch_next(decay_gate_kernel<D>, (unsigned)std::min<long long>(a.slots * a.Hv, 2 * sms), kGateThreads, smem, stream, a));
 }
 
 // dq and (with the states that it leaves) dk and dv are walks, dg a kernel of its own.
@@ -212,8 +216,8 @@ int backward16(const DeltaArgs &d, int dev, int sms, cudaStream_t stream) {
     rc = launch_walk<WALK_DV>(a, D, seg, true, stream);
     if (rc != QS_OK || d.B * d.S == 0) return rc;
     g.g = d.g, g.dg = d.dg, g.a = dota, g.b = dotb, g.cross = cross, g.offsets = d.offsets;
-    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.ahead = 2 * (unsigned)sms, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
-    rc = D == 64 ? launch_gates<64>(g, stream) : launch_gates<128>(g, stream);
+    g.B = d.B, g.S = d.S, g.N = d.N, g.NC = a.NC, g.slots = slots, g.Hv = d.Hv, g.shared = group, g.gate16 = d.gate16, g.scale = d.scale, g.ctl = a.ctl;
+    rc = D == 64 ? launch_gates<64>(g, sms, stream) : launch_gates<128>(g, sms, stream);
     if (rc != QS_OK || !shared) return rc;
     DeltaArgs sum = d;
     sum.dqh = dqh, sum.dkh = dkh;

@@ -34,7 +34,7 @@
 // as well (dots), M has two terms.
 //
 // Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 111 us (4.8 TB/s, 0.71 of a copy's rate),
-// 3.4 us a chunk; dv 109, dq 156 and dk 204 us (they also write and read the states, 268 MB each).
+// 3.4 us a chunk; dv 109, dq 158 and dk 181 us (they also write and read the states, 268 MB each).
 // 1 x 131072 x 16 x 64 in 19 segments: 441 us.
 // Bound: shared memory.  The tensor cores read 64 KB (S) + 64 KB (Y) + 32 KB (P z) + 96 KB (dM) of
 // operands a chunk, the copies write 96 KB and read 32 KB, conversions write M (32 KB) and out (32 KB)
@@ -337,7 +337,15 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         float whole = 0.f;
 #pragma unroll
         for (int i = 0; i < HALF / 2; ++i) m[i] = make_float2(0.f, 0.f);
-        if (!SUM && a.segs > 1 && tid < D) {
+        if (KIND == WALK_DV && a.segs > 1 && tid < D) {   // dk's states, whose rows are these columns
+            const float *p = ro.seg_m + seg_at * D * D + state_at<D>(tid % HALF / 4, tid / HALF, col0) + tid % 4;
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                const float v = p[4 * i];
+                if (i % 2) m[i / 2].y = v;
+                else m[i / 2].x = v;
+            }
+        } else if (!SUM && a.segs > 1 && tid < D) {
 #pragma unroll
             for (int j = 0; j < HALF / 4; ++j) {
                 const float4 v = *reinterpret_cast<const float4 *>(ro.seg_m + seg_at * D * D + state_at<D>(j, wg, tid));
@@ -381,6 +389,24 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 #pragma unroll
             for (int p = 0; p < HALF / 16; ++p) put_m(p);
         }
+        // <other's state, M>, quarters of a thread's columns at a time, on their way while it waits
+        // (all at once before the chunk's products are asked for: dk 204 us instead of 181; behind h z's second half 221).
+        constexpr int Q = HALF / 16;
+        float4 theirs[2 * Q];
+        float2 dot = make_float2(0.f, 0.f);
+        auto fetch = [&](size_t kept, int quarter, int n) {
+            if (tid < D)
+#pragma unroll
+                for (int j = 0; j < n * Q; ++j) theirs[j] = *reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(quarter * Q + j, wg, tid));
+        };
+        auto multiply = [&](int quarter, int n) {
+            if (tid < D)
+#pragma unroll
+                for (int j = 0; j < n * Q; ++j) {
+                    dot = fma2(m[2 * (quarter * Q + j)], make_float2(theirs[j].x, theirs[j].y), dot);
+                    dot = fma2(m[2 * (quarter * Q + j) + 1], make_float2(theirs[j].z, theirs[j].w), dot);
+                }
+        };
         give_m();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
@@ -389,33 +415,29 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const WalkGates &gt = gates[gb];
             const int left = (int)min((long long)WC, len - t0);
             const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
+            const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
+            if (cross) dot = make_float2(0.f, 0.f), fetch(kept, 0, 2);
             ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             whole = gt.whole;
             __syncwarp();
-            const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
-            if constexpr (cross) {   // (before the chunk's products are asked for: 204 us; behind h z's second half 221)
-                float2 dot = make_float2(0.f, 0.f);
-                if (tid < D)
+            ok &= wait_tile(tile(it, L::Z));
+            ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
+            if (cross) multiply(0, 2), fetch(kept, 2, 1);
+            values(it, 1);
+            warp_arrive(&bar.gfree[gb]);
+            if (cross) multiply(2, 1), fetch(kept, 3, 1);
+            if (dump && tid < D)   // while Y and the rest of dM are made (175 us before them, 156 here)
 #pragma unroll
-                    for (int j = 0; j < HALF / 4; ++j) {
-                        const float4 v = *reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(j, wg, tid));
-                        dot = fma2(m[2 * j], make_float2(v.x, v.y), dot);
-                        dot = fma2(m[2 * j + 1], make_float2(v.z, v.w), dot);
-                    }
+                for (int j = 0; j < HALF / 4; ++j)
+                    *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
+            if (cross) {
+                multiply(3, 1);
                 float sum = (dot.x + dot.y) * whole;
                 __syncwarp();
 #pragma unroll
                 for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
             }
-            ok &= wait_tile(tile(it, L::Z));
-            ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
-            values(it, 1);
-            warp_arrive(&bar.gfree[gb]);
-            if (dump && tid < D)   // while Y and the rest of dM are made (175 us before them, 156 here)
-#pragma unroll
-                for (int j = 0; j < HALF / 4; ++j)
-                    *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
             ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
             if (rows)
 #pragma unroll
@@ -818,13 +840,20 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
         }
     }
     float *enter = const_cast<float *>(ro.seg_m);
-    for (int s = 0; s < a.segs; ++s) {
-        const size_t at = pair * a.segs + (REV ? a.segs - 1 - s : s);
-        *reinterpret_cast<float4 *>(enter + at * D * D + (size_t)i * 4) = m;
-        if (s + 1 == a.segs) break;
-        const float4 own = *reinterpret_cast<const float4 *>(ro.seg_own + at * D * D + (size_t)i * 4);
-        const float d = ro.seg_decay[at];
-        m = make_float4(fmaf(d, m.x, own.x), fmaf(d, m.y, own.y), fmaf(d, m.z, own.z), fmaf(d, m.w, own.w));
+    constexpr int AHEAD = 8;   // sums on their way at a time
+    for (int s0 = 0; s0 < a.segs; s0 += AHEAD) {
+        float4 own[AHEAD];
+        float d[AHEAD];
+        auto at = [&](int k) { return pair * a.segs + (REV ? a.segs - 1 - (s0 + k) : s0 + k); };
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (s0 + k + 1 < a.segs) own[k] = *reinterpret_cast<const float4 *>(ro.seg_own + at(k) * D * D + (size_t)i * 4), d[k] = ro.seg_decay[at(k)];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (s0 + k < a.segs) {
+                *reinterpret_cast<float4 *>(enter + at(k) * D * D + (size_t)i * 4) = m;
+                m = make_float4(fmaf(d[k], m.x, own[k].x), fmaf(d[k], m.y, own[k].y), fmaf(d[k], m.z, own[k].z), fmaf(d[k], m.w, own[k].w));
+            }
     }
 }
 
