@@ -53,7 +53,8 @@ int launch_states(const DeltaArgs &d, float *states, float *whole, const float *
 
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
 // sums up every segment but one, the join hands the states on, and the real walk starts each
-// segment from its own.
+// segment from its own.  Costs are in chunks; a summing walk counts as half a real one (1 x 131072 x
+// 16 x 64: 121 and 256 us).
 void cut_walks(DecayArgs &a, int sms) {
     a.segs = 1, a.seg_chunks = a.NC;
     a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;
@@ -63,7 +64,7 @@ void cut_walks(DecayArgs &a, int sms) {
     for (long long want = 2; want <= 64 && want <= a.NC && pairs * want <= 4 * sms; ++want) {
         const long long sc = (a.NC + want - 1) / want, n = (a.NC + sc - 1) / sc;
         if (n < 2) continue;
-        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.6 * (double)((pairs * (n - 1) + sms - 1) / sms);
+        const double waves = (double)((pairs * n + sms - 1) / sms) + 0.5 * (double)((pairs * (n - 1) + sms - 1) / sms);
         const double cost = waves * sc + 0.1 * n + 3;
         if (cost < best) best = cost, a.segs = (int)n, a.seg_chunks = sc;
     }

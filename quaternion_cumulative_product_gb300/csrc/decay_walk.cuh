@@ -30,16 +30,19 @@
 // Terms (tensor_core.cuh): h z in three, so that states have fp32 precision (they add up rounded
 // once a chunk).  P and the M of Y, of which only bfloat16 outputs are made, in one: rounded to
 // nearest, their errors are as large as the output's own rounding and independent of it (measured
-// against 64 bits: 1.4 times its error alone; two terms of each took 157 instead of 132 us).  Where Y goes into d_g
-// as well (dots), M has two terms.
+// against 64 bits: 1.4 times its error alone; two terms of each took 157 instead of 132 us).  Where Y
+// goes into d_g as well (dots), M has two terms, and a third one for fp32 gates (d_g is then 3e-7 to
+// 6e-7 from 64 bits, with two 2e-6; dq 170 instead of 160 us, dk 190 instead of 181).
 //
 // Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 111 us (4.8 TB/s, 0.71 of a copy's rate),
-// 3.4 us a chunk; dv 109, dq 158 and dk 181 us (they also write and read the states, 268 MB each).
-// 1 x 131072 x 16 x 64 in 19 segments: 441 us.
+// 3.4 us a chunk; dv 109, dq 170 and dk 190 us (they also write and read the states, 268 MB each).
+// 1 x 131072 x 16 x 64 in 19 segments: 384 us, the sums 121 and the walk 256 of them.
 // Bound: shared memory.  The tensor cores read 64 KB (S) + 64 KB (Y) + 32 KB (P z) + 96 KB (dM) of
 // operands a chunk, the copies write 96 KB and read 32 KB, conversions write M (32 KB) and out (32 KB)
 // and read h z's columns two bytes a lane.
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -94,7 +97,7 @@ struct __align__(16) WalkGates {
 
 struct DecayBars {
     uint64_t full[8], empty[8], aux, beside, gfull[2], gfree[2];
-    uint64_t s, p, y, scaled, out, ofree, staged, vl, dm0, dm, m, drain;
+    uint64_t s, p, y, scaled, out, ofree, staged, vl, dm0, dm, m, y2, m3, drain;
     uint32_t tmem;
     int gone;
 };
@@ -121,6 +124,8 @@ constexpr uint32_t S = 0;     // x y^T (128), then P: each 32 columns give way t
 constexpr uint32_t O = 128;   // x M, scaled, then out
 constexpr uint32_t DM = 256;  // the chunk's part of M'^T
 constexpr uint32_t VL = 384;  // terms of h z, 64 steps (3 x 32)
+// Where only states are summed up, a place for each half of a chunk and two for dM.
+constexpr uint32_t VL2 = S, DM2 = O;
 }  // namespace decay_tmem
 
 // A warpgroup's share of the registers: 640 x 96 at launch are 2 x 128 x 128 + 2 x 128 x 88 + 128 x 48.
@@ -270,8 +275,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 8; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
-        for (uint64_t *x : {&bar.aux, &bar.beside, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
-        for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.staged, &bar.vl, &bar.m}) mbar_init(x, 8);   // two warpgroups' warps
+        for (uint64_t *x : {&bar.aux, &bar.beside, &bar.gfull[0], &bar.gfull[1], &bar.s, &bar.y, &bar.y2, &bar.out, &bar.dm0, &bar.dm, &bar.drain}) mbar_init(x, 1);
+        for (uint64_t *x : {&bar.p, &bar.scaled, &bar.ofree, &bar.staged, &bar.vl, &bar.m, &bar.m3}) mbar_init(x, 8);   // two warpgroups' warps
         mbar_init(&bar.gfree[0], 16), mbar_init(&bar.gfree[1], 16);
         *gone = 0;
         fence_mbar_init();
@@ -281,7 +286,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = __reduce_min_sync(0xffffffffu, bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
-    constexpr int terms = dots ? 2 : 1;   // of M
+    constexpr int terms = dots ? 2 : 1;      // of M
+    const bool third = dots && !a.gate16;   // and one more, in the first one's place once that has been multiplied
     bool ok = true;   // none of this thread's waits has run out
     auto tile = [&](int it, int which) { return L::PER * it + which; };   // the it-th chunk's; tile i is in slot i % SLOTS
     auto stage_at = [&](int it) { return dots ? (uint32_t)(L::ROOM - 1) * L::TILE_BYTES : (uint32_t)(tile(it, L::X) % L::SLOTS) * L::TILE_BYTES; };
@@ -295,15 +301,16 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     // row lane / 4 (+ 8, 16, 24), which is how the 16-lane stores to tensor memory want them.
     const bool rows = D == 128 || warp % 4 < 2;   // this warp's value rows exist
     auto values = [&](int it, int h) {
+        uint64_t *there = SUM && h ? &bar.p : &bar.vl;
         if (!rows) {
-            warp_arrive(&bar.vl);
+            warp_arrive(there);
             return;
         }
         const int lane = threadIdx.x % 32, step0 = h * 64 + wg % 2 * 32, row0 = warp % 4 * 32 % D;
         uint32_t at = sm32 + slot(tile(it, L::Z)) + (uint32_t)(row0 / 64) * L::HALF + (uint32_t)(step0 + lane / 8 % 2 * 8 + lane % 8) * 128 +
                       (uint32_t)(((row0 % 64 / 8 + lane / 16) ^ (lane % 8)) << 4);
         const float *f = &gates[it % L::GB].mid[step0 + lane % 4 * 2], edge = gates[it % L::GB].edge[h * 2 + wg % 2] * (rev ? a.scale : 1.f);
-        uint32_t to = tl + tmem::VL + wg % 2 * 16;
+        uint32_t to = tl + (SUM && h ? tmem::VL2 : tmem::VL) + wg % 2 * 16;
 #pragma unroll 1
         for (int q = 0; q < 2; ++q, at += 16 * 128, f += 16, to += 8) {
             const float2 lo = mul2(*reinterpret_cast<const float2 *>(f), make_float2(edge, edge));        // h of steps 0 .. 7
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         }
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(&bar.vl);
+        warp_arrive(there);
     };
 
     let_next_start();
@@ -360,99 +367,135 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             }
         }
         // Terms of M: row tid of [term][half of dk][D rows][64].
-        auto put_m = [&](int p) {   // columns 16p ..
+        auto put_m = [&](int p, auto last) {   // columns 16p ..; `last`: the third term, in the first one's place
+            constexpr bool LAST = decltype(last)::value;
             if (!rows) return;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int c = col0 + p * 16 + u * 8;
                 const uint32_t at = sm32 + L::M_AT + (uint32_t)(c / 64) * L::M_HALF + swizzled(tid, c % 64 / 8);
-                uint32_t t[4][2];
+                uint32_t t[4][3];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (terms == 2) split2<2>(m[p * 8 + u * 4 + i], t[i]);
-                    else split2<1>(m[p * 8 + u * 4 + i], t[i]);
+                for (int i = 0; i < 4; ++i) split2<LAST ? 3 : terms>(m[p * 8 + u * 4 + i], t[i]);
+#pragma unroll
+                for (int j = LAST ? 2 : 0; j < (LAST ? 3 : terms); ++j) {
+                    const uint32_t v[4] = {t[0][j], t[1][j], t[2][j], t[3][j]};
+                    st_shared16(at + (LAST ? 0 : j) * L::M_TERM, v);
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (j < terms) {
-                        const uint32_t v[4] = {t[0][j], t[1][j], t[2][j], t[3][j]};
-                        st_shared16(at + j * L::M_TERM, v);
-                    }
             }
         };
-        auto give_m = [&] {   // M's terms are there (SUM: dM has been read)
-            if (!SUM) fence_proxy_async_smem();
+        auto give_m = [&] {   // M's terms are there
+            fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(&bar.m);
         };
-        if (!SUM) {
-#pragma unroll
-            for (int p = 0; p < HALF / 16; ++p) put_m(p);
-        }
-        // <other's state, M>, quarters of a thread's columns at a time, on their way while it waits
-        // (all at once before the chunk's products are asked for: dk 204 us instead of 181; behind h z's second half 221).
-        constexpr int Q = HALF / 16;
-        float4 theirs[2 * Q];
-        float2 dot = make_float2(0.f, 0.f);
-        auto fetch = [&](size_t kept, int quarter, int n) {
-            if (tid < D)
-#pragma unroll
-                for (int j = 0; j < n * Q; ++j) theirs[j] = *reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(quarter * Q + j, wg, tid));
-        };
-        auto multiply = [&](int quarter, int n) {
-            if (tid < D)
-#pragma unroll
-                for (int j = 0; j < n * Q; ++j) {
-                    dot = fma2(m[2 * (quarter * Q + j)], make_float2(theirs[j].x, theirs[j].y), dot);
-                    dot = fma2(m[2 * (quarter * Q + j) + 1], make_float2(theirs[j].z, theirs[j].w), dot);
-                }
-        };
-        give_m();
-#pragma unroll 1
-        for (int it = 0; it < chunks; ++it) {
-            const int c = chunk_at(it), gb = it % L::GB;
-            const long long t0 = (long long)c * WC;
-            const WalkGates &gt = gates[gb];
-            const int left = (int)min((long long)WC, len - t0);
-            const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
-            const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
-            if (cross) dot = make_float2(0.f, 0.f), fetch(kept, 0, 2);
-            ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
-            whole = gt.whole;
-            __syncwarp();
-            ok &= wait_tile(tile(it, L::Z));
-            ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
-            if (cross) multiply(0, 2), fetch(kept, 2, 1);
-            values(it, 1);
-            warp_arrive(&bar.gfree[gb]);
-            if (cross) multiply(2, 1), fetch(kept, 3, 1);
-            if (dump && tid < D)   // while Y and the rest of dM are made (175 us before them, 156 here)
-#pragma unroll
-                for (int j = 0; j < HALF / 4; ++j)
-                    *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
-            if (cross) {
-                multiply(3, 1);
-                float sum = (dot.x + dot.y) * whole;
-                __syncwarp();
-#pragma unroll
-                for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
-            }
-            ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
-            if (rows)
+        auto absorb = [&](uint32_t dm) {   // M' = exp(G_C) M + dM
+            if (!rows) return;
 #pragma unroll
             for (int p = 0; p < HALF / 16; p += 2) {
                 uint32_t r[32];
-                tmem_ld32(tl + tmem::DM + col0 + p * 16, r);
+                tmem_ld32(tl + dm + col0 + p * 16, r);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     m[p * 8 + i] = fma2(make_float2(whole, whole), m[p * 8 + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
-                if (!SUM) put_m(p), put_m(p + 1);
+                if (!SUM) put_m(p, std::false_type()), put_m(p + 1, std::false_type());
                 __syncwarp();
             }
+        };
+        if constexpr (SUM) {
+            // A chunk's second half of h z is made before the last one's dM is read: the products always have something to do.
+            float before = 0.f;
+            auto last = [&](int it) {
+                if (it > 0) {
+                    whole = before;
+                    absorb(it & 1 ? tmem::DM : tmem::DM2);
+                    tc_fence_before();
+                    warp_arrive(it & 1 ? &bar.m : &bar.scaled);
+                }
+            };
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                const int gb = it % L::GB;
+                ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+                const float now = gates[gb].whole;
+                __syncwarp();
+                ok &= wait_tile(tile(it, L::Z));
+                if (it > 0) ok &= walk_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);
+                values(it, 1);
+                warp_arrive(&bar.gfree[gb]);
+                last(it);
+                before = now;
+            }
+            if (chunks > 0) ok &= walk_wait_warp(&bar.dm, (chunks - 1) & 1, gone, a.ctl);
+            last(chunks);
+            if (tid < D)
+#pragma unroll
+                for (int j = 0; j < HALF / 4; ++j)
+                    *reinterpret_cast<float4 *>(ro.seg_own + seg_at * D * D + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
+        } else {
+#pragma unroll
+            for (int p = 0; p < HALF / 16; ++p) put_m(p, std::false_type());
+            // <other's state, M>, quarters of a thread's columns at a time, on their way while it waits
+            // (all at once before the chunk's products are asked for: dk 204 us instead of 181, of two terms; behind h z's second half 221).
+            constexpr int Q = HALF / 16;
+            float4 theirs[2 * Q];
+            float2 dot = make_float2(0.f, 0.f);
+            auto fetch = [&](size_t kept, int quarter, int n) {
+                if (tid < D)
+#pragma unroll
+                    for (int j = 0; j < n * Q; ++j) theirs[j] = *reinterpret_cast<const float4 *>(ro.other + kept + state_at<D>(quarter * Q + j, wg, tid));
+            };
+            auto multiply = [&](int quarter, int n) {
+                if (tid < D)
+#pragma unroll
+                    for (int j = 0; j < n * Q; ++j) {
+                        dot = fma2(m[2 * (quarter * Q + j)], make_float2(theirs[j].x, theirs[j].y), dot);
+                        dot = fma2(m[2 * (quarter * Q + j) + 1], make_float2(theirs[j].z, theirs[j].w), dot);
+                    }
+            };
             give_m();
-            if constexpr (!SUM) {
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                const int c = chunk_at(it), gb = it % L::GB;
+                const long long t0 = (long long)c * WC;
+                const WalkGates &gt = gates[gb];
+                const int left = (int)min((long long)WC, len - t0);
+                const size_t row = (size_t)(b * a.S + s0 + t0 + tid) * a.Hv + head;
+                const size_t kept = ((size_t)(slot0 + c) * a.Hv + head) * D * D;
+                if (cross) dot = make_float2(0.f, 0.f), fetch(kept, 0, 2);
+                ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
+                whole = gt.whole;
+                __syncwarp();
+                ok &= wait_tile(tile(it, L::Z));
+                ok &= walk_wait_warp(&bar.dm0, it & 1, gone, a.ctl);
+                if (cross) multiply(0, 2), fetch(kept, 2, 1);
+                values(it, 1);
+                warp_arrive(&bar.gfree[gb]);
+                if (third) {
+                    ok &= walk_wait_warp(&bar.y2, it & 1, gone, a.ctl);
+#pragma unroll
+                    for (int p = 0; p < HALF / 16; ++p) put_m(p, std::bool_constant<dots>());
+                    fence_proxy_async_smem();
+                    warp_arrive(&bar.m3);
+                }
+                if (cross) multiply(2, 1), fetch(kept, 3, 1);
+                if (dump && tid < D)   // while Y and the rest of dM are made (175 us before them, 156 here)
+#pragma unroll
+                    for (int j = 0; j < HALF / 4; ++j)
+                        *reinterpret_cast<float4 *>(ro.dump + kept + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
+                if (cross) {
+                    multiply(3, 1);
+                    float sum = (dot.x + dot.y) * whole;
+                    __syncwarp();
+#pragma unroll
+                    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (tid % 32 == 0) ro.cross[((size_t)(slot0 + c) * a.Hv + head) * 8 + warp] = sum;
+                }
+                ok &= walk_wait_warp(&bar.dm, it & 1, gone, a.ctl);   // (behind Y, which reads M)
+                if (third) ok &= walk_wait_warp(&bar.y, it & 1, gone, a.ctl);
+                absorb(tmem::DM);
+                give_m();
                 ok &= walk_wait_warp(&bar.out, it & 1, gone, a.ctl);
                 // Whole chunks leave by TMA, from x's place (dots: from `beside`'s), which is done with.
                 if (ro.out32 || (a.offsets && left < WC)) {
@@ -491,16 +534,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 }
                 warp_arrive(&bar.staged);
             }
-        }
-        if (SUM) {
-            if (tid < D)
+            if (ro.fin && in && seg == (rev ? 0 : a.segs - 1)) {
 #pragma unroll
-                for (int j = 0; j < HALF / 4; ++j)
-                    *reinterpret_cast<float4 *>(ro.seg_own + seg_at * D * D + state_at<D>(j, wg, tid)) = make_float4(m[2 * j].x, m[2 * j].y, m[2 * j + 1].x, m[2 * j + 1].y);
-        } else if (ro.fin && in && seg == (rev ? 0 : a.segs - 1)) {
-#pragma unroll
-            for (int i = 0; i < HALF; ++i)
-                if (col0 + i < ro.dk) ro.fin[outside + (size_t)(col0 + i) * ro.col] = i % 2 ? m[i / 2].y : m[i / 2].x;
+                for (int i = 0; i < HALF; ++i)
+                    if (col0 + i < ro.dk) ro.fin[outside + (size_t)(col0 + i) * ro.col] = i % 2 ? m[i / 2].y : m[i / 2].x;
+            }
         }
         __syncwarp();
     } else if (wg < 4) {
@@ -514,7 +552,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             const WalkGates &gt = gates[gb];
             ok &= walk_wait(&bar.gfull[gb], (it / L::GB) & 1, gone, a.ctl);
             ok &= wait_tile(tile(it, L::Z));
-            if (it > 0) ok &= walk_wait_warp(&bar.dm, (it - 1) & 1, gone, a.ctl);   // the last half's terms are done with
+            if (it > 0) ok &= walk_wait_warp(SUM ? &bar.dm0 : &bar.dm, (it - 1) & 1, gone, a.ctl);   // the last half's terms are done with
             values(it, 0);
             if constexpr (!SUM) {
                 const Sum2 mine = gt.sum(rb * 32 + threadIdx.x % 32);
@@ -628,14 +666,15 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             __syncwarp();
         };
         auto update = [&](int it, int h) {   // dM += (h z)^T y over 64 steps
-            ok &= all_wait(&bar.vl, h);
+            ok &= SUM ? all_wait(h ? &bar.p : &bar.vl, it & 1) : all_wait(&bar.vl, h);
+            const uint32_t to = tm + (SUM && it % 2 ? tmem::DM2 : tmem::DM), from = tm + (SUM && h ? tmem::VL2 : tmem::VL);
             const uint64_t y = smem_desc(tile_at(tile(it, L::Y)) + h * 64 * 128, L::HALF, 1024);
             if (elect_one() && ok) {
 #pragma unroll 1
                 for (int j = 2; j >= 0; --j)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + tmem::DM, tm + tmem::VL + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
+                        mma_ts(to, from + j * 32 + k * 8, y + ((k * 2048) >> 4), id_mn, h > 0 || j < 2 || k > 0);
                 mma_commit(h ? &bar.dm : &bar.dm0);
                 if (h) mma_commit(&bar.empty[tile(it, L::Y) % L::SLOTS]);
                 if (h && SUM) mma_commit(&bar.empty[tile(it, L::Z) % L::SLOTS]);
@@ -644,9 +683,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         };
         // What a chunk begins with: its scores and the first half of its dM (behind the last chunk's out).
         auto begin = [&](int it) {
-            if (!SUM) scores(it);
-            else ok &= all_tile(tile(it, L::Y));
-            ok &= all_wait(&bar.m, it & 1);   // dM has been read (and M's terms are there)
+            if constexpr (!SUM) {
+                scores(it);
+                ok &= all_wait(&bar.m, it & 1);   // dM has been read (and M's terms are there)
+            } else {
+                ok &= all_tile(tile(it, L::Y));
+                if (it > 1) ok &= all_wait(it % 2 ? &bar.scaled : &bar.m, (it / 2 - 1) & 1);   // this dM has been read
+            }
             update(it, 0);
         };
 #pragma unroll 1
@@ -661,12 +704,23 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
                             mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j < terms - 1 || k > 0);
-                    mma_commit(&bar.y);
-                    if (dots) mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
+                    mma_commit(third ? &bar.y2 : &bar.y);
+                    if (dots && !third) mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
                 }
                 __syncwarp();
             }
             update(it, 1);
+            if (third) {
+                ok &= all_wait(&bar.m3, it & 1);
+                const uint64_t x = smem_desc(tile_at(tile(it, L::X)), 16, 1024), y = smem_desc(__reduce_min_sync(0xffffffffu, sm32 + L::M_AT), 16, 1024);
+                if (elect_one() && ok) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::O, x + k_major(k), y + (((k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, true);
+                    mma_commit(&bar.y);
+                    mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
+                }
+                __syncwarp();
+            }
             if constexpr (!SUM) {   // out = f Y + P z
                 ok &= all_wait(&bar.p, it & 1);
                 ok &= all_wait(&bar.scaled, it & 1);
@@ -746,7 +800,17 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) raw[i] = t0 + i < len ? load_any(a.g, a.gate16, row + (long long)i * a.Hv) : 0.f;
         };
+        // (Chunks of a sum are short, and dk's loads many: 121 and 172 us instead of 133 and 181.  For the others it is code: 165 for 162.)
+        constexpr bool far = SUM || cross;
+        auto ahead = [&](int it) {   // into L2
+            const long long t0 = (long long)chunk_at(it) * WC + 4 * lane, row = (b * a.S + s0 + t0) * a.Hv + head;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t0 + i < len) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(a.g) + (row + (long long)i * a.Hv) * (a.gate16 ? 2 : 4)));
+        };
         if (chunks > 0) read(0);
+        if (far)
+            for (int it = 1; it < min(chunks, 3); ++it) ahead(it);
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
             const int gb = it % L::GB;
@@ -757,6 +821,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             warp_arrive(&bar.gfull[gb]);
             if (it + 1 < chunks) {
                 read(it + 1);
+                if (far && it + 3 < chunks) ahead(it + 3);
                 if (cross && lane == 0)   // and the states that the next chunk's are compared with, into L2
                     bulk_prefetch(ro.other + ((size_t)(slot0 + chunk_at(it + 1)) * a.Hv + head) * D * D, D * D * 4);
             }
