@@ -13,8 +13,9 @@
  * quat_cumprod_status(); outputs must not overlap inputs (quat_delta_step's
  * state is updated in place).  Status codes are quat_cumprod.h's.
  *
- * quat_cumprod_debug_stall_tile(k) makes CTA k of quat_delta_fwd's and _bwd's
- * bfloat16 walks wait for rows that never come, as it does a tile of the scan.
+ * quat_cumprod_debug_stall_tile(k) makes CTA k of quat_delta_fwd's and _bwd's and
+ * of quat_decay_fwd's and _bwd's bfloat16 walks wait for rows that never come, as it
+ * does a tile of the scan.
  *
  * Element types: QS_F32 or QS_BF16.  Sums, norms and states are fp32.  The delta rule's
  * products leave out at most 2^-24 of a product, or, where only bfloat16 outputs are made
@@ -152,7 +153,13 @@ int quat_delta_step(int dtype, int gate_dtype, float scale,
  * Tensors, sequences, strides and sizes are those of quat_delta_fwd (without beta);
  * init NULL: zeros, final_state NULL: not written.  A NaN or infinity at a step
  * spoils the outputs of its sequence from the start of its chunk (at most 128 steps)
- * on, never another sequence's.
+ * on, never another sequence's.  With offsets, rows from offsets[N] on (where that is
+ * less than S) are not used, and left as they were in every output.
+ *
+ * Precision: as the delta rule, but for the values of which only bfloat16 outputs are
+ * made (o; d_q, d_k, d_v): the products <q_t, k_s> D_ts and the state that enters a chunk
+ * are rounded to bfloat16 there (2^-9 each, independent of the output's own rounding; the
+ * state itself stays fp32).  d_g leaves out 2^-24 of a product, with bfloat16 gates 2^-15.
  */
 int quat_decay_fwd(int dtype, int gate_dtype, float scale,
                    const void *q, const void *k, const void *v, const void *g, const float *init,

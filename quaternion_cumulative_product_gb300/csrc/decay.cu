@@ -4,7 +4,7 @@
 // bfloat16: the walk of decay_walk.cuh; backward three of them (dq, dk, dv) and decay_gate.cuh.
 // fp32, whose values are three terms each and take three times the room: the states of all chunks
 // at once (decay_states.cuh), then the delta rule's kernels without its errors (RULE,
-// delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 201 us; with the states walked,
+// delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 190 us; with the states walked,
 // twice where sequences are cut, 326 us.
 #include <algorithm>
 
@@ -30,25 +30,24 @@ void cut_states(DeltaArgs &a, int sms) {
     a.seg_chunks = (a.NC + want - 1) / want, a.segs = (int)((a.NC + a.seg_chunks - 1) / a.seg_chunks);
 }
 
-template <bool REV>
-int launch_states(const DeltaArgs &d, float *states, float *whole, const float *first, float *last, cudaStream_t stream) {
-    const StateArgs s = {d, states, whole, first, last};
+int launch_states(const StateArgs &s, unsigned sides, cudaStream_t stream) {
+    const DeltaArgs &d = s.d;
     auto own = [&](auto kernel, int D) {
         const int smem = 2 * DC * D * 4;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             cudaGetLastError();
             return (int)QS_ERR_CUDA;
         }
-        kernel<<<(unsigned)(d.slots * d.Hv), kOwnThreads, smem, stream>>>(s);
+        kernel<<<dim3((unsigned)(d.slots * d.Hv), sides), kOwnThreads, smem, stream>>>(s);
         return launched();
     };
     if (d.slots > 0) {
-        const int rc = d.Dk <= 64 && d.Dv <= 64 ? own(decay_own_kernel<64, REV>, 64) : own(decay_own_kernel<128, REV>, 128);
+        const int rc = d.Dk <= 64 && d.Dv <= 64 ? own(decay_own_kernel<64>, 64) : own(decay_own_kernel<128>, 128);
         if (rc != QS_OK) return rc;
     }
     const long long parts = (d.Dk * d.Dv / 4 + 255) / 256;
     if (d.N * d.Hv * parts >= 1ll << 31) return QS_ERR_DIMS;
-    return early(qsh::launch_next(decay_run_kernel<REV>, (unsigned)(d.N * d.Hv * parts), 256, 0, stream, s, (unsigned)parts));
+    return early(qsh::launch_next(decay_run_kernel, dim3((unsigned)(d.N * d.Hv * parts), sides), 256, 0, stream, s, (unsigned)parts));
 }
 
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
@@ -261,7 +260,7 @@ extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void
     if (wc != QS_OK) return wc;
     float *carries = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    if (a.segs > 1) wc = launch_states<false>(a, carries, carries + kept, init, nullptr, stream);
+    if (a.segs > 1) wc = launch_states({a, carries + kept, {{carries, init, nullptr, false}}}, 1, stream);
     if (wc != QS_OK) return wc;
     a.carries_in = carries;
     return launch_walks<false, float, 3, false>(a, nullptr, stream);
@@ -320,11 +319,10 @@ extern "C" int quat_decay_bwd(int dtype, int gate_dtype, float scale, const void
     a.ds = reinterpret_cast<float *>(p + nds);
     a.dqh = reinterpret_cast<float *>(p + 2 * nds), a.dkh = reinterpret_cast<float *>(p + 2 * nds + nh);
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};
-    rc = launch_states<true>(a, a.ds, whole, d_final, d_init, stream);   // (without steps: d_init is d_final, or zeros)
+    rc = launch_states({a, whole, {{carries, init, nullptr, false}, {a.ds, d_final, d_init, true}}}, 2, stream);   // (without steps: d_init is d_final, or zeros)
     if (rc != QS_OK || !some) return rc;
-    rc = launch_states<false>(a, carries, whole, init, nullptr, stream);
     a.carries_in = carries, a.d_init = nullptr;
-    if (rc == QS_OK) rc = launch_walks<true, float, 3, false>(a, nullptr, stream);   // dv
+    rc = launch_walks<true, float, 3, false>(a, nullptr, stream);   // dv
     if (rc == QS_OK) rc = launch_chunks<float, 3, 3, false>(a, stream);
     if (rc != QS_OK || !shared) return rc;
     const long long quads = B * S * Hk * Dk / 4;

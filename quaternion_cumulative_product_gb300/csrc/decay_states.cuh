@@ -16,22 +16,29 @@
 
 namespace qs {
 
+// One direction; the backward takes both in one launch.
+struct StateSide {
+    float *states;        // [slots, Hv, Dk, Dv]: the chunks' own parts, then the state that enters each (rev: the cotangent of the one that leaves it)
+    const float *first;   // state that enters the first chunk (rev: cotangent that leaves the last) [N, Hv, Dk, Dv], or NULL
+    float *last;          // what the run ends with, or NULL
+    bool rev;
+};
+
 struct StateArgs {
     DeltaArgs d;
-    float *states;        // [slots, Hv, Dk, Dv]: the chunks' own parts, then the state that enters each (REV: the cotangent of the one that leaves it)
     float *whole;         // [slots, Hv]
-    const float *first;   // state that enters the first chunk (REV: cotangent that leaves the last) [N, Hv, Dk, Dv], or NULL
-    float *last;          // what the run ends with, or NULL
+    StateSide side[2];
 };
 
 constexpr int kOwnThreads = 256;
 
 // D: 64 or 128, at least Dk and Dv.
-template <int D, bool REV>
+template <int D>
 __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_constant__ StateArgs s) {
     extern __shared__ __align__(16) float rows[];   // [64][D] k (q), [64][D] v (dO)
     __shared__ ChunkGates gt;
     const DeltaArgs &a = s.d;
+    const bool rev = s.side[blockIdx.y].rev;
     let_next_start();
     const int head = blockIdx.x % a.Hv, kh = head / (a.Hv / a.Hk), tid = threadIdx.x;
     const long long slot = blockIdx.x / a.Hv;
@@ -44,14 +51,14 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
     __syncthreads();
     float *x = rows, *y = rows + DC * D;
     const qsh::Strides so = {(long long)a.S * a.Hv * a.Dv, (long long)a.Hv * a.Dv, a.Dv};
-    const qsh::Strides &sx = REV ? a.sq : a.sk, &sy = REV ? so : a.sv;
-    const float *px = static_cast<const float *>(REV ? a.q : a.k) + seq.b * sx.b + (seq.s0 + t0) * sx.s + (long long)kh * sx.h;
-    const float *py = static_cast<const float *>(REV ? a.d_o : a.v) + seq.b * sy.b + (seq.s0 + t0) * sy.s + (long long)head * sy.h;
+    const qsh::Strides &sx = rev ? a.sq : a.sk, &sy = rev ? so : a.sv;
+    const float *px = static_cast<const float *>(rev ? a.q : a.k) + seq.b * sx.b + (seq.s0 + t0) * sx.s + (long long)kh * sx.h;
+    const float *py = static_cast<const float *>(rev ? a.d_o : a.v) + seq.b * sy.b + (seq.s0 + t0) * sy.s + (long long)head * sy.h;
     for (int i = tid; i < DC * D / 4; i += kOwnThreads) {
         const int r = i / (D / 4), col = i % (D / 4) * 4;
         float4 u = q_zero(), v = q_zero();
         if (r < left && col < a.Dk) {
-            const float f = REV ? a.scale * gt.grown[r] : gt.left[r];
+            const float f = rev ? a.scale * gt.grown[r] : gt.left[r];
             u = load4(px + r * sx.s + col);
             u = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
         }
@@ -83,7 +90,7 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
             }
         }
     }
-    float *out = s.states + (size_t)blockIdx.x * a.Dk * a.Dv;
+    float *out = s.side[blockIdx.y].states + (size_t)blockIdx.x * a.Dk * a.Dv;
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         const int r = i / 4 * 64 + i0 + i % 4;
@@ -92,35 +99,35 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
             for (int j = 0; j < H; ++j)
                 if (j * 64 + j0 < a.Dv) store4(out + (size_t)r * a.Dv + j * 64 + j0, make_float4(m[i][2 * j].x, m[i][2 * j].y, m[i][2 * j + 1].x, m[i][2 * j + 1].y));
     }
-    if (tid == 0) s.whole[blockIdx.x] = gt.whole;
+    if (tid == 0 && blockIdx.y == 0) s.whole[blockIdx.x] = gt.whole;
 }
 
 // A thread per four values of a (sequence, head); eight chunks' parts on their way at a time.
-template <bool REV>
 __global__ void __launch_bounds__(256) decay_run_kernel(const __grid_constant__ StateArgs s, unsigned parts) {
     const DeltaArgs &a = s.d;
+    const StateSide &side = s.side[blockIdx.y];
     wait_for_last();
     const size_t size = (size_t)a.Dk * a.Dv, e = ((size_t)(blockIdx.x % parts) * 256 + threadIdx.x) * 4, nh = blockIdx.x / parts;
     if (e >= size) return;
     const Seq seq = seq_of(a, (long long)(nh / a.Hv));
     const int head = (int)(nh % a.Hv), chunks = (int)((seq.len + DC - 1) / DC);
-    auto at = [&](int i) { return (size_t)(seq.slot0 + (REV ? chunks - 1 - i : i)) * a.Hv + head; };
-    float4 m = s.first ? __ldg(reinterpret_cast<const float4 *>(s.first + nh * size + e)) : q_zero();
+    auto at = [&](int i) { return (size_t)(seq.slot0 + (side.rev ? chunks - 1 - i : i)) * a.Hv + head; };
+    float4 m = side.first ? __ldg(reinterpret_cast<const float4 *>(side.first + nh * size + e)) : q_zero();
     constexpr int AHEAD = 8;
     for (int i0 = 0; i0 < chunks; i0 += AHEAD) {
         float4 own[AHEAD];
         float f[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
-            if (i0 + k < chunks) own[k] = *reinterpret_cast<const float4 *>(s.states + at(i0 + k) * size + e), f[k] = s.whole[at(i0 + k)];
+            if (i0 + k < chunks) own[k] = *reinterpret_cast<const float4 *>(side.states + at(i0 + k) * size + e), f[k] = s.whole[at(i0 + k)];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
             if (i0 + k < chunks) {
-                *reinterpret_cast<float4 *>(s.states + at(i0 + k) * size + e) = m;
+                *reinterpret_cast<float4 *>(side.states + at(i0 + k) * size + e) = m;
                 m = make_float4(fmaf(f[k], m.x, own[k].x), fmaf(f[k], m.y, own[k].y), fmaf(f[k], m.z, own[k].z), fmaf(f[k], m.w, own[k].w));
             }
     }
-    if (s.last) *reinterpret_cast<float4 *>(s.last + nh * size + e) = m;
+    if (side.last) *reinterpret_cast<float4 *>(side.last + nh * size + e) = m;
 }
 
 }  // namespace qs

@@ -800,7 +800,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) raw[i] = t0 + i < len ? load_any(a.g, a.gate16, row + (long long)i * a.Hv) : 0.f;
         };
-        // (Chunks of a sum are short, and dk's loads many: 121 and 172 us instead of 133 and 181.  For the others it is code: 165 for 162.)
+        // (A sum's chunks are short, and dk loads states besides: 1 x 131072 x 16 x 64 forward 409 -> 384 us, dk
+        // at 8 x 4096 x 16 x 128 181 -> 172, of two terms.  For the others it is more code: dq 162 -> 165.)
         constexpr bool far = SUM || cross;
         auto ahead = [&](int it) {   // into L2
             const long long t0 = (long long)chunk_at(it) * WC + 4 * lane, row = (b * a.S + s0 + t0) * a.Hv + head;

@@ -122,6 +122,8 @@ class QuatMixerBlock(torch.nn.Module):
 
     ``key`` (a buffer: seed, offset) draws the dropout's mask; its offset is counted up by one
     each time the block trains, on the device, so that a captured step draws anew too.
+    (A forward that is run again for its gradients, as under activation checkpointing, would draw
+    another mask than the first one's: ``p`` must be 0 there.)
     """
 
     def __init__(self, mixer, width, p=0.0, eps=1e-5, seed=0, device="cuda"):
