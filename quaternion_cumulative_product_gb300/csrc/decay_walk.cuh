@@ -36,10 +36,10 @@
 //
 // Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 111 us (4.8 TB/s, 0.71 of a copy's rate),
 // 3.4 us a chunk; dv 109, dq 170 and dk 190 us (they also write and read the states, 268 MB each).
-// 1 x 131072 x 16 x 64 in 19 segments: 384 us, the sums 121 and the walk 256 of them.
-// Bound: shared memory.  The tensor cores read 64 KB (S) + 64 KB (Y) + 32 KB (P z) + 96 KB (dM) of
-// operands a chunk, the copies write 96 KB and read 32 KB, conversions write M (32 KB) and out (32 KB)
-// and read h z's columns two bytes a lane.
+// 1 x 131072 x 16 x 64 in 19 segments: 375 us, the sums 121 and the walk 250 of them.
+// Bound: the products, beside the other roles' use of shared memory.  48 of 128 x 128 x 16 a chunk (S 8,
+// Y 8, dM 24, P z 8) take 80 to 100 cycles each (64 alone), 4 400 of a chunk's 6 500; the rest is
+// the way from one to the next: out, then the next chunk's S, then its P.
 #pragma once
 
 #include <type_traits>
@@ -149,15 +149,15 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 __device__ __forceinline__ bool walk_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
-    if (mbar_sleep(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    do {
-        if (*gone) return false;
-        if (global_timer_ns() - t0 > ctl.timeout_ns) {
+    unsigned long long t0 = 0;
+    while (!mbar_sleep(bar, parity)) {
+        const unsigned long long now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (*gone || now - t0 > ctl.timeout_ns) {
             *gone = 1;   // (recorded once, at the kernel's end: the code of each wait stays short)
             return false;
         }
-    } while (!mbar_sleep(bar, parity));
+    }
     return true;
 }
 __device__ __forceinline__ bool walk_wait_warp(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
@@ -293,7 +293,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     auto stage_at = [&](int it) { return dots ? (uint32_t)(L::ROOM - 1) * L::TILE_BYTES : (uint32_t)(tile(it, L::X) % L::SLOTS) * L::TILE_BYTES; };
     auto slot = [&](int i) { return (uint32_t)(i % L::SLOTS) * L::TILE_BYTES; };
     // Waits of the warps that issue: whole warps go on or stop together.
-    auto all_wait = [&](uint64_t *x, uint32_t parity) { return __all_sync(0xffffffffu, walk_wait_warp(x, parity, gone, a.ctl)) != 0; };
+    auto all_wait = [&](uint64_t *x, uint32_t parity) {
+        const bool there = __all_sync(0xffffffffu, walk_wait(x, parity, gone, a.ctl)) != 0;
+        tc_fence_after();
+        return there;
+    };
     auto wait_tile = [&](int i) { return walk_wait_warp(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1, gone, a.ctl); };
 
     // Terms of h z, 32 of the chunk's steps 64h .. (the first half by `convert`, the second by `state`):
@@ -605,9 +609,6 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     }
                     tmem_st8(to, r);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar.p);
                 // f Y in place, and its product with the row of `beside`.
                 const float f = rev ? decay(gt.sum(WC - 1), mine) : a.scale * decay(mine, {0.f, 0.f});
                 const int row = rb * 32 + threadIdx.x % 32;
@@ -651,7 +652,6 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     if (warp == 16) {
         // ------------------------------------------------------------------ products
         const uint32_t id_s = mma_desc(128, 128), id_y = mma_desc(128, D), id_mn = mma_desc(128, D, false, true);
-        auto k_major = [](int k) { return (uint32_t)((k / 4) * L::HALF + (k % 4) * 32) >> 4; };
         auto tile_at = [&](int i) { return __reduce_min_sync(0xffffffffu, sm32 + slot(i)); };   // (uniform descriptors: tensor_core.cuh)
         auto all_tile = [&](int i) { return all_wait(&bar.full[i % L::SLOTS], (i / L::SLOTS) & 1); };
         auto scores = [&](int it) {   // S = x y^T
@@ -659,8 +659,10 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
             ok &= all_tile(tile(it, L::X));
             const uint64_t x = smem_desc(tile_at(tile(it, L::X)), 16, 1024), y = smem_desc(tile_at(tile(it, L::Y)), 16, 1024);
             if (elect_one() && ok) {
+#pragma unroll 1
+                for (int h = 0; h < L::HALVES; ++h)
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::S, x + k_major(k), y + k_major(k), id_s, k > 0);
+                    for (int k = 0; k < 4; ++k) mma_ss(tm + tmem::S, x + (h * L::HALF + k * 32 >> 4), y + (h * L::HALF + k * 32 >> 4), id_s, h > 0 || k > 0);
                 mma_commit(&bar.s);
             }
             __syncwarp();
@@ -701,9 +703,11 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 if (elect_one() && ok) {
 #pragma unroll 1
                     for (int j = terms - 1; j >= 0; --j)   // the small term first
+#pragma unroll 1
+                        for (int h = 0; h < L::HALVES; ++h)
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_ss(tm + tmem::O, x + k_major(k), y + ((j * L::M_TERM + (k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, j < terms - 1 || k > 0);
+                            for (int k = 0; k < 4; ++k)
+                                mma_ss(tm + tmem::O, x + (h * L::HALF + k * 32 >> 4), y + (j * L::M_TERM + h * L::M_HALF + k * 32 >> 4), id_y, j < terms - 1 || h > 0 || k > 0);
                     mma_commit(third ? &bar.y2 : &bar.y);
                     if (dots && !third) mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
                 }
@@ -714,21 +718,23 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 ok &= all_wait(&bar.m3, it & 1);
                 const uint64_t x = smem_desc(tile_at(tile(it, L::X)), 16, 1024), y = smem_desc(__reduce_min_sync(0xffffffffu, sm32 + L::M_AT), 16, 1024);
                 if (elect_one() && ok) {
+#pragma unroll 1
+                    for (int h = 0; h < L::HALVES; ++h)
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) mma_ss(tm + tmem::O, x + k_major(k), y + (((k / 4) * L::M_HALF + (k % 4) * 32) >> 4), id_y, true);
+                        for (int k = 0; k < 4; ++k) mma_ss(tm + tmem::O, x + (h * L::HALF + k * 32 >> 4), y + (h * L::M_HALF + k * 32 >> 4), id_y, true);
                     mma_commit(&bar.y);
                     mma_commit(&bar.empty[tile(it, L::X) % L::SLOTS]);
                 }
                 __syncwarp();
             }
             if constexpr (!SUM) {   // out = f Y + P z
-                ok &= all_wait(&bar.p, it & 1);
-                ok &= all_wait(&bar.scaled, it & 1);
-                ok &= all_tile(tile(it, L::Z));
+                ok &= all_wait(&bar.scaled, it & 1);   // (and P, made before; z has been read for h z)
                 const uint64_t z = smem_desc(tile_at(tile(it, L::Z)), L::HALF, 1024);
                 if (elect_one() && ok) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) mma_ts(tm + tmem::O, tm + tmem::S + k / 2 * 32 + k % 2 * 8, z + ((k * 2048) >> 4), id_mn, true);
+                        for (int k = 0; k < 4; ++k) mma_ts(tm + tmem::O, tm + tmem::S + h * 64 + k / 2 * 32 + k % 2 * 8, z + ((h * 4 + k) * 2048 >> 4), id_mn, true);
                     mma_commit(&bar.out);
                     mma_commit(&bar.empty[tile(it, L::Z) % L::SLOTS]);
                 }
