@@ -121,6 +121,13 @@ def test_decay(torch, shape, dt, gates):
     check(torch, inputs(torch, *shape, dt, gates, init=shape[1] % 2 == 1))
 
 
+@pytest.mark.parametrize("dt,gates", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("shape", [(1, 2100, 1, 2, 96, 128), (2, 1100, 2, 4, 128, 72), (1, 1700, 1, 1, 64, 24), (3, 1030, 4, 16, 64, 64)], ids=str)
+def test_many_chunks(torch, shape, dt, gates):
+    """Sequences in many segments, heads of two lengths, and more chunks than CTAs run at once."""
+    check(torch, inputs(torch, *shape, dt, gates))
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_scale_and_no_decay(torch, dt):
     """g = 0: a plain running sum."""
