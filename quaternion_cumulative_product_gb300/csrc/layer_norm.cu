@@ -68,8 +68,6 @@ struct Raw<T, 1> {
     __device__ __forceinline__ void get(float *f) const { f[0] = qs::to_float(r); }
 };
 
-__device__ __forceinline__ float4 shared4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 shared4(const __nv_bfloat16 *p) { return qs::IoBF16::get(*reinterpret_cast<const uint2 *>(p)); }
 
 __device__ __forceinline__ float2 add2(const float2 a, const float2 b) {
     float2 r;
@@ -372,16 +370,16 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-// Backward of aligned rows, 16 / WPR of them at a time: bulk copies bring the tiles into a ring of
+// Backward of aligned fp32 rows, 16 / WPR of them at a time: bulk copies bring the tiles into a ring of
 // three; WPR warps take a row's four sums (each lane four units, as they are in memory); then
 // each thread takes four columns (PB times) of all rows, and keeps their weights and sums.  A
-// row's threads meet at three barriers a tile instead of two a row: 99 against 85 us at
-// 32768 x 2048 bfloat16, 148 and 123 in fp32.
+// row's threads meet at three barriers a tile instead of two a row: 123 instead of 148 us at 32768 x 2048.
 constexpr int kTileThreads = 512, kTileStages = 3, kTileUnits = 4;   // units of a lane
 
-template <typename T, int VEC, int WPR, int PB>
+template <int WPR, int PB>
 __global__ void __launch_bounds__(kTileThreads, 1) norm_tile_kernel(const NormArgs a) {
-    constexpr int RT = 16 / WPR, UNITS = kTileUnits;
+    using T = float;
+    constexpr int RT = 16 / WPR, UNITS = kTileUnits, VEC = 4;
     __shared__ uint64_t full[kTileStages];
     __shared__ __align__(16) float stats[RT][4], slots[2][16][2];   // (read four and two at a time)
     extern __shared__ __align__(16) unsigned char dynamic[];
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) norm_tile_kernel(const NormAr
 #pragma unroll 4
             for (int i = 0; i < rows; ++i) {
                 const float4 st4 = *reinterpret_cast<const float4 *>(stats[i]);
-                const float4 xv = shared4(xs + i * D + c), dv = shared4(ds + i * D + c);
+                const float4 xv = *reinterpret_cast<const float4 *>(xs + i * D + c), dv = *reinterpret_cast<const float4 *>(ds + i * D + c);
                 const float2 m2 = make_float2(-st4.x, -st4.x), r2 = make_float2(st4.y, st4.y), dn2 = make_float2(-st4.z, -st4.z), dot2 = make_float2(-st4.w, -st4.w);
                 const float2 nl = mul2(add2(make_float2(xv.x, xv.y), m2), r2), nh = mul2(add2(make_float2(xv.z, xv.w), m2), r2);
                 const float2 dl = make_float2(dv.x, dv.y), dh = make_float2(dv.z, dv.w);
@@ -518,6 +516,140 @@ __global__ void __launch_bounds__(kTileThreads, 1) norm_tile_kernel(const NormAr
         const int c = (p * kTileThreads + tid) * 4;
         if (c < D) qs::store4(part_out + c, dw[p]), qs::store4(part_out + D + c, db[p]);
     }
+}
+
+// The same for bfloat16, whose conversions cost most there: WPR warps keep a row in fp32 registers from its
+// first sum to its gradient, and their columns' weights and sums from row to row.  256 threads, for the
+// registers; the rows come from the same kind of ring, 8 / WPR to a tile.  32768 x 2048: 79.5 us, 0.75 of a
+// copy's rate (as fp32 rows, every value converted twice and read twice: 84.6; 8192 x 8192: 88 and 104; 65536 x
+// 768: 76.5 and 74.4).
+constexpr int kRowThreads = 256, kRowStages = 4;
+
+template <int WPR>
+__global__ void __launch_bounds__(kRowThreads, 1) norm_row_kernel(const NormArgs a) {
+    using T = __nv_bfloat16;
+    constexpr int RT = 8 / WPR, UNITS = kTileUnits, VEC = 8, P = UNITS * VEC / 2;   // pairs of values of a lane
+    __shared__ uint64_t full[kRowStages];
+    __shared__ __align__(16) float slots[2][8][2];
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    const int D = a.D, tid = threadIdx.x, warp = tid / 32, lane = tid % 32, mine = warp / WPR, part = warp % WPR;
+    const uint32_t rowb = (uint32_t)D * sizeof(T), stageb = 2 * RT * rowb;
+    const long long tiles = (a.R + RT - 1) / RT;
+    bool ok = true;
+    int sent = 0, seen = 0;
+    qs::let_next_start();
+    auto send = [&](long long tile) {   // thread 0
+        if (tile >= tiles || !ok) return;
+        unsigned char *to = dynamic + (size_t)(sent % kRowStages) * stageb;
+        uint64_t *bar = &full[sent % kRowStages];
+        const long long row = tile * RT;
+        const int rows = (int)(a.R - row < RT ? a.R - row : RT);
+        qs::mbar_arrive_expect_tx(bar, 2 * rows * rowb);
+        const T *x = static_cast<const T *>(a.x) + row * a.ld;
+        if (a.ld == D) bulk_load(to, x, rows * rowb, bar);
+        else
+            for (int i = 0; i < rows; ++i) bulk_load(to + i * rowb, x + i * a.ld, rowb, bar);
+        bulk_load(to + RT * rowb, static_cast<const T *>(a.dy) + row * D, rows * rowb, bar);
+        ++sent;
+    };
+    if (tid == 0) {
+        for (int i = 0; i < kRowStages; ++i) qs::mbar_init(&full[i], 1);
+        qs::fence_mbar_init();
+        for (int i = 0; i < kRowStages; ++i) send(blockIdx.x + (long long)i * gridDim.x);
+    }
+    const int c0 = part * UNITS * 32 * VEC + lane * VEC;   // this lane's columns: c0 + 256 j ..
+    float2 w[P], dw[P], db[P];
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+        Vals<VEC> v;
+        v.fill(1.f);
+        if (a.w && c0 + 256 * j < D) v.load(a.w + c0 + 256 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[j * 4 + i] = v.p[i], dw[j * 4 + i] = db[j * 4 + i] = make_float2(0.f, 0.f);
+    }
+    __syncthreads();
+    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int st = seen % kRowStages;
+        if (ok) ok = rows_wait(&full[st], (seen / kRowStages) & 1, a.ctl);
+        ++seen;
+        __syncwarp();
+        const T *xs = reinterpret_cast<const T *>(dynamic + (size_t)st * stageb) + mine * D, *ds = xs + RT * D;
+        const long long row = tile * RT + mine;
+        const bool live = row < a.R;
+        float2 x[P], d[P], s = make_float2(0.f, 0.f), sd = s, t = s, td = s;
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            Raw<T, VEC> rx, rd;
+            rx.zero(), rd.zero();
+            if (live && c0 + 256 * j < D) rx.shared(xs + c0 + 256 * j), rd.shared(ds + c0 + 256 * j);
+            rx.get(reinterpret_cast<float *>(x + j * 4)), rd.get(reinterpret_cast<float *>(d + j * 4));
+#pragma unroll
+            for (int i = j * 4; i < j * 4 + 4; ++i) s = add2(s, x[i]), sd = fma2(d[i], w[i], sd);
+        }
+        __syncthreads();   // the tile has been read
+        if (tid == 0) send(tile + (long long)kRowStages * gridDim.x);
+        auto row_sum = [&](float &u, float &v, int round) {
+#pragma unroll
+            for (int o = 16; o; o /= 2) u += __shfl_xor_sync(0xffffffffu, u, o), v += __shfl_xor_sync(0xffffffffu, v, o);
+            if constexpr (WPR > 1) {
+                if (lane == 0) slots[round][warp][0] = u, slots[round][warp][1] = v;
+                qs::named_bar_sync(1 + mine, WPR * 32);
+                u = v = 0.f;
+#pragma unroll
+                for (int i = 0; i < WPR; ++i) u += slots[round][mine * WPR + i][0], v += slots[round][mine * WPR + i][1];
+            }
+        };
+        float u = total(s), v = total(sd);
+        row_sum(u, v, 0);
+        const float m = u * a.inv_d, dn = v * a.inv_d;
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j)
+            if (c0 + 256 * j < D)
+#pragma unroll
+                for (int i = j * 4; i < j * 4 + 4; ++i) {
+                    x[i] = add2(x[i], make_float2(-m, -m));
+                    t = fma2(x[i], x[i], t);
+                    td = fma2(mul2(d[i], w[i]), x[i], td);
+                }
+        u = total(t), v = total(td);
+        row_sum(u, v, 1);
+        const float r = 1.f / sqrtf(fmaf(u, a.inv_d, a.eps)), dot = v * r * a.inv_d;
+        if (live) {
+            T *out = static_cast<T *>(a.y) + row * D;
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j)
+                if (c0 + 256 * j < D) {
+                    Vals<VEC> o;
+#pragma unroll
+                    for (int i = j * 4; i < j * 4 + 4; ++i) {
+                        const float2 n = mul2(x[i], make_float2(r, r));
+                        dw[i] = fma2(d[i], n, dw[i]), db[i] = add2(db[i], d[i]);
+                        o.p[i - j * 4] = mul2(fma2(n, make_float2(-dot, -dot), fma2(d[i], w[i], make_float2(-dn, -dn))), make_float2(r, r));
+                    }
+                    o.store(out + c0 + 256 * j);
+                }
+        }
+    }
+    if (tid == 0 && !ok)   // a wait ran out: copies may still be in flight
+        for (int i = sent > kRowStages ? sent - kRowStages : 0; i < sent; ++i) rows_wait(&full[i % kRowStages], (i / kRowStages) & 1, a.ctl);
+    if (!a.part) return;
+    // The rows' groups one after the other, in the ring's place.
+    float *sums = reinterpret_cast<float *>(dynamic), *out = a.part + (size_t)blockIdx.x * 2 * D;
+    for (int y = 0; y < RT; ++y) {
+        __syncthreads();
+        if (mine == y)
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j)
+                if (c0 + 256 * j < D)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int c = c0 + 256 * j + i;
+                        const float p = reinterpret_cast<const float *>(dw)[j * VEC + i], q = reinterpret_cast<const float *>(db)[j * VEC + i];
+                        sums[c] = y ? sums[c] + p : p, sums[D + c] = y ? sums[D + c] + q : q;
+                    }
+    }
+    __syncthreads();
+    for (int c = tid; c < 2 * D; c += kRowThreads) out[c] = sums[c];
 }
 
 // dw and db: the sum of the CTAs' parts, 32 columns and 32 groups of parts per CTA.
@@ -687,27 +819,27 @@ extern "C" int quat_layer_norm_bwd(int dtype, float eps, const void *x, const fl
     const int vec = 16 / es;
     const bool wide = D % vec == 0 && ld % vec == 0 && !qsh::misaligned(x) && !qsh::misaligned(d_y) && !qsh::misaligned(d_x) && !qsh::misaligned(w);
     const long long units = wide ? D / vec : D;
-    // Tiles where there are enough of them, and rows fit (8192 values of bfloat16, 4096 of fp32).
+    // Rings of tiles where there are enough of them, and rows fit (8192 values of bfloat16, 4096 of fp32).
     const int cols = 32 * kTileUnits * vec, wpr = D <= cols ? 1 : D <= 2 * cols ? 2 : D <= 4 * cols ? 4 : 8;
     if (wide && D >= 256 && D <= 8 * cols && R >= 32 * (int64_t)sms / wpr) {
-        auto go = [&](auto kernel) {
-            const size_t smem = (size_t)kTileStages * 2 * (16 / wpr) * D * es;
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileStages * 2 * 16 * 32 * kTileUnits * 16) != cudaSuccess) return cudaGetLastError(), (int)QS_ERR_CUDA;
+        auto go = [&](auto kernel, int threads, int stages, int rows, int most) {
+            const size_t smem = (size_t)stages * 2 * rows * D * es;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return cudaGetLastError(), (int)QS_ERR_CUDA;
             unsigned char *ws = nullptr;
             qsh::Hold hold;
             int rc = qsh::workspace(dev, stream, sizeof(qs::WsHeader) + (size_t)sms * 2 * D * 4, &ws, &hold);
             if (rc != QS_OK) return rc;
             a.ctl = {reinterpret_cast<qs::WsHeader *>(ws), -1, qsh::timeout_ns()};
             if (d_w || d_b) a.part = reinterpret_cast<float *>(ws + sizeof(qs::WsHeader));
-            kernel<<<(unsigned)sms, kTileThreads, smem, stream>>>(a);
+            kernel<<<(unsigned)sms, threads, smem, stream>>>(a);
             rc = launched();
             if (rc != QS_OK || !a.part) return rc;
             return weights(a, d_w, d_b, (unsigned)sms, stream);
         };
-        using B = __nv_bfloat16;
-        if (dtype == QS_BF16)
-            return wpr == 1 ? go(norm_tile_kernel<B, 8, 1, 1>) : wpr == 2 ? go(norm_tile_kernel<B, 8, 2, 1>) : wpr == 4 ? go(norm_tile_kernel<B, 8, 4, 2>) : go(norm_tile_kernel<B, 8, 8, 4>);
-        return wpr == 1 ? go(norm_tile_kernel<float, 4, 1, 1>) : wpr == 2 ? go(norm_tile_kernel<float, 4, 2, 1>) : wpr == 4 ? go(norm_tile_kernel<float, 4, 4, 1>) : go(norm_tile_kernel<float, 4, 8, 2>);
+        auto tile = [&](auto kernel) { return go(kernel, kTileThreads, kTileStages, 16 / wpr, kTileStages * 2 * 16 * 32 * kTileUnits * 16); };
+        auto row = [&](auto kernel) { return go(kernel, kRowThreads, kRowStages, 8 / wpr, kRowStages * 2 * 8 * 32 * kTileUnits * 16); };
+        if (dtype == QS_BF16) return wpr == 1 ? row(norm_row_kernel<1>) : wpr == 2 ? row(norm_row_kernel<2>) : wpr == 4 ? row(norm_row_kernel<4>) : row(norm_row_kernel<8>);
+        return wpr == 1 ? tile(norm_tile_kernel<1, 1>) : wpr == 2 ? tile(norm_tile_kernel<2, 1>) : wpr == 4 ? tile(norm_tile_kernel<4, 1>) : tile(norm_tile_kernel<8, 2>);
     }
     return launch<true>(a, dtype, wide, units, sms, d_w, d_b, dev, stream);
 }
