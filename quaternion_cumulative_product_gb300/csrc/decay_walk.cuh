@@ -20,9 +20,10 @@
 // sum in registers: the tensor cores are kept busy across chunks by roles that run at the same time:
 //
 //     state    two warpgroups: M^T [dv][dk] in fp32 registers, one value row per thread, half of dk
-//              each; M's terms to shared memory; the scaling of x M; out to memory
-//     convert  two warpgroups: P from S = x y^T (in place, in tensor memory), h z as three terms
-//     one warp each: products, copies (TMA into a ring of tiles), gates
+//              each; M's terms to shared memory; the terms of the second half of h z; out to memory
+//     convert  two warpgroups: the terms of the first half of h z; P from S = x y^T (in place, in tensor
+//              memory); f Y and its products with `beside`
+//     one warp each: products, copies (TMA into a ring of tiles), gates, stores
 //
 // Per chunk, in the order of issue: S, dM = (h z)^T y over the first 64 steps, Y = x M, dM over the
 // other 64, out = f Y + P z.
@@ -38,7 +39,7 @@
 // 3.4 us a chunk; dv 109, dq 170 and dk 190 us (they also write and read the states, 268 MB each).
 // 1 x 131072 x 16 x 64 in 19 segments: 375 us, the sums 121 and the walk 250 of them.
 // Bound: the products, beside the other roles' use of shared memory.  48 of 128 x 128 x 16 a chunk (S 8,
-// Y 8, dM 24, P z 8) take 80 to 100 cycles each (64 alone), 4 400 of a chunk's 6 500; the rest is
+// Y 8, dM 24, P z 8) take 80 to 100 cycles each (64 at the peak rate), 4 400 of a chunk's 6 500; the rest is
 // the way from one to the next: out, then the next chunk's S, then its P.
 #pragma once
 
