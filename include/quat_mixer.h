@@ -156,10 +156,9 @@ int quat_delta_step(int dtype, int gate_dtype, float scale,
  * on, never another sequence's.  With offsets, rows from offsets[N] on (where that is
  * less than S) are not used, and left as they were in every output.
  *
- * Precision: as the delta rule, but for the values of which only bfloat16 outputs are
- * made (o; d_q, d_k, d_v): the products <q_t, k_s> D_ts and the state that enters a chunk
- * are rounded to bfloat16 there (2^-9 each, independent of the output's own rounding; the
- * state itself stays fp32).  d_g leaves out 2^-24 of a product, with bfloat16 gates 2^-15.
+ * Precision: as the delta rule (o, d_q, d_k and d_v in bfloat16 leave out 2^-17 of a
+ * product; states and fp32 outputs 2^-24).  d_g leaves out 2^-24 of a product, with bfloat16
+ * gates 2^-17.
  */
 int quat_decay_fwd(int dtype, int gate_dtype, float scale,
                    const void *q, const void *k, const void *v, const void *g, const float *init,

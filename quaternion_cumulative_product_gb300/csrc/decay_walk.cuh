@@ -29,17 +29,17 @@
 // other 64, out = f Y + P z.
 //
 // Terms (tensor_core.cuh): h z in three, so that states have fp32 precision (they add up rounded
-// once a chunk).  P and the M of Y, of which only bfloat16 outputs are made, in one: rounded to
-// nearest, their errors are as large as the output's own rounding and independent of it (measured
-// against 64 bits: 1.4 times its error alone; two terms of each took 157 instead of 132 us).  Where Y
-// goes into d_g as well (dots), M has two terms, and a third one for fp32 gates (d_g is then 3e-7 to
-// 6e-7 from 64 bits, with two 2e-6; dq 170 instead of 160 us, dk 190 instead of 181).
+// once a chunk).  P and the M of Y, of which only bfloat16 outputs are made, in two: at most 2^-17 of
+// them is left out, far below the output's own rounding (one term each, 2^-8, would be as large as
+// that: 2.3e-3 instead of 1.7e-3 from 64 bits, for 111 instead of 121 us forward).  Where Y
+// goes into d_g as well (dots) M has a third one for fp32 gates (d_g is then 3e-7 to 6e-7 from 64
+// bits, with two 2e-6).
 //
-// Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 111 us (4.8 TB/s, 0.71 of a copy's rate),
-// 3.4 us a chunk; dv 109, dq 170 and dk 190 us (they also write and read the states, 268 MB each).
-// 1 x 131072 x 16 x 64 in 19 segments: 375 us, the sums 121 and the walk 250 of them.
-// Bound: the products, beside the other roles' use of shared memory.  48 of 128 x 128 x 16 a chunk (S 8,
-// Y 8, dM 24, P z 8) take 80 to 100 cycles each (64 at the peak rate), 4 400 of a chunk's 6 500; the rest is
+// Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 121 us (4.4 TB/s, 0.65 of a copy's rate),
+// 3.7 us a chunk; backward, three walks and the gates' kernel, 625.
+// 1 x 131072 x 16 x 64 in 19 segments: 405 us.
+// Bound: the products, beside the other roles' use of shared memory.  64 of 128 x 128 x 16 a chunk (S 8,
+// Y 16, dM 24, P z 16) take 80 to 100 cycles each where they come in a row (64 at the peak rate); the rest is
 // the way from one to the next: out, then the next chunk's S, then its P.
 #pragma once
 
@@ -121,7 +121,7 @@ struct DecayLayout {
 };
 
 namespace decay_tmem {
-constexpr uint32_t S = 0;     // x y^T (128), then P: each 32 columns give way to their two terms
+constexpr uint32_t S = 0;     // x y^T (128), then P: each 16 columns give way to their two terms
 constexpr uint32_t O = 128;   // x M, scaled, then out
 constexpr uint32_t DM = 256;  // the chunk's part of M'^T
 constexpr uint32_t VL = 384;  // terms of h z, 64 steps (3 x 32)
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = __reduce_min_sync(0xffffffffu, bar.tmem), tl = tm + ((uint32_t)(warp % 4 * 32) << 16);   // this warp's lanes
-    constexpr int terms = dots ? 2 : 1;      // of M
+    constexpr int terms = 2;                // of M
     const bool third = dots && !a.gate16;   // and one more, in the first one's place once that has been multiplied
     bool ok = true;   // none of this thread's waits has run out
     auto tile = [&](int it, int which) { return L::PER * it + which; };   // the it-th chunk's; tile i is in slot i % SLOTS
@@ -565,15 +565,15 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {   // 16 columns of P: every other block of 32, half of it at a time
                     const int cb = part + h / 2 * 2, c0 = cb * 32 + h % 2 * 16;
-                    const uint32_t from = tl + tmem::S + c0, to = tl + tmem::S + cb * 32 + h % 2 * 8;
+                    const uint32_t at = tl + tmem::S + c0;
                     uint32_t r[16];
                     if (rev ? cb < rb : cb > rb) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) r[i] = 0;
-                        tmem_st8(to, r);
+                        for (int i = 0; i < 16; ++i) r[i] = 0;
+                        tmem_st16(at, r);
                         continue;
                     }
-                    tmem_ld16(from, r);
+                    tmem_ld16(at, r);
                     // D_ts = mid_s row, the second factor at most 1 off the diagonal; on it the other way
                     // round, as long as the block's decay is no more than 2^-60, else one exp2 a value.
                     const Sum2 face = rev ? cb ? gt.sum(cb * 32 - 1) : Sum2{0.f, 0.f} : gt.sum(cb * 32 + 31);
@@ -604,11 +604,14 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                     __syncwarp();
                     tmem_wait_ld();
 #pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = mul2(w[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+#pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float2 x = mul2(w[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
-                        r[i] = pack_bf16(x.x, x.y);
+                        uint32_t t[2];
+                        split2<2>(w[i], t);
+                        r[i] = t[0], r[8 + i] = t[1];
                     }
-                    tmem_st8(to, r);
+                    tmem_st16(at, r);
                 }
                 // f Y in place, and its product with the row of `beside`.
                 const float f = rev ? decay(gt.sum(WC - 1), mine) : a.scale * decay(mine, {0.f, 0.f});
@@ -733,9 +736,9 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
                 const uint64_t z = smem_desc(tile_at(tile(it, L::Z)), L::HALF, 1024);
                 if (elect_one() && ok) {
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h)
+                    for (int j = 1; j >= 0; --j)   // the small term first
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ts(tm + tmem::O, tm + tmem::S + h * 64 + k / 2 * 32 + k % 2 * 8, z + ((h * 4 + k) * 2048 >> 4), id_mn, true);
+                        for (int k = 0; k < 8; ++k) mma_ts(tm + tmem::O, tm + tmem::S + k * 16 + j * 8, z + (k * 2048 >> 4), id_mn, true);
                     mma_commit(&bar.out);
                     mma_commit(&bar.empty[tile(it, L::Z) % L::SLOTS]);
                 }
