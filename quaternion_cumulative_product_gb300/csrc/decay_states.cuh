@@ -28,6 +28,7 @@ struct StateArgs {
     DeltaArgs d;
     float *whole;         // [slots, Hv]
     StateSide side[2];
+    bool cut_only;        // of the sequences that are cut only
 };
 
 constexpr int kOwnThreads = 256;
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(kOwnThreads) decay_own_kernel(const __grid_con
     const long long slot = blockIdx.x / a.Hv;
     Seq seq;
     long long c;
-    if (!chunk_of(a, slot, &seq, &c)) return;
+    if (!chunk_of(a, slot, &seq, &c) || (s.cut_only && !is_cut(a, seq))) return;
     const long long t0 = c * DC;
     const int left = (int)min((long long)DC, seq.len - t0);
     if (tid < 32) warp_gates(gt, read_gates<false>(a, seq, t0, head));
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(256) decay_run_kernel(const __grid_constant__ 
     if (e >= size) return;
     const Seq seq = seq_of(a, (long long)(nh / a.Hv));
     const int head = (int)(nh % a.Hv), chunks = (int)((seq.len + DC - 1) / DC);
+    if (s.cut_only && !is_cut(a, seq)) return;
     auto at = [&](int i) { return (size_t)(seq.slot0 + (side.rev ? chunks - 1 - i : i)) * a.Hv + head; };
     float4 m = side.first ? __ldg(reinterpret_cast<const float4 *>(side.first + nh * size + e)) : q_zero();
     constexpr int AHEAD = 8;

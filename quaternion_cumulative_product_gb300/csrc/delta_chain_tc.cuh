@@ -46,11 +46,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     volatile int *gone = &bar.gone;
     const ChunkGates *gates = reinterpret_cast<const ChunkGates *>(sm + L::GATES_AT);
 
-    const Walk walk = walk_of<SUM, true>(a);
+    const Walk walk = walk_of<SUM, true, RULE>(a);
+    if (!RULE && !walk.any) return;
     const int head = walk.head;
     const long long n = walk.n;
     Seq seq = seq_of(a, n);
-    if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
+    const bool parts = a.segs > 1 || (!RULE && is_cut(a, seq));
+    if (parts) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L>(bar, sm32);
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float whole = 0.f;
         bool ok = true;   // none of this thread's waits has run out
         const float *from = a.d_final ? a.d_final + state : nullptr;
-        if (a.segs > 1) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.ds + ((size_t)(seq.slot0 + max(chunks - 1, 0)) * a.Hv + head) * a.Dk * a.Dv) + dv;
+        if (parts) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.ds + ((size_t)(seq.slot0 + max(chunks - 1, 0)) * a.Hv + head) * a.Dk * a.Dv) + dv;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
             float v;

@@ -71,6 +71,7 @@ struct DeltaArgs {
     int sms;   // of the device
     bool gate16;
     bool longest_first;   // packed sequences are walked in order of length
+    long long uncut;      // linear attention, packed: sequences of more chunks than that are walked in segments (segs: 1); 0: none is
     float scale;
     Control ctl;
 };
@@ -96,6 +97,9 @@ __device__ __forceinline__ Seq segment_of(const DeltaArgs &a, const Seq &s, int 
     const long long left = s.len > off ? s.len - off : 0;
     return {s.b, s.s0 + off, left < most ? left : most, s.slot0 + c0};
 }
+
+// Whether a packed sequence is walked in segments.
+__device__ __forceinline__ bool is_cut(const DeltaArgs &a, const Seq &s) { return a.uncut && s.len > a.uncut * DC; }
 
 // The sequence and chunk in a carry slot; false when the slot holds no chunk.
 __device__ __forceinline__ bool chunk_of(const DeltaArgs &a, long long slot, Seq *seq, long long *chunk) {

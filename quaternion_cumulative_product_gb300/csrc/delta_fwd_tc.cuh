@@ -60,11 +60,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     volatile int *gone = &bar.gone;
     const ChunkGates *gates = reinterpret_cast<const ChunkGates *>(sm + L::GATES_AT);
 
-    const Walk walk = walk_of<SUM, false>(a);
+    const Walk walk = walk_of<SUM, false, RULE>(a);
+    if (!RULE && !walk.any) return;
     const int head = walk.head;
     const long long n = walk.n;
     Seq seq = seq_of(a, n);
-    if (a.segs > 1) seq = segment_of(a, seq, walk.seg);
+    const bool parts = a.segs > 1 || (!RULE && is_cut(a, seq));   // it starts from a state between chunks
+    const bool last = !RULE && is_cut(a, seq) ? (walk.seg + 1) * a.seg_chunks * DC >= seq.len : walk.seg == a.segs - 1;
+    if (parts) seq = segment_of(a, seq, walk.seg);
     const int chunks = (int)((seq.len + DC - 1) / DC);
     const int wg = warp_uniform(threadIdx.x / 128), tid = threadIdx.x % 128, warp = warp_uniform(threadIdx.x / 32);
     const uint32_t tm = walk_setup<L>(bar, sm32);
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float whole = 0.f;
         bool ok = true;   // none of this thread's waits has run out
         const float *from = a.init ? a.init + state : nullptr;
-        if (a.segs > 1) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.carries_in + ((size_t)seq.slot0 * a.Hv + head) * a.Dk * a.Dv) + dv;
+        if (parts) from = (RULE ? a.seg_m + walk.at * a.Dk * a.Dv : a.carries_in + ((size_t)seq.slot0 * a.Hv + head) * a.Dk * a.Dv) + dv;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
             float v;
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                 for (int i = 0; i < HALF; ++i)
                     if (col0 + i < a.Dk) *row.sum_out(a, walk, col0 + i) = i % 2 ? m[i / 2].y : m[i / 2].x;
-        } else if (a.fin && in && walk.seg == a.segs - 1)
+        } else if (a.fin && in && last)
 #pragma unroll
             for (int i = 0; i < HALF; ++i)
                 if (col0 + i < a.Dk) a.fin[state + (size_t)(col0 + i) * a.Dv] = i % 2 ? m[i / 2].y : m[i / 2].x;

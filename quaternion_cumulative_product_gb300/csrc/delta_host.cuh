@@ -163,7 +163,7 @@ int launch_walks(DeltaArgs &a, float *seg, cudaStream_t stream) {
         rc = launched();
         if (rc != QS_OK) return rc;
     }
-    return walk(std::false_type(), pairs * a.segs);
+    return walk(std::false_type(), a.uncut ? (a.slots / a.seg_chunks + a.N) * a.Hv : pairs * a.segs);
 }
 
 template <typename T, int NT, int CT, bool RULE = true>

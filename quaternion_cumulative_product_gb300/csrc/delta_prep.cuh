@@ -312,6 +312,7 @@ struct Walk {
     long long n;
     int head, seg, map_from;
     size_t at;   // (n * Hv + head) * segs + seg
+    bool any;    // there is one (linear attention's cuts of packed sequences: the host knows a bound only)
 };
 
 // The sequence of CTA row i where packed sequences are walked longest first: the one that
@@ -337,11 +338,56 @@ __device__ __forceinline__ unsigned by_length(const int *offsets, long long N, l
     return *mine;
 }
 
-template <bool SUM, bool BWD>
+// The i-th segment of a packed batch whose long sequences are cut into segments of `most` chunks (the others,
+// empty ones too, are one), false past the last: longest sequences first, or, of more than kMostOrdered sequences, at
+// (first slot of the sequence) / most + n + segment.  All threads of the CTA.
+template <int THREADS>
+__device__ __forceinline__ bool cut_segment(const DeltaArgs &a, unsigned i, int *chunks, int *before, volatile unsigned *mine, Walk *w) {
+    const int most = (int)a.seg_chunks;
+    if (a.N > kMostOrdered) {
+        long long lo = 0, hi = a.N;
+        while (hi - lo > 1) {
+            const long long mid = (lo + hi) / 2;
+            if (seq_of(a, mid).slot0 / most + mid <= i) lo = mid;
+            else hi = mid;
+        }
+        const Seq seq = seq_of(a, lo);
+        const long long seg = (long long)i - (seq.slot0 / most + lo);
+        w->n = lo, w->seg = (int)seg;
+        return seg == 0 || (seg > 0 && is_cut(a, seq) && seg * most * DC < seq.len);
+    }
+    const unsigned t = threadIdx.x % kMostOrdered, part = threadIdx.x / kMostOrdered;
+    constexpr unsigned kParts = THREADS / kMostOrdered;
+    int *segs = chunks + kMostOrdered;
+    if (part == 0) {
+        chunks[t] = -1, segs[t] = 0;
+        if (t < a.N) {
+            const Seq seq = seq_of(a, t);
+            chunks[t] = (int)((seq.len + DC - 1) / DC);
+            segs[t] = is_cut(a, seq) ? (chunks[t] + most - 1) / most : 1;
+        }
+        before[t] = 0;
+        if (t == 0) mine[0] = kMostOrdered;
+    }
+    __syncthreads();
+    const int c = chunks[t];
+    int n = 0;
+#pragma unroll 8
+    for (unsigned u = part; u < kMostOrdered; u += kParts) n += chunks[u] > c || (chunks[u] == c && u < t) ? segs[u] : 0;
+    atomicAdd(&before[t], n);   // (whole numbers: their order changes nothing)
+    __syncthreads();
+    if (part == 0 && (int)i >= before[t] && (int)i < before[t] + segs[t]) mine[0] = t, mine[1] = i - before[t];
+    __syncthreads();
+    w->n = mine[0], w->seg = (int)mine[1];
+    return mine[0] < kMostOrdered;
+}
+
+template <bool SUM, bool BWD, bool RULE = true>
 __device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
     Walk w;
     unsigned i = blockIdx.x;
     w.map_from = 128;
+    w.any = true;
     int segs = a.segs;
     if (SUM) {
         segs -= 1;
@@ -355,9 +401,10 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &a) {
     w.head = i % a.Hv, i /= a.Hv;
     w.seg = i % segs + (SUM && BWD ? 1 : 0);
     w.n = i / segs;
-    __shared__ int lengths[2][kMostOrdered];
-    __shared__ unsigned mine;
-    if (!SUM && a.longest_first) w.n = by_length<kWalkThreads>(a.offsets, a.N, a.S, (unsigned)w.n, lengths[0], lengths[1], &mine);
+    __shared__ int lengths[RULE ? 2 : 3][kMostOrdered];
+    __shared__ unsigned mine[RULE ? 1 : 2];
+    if (!RULE && a.uncut) w.any = cut_segment<kWalkThreads>(a, i, lengths[0], lengths[RULE ? 0 : 2], mine, &w);
+    else if (!SUM && a.longest_first) w.n = by_length<kWalkThreads>(a.offsets, a.N, a.S, (unsigned)w.n, lengths[0], lengths[1], mine);
     w.at = ((size_t)w.n * a.Hv + w.head) * a.segs + w.seg;
     return w;
 }
