@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
     if (!SUM && a.longest_first) {
         int *scratch = reinterpret_cast<int *>(sm);
         n = by_length<kDecayThreads>(a.offsets, a.N, a.S, (unsigned)n, scratch, scratch + kMostOrdered, reinterpret_cast<unsigned *>(scratch + 2 * kMostOrdered));
-        __syncthreads();   // (all have read it before the tiles come)
+        fence_proxy_async_smem();   // (the tiles come there, by the async proxy, once all have read it)
+        __syncthreads();
     }
     long long b = n, s0 = 0, len = a.S, slot0 = n * a.NC;
     if (a.offsets) {

@@ -149,3 +149,20 @@ def test_one_sequence_packed_or_not(torch):
     for name in packed:
         a, b = wide(packed[name]), wide(whole[name])
         assert np.abs(a - b).max() <= 2 * F32 * np.abs(b).max(), name
+
+
+def test_walks_in_order_of_length_repeat(torch):
+    """More bfloat16 walks than run at once, the longest first: their order is worked out where the tiles then come,
+    and the results are the same every time, and those of the sequences by themselves."""
+    offsets = [0, 130, 1430, 1500, 2100, 2101, 3000]
+    x = inputs(torch, offsets, 32, 32, 64, 64, seed=9, dtype=torch.bfloat16)
+    first = run(x)
+    for _ in range(20):
+        for name, again in run(x).items():
+            assert torch.equal(again, first[name]), name
+    a, b = offsets[1:3]
+    alone = {n: x[n][:, a:b].contiguous() for n in ("q", "k", "v", "g", "d_o")}
+    alone |= {"init": x["init"][1:2].clone(), "d_final": x["d_final"][1:2].clone(), "offsets": torch.tensor([0, b - a], dtype=torch.int32, device="cuda")}
+    for name, got in run(alone).items():
+        want = first[name][1:2] if name in ("final", "d_init") else first[name][:, a:b]
+        assert torch.equal(got, want), name
