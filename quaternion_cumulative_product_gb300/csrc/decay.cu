@@ -58,7 +58,10 @@ int launch_states(const StateArgs &s, unsigned sides, cudaStream_t stream) {
     }
     const long long parts = (d.Dk * d.Dv / 4 + 255) / 256;
     if (d.N * d.Hv * parts >= 1ll << 31) return QS_ERR_DIMS;
-    return early(qsh::launch_next(decay_run_kernel, dim3((unsigned)(d.N * d.Hv * parts), sides), 256, 0, stream, s, (unsigned)parts));
+    const dim3 grid((unsigned)(d.N * d.Hv * parts), sides);
+    if (d.slots > 0) return early(qsh::launch_next(decay_run_kernel, grid, 256, 0, stream, s, (unsigned)parts));
+    decay_run_kernel<<<grid, 256, 0, stream>>>(s, (unsigned)parts);   // the call's first kernel: it reads what others have left on the stream
+    return launched();
 }
 
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
