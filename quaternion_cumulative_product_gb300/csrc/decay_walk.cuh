@@ -152,8 +152,11 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ bool walk_wait(uint64_t *bar, uint32_t parity, volatile int *gone, const Control &ctl) {
     unsigned long long t0 = 0;
     while (!mbar_sleep(bar, parity)) {
+        if (t0 == 0) {
+            wait_for_last();   // (the limit is this kernel's own: what it waits for may in turn wait for the kernel before)
+            t0 = global_timer_ns();
+        }
         const unsigned long long now = global_timer_ns();
-        if (t0 == 0) t0 = now;
         if (*gone || now - t0 > ctl.timeout_ns) {
             *gone = 1;   // (recorded once, at the kernel's end: the code of each wait stays short)
             return false;

@@ -33,3 +33,27 @@ def test_without_steps_behind_a_writer(torch, dt):
     for i, pair in enumerate(got, 1):
         for t in pair:
             assert (t == i).all(), i
+
+
+def test_limit_of_waits_is_a_kernels_own(torch):
+    """A walk of one long packed sequence takes many times the limit of a wait, and the next walk, started early, waits
+    for it: none of the waits inside either is long, and none is reported.  (2^19 steps: 4096 chunks of at least 2 us a walk,
+    8 ms; a limit of 2 ms.)"""
+    S = 1 << 19
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v, d_o = (torch.randn(1, S, 1, 64, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    g = -torch.rand(1, S, 1, generator=gen, device="cuda")
+    offsets = torch.tensor([0, S], dtype=torch.int32, device="cuda")
+    args = (q, k, v, g, d_o)
+    want = qs.quat_decay_bwd(*args, offsets=offsets)
+    assert qs.quat_cumprod_status() == qs.QS_OK
+    lib = qs.load_library()
+    try:
+        lib.quat_cumprod_debug_set_timeout_ns(2_000_000)
+        got = qs.quat_decay_bwd(*args, offsets=offsets)
+        torch.cuda.synchronize()
+    finally:
+        lib.quat_cumprod_debug_set_timeout_ns(0)
+    assert qs.quat_cumprod_status() == qs.QS_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
