@@ -62,7 +62,7 @@ struct DecayRole {
     float *fin;              // state that leaves, or NULL
     float *dump;             // state that enters each chunk [slots, Hv, D * D], or NULL
     const float *other;      // another walk's states at the same places: cross = exp(G_C) <other, M>
-    float *cross;            // [slots, Hv]
+    float *cross;            // [slots, Hv, 8]: a part for each warp of the state's
     const float *seg_m;      // state that enters each segment
     float *seg_own, *seg_decay;
     int gx, gy, gz, gb;      // value heads that share a head of x, y, z, beside
@@ -91,7 +91,7 @@ __device__ __forceinline__ size_t state_at(int j4, int wg, int lane) {
 struct __align__(16) WalkGates {
     float hi[WC];      // G_t = hi + lo, in base-2 units
     float mid[WC];     // decay between s and the end of its 32 steps that faces the others: h_s = mid_s edge_{s/32}
-    __half lo[WC];     // (at most half an ulp of hi: 11 bits of it leave out 2^-36 of G)
+    __half lo[WC];     // (at most half an ulp of hi; its rounding leaves out at most 2^-25 of G's unit below 1024, 2^-36 of G above)
     float edge[4], whole;   // decay between the blocks' faces and where the chunk's state is; exp(G_C)
     __device__ __forceinline__ Sum2 sum(int t) const { return {hi[t], __half2float(lo[t])}; }
 };
@@ -190,8 +190,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
-// One warp: the gates of a chunk from its log decays (four steps per lane, zeros past the end).
-__device__ __forceinline__ void walk_gates(WalkGates &s, const float *raw, bool rev) {
+// One warp: the gates of a chunk from its log decays (four steps per lane, zeros past the end); returns their whole sum.
+__device__ __forceinline__ Sum2 walk_gates(WalkGates &s, const float *raw, bool rev) {
     const int lane = threadIdx.x % 32;
     Sum2 in[4], run = {0.f, 0.f};
 #pragma unroll
@@ -215,6 +215,7 @@ __device__ __forceinline__ void walk_gates(WalkGates &s, const float *raw, bool 
     }
     if (lane % 8 == 0) s.edge[lane / 8] = rev ? decay(face, {0.f, 0.f}) : decay(end, face);
     if (lane == 31) s.whole = decay(end, {0.f, 0.f});
+    return end;
 }
 
 // Sixteen values of a row, n of them exist (a multiple of 8).
@@ -830,9 +831,9 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_walk_kernel(const __gr
         for (int it = 0; it < chunks; ++it) {
             const int gb = it % L::GB;
             ok &= all_wait(&bar.gfree[gb], ((it / L::GB) & 1) ^ 1);
-            walk_gates(gates[gb], raw, rev);
+            const Sum2 end = walk_gates(gates[gb], raw, rev);
+            if (SUM) all = sum2_add(all, end);
             __syncwarp();
-            if (SUM) all = sum2_add(all, gates[gb].sum(WC - 1));
             warp_arrive(&bar.gfull[gb]);
             if (it + 1 < chunks) {
                 read(it + 1);

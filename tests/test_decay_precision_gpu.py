@@ -125,3 +125,16 @@ def test_gates_gradient_has_three_terms_of_the_state(torch, D):
     d_g = wide(qs.quat_decay_bwd(none, pick, pick, g, none, ones, None, scale=scale)[3])[0, :, 0]
     want = c * np.arange(S)
     assert (np.abs(d_g - want) <= 2.0 ** -20 * want).all(), np.abs(d_g[1:] / want[1:] - 1).max()
+
+
+def test_decay_of_long_segments(torch):
+    """An initial state alone, decayed over 1024 chunks in many segments: exp(sum of g) of it.  A segment's decay comes from
+    the sum of its log decays, kept in two floats: the total's rounding in base-2 units (2^-24 of 24 at most), and in each of at most
+    64 segments and, in the last, 1024 / 2 chunks an exp2 (2^-22) and a product (2^-24)."""
+    S = 131072
+    g = torch.full((1, S, 1), -1.3e-4, device="cuda")
+    zero = torch.zeros(1, S, 1, 64, device="cuda", dtype=torch.bfloat16)
+    init = torch.ones(1, 1, 64, 64, device="cuda")
+    _, final = qs.quat_decay_fwd(zero, zero, zero, g, init)
+    want = np.exp(g.double().sum().item())
+    assert np.abs(wide(final) / want - 1).max() <= 24 * 2.0 ** -24 + (64 + 512) * (2.0 ** -22 + 2.0 ** -24)
