@@ -121,16 +121,21 @@ class QuatMixerBlock(torch.nn.Module):
     """``x + dropout(mixer(layer_norm(x)))`` around a mixer of ``width``.
 
     ``key`` (a buffer: seed, offset) draws the dropout's mask; its offset is counted up by one
-    each time the block trains, on the device, so that a captured step draws anew too.
+    each time the block trains, on the device, so that a captured step draws anew too.  Equal keys
+    drop the same positions: without a ``seed`` a block takes one from torch's generator (``torch.manual_seed``),
+    another for each block.  Replicas of a block want seeds of their own (a copy of a block, or a
+    wrapper that broadcasts buffers, hands the first one's on).
     (A forward that is run again for its gradients, as under activation checkpointing, would draw
     another mask than the first one's: ``p`` must be 0 there.)
     """
 
-    def __init__(self, mixer, width, p=0.0, eps=1e-5, seed=0, device="cuda"):
+    def __init__(self, mixer, width, p=0.0, eps=1e-5, seed=None, device="cuda"):
         super().__init__()
         self.mixer, self.p, self.eps = mixer, p, eps
         self.w = torch.nn.Parameter(torch.ones(width, device=device))
         self.b = torch.nn.Parameter(torch.zeros(width, device=device))
+        if seed is None:
+            seed = int(torch.randint(2 ** 63 - 1, (), device="cpu"))
         self.register_buffer("key", torch.tensor([seed, 0], dtype=torch.int64, device=device))
 
     def forward(self, x, cache: MixerCache | None = None):

@@ -1,0 +1,48 @@
+"""The residual block's keys on the CPU, around plain forms: which masks blocks draw, and when they are the same."""
+from __future__ import annotations
+
+import pytest
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    pytest.importorskip("torch")
+    import block_plain
+    from quaternion_cumulative_product_gb300 import layer
+    block_plain.install(monkeypatch, layer)
+    return layer
+
+
+def stack(layer, n=2, **kw):
+    """Blocks of one shape, whose mixers give ones: what a block drops is seen in its output."""
+    import torch
+
+    class Ones(torch.nn.Module):
+        def forward(self, x, cache):
+            return torch.ones_like(x), cache
+
+    return [layer.QuatMixerBlock(Ones(), 16, p=0.5, device="cpu", **kw) for _ in range(n)]
+
+
+def dropped(block):
+    import torch
+    return block(torch.zeros(2, 32, 16))[0] == 0
+
+
+def test_blocks_of_a_stack_drop_different_positions(layer):
+    import torch
+    a, b = (dropped(block) for block in stack(layer))
+    # 1024 positions, half of them dropped in each: half of them alike, 512 of deviation 16.
+    assert 512 - 160 < int((a == b).sum()) < 512 + 160
+    torch.manual_seed(3)
+    first = [dropped(block) for block in stack(layer)]
+    torch.manual_seed(3)
+    assert all(torch.equal(x, dropped(block)) for x, block in zip(first, stack(layer)))
+
+
+def test_a_seed_is_taken_as_it_is(layer):
+    import torch
+    state = torch.get_rng_state()
+    a, b = stack(layer, seed=5)
+    assert a.key.tolist() == b.key.tolist() == [5, 0] and torch.equal(torch.get_rng_state(), state)
+    assert torch.equal(dropped(a), dropped(b))
