@@ -125,8 +125,10 @@ class QuatMixerBlock(torch.nn.Module):
     drop the same positions: without a ``seed`` a block takes one from torch's generator (``torch.manual_seed``),
     another for each block.  Replicas of a block want seeds of their own (a copy of a block, or a
     wrapper that broadcasts buffers, hands the first one's on).
-    (A forward that is run again for its gradients, as under activation checkpointing, would draw
-    another mask than the first one's: ``p`` must be 0 there.)
+
+    A forward that is run again for its gradients (activation checkpointing) has to draw the first
+    one's mask: take ``key = block.next_key()`` outside of it and pass ``block(x, cache, key)``.  Without
+    a key such a forward raises.
     """
 
     def __init__(self, mixer, width, p=0.0, eps=1e-5, seed=None, device="cuda"):
@@ -138,13 +140,23 @@ class QuatMixerBlock(torch.nn.Module):
             seed = int(torch.randint(2 ** 63 - 1, (), device="cpu"))
         self.register_buffer("key", torch.tensor([seed, 0], dtype=torch.int64, device=device))
 
-    def forward(self, x, cache: MixerCache | None = None):
-        """``x`` [B,S,width] -> (y [B,S,width], cache), as the mixer's."""
-        y, cache = self.mixer(quat_layer_norm(x, self.w, self.b, eps=self.eps), cache)
-        if not self.training or self.p == 0:
-            return x + y, cache
-        y = quat_dropout(y, self.key, self.p, x)
+    def next_key(self):
+        """The key that the next mask is drawn with, counted up: for a forward that is given its key."""
+        key = self.key.clone()
         self.key[1] += 1
+        return key
+
+    def forward(self, x, cache: MixerCache | None = None, key=None):
+        """``x`` [B,S,width] -> (y [B,S,width], cache), as the mixer's.  ``key``: the dropout's (None: the block's, counted up)."""
+        drop = self.training and self.p > 0
+        if drop and key is None and torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("a forward that runs again inside a backward needs the key of its first run: pass key=block.next_key()")
+        y, cache = self.mixer(quat_layer_norm(x, self.w, self.b, eps=self.eps), cache)
+        if not drop:
+            return x + y, cache
+        y = quat_dropout(y, self.key if key is None else key, self.p, x)
+        if key is None:
+            self.key[1] += 1
         return y, cache
 
     @torch.no_grad()

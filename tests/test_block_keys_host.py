@@ -46,3 +46,34 @@ def test_a_seed_is_taken_as_it_is(layer):
     a, b = stack(layer, seed=5)
     assert a.key.tolist() == b.key.tolist() == [5, 0] and torch.equal(torch.get_rng_state(), state)
     assert torch.equal(dropped(a), dropped(b))
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_checkpointing(layer, reentrant):
+    """With its key handed in, a forward that runs again gives the gradients of the first; without one it is refused."""
+    import torch
+    from torch.utils.checkpoint import checkpoint
+    torch.manual_seed(0)
+    block = layer.QuatMixerBlock(layer.QuatDecayMixer(16, 1, 8, dtype=torch.float32, device="cpu"), 16, p=0.5, seed=7, device="cpu")
+    x, d_y = torch.randn(1, 6, 16, requires_grad=True), torch.randn(1, 6, 16)
+    leaves = [x, *block.parameters()]
+
+    def grads(y):
+        for t in leaves:
+            t.grad = None
+        (y * d_y).sum().backward()
+        return [t.grad for t in leaves]
+
+    want = grads(block(x)[0])
+    assert block.key.tolist() == [7, 1]
+    block.key[1] = 0
+    key = block.next_key()
+    assert key.tolist() == [7, 0] and block.key.tolist() == [7, 1]
+    got = grads(checkpoint(lambda t, k: block(t, None, k)[0], x, key, use_reentrant=reentrant))
+    assert block.key.tolist() == [7, 1] and all(torch.equal(a, b) for a, b in zip(got, want))
+    y = checkpoint(lambda t: block(t)[0], x, use_reentrant=reentrant)
+    with pytest.raises(RuntimeError, match="next_key"):
+        y.sum().backward()
+    block.eval()
+    y = checkpoint(lambda t: block(t)[0], x, use_reentrant=reentrant)   # nothing is drawn
+    y.sum().backward()
