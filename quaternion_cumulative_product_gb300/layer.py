@@ -84,7 +84,7 @@ class QuatDeltaMixer(torch.nn.Module):
         q, k, v, gates, turn = self._project(x)
         start = self._identity(B, x.device) if cache is None else cache.turn
         cum = quat_cumprod(turn, start, save_carries=True)
-        q, k = quat_norm_rotate(q, k, cum, self.w_q, self.w_k)
+        q, k = quat_norm_rotate(q, k, cum, self.w_q.float(), self.w_k.float())
         o, state = self._attend(q, k, v, gates, None if cache is None else cache.state)
         # A copy: a view would keep all of cum, and step() would write into what autograd has saved.
         last = (cum[:, -1] if S else start).detach().clone(memory_format=torch.contiguous_format)
@@ -96,7 +96,7 @@ class QuatDeltaMixer(torch.nn.Module):
         q, k, v, gates, turn = self._project(x)
         cum = quat_cumprod_fwd(turn, cache.turn)
         cache.turn.copy_(cum[:, -1])
-        q, k = quat_norm_rotate_fwd(q, k, cum, self.w_q, self.w_k)
+        q, k = quat_norm_rotate_fwd(q, k, cum, self.w_q.float(), self.w_k.float())
         o = self._attend_step(q, k, v, gates, cache.state)
         return self.out(o.flatten(2))
 
@@ -151,7 +151,7 @@ class QuatMixerBlock(torch.nn.Module):
         drop = self.training and self.p > 0
         if drop and key is None and torch._C._current_graph_task_id() != -1:
             raise RuntimeError("a forward that runs again inside a backward needs the key of its first run: pass key=block.next_key()")
-        y, cache = self.mixer(quat_layer_norm(x, self.w, self.b, eps=self.eps), cache)
+        y, cache = self.mixer(quat_layer_norm(x, self.w.float(), self.b.float(), eps=self.eps), cache)
         if not drop:
             return x + y, cache
         y = quat_dropout(y, self.key if key is None else key, self.p, x)
@@ -162,4 +162,4 @@ class QuatMixerBlock(torch.nn.Module):
     @torch.no_grad()
     def step(self, x, cache: MixerCache):
         """One token per sequence: ``x`` [B,1,width] -> y [B,1,width]; ``cache`` moves on in place."""
-        return x + self.mixer.step(quat_layer_norm_fwd(x, self.w, self.b, eps=self.eps), cache)
+        return x + self.mixer.step(quat_layer_norm_fwd(x, self.w.float(), self.b.float(), eps=self.eps), cache)
