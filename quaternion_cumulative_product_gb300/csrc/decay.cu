@@ -268,10 +268,14 @@ extern "C" int quat_decay_fwd(int dtype, int gate_dtype, float scale, const void
     if (dtype == QS_BF16) return forward16(a, dev, sms, stream);
     unsigned char *ws = nullptr;
     cut_states(a, sms);
-    const bool parts = a.segs > 1 || a.uncut;
+    bool parts = a.segs > 1 || a.uncut;
     const size_t kept = parts ? (size_t)a.slots * Hv * Dk * Dv : 0, wholes = parts ? (size_t)a.slots * Hv : 0;
     qsh::Hold hold;
     int wc = qsh::workspace(dev, stream, sizeof(WsHeader) + (kept + wholes) * 4, &ws, &hold);
+    if (wc == QS_ERR_NOMEM && a.uncut) {   // no room for the states (half of the tensors' bytes): whole walks, which take none
+        hold = {}, parts = false, a.uncut = 0;
+        wc = qsh::workspace(dev, stream, sizeof(WsHeader), &ws, &hold);
+    }
     if (wc != QS_OK) return wc;
     float *carries = reinterpret_cast<float *>(ws + sizeof(WsHeader));
     a.ctl = {reinterpret_cast<WsHeader *>(ws), qsh::stall_tile(), qsh::timeout_ns()};

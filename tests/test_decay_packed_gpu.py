@@ -166,3 +166,26 @@ def test_walks_in_order_of_length_repeat(torch):
     for name, got in run(alone).items():
         want = first[name][1:2] if name in ("final", "d_init") else first[name][:, a:b]
         assert torch.equal(got, want), name
+
+
+def test_without_room_for_the_states(torch):
+    """In a capture scratch does not grow: without room for the states of a cut, sequences are walked whole, as a call with
+    little memory left does, and the results are as near."""
+    x = inputs(torch, [0, 1500, 2000], 1, 2, 64, 64, seed=10)
+    small = inputs(torch, [0, 20], 1, 1, 64, 64, seed=11)
+    forward = lambda x: qs.quat_decay_fwd(x["q"], x["k"], x["v"], x["g"], x["init"], offsets=x["offsets"])  # noqa: E731
+    want = reference(x, 64 ** -0.5)
+    # Scratch goes with the stream, which torch may hand out again: one of many that has none of this size yet.
+    for _ in range(40):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            forward(small)
+            stream.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                out = forward(x)
+            graph.replay()
+            stream.synchronize()
+            assert qs.quat_cumprod_status(stream=stream) == qs.QS_OK
+        for name, got in zip(("o", "final"), out):
+            assert np.abs(wide(got) - want[name]).max() <= F32 * np.abs(want[name]).max(), name
