@@ -4,7 +4,7 @@
 // bfloat16: the walk of decay_walk.cuh; backward three of them (dq, dk, dv) and decay_gate.cuh.
 // fp32, whose values are three terms each and take three times the room: the states of all chunks
 // at once (decay_states.cuh), then the delta rule's kernels without its errors (RULE,
-// delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 190 us; with the states walked,
+// delta_prep.cuh).  4 x 1000 x 8 heads of 64, fp32, both ways: 194 us; with the states walked,
 // twice where sequences are cut, 326 us.
 #include <algorithm>
 
@@ -67,7 +67,7 @@ int launch_states(const StateArgs &s, unsigned sides, cudaStream_t stream) {
 // Cuts each sequence into segments where there are too few walks to fill the GPU: a first walk
 // sums up every segment but one, the join hands the states on, and the real walk starts each
 // segment from its own.  Costs are in chunks; a summing walk counts as half a real one (1 x 131072 x
-// 16 x 64: 121 and 256 us).
+// 16 x 64: 125 and 277 us).
 void cut_walks(DecayArgs &a, int sms) {
     a.segs = 1, a.seg_chunks = a.NC;
     a.longest_first = a.offsets && a.N > 1 && a.N <= kMostOrdered && a.N * a.Hv > sms && a.S >= 128 * a.N;

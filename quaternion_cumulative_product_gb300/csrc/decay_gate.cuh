@@ -16,7 +16,7 @@
 // columns a lane still holds; sums of whole rows carry over to the pieces on the right.  The next
 // chunk's tiles come in meanwhile.
 //
-// Bound: memory (the four tensors once more) and the latency of a chunk's steps: 118 us at
+// Bound: memory (the four tensors once more) and the latency of a chunk's steps: 120 us at
 // 8 x 4096 x 16 x 128, 537 MB, 4.5 TB/s (a CTA for each chunk 142 us; with eight warps instead of
 // sixteen and without the next CTA's tiles in L2 180).
 #pragma once

@@ -36,8 +36,8 @@
 // bits, with two 2e-6).
 //
 // Measured, 8 x 4096 x 16 x 128 (128 walks of 32 chunks): forward 121 us (4.4 TB/s, 0.65 of a copy's rate),
-// 3.7 us a chunk; backward, three walks and the gates' kernel, 625.
-// 1 x 131072 x 16 x 64 in 19 segments: 405 us.
+// 3.7 us a chunk; dv 118, dq 174 and dk 193 us (they also write and read the states, 268 MB each).
+// 1 x 131072 x 16 x 64 in 19 segments: 409 us, the sums 125 and the walk 277 of them.
 // Bound: the products, beside the other roles' use of shared memory.  64 of 128 x 128 x 16 a chunk (S 8,
 // Y 16, dM 24, P z 16) take 80 to 100 cycles each where they come in a row (64 at the peak rate); the rest is
 // the way from one to the next: out, then the next chunk's S, then its P.

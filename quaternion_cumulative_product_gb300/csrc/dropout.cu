@@ -7,8 +7,9 @@
 // Values are selected, not multiplied: a dropped NaN is gone.
 //
 // Bound: fp32, memory (8 or 12 bytes a value: 60 us with a residual, 44 us without at 32 M values,
-// 0.99 and 0.91 of a copy's rate); bfloat16, the generator (two 32 x 32 -> 64 bit products a
-// round for four values: 87 and 70 us at 64 M values, 0.68 and 0.56).  CTAs are persistent: a
+// 0.99 and 0.91 of a copy's rate); bfloat16, arithmetic (the generator's two 32 x 32 -> 64 bit products a
+// round for four values keep their pipe busy for 65 and 61% of the time, the other integer pipe 54%, issue
+// slots 60 and 56%: 87 and 70 us at 64 M values, 0.68 and 0.56).  CTAs are persistent: a
 // thread makes the rounds' keys once, and its next piece is on its way while one is worked on.
 #include <cmath>
 

@@ -382,6 +382,7 @@ def quat_decay_fwd(q, k, v, g, init=None, *, scale=None, offsets=None):
     ``M_t = exp(g_t) M_{t-1} + k_t v_t^T``, ``o_t = scale * M_t^T q_t`` for each value head,
     with the key head ``h // (Hv // Hk)``.  Tensors, ``init``, ``scale`` and ``offsets`` are
     those of :func:`quat_delta_fwd`, without ``beta`` (a write strength is a factor of ``v``).
+    (Steps behind the last of ``offsets`` belong to no sequence: their outputs and gradients are left unwritten.)
     """
     device, code, gate, (B, S, Hk, Hv, Dk, Dv) = _delta_args(q, k, v, g)
     _no_expanded(q=q, k=k, v=v)
